@@ -69,6 +69,21 @@ class fp8_adam_hyper(ctypes.Structure):
                 ("margin", ctypes.c_int32)]
 
 
+class fp8_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class fp8_block_tensor(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("scale_type", ctypes.c_int32)]
+
+
+SCALE_E8M0, SCALE_F32 = 0, 1
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; call fp8_mixed_precision_amax_gb300.build.build()")
@@ -112,6 +127,19 @@ def _load() -> ctypes.CDLL:
                                     ctypes.POINTER(fp8_recipe), vp, vp, vp, vp, vp],
                                    ctypes.c_int),
     }
+    pm, pb = ctypes.POINTER(fp8_matrix), ctypes.POINTER(fp8_block_tensor)
+    st = ctypes.c_int
+    sig.update({
+        "fp8_block_quantize": ([pm, pb, pb, vp], st),
+        "fp8_block_dequantize": ([pb, pm, vp], st),
+        "fp8_block_gemm_tn": ([pb, pb, pm, vp], st),
+        "fp8_layernorm_fwd": ([pm, vp, vp, i32, ctypes.c_float, pm, pb, pb, vp, vp, vp], st),
+        "fp8_layernorm_bwd": ([pm, pm, pb, vp, i32, vp, vp, pm, vp, vp, vp, i64, vp], st),
+        "fp8_layernorm_bwd_workspace": ([i64, i64], i64),
+        "fp8_layernorm_recompute": ([pb, vp, vp, i32, vp, vp, pb, vp], st),
+        "fp8_swiglu_fwd": ([pm, pb, pb, vp], st),
+        "fp8_swiglu_bwd": ([pm, pb, pb, pb, pb, vp], st),
+    })
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
@@ -681,3 +709,215 @@ def fp8_allreduce(grad: torch.Tensor, fmt: int, margin: int = 0, group=None,
         out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
     out.view(-1).copy_(full[:n])
     return out
+
+
+# ---------------------------------------------------------- block scaling --
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_SCALE_TYPES = {torch.uint8: SCALE_E8M0, torch.float32: SCALE_F32}
+
+
+class BlockFp8:
+    """An FP8 matrix with one scale for each 128 columns of a row (``block_rows``
+    1: activations, gradients) or for each 128 x 128 tile (128: weights).
+
+    ``codes``   [rows, pitch] uint8, the pitch a multiple of 16 and at least
+                ``cols``; columns from ``cols`` on are ignored
+    ``scales``  [ceil(rows / block_rows), pitch]: uint8, a byte b for
+                2^(b - 127), the pitch a multiple of 4; or float32
+    """
+    __slots__ = ("codes", "scales", "cols", "fmt", "block_rows")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int = E4M3,
+                 block_rows: int = 1):
+        self.codes, self.scales, self.cols = codes, scales, cols
+        self.fmt, self.block_rows = fmt, block_rows
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, fmt: int = E4M3, block_rows: int = 1,
+              scale_dtype=torch.uint8, device="cuda") -> "BlockFp8":
+        """Buffers of a [rows, cols] matrix, their contents undefined."""
+        codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.uint8, device=device)
+        scales = torch.empty((-(-rows // block_rows), -(-cols // 512) * 4), dtype=scale_dtype,
+                             device=device)
+        return cls(codes, scales, cols, fmt, block_rows)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.cols)
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes of the codes and the scales."""
+        return self.codes.numel() + self.scales.numel() * self.scales.element_size()
+
+    def dequantize(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        """The matrix in 16 or 32 bits."""
+        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        fp8_block_dequantize(self, out, stream)
+        return out
+
+
+def _block(q: BlockFp8 | None, name: str):
+    if q is None:
+        return None
+    codes, scales = q.codes, q.scales
+    if not codes.is_cuda or not scales.is_cuda:
+        raise ValueError(f"{name} must be in CUDA memory")
+    if not _fp8_view_ok(codes) or codes.dim() != 2:
+        raise ValueError(f"{name}: codes must be a matrix of FP8 codes (uint8 / float8)")
+    if scales.dtype not in _SCALE_TYPES or scales.dim() != 2:
+        raise ValueError(f"{name}: scales must be a matrix of uint8 (E8M0) or float32")
+    rows, pitch = codes.shape
+    if rows and (codes.stride(1) != 1 or pitch < -(-q.cols // 16) * 16):
+        raise ValueError(f"{name}: codes must be contiguous along the columns, {q.cols} of them "
+                         f"rounded up to a multiple of 16; got {tuple(codes.shape)}")
+    nb = -(-q.cols // 128)
+    srows, spitch = scales.shape
+    if q.block_rows > 0 and (srows < -(-rows // q.block_rows) or spitch < nb
+                             or (srows and spitch and scales.stride(1) != 1)):
+        raise ValueError(f"{name}: scales must be [{-(-rows // q.block_rows)}, >= {nb}] and "
+                         f"contiguous along the columns; got {tuple(scales.shape)}")
+    if scales.dtype == torch.uint8 and spitch < -(-nb // 4) * 4:
+        raise ValueError(f"{name}: rows of E8M0 scales must hold whole words of 4; got {spitch}")
+    return fp8_block_tensor(codes.data_ptr(), rows, q.cols, codes.stride(0) if rows > 1 and pitch else pitch,
+                            scales.data_ptr(), scales.stride(0) if srows > 1 and spitch else spitch, q.fmt,
+                            q.block_rows, _SCALE_TYPES[scales.dtype])
+
+
+def _matrix(t: torch.Tensor | None, name: str):
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if cols > 1 and rows and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its columns")
+    return fp8_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 and cols else cols,
+                      _DTYPES[t.dtype])
+
+
+def _param(t: torch.Tensor, n: int, name: str):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return _ptr(t, None, name)
+
+
+def _stat(t: torch.Tensor, n: int, name: str):
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return _ptr(t, torch.float32, name)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Device memory that is free again once the work on ``stream`` is done."""
+    if stream is None or (isinstance(stream, torch.cuda.Stream)
+                          and stream == torch.cuda.current_stream()):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def fp8_block_quantize(x: torch.Tensor, q: BlockFp8 | None = None, qt: BlockFp8 | None = None,
+                       stream=None) -> None:
+    """x into ``q`` and / or its transpose into ``qt``, with a power-of-two
+    scale for each block of 128 (of format and ``block_rows`` as they say)."""
+    _check(_lib.fp8_block_quantize(_matrix(x, "x"), _block(q, "q"), _block(qt, "qt"),
+                                   _stream(stream)))
+
+
+def fp8_block_dequantize(q: BlockFp8, out: torch.Tensor, stream=None) -> None:
+    _check(_lib.fp8_block_dequantize(_block(q, "q"), _matrix(out, "out"), _stream(stream)))
+
+
+def fp8_block_gemm_tn(A: BlockFp8, B: BlockFp8, D: torch.Tensor, stream=None) -> None:
+    """D [M, N] (bfloat16) = A [M, K] B [N, K]^T of two block-scaled matrices."""
+    _check(_lib.fp8_block_gemm_tn(_block(A, "A"), _block(B, "B"), _matrix(D, "D"),
+                                  _stream(stream)))
+
+
+def fp8_layernorm_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, eps: float,
+                      mean: torch.Tensor, rstd: torch.Tensor, y: torch.Tensor | None = None,
+                      y8: BlockFp8 | None = None, x8: BlockFp8 | None = None,
+                      stream=None) -> None:
+    """LayerNorm of x: mean and rstd (float32), and any of y (of x's type),
+    y8 (y block quantized) and x8 (x kept in 8 bits for the backward pass)."""
+    xm = _matrix(x, "x")
+    if gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have the same dtype")
+    _check(_lib.fp8_layernorm_fwd(
+        xm, _param(gamma, xm.cols, "gamma"), _param(beta, xm.cols, "beta"), _DTYPES[gamma.dtype],
+        eps, _matrix(y, "y"), _block(y8, "y8"), _block(x8, "x8"), _stat(mean, xm.rows, "mean"),
+        _stat(rstd, xm.rows, "rstd"), _stream(stream)))
+
+
+def fp8_layernorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: torch.Tensor,
+                      mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                      dgamma: torch.Tensor, dbeta: torch.Tensor,
+                      workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Backward of LayerNorm from the forward's input, ``x`` itself or its
+    8-bit copy (the forward's ``x8``): dx (of dy's type; may be dy), dgamma and
+    dbeta (float32).  ``workspace``: at least
+    ``fp8_layernorm_bwd_workspace(rows, cols)`` bytes of CUDA memory; taken
+    from torch's allocator when None."""
+    dym = _matrix(dy, "dy")
+    rows, cols = dym.rows, dym.cols
+    need = _lib.fp8_layernorm_bwd_workspace(rows, cols)
+    if workspace is None:
+        workspace = _scratch(need, dy.device, stream)
+    saved = isinstance(x, BlockFp8)
+    _check(_lib.fp8_layernorm_bwd(
+        dym, None if saved else _matrix(x, "x"), _block(x, "x") if saved else None,
+        _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), _matrix(dx, "dx"), _stat(dgamma, cols, "dgamma"),
+        _stat(dbeta, cols, "dbeta"), _ptr(workspace, None, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def fp8_layernorm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that fp8_layernorm_bwd needs."""
+    return _lib.fp8_layernorm_bwd_workspace(rows, cols)
+
+
+def fp8_layernorm_recompute(x8: BlockFp8, gamma: torch.Tensor, beta: torch.Tensor,
+                            mean: torch.Tensor, rstd: torch.Tensor, yt: BlockFp8,
+                            stream=None) -> None:
+    """LayerNorm's output again from the 8-bit copy of its input, transposed
+    and block quantized along the tokens: the weight gradient's operand."""
+    if gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have the same dtype")
+    rows, cols = x8.shape
+    _check(_lib.fp8_layernorm_recompute(
+        _block(x8, "x8"), _param(gamma, cols, "gamma"), _param(beta, cols, "beta"),
+        _DTYPES[gamma.dtype], _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"),
+        _block(yt, "yt"), _stream(stream)))
+
+
+def fp8_swiglu_fwd(h: torch.Tensor, a8: BlockFp8, h8: BlockFp8 | None = None,
+                   stream=None) -> None:
+    """SwiGLU of h = [gate | value], block quantized into ``a8``; ``h8``: h
+    itself in 8 bits, for fp8_swiglu_bwd."""
+    _check(_lib.fp8_swiglu_fwd(_matrix(h, "h"), _block(a8, "a8"), _block(h8, "h8"),
+                               _stream(stream)))
+
+
+def fp8_swiglu_bwd(da: torch.Tensor, h8: BlockFp8, dh8: BlockFp8 | None = None,
+                   dh8t: BlockFp8 | None = None, a8t: BlockFp8 | None = None,
+                   stream=None) -> None:
+    """Backward of SwiGLU from its 8-bit input: the gradient of h, block
+    quantized as it is (``dh8``) and transposed (``dh8t``), and the forward's
+    output again, transposed (``a8t``)."""
+    _check(_lib.fp8_swiglu_bwd(_matrix(da, "da"), _block(h8, "h8"), _block(dh8, "dh8"),
+                               _block(dh8t, "dh8t"), _block(a8t, "a8t"), _stream(stream)))

@@ -597,6 +597,10 @@ cudaError_t read_and_clear_error_flag(unsigned *flags, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = read_and_clear_sum_error_flag(&sum_flags);
     *flags |= sum_flags;
+    if (e != cudaSuccess) return e;
+    unsigned block_flags = 0;
+    e = read_and_clear_block_gemm_error_flag(&block_flags);
+    *flags |= block_flags;
     return e;
 }
 

@@ -24,8 +24,10 @@ struct CallRange {
 // Tiled 2-D TMA descriptor of a row-major [outer][inner] tensor of 1- or
 // 2-byte elements with a box of box_outer x box_inner elements, optionally
 // with 128-byte swizzling (tmap.cu).  False if cuTensorMapEncodeTiled rejects it.
+// Rows are ld elements apart (0: inner).
 bool encode_tmap_2d(CUtensorMap *map, const void *base, bool two_byte, int64_t inner,
-                    int64_t outer, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+                    int64_t outer, uint32_t box_inner, uint32_t box_outer, bool swizzle128,
+                    int64_t ld = 0);
 
 // amax of n BF16 values into *amax (zeroed first).
 cudaError_t launch_amax(const void *x, int64_t n, float *amax, int sm_count, cudaStream_t st);
@@ -164,6 +166,58 @@ cudaError_t launch_adam_init(const AdamInitSpec &s, int sm_count, cudaStream_t s
 // Decode-and-sum of nranks FP8 parts [nranks][n] sharing one scale (optim.cu).
 cudaError_t launch_dequant_sum(const uint8_t *parts, int nranks, int64_t n, int fmt,
                                const float *scale, void *out, int sm_count, cudaStream_t st);
+
+// ---- block scaling (one scale per 128 columns of a row, or per 128 x 128 tile) --
+
+// Element types of fp8_dtype.
+constexpr int kTypeF32 = 0, kTypeBF16 = 1, kTypeF16 = 2;
+
+// A matrix [rows][ld] in 32 or 16 bits (data null: not there).
+struct MatView {
+    void *data;
+    int64_t rows, cols, ld;
+    int type;
+};
+
+// A block-scaled FP8 matrix (codes null: not there): codes [rows][ld], scales
+// [ceil(rows / block_rows)][ld_s], E8M0 bytes or, with scale_f32, floats.
+struct BlockView {
+    uint8_t *codes;
+    int64_t rows, cols, ld;
+    void *scales;
+    int64_t ld_s;
+    int fmt, block_rows, scale_f32;
+};
+
+// x into q and / or its transpose into qt (block_quant.cu).
+cudaError_t launch_block_quantize(const MatView &x, const BlockView &q, const BlockView &qt,
+                                  cudaStream_t st);
+cudaError_t launch_block_dequantize(const BlockView &q, const MatView &out, int sm_count,
+                                    cudaStream_t st);
+// D [M][N] (BF16) = A [M][K] . B [N][K]^T (block_gemm.cu).
+cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatView &D,
+                              int sm_count, cudaStream_t st, const char **what);
+// LayerNorm forward and backward (layernorm.cu).
+cudaError_t launch_ln_fwd(const MatView &x, const void *gamma, const void *beta, int wtype,
+                          float eps, const MatView &y, const BlockView &y8, const BlockView &x8,
+                          float *mean, float *rstd, int sm_count, cudaStream_t st);
+int64_t ln_bwd_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
+                          const void *gamma, int wtype, const float *mean, const float *rstd,
+                          const MatView &dx, float *dgamma, float *dbeta, void *ws,
+                          cudaStream_t st);
+// yt = quantized transpose of LayerNorm(x8) (block_quant.cu).
+cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,
+                                const float *mean, const float *rstd, const BlockView &yt,
+                                cudaStream_t st);
+// SwiGLU (block_quant.cu).
+cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const BlockView &h8,
+                              int sm_count, cudaStream_t st);
+cudaError_t launch_swiglu_bwd(const MatView &da, const BlockView &h8, const BlockView &dh8,
+                              const BlockView &dh8t, const BlockView &a8t, cudaStream_t st);
+
+// Read and clear the block GEMM's device error flag (block_gemm.cu).
+cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags);
 
 // Diagnostic: while acc is not null, the first CTA of every GEMM launch adds
 // its SM clock cycles to acc[0] and its nanoseconds to acc[1] (gemm.cu).

@@ -16,7 +16,8 @@ std::once_flag g_encode_once;
 }  // namespace
 
 bool encode_tmap_2d(CUtensorMap *map, const void *base, bool two_byte, int64_t inner,
-                    int64_t outer, uint32_t box_inner, uint32_t box_outer, bool swizzle128) {
+                    int64_t outer, uint32_t box_inner, uint32_t box_outer, bool swizzle128,
+                    int64_t ld) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -28,7 +29,7 @@ bool encode_tmap_2d(CUtensorMap *map, const void *base, bool two_byte, int64_t i
     if (g_encode == nullptr) return false;
     const cuuint64_t esize = two_byte ? 2 : 1;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner) * esize};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld ? ld : inner) * esize};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = g_encode(map,

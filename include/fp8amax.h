@@ -42,7 +42,8 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  All work is enqueued on it, in order; scales are read on the
  *    device, so a training step needs no host round trip.
- *  - Tensors are dense row-major.  Row and column counts must be multiples of
+ *  - Tensors are dense row-major (the block-scaled ones at the end of this
+ *    file take row strides and any size).  Row and column counts must be multiples of
  *    16 and tensor pointers 16-byte aligned (else FP8_ERR_ALIGN), so that
  *    every row of every FP8 and BF16 tensor starts on a 16-byte boundary.
  *    Pointers to fp32 scalars and to the fp8_meta buffers need 4-byte
@@ -454,6 +455,131 @@ fp8_status fp8_linear_bwd_noalloc(const void *dY, int64_t M, int64_t N, int64_t 
                                   const fp8_meta *meta, const fp8_recipe *recipe,
                                   const uint8_t *X8t, const uint8_t *W8t, void *dX, void *dW,
                                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * Block scaling: one scale for each block of 128
+ *
+ * Beside the per-tensor scales above, a tensor can carry one scale for each
+ * 128 consecutive columns of a row (block_rows = 1: activations, gradients)
+ * or for each 128 x 128 tile (block_rows = 128: weights).  An element stands
+ * for code * scale of its block.  Blocks start at row 0 and column 0; the last
+ * ones may be partly filled.  The quantizers choose powers of two, so that
+ * dividing by a scale is exact and the only rounding is the code's own:
+ *   amax  = the largest finite magnitude in the block
+ *   scale = 2^e, e the smallest integer >= -127 with amax <= fmax * 2^e
+ *           (fmax 448 or 57344), so the smallest scale for a block of zeros
+ *   code  = x / scale rounded to nearest, ties to the even code; infinities
+ *           saturate to +-fmax, NaN stays NaN, the sign of zero is kept.
+ * Sizes are free (odd ones too; 0 rows or columns: nothing is done).
+ * Everything is dense along the columns; `ld` is the distance between rows
+ * in elements. */
+
+typedef enum { FP8_DTYPE_F32 = 0, FP8_DTYPE_BF16 = 1, FP8_DTYPE_F16 = 2 } fp8_dtype;
+
+/* How a block's scale is stored: FP8_SCALE_E8M0, a byte b for 2^(b - 127)
+ * (255: NaN), or FP8_SCALE_F32, the factor itself, any float. */
+typedef enum { FP8_SCALE_E8M0 = 0, FP8_SCALE_F32 = 1 } fp8_scale_type;
+
+/* A matrix in 32 or 16 bits: DEVICE data [rows][ld], ld >= cols, aligned to
+ * its element.  16-byte aligned rows (data, and ld * element size) are faster. */
+typedef struct {
+    void *data;
+    int64_t rows, cols, ld;
+    int32_t dtype;
+} fp8_matrix;
+
+/* A block-scaled FP8 matrix, all DEVICE memory of the caller's:
+ *   codes  [rows][ld] FP8 codes of format fmt; 16-byte aligned, ld >= cols a
+ *          multiple of 16.  Columns from cols on are neither read as values
+ *          nor written.
+ *   scales [ceil(rows / block_rows)][ld_scales]; column j holds the scale of
+ *          columns 128 j .. 128 j + 127; ld_scales >= ceil(cols / 128), for
+ *          E8M0 a multiple of 4; 4-byte aligned. */
+typedef struct {
+    uint8_t *codes;
+    int64_t rows, cols, ld;
+    void *scales;
+    int64_t ld_scales;
+    int32_t fmt;
+    int32_t block_rows;
+    int32_t scale_type;
+} fp8_block_tensor;
+
+/* Quantizes x [rows][cols] into q and / or its transpose into qt [cols][rows]
+ * (either may be NULL, not both).  q and qt have the same format, block_rows
+ * and scale type.  With block_rows = 1, q's blocks run along x's rows and
+ * qt's along its columns, the operands of products that sum over columns and
+ * over rows; with 128 both hold the same tiles.  One kernel. */
+fp8_status fp8_block_quantize(const fp8_matrix *x, const fp8_block_tensor *q,
+                              const fp8_block_tensor *qt, void *stream);
+
+/* out [rows][cols] = code * scale, rounded to out's type.  One kernel. */
+fp8_status fp8_block_dequantize(const fp8_block_tensor *q, const fp8_matrix *out, void *stream);
+
+/* D [M][N] (BF16) = A [M][K] . B [N][K]^T of two block-scaled matrices:
+ *   D[i][j] = bf16_rne( sum over blocks k of sA(i, k) * sB(j, k) * dot_k ),
+ *   dot_k = sum over the block's 128 columns of a[i][c] * b[j][c],
+ * with the products summed in fp32.  A and B each E4M3 or E5M2, each with
+ * block_rows 1 or 128, both with one scale type; a product sA * sB has to be
+ * a normal fp32 number or zero.  M, N, K >= 0; K = 0 gives zeros. */
+fp8_status fp8_block_gemm_tn(const fp8_block_tensor *A, const fp8_block_tensor *B,
+                             const fp8_matrix *D, void *stream);
+
+/* LayerNorm of x [rows][cols], in fp32:
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = ((x - mean) * rstd) * gamma + beta.
+ * Writes mean and rstd (fp32 [rows]) and any of: y (of x's type); y8, y block
+ * quantized straight from fp32 (block_rows 1), the operand of a following
+ * product; x8, x itself in 8 bits (block_rows 1), which
+ * fp8_layernorm_bwd and fp8_layernorm_recompute take in x's place, so that
+ * neither x nor y has to be kept until the backward pass.  gamma and beta
+ * [cols] are of type wtype (fp8_dtype).  cols >= 1. */
+fp8_status fp8_layernorm_fwd(const fp8_matrix *x, const void *gamma, const void *beta,
+                             int32_t wtype, float eps, const fp8_matrix *y,
+                             const fp8_block_tensor *y8, const fp8_block_tensor *x8, float *mean,
+                             float *rstd, void *stream);
+
+/* Backward of LayerNorm from dy [rows][cols] and the forward's input, either
+ * x or its 8-bit copy x8 (the other NULL), with the forward's mean and rstd:
+ *   xhat = (x - mean) * rstd,  u = dy * gamma,
+ *   dx = rstd * (u - sum(u) / cols - xhat * sum(u * xhat) / cols)  (per row),
+ *   dgamma = sum over rows of dy * xhat,  dbeta = sum over rows of dy.
+ * dy, x and dx are of one type; dgamma and dbeta are fp32 [cols], overwritten;
+ * dx may be dy.  workspace: DEVICE, 16-byte aligned, of at least
+ * fp8_layernorm_bwd_workspace(rows, cols) bytes, in use until the call's
+ * kernels are done.  The sums' order is fixed: equal calls give equal bits. */
+fp8_status fp8_layernorm_bwd(const fp8_matrix *dy, const fp8_matrix *x,
+                             const fp8_block_tensor *x8, const void *gamma, int32_t wtype,
+                             const float *mean, const float *rstd, const fp8_matrix *dx,
+                             float *dgamma, float *dbeta, void *workspace, int64_t workspace_bytes,
+                             void *stream);
+int64_t fp8_layernorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* LayerNorm's output again from the 8-bit copy of its input, transposed:
+ * yt [cols][rows] (block_rows 1: blocks along the tokens), the operand of the
+ * weight gradient of the product that follows the LayerNorm. */
+fp8_status fp8_layernorm_recompute(const fp8_block_tensor *x8, const void *gamma,
+                                   const void *beta, int32_t wtype, const float *mean,
+                                   const float *rstd, const fp8_block_tensor *yt, void *stream);
+
+/* SwiGLU of h [M][2F] = [gate | value]: a = gate / (1 + exp(-gate)) * value in
+ * fp32, block quantized into a8 [M][F] (block_rows 1).  h8 (or NULL): h itself
+ * in 8 bits [M][2F], for fp8_swiglu_bwd.  F a multiple of 128, so that no
+ * block of h holds columns of both halves.  One kernel. */
+fp8_status fp8_swiglu_fwd(const fp8_matrix *h, const fp8_block_tensor *a8,
+                          const fp8_block_tensor *h8, void *stream);
+
+/* Backward of SwiGLU from da [M][F] and the 8-bit h8 [M][2F].  With
+ * s = 1 / (1 + exp(-gate)), in fp32:
+ *   d gate = da * value * s * (1 + gate * (1 - s)),  d value = da * (gate * s)
+ * block quantized into dh8 [M][2F] and dh8t [2F][M], the operands of the input
+ * gradient's and the weight gradient's product, and the forward's output
+ * again, gate * s * value, into a8t [F][M], the operand of the next layer's
+ * weight gradient.  All block_rows 1; any of the three may be NULL, not all;
+ * dh8 and dh8t have the same format.  One kernel. */
+fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
+                          const fp8_block_tensor *dh8, const fp8_block_tensor *dh8t,
+                          const fp8_block_tensor *a8t, void *stream);
 
 #ifdef __cplusplus
 }
