@@ -3,20 +3,22 @@
 //   D[i][j] = bf16_rne( sum over k-blocks b of sA(i, b) * sB(j, b) * dot_b ),
 //   dot_b = sum over the block's 128 columns of A[i][c] * B[j][c]   (fp32)
 // A is [M][K], B [N][K], both contiguous along K; sA and sB belong to one row
-// or to 128 rows, and are E8M0 bytes or floats.
+// or to 128 rows, and are E8M0 bytes or floats.  Three kernels:
 //
-// One CTA per SM, persistent over 128 x 128 output tiles:
-//   warp 0     TMA producer: 128-byte-swizzled 128-deep slices of A and B;
-//   warp 1     issues tcgen05.mma: each k-block's four MMAs start a fresh
-//              accumulator in one of two TMEM buffers;
-//   warps 2-5  read each finished dot_b from TMEM and add it, times its scale,
-//              to sums in registers; after the last k-block they round and
-//              store the tile.
+//   mx    E8M0 scales, many rows: the tensor cores take the scales themselves
+//         (kind::mxf8f6f4), so a tile's sums stay in TMEM over all of K;
+//   f32   float scales, many rows: each k-block's dot_b goes from TMEM into
+//         register sums, times its scale;
+//   few   few rows (tokens being decoded): the rows of B, the weights, take the
+//         instruction's 128-row side and the tokens its columns, and K is split
+//         over a cluster whose CTAs join their sums in shared memory.
+//
 // Every wait is bounded.
 #include <cstdint>
 #include <mutex>
 
 #include "block.cuh"
+#include "raster.cuh"
 
 namespace fp8k {
 
@@ -24,112 +26,450 @@ namespace {
 
 __device__ unsigned g_block_gemm_error_flags = 0;
 
-constexpr int BM = 128, BN = 128, BK = 128;
-constexpr int STAGES = 6;
-constexpr int NUM_THREADS = 192;
-constexpr int A_STAGE = BM * BK, B_STAGE = BN * BK;
-constexpr int TMEM_COLS = 2 * BN;
-constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
-constexpr size_t SMEM =
-    1024 + STAGES * (A_STAGE + B_STAGE) + 2 * BN * sizeof(float) + NUM_BARS * 8 + 16;
-
-struct Args {
-    CUtensorMap mapA, mapB;
-    BlockView A, B;
-    __nv_bfloat16 *D;
-    int64_t M, N, ldd;
-    bool vecd;
-    int tiles_n, num_tiles, num_kb;
-    uint32_t idesc;
-};
+constexpr int BM = 128, BN = 256, BK = 128;   // a CTA's rows, the pair's columns, a k-block
+constexpr int HALF = BM * BK;                 // bytes of a CTA's A (or B) slice of one k-block
+constexpr int EPI_COLS = 64;                  // output columns staged at a time (128 B of BF16)
+constexpr int EPI_BUF = 32 * EPI_COLS * 2;    // a warp's staging buffer: 32 rows x 128 B
 
 __device__ __forceinline__ void raise_error(volatile int *abort_flag) {
     atomicOr(&g_block_gemm_error_flags, kErrWaitTimeout);
     *abort_flag = 1;
 }
 
-__global__ void __launch_bounds__(NUM_THREADS, 1) block_gemm_kernel(const __grid_constant__ Args a) {
+// ------------------------------------------------------- pair kernels: common --
+// Two CTAs on two SMs (a cluster) share each 256 x 256 tile (cta_group::2): each
+// loads its own 128 rows of A and 128 of the 256 rows of B, and the even CTA
+// issues MMAs that read both CTAs' shared memory and write both CTAs' TMEM.
+
+struct PairArgs {
+    CUtensorMap mapA, mapB, mapD;
+    BlockView A, B;
+    __nv_bfloat16 *D;
+    int64_t M, N, ldd;
+    bool tma_d;     // D's rows are 16-byte aligned: store by TMA
+    bool pairs_d;   // D's rows are 4-byte aligned
+    int tiles_m, tiles_n, num_tiles, num_kb, group_m;
+    uint32_t idesc;
+};
+
+// The producer warp's lane 0: A and B slices of every k-block of the pair's tiles.
+template <int STAGES>
+__device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int unit, int num_units,
+                                        uint32_t sA, uint32_t sB, uint32_t full0, uint32_t empty0,
+                                        volatile int *abort_flag) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+        int mb, nb;
+        tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+        const int32_t arow = mb * 2 * BM + static_cast<int32_t>(rank) * BM;
+        const int32_t brow = nb * BN + static_cast<int32_t>(rank) * (BN / 2);
+        for (int kb = 0; kb < a.num_kb; ++kb) {
+            if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+                raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            // both CTAs' halves complete on the even CTA's barrier
+            const uint32_t fb = full0 + 8 * stage, fb0 = mapa_shared(fb, 0);
+            if (rank == 0) mbar_arrive_expect_tx(fb, 4 * HALF);
+            tma_load_2d_pair(sA + stage * HALF, &a.mapA, fb0, kb * BK, arow);
+            tma_load_2d_pair(sB + stage * HALF, &a.mapB, fb0, kb * BK, brow);
+            ++issued;
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    }
+    if (ok) {
+        // every stage's last release is signalled from the even SM: it must have
+        // arrived before this CTA exits
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (rank == 0) {
+        // let the copies already issued land before the CTA exits
+        for (int i = 0; i < STAGES && issued > 0; ++i, --issued) {
+            stage = stage == 0 ? STAGES - 1 : stage - 1;
+            if (stage == STAGES - 1) phase ^= 1u;
+            mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
+        }
+    }
+}
+
+// A warp's 32 rows x 64 columns of BF16 (lane = row, packed[j] = columns 2j, 2j + 1)
+// to D at (row0, col0) by way of its staging buffer, where 16-byte chunk j of row r
+// sits at j ^ (r mod 8): the 128-byte swizzle of D's tensor map.  Rows of D that TMA
+// cannot address go out with each warp instruction along one row.
+__device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, int64_t row0,
+                                            int64_t col0, const uint32_t (&packed)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        st_shared_v4(sbuf + lane * 128 + ((j ^ (lane & 7)) << 4), packed[4 * j], packed[4 * j + 1],
+                     packed[4 * j + 2], packed[4 * j + 3]);
+    // a TMA store clips at 16-byte steps: a chunk that ends inside one goes the other way
+    if (a.tma_d && (col0 + EPI_COLS <= a.N || a.N % 8 == 0)) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (row0 < a.M && col0 < a.N)   // boxes wholly outside D are skipped
+                tma_store_2d(&a.mapD, sbuf, static_cast<int32_t>(col0), static_cast<int32_t>(row0));
+            bulk_commit_group();
+        }
+        return;
+    }
+    __syncwarp();
+    const int64_t c = col0 + 2 * lane;
+    const int rows = row0 >= a.M ? 0 : a.M - row0 < 32 ? static_cast<int>(a.M - row0) : 32;
+    for (int r = 0; r < rows; ++r) {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];"
+                     : "=r"(w)
+                     : "r"(sbuf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2))
+                     : "memory");
+        uint16_t *d = reinterpret_cast<uint16_t *>(a.D + (row0 + r) * a.ldd + c);
+        if (a.pairs_d && c + 1 < a.N) {
+            *reinterpret_cast<uint32_t *>(d) = w;
+        } else {
+            if (c < a.N) d[0] = static_cast<uint16_t>(w);
+            if (c + 1 < a.N) d[1] = static_cast<uint16_t>(w >> 16);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) bulk_commit_group();   // an empty one: each chunk is one group
+}
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
+                                       ~static_cast<uintptr_t>(1023));
+}
+
+// ------------------------------------------------------------------ mx kernel --
+// Warps: 0 TMA, 1 MMA, 4-7 scales, 8-11 epilogue (2 and 3 idle: tcgen05.st and .ld
+// reach the lane quarter of the warp's number mod 4).
+//
+// TMEM (512 columns): a 256-column accumulator fills half, and two of them leave no
+// room for scales.  So the two overlap: tile i uses columns 0-255 or 224-479 in turn.
+// The epilogue reads the shared 32 columns first and then lets the next tile's MMAs
+// start, which costs them one 64-column read (an eighth of the epilogue) instead of
+// all of it.  Columns 480-511 hold two stages of scales: the word of lane l, column
+// j is row 32 j + l's four E8M0 bytes of k-blocks 4 g .. 4 g + 3 (4 columns for the
+// CTA's rows of A, 8 for the tile's rows of B, the same in all four lane quarters);
+// the MMAs of k-block 4 g + b name byte b in their descriptor.  A block of 128 is
+// four of the instruction's blocks of 32 with the same scale.
+
+constexpr int MX_STAGES = 6;
+constexpr int MX_THREADS = 384;
+constexpr int MX_ACC1 = 224;       // first column of the second accumulator
+constexpr int MX_SF = 480;         // first column of the scales
+constexpr int MX_SF_STRIDE = 16;   // columns per stage of scales: 4 for A, 8 for B
+constexpr int MX_BARS = 2 * MX_STAGES + 2 + 1 + 4 + 1;
+constexpr size_t MX_SMEM = 1024 + MX_STAGES * 2 * HALF + 4 * 2 * EPI_BUF + MX_BARS * 8 + 16;
+
+__global__ void __launch_bounds__(MX_THREADS, 1)
+    block_gemm_mx_kernel(const __grid_constant__ PairArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *sA = smem;
-    uint8_t *sB = smem + STAGES * A_STAGE;
-    float *sbs = reinterpret_cast<float *>(sB + STAGES * B_STAGE);   // [2][BN] scales of B
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sbs + 2 * BN);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
+    uint8_t *smem = align1024(smem_raw);
+    const uint32_t sA = smem_u32(smem), sB = sA + MX_STAGES * HALF;
+    const uint32_t sD = sB + MX_STAGES * HALF;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + MX_STAGES * 2 * HALF + 4 * 2 * EPI_BUF);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + MX_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
-    const uint32_t accf0 = smem_u32(bars + 2 * STAGES), acce0 = smem_u32(bars + 2 * STAGES + 2);
-    const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
+    const uint32_t rank = cluster_ctarank();   // 0 = the CTA that issues MMAs
+    const int unit = static_cast<int>(blockIdx.x >> 1), num_units = static_cast<int>(gridDim.x >> 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * MX_STAGES;
+    const uint32_t accf0 = empty0 + 8 * MX_STAGES, acce = accf0 + 16;
+    const uint32_t sff0 = acce + 8, sfe0 = sff0 + 16, drain = sfe0 + 16;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < MX_STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, 4);
+            mbar_init(sff0 + 8 * b, 8);   // four scale warps of each CTA
+            mbar_init(sfe0 + 8 * b, 1);
         }
-        mbar_init(drain_bar, 1);
+        mbar_init(acce, 8);               // four epilogue warps of each CTA
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&a.mapA);
         prefetch_tmap(&a.mapB);
+        if (a.tma_d) prefetch_tmap(&a.mapD);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        tmem_relinquish_pair();
         tc_fence_before();
     }
     __syncthreads();
+    __syncwarp();
+    cluster_sync();   // both CTAs' barriers exist before any remote signal
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < a.num_tiles; tile += gridDim.x) {
-                const int mb = tile / a.tiles_n, nb = tile % a.tiles_n;
+        if (lane == 0)
+            produce<MX_STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, sf = 0, it = 0;
+            uint32_t phase = 0, sf_phase = 0;
+            bool ok = true, any = false;
+            for (int tile = unit; ok && tile < a.num_tiles; tile += num_units, ++it) {
+                // the previous tile's epilogue has read the columns the two share
+                if (it > 0 && !mbar_wait(acce, static_cast<uint32_t>(it - 1) & 1u, abort_flag)) {
+                    raise_error(abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + ((it & 1) ? MX_ACC1 : 0);
                 for (int kb = 0; kb < a.num_kb; ++kb) {
-                    if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+                    if (((kb & 3) == 0 && !mbar_wait(sff0 + 8 * sf, sf_phase, abort_flag)) ||
+                        !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
                         raise_error(abort_flag);
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = full0 + 8 * stage;
-                    mbar_arrive_expect_tx(fb, A_STAGE + B_STAGE);
-                    tma_load_2d(smem_u32(sA + stage * A_STAGE), &a.mapA, fb, kb * BK, mb * BM);
-                    tma_load_2d(smem_u32(sB + stage * B_STAGE), &a.mapB, fb, kb * BK, nb * BN);
-                    ++issued;
-                    if (++stage == STAGES) {
+                    tc_fence_after();
+                    const uint32_t sfa = tmem + MX_SF + sf * MX_SF_STRIDE, sfb = sfa + 4;
+                    const uint32_t idesc = a.idesc | static_cast<uint32_t>(kb & 3) << 4 |
+                                           static_cast<uint32_t>(kb & 3) << 29;
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        mma_mxf8_pair(d, smem_desc_sw128(sA + stage * HALF + 32 * k),
+                                      smem_desc_sw128(sB + stage * HALF + 32 * k), idesc, sfa, sfb,
+                                      (kb | k) != 0);
+                    mma_commit_pair(empty0 + 8 * stage, 0x3);
+                    any = true;
+                    if (++stage == MX_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if ((kb & 3) == 3 || kb == a.num_kb - 1) {
+                        mma_commit_pair(sfe0 + 8 * sf, 0x3);
+                        if (++sf == 2) {
+                            sf = 0;
+                            sf_phase ^= 1u;
+                        }
+                    }
                 }
+                if (!ok) break;
+                mma_commit_pair(accf0 + 8 * (it & 1), 0x3);
             }
-            if (!ok) {
-                // let the copies already issued land before the CTA exits
-                for (int i = 0; i < STAGES && issued > 0; ++i, --issued) {
-                    stage = stage == 0 ? STAGES - 1 : stage - 1;
-                    if (stage == STAGES - 1) phase ^= 1u;
-                    mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
+            if (!ok && any) {
+                // wait (bounded) for the MMAs in flight before TMEM is freed
+                mma_commit_pair(drain, 0x1);
+                mbar_wait(drain, 0, nullptr, 100000000ull);
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // scales: every lane fetches its word of each 32 rows; rows past the end
+        // repeat the last one (their codes are zeros and their results are not stored)
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + MX_SF;
+        const uint8_t *pa = static_cast<const uint8_t *>(a.A.scales);
+        const uint8_t *pb = static_cast<const uint8_t *>(a.B.scales);
+        int sf = 0;
+        uint32_t sf_phase = 0;
+        bool ok = true;
+        for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+            int mb, nb;
+            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+            const uint8_t *ra[4], *rb[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t r = min(static_cast<int64_t>(mb) * 2 * BM + rank * BM + 32 * j + lane,
+                                      a.M - 1);
+                ra[j] = pa + (a.A.block_rows == 1 ? r : r >> 7) * a.A.ld_s;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t r = min(static_cast<int64_t>(nb) * BN + 32 * j + lane, a.N - 1);
+                rb[j] = pb + (a.B.block_rows == 1 ? r : r >> 7) * a.B.ld_s;
+            }
+            for (int kb = 0; kb < a.num_kb; kb += 4) {
+                uint32_t wa[4], wb[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) wa[j] = *reinterpret_cast<const uint32_t *>(ra[j] + kb);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wb[j] = *reinterpret_cast<const uint32_t *>(rb[j] + kb);
+                const bool got = mbar_wait(sfe0 + 8 * sf, sf_phase ^ 1u, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, got)) {
+                    if (lane == 0) raise_error(abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_store_4cols(lane_base + sf * MX_SF_STRIDE, wa[0], wa[1], wa[2], wa[3]);
+                tmem_store_8cols(lane_base + sf * MX_SF_STRIDE + 4, wb);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(sff0 + 8 * sf, 0));
+                if (++sf == 2) {
+                    sf = 0;
+                    sf_phase ^= 1u;
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        // the last releases come from the even SM: let them arrive
+        for (int i = 0; ok && i < 2; ++i) {
+            mbar_wait(sfe0 + 8 * sf, sf_phase ^ 1u, abort_flag);
+            if (++sf == 2) {
+                sf = 0;
+                sf_phase ^= 1u;
+            }
+        }
+    } else if (warp >= 8) {
+        const int q = warp & 3;   // TMEM lane quarter
+        uint32_t chunk = 0;       // chunks staged so far (selects the buffer)
+        int it = 0;
+        for (int tile = unit; tile < a.num_tiles; tile += num_units, ++it) {
+            int mb, nb;
+            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+            const bool got = mbar_wait(accf0 + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                if (lane == 0) raise_error(abort_flag);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + ((it & 1) ? MX_ACC1 : 0);
+            const int64_t row0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32;
+#pragma unroll 1
+            for (int i = 0; i < BN / EPI_COLS; ++i) {
+                const int c = (it & 1) ? i : BN / EPI_COLS - 1 - i;   // the shared columns first
+                uint32_t r[2][32];
+                tmem_load_32cols(t + c * EPI_COLS, r[0]);
+                tmem_load_32cols(t + c * EPI_COLS + 32, r[1]);
+                if (i == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(acce, 0));
+                }
+                uint32_t packed[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        packed[16 * h + j] = pack2<__nv_bfloat16>(__uint_as_float(r[h][2 * j]),
+                                                                  __uint_as_float(r[h][2 * j + 1]));
+                // this buffer's previous store (two chunks back) has read it
+                if (lane == 0) bulk_wait_group_read<1>();
+                __syncwarp();
+                store_chunk(a, sD + (q * 2 + (chunk & 1)) * EPI_BUF, row0,
+                            static_cast<int64_t>(nb) * BN + c * EPI_COLS, packed);
+                ++chunk;
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>();
+        __syncwarp();
+    }
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();   // the other SM is done with this CTA's memory
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// Named barrier of n threads that tells all of them whether pred held for each.
+__device__ __forceinline__ bool barrier_and(int id, int n, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"(static_cast<uint32_t>(pred))
+        : "memory");
+    return r != 0;
+}
+
+// ----------------------------------------------------------------- f32 kernel --
+// Warps: 0 TMA, 1 MMA (2 and 3 idle), 4-11 sums: warp w has lane quarter w mod 4 and
+// half (w - 4) / 4 of the tile's columns, 128 sums per thread.  Each k-block's MMAs
+// start a fresh accumulator in one of two TMEM buffers; while one is summed the other
+// is computed.  Of the launch's 384 x 168 registers the first four warps hand back
+// 80 each per thread and the eight summing warps take 40 more: 128 x 88 + 256 x 208.
+
+constexpr int FS_STAGES = 5;
+constexpr int FS_THREADS = 384;
+constexpr int FS_REGS_CONTROL = 88, FS_REGS_SUMS = 208;
+static_assert(128 * FS_REGS_CONTROL + 256 * FS_REGS_SUMS <= FS_THREADS * 168, "register split");
+constexpr int FS_BARS = 2 * FS_STAGES + 4 + 1;
+constexpr size_t FS_SMEM = 1024 + FS_STAGES * 2 * HALF + 8 * EPI_BUF + 2 * BN * 4 + FS_BARS * 8 + 16;
+
+__global__ void __launch_bounds__(FS_THREADS, 1)
+    block_gemm_f32_kernel(const __grid_constant__ PairArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    const uint32_t sA = smem_u32(smem), sB = sA + FS_STAGES * HALF;
+    const uint32_t sD = sB + FS_STAGES * HALF;
+    float *sbs = reinterpret_cast<float *>(smem + FS_STAGES * 2 * HALF + 8 * EPI_BUF);   // [2][BN]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sbs + 2 * BN);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + FS_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int unit = static_cast<int>(blockIdx.x >> 1), num_units = static_cast<int>(gridDim.x >> 1);
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * FS_STAGES;
+    const uint32_t accf0 = empty0 + 8 * FS_STAGES, acce0 = accf0 + 16, drain = acce0 + 16;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < FS_STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf0 + 8 * b, 1);
+            mbar_init(acce0 + 8 * b, 16);   // eight warps of each CTA
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&a.mapA);
+        prefetch_tmap(&a.mapB);
+        if (a.tma_d) prefetch_tmap(&a.mapD);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        tmem_relinquish_pair();
+        tc_fence_before();
+    }
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FS_REGS_CONTROL));
+        if (warp == 0 && lane == 0)
+            produce<FS_STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
+        if (warp == 1 && lane == 0 && rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, any = false;
-            for (int tile = blockIdx.x; ok && tile < a.num_tiles; tile += gridDim.x) {
+            for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
                 for (int kb = 0; kb < a.num_kb; ++kb) {
                     if (!mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) ||
                         !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
@@ -138,16 +478,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_gemm_kernel(const __grid
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * A_STAGE);
-                    const uint32_t b0 = smem_u32(sB + stage * B_STAGE);
 #pragma unroll
                     for (int k = 0; k < BK / 32; ++k)
-                        mma_f8f6f4(tmem_base + acc * BN, smem_desc_sw128(a0 + 32 * k),
-                                   smem_desc_sw128(b0 + 32 * k), a.idesc, k != 0);
-                    mma_commit(empty0 + 8 * stage);
-                    mma_commit(accf0 + 8 * acc);
+                        mma_f8f6f4_pair(tmem + acc * BN, smem_desc_sw128(sA + stage * HALF + 32 * k),
+                                        smem_desc_sw128(sB + stage * HALF + 32 * k), a.idesc, k != 0);
+                    mma_commit_pair(empty0 + 8 * stage, 0x3);
+                    mma_commit_pair(accf0 + 8 * acc, 0x3);
                     any = true;
-                    if (++stage == STAGES) {
+                    if (++stage == FS_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -158,87 +496,457 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_gemm_kernel(const __grid
                 }
             }
             if (!ok && any) {
-                mma_commit(drain_bar);
-                mbar_wait(drain_bar, 0, nullptr, 100000000ull);
+                mma_commit_pair(drain, 0x1);
+                mbar_wait(drain, 0, nullptr, 100000000ull);
             }
         }
     } else {
-        const int q = warp & 3;             // TMEM lane quarter this warp may access
-        const int et = threadIdx.x - 64;    // 0..127: the column whose scale this thread fetches
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FS_REGS_SUMS));
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const int et = threadIdx.x - 128;   // 0..255: the column whose scale this thread fetches
+        const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+        const uint32_t sbuf = sD + (warp - 4) * EPI_BUF;
+        const bool per_row = a.B.block_rows == 1;   // otherwise one scale of B per half
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < a.num_tiles; tile += gridDim.x) {
-            const int mb = tile / a.tiles_n, nb = tile % a.tiles_n;
-            const int64_t row = static_cast<int64_t>(mb) * BM + q * 32 + lane;
-            const int64_t col = static_cast<int64_t>(nb) * BN + et;
-            const int64_t ra = row < a.M ? row / a.A.block_rows : 0;
-            const int64_t rb = col < a.N ? col / a.B.block_rows : 0;
-            float sum[BN];
+        for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+            int mb, nb;
+            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+            const int64_t row0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32;
+            const int64_t col0 = static_cast<int64_t>(nb) * BN;
+            // rows and columns past the end repeat the last one
+            const int64_t row = min(row0 + lane, a.M - 1);
+            const int64_t col = min(col0 + (per_row ? et : half * 128), a.N - 1);
+            const float *pa = static_cast<const float *>(a.A.scales) +
+                              (a.A.block_rows == 1 ? row : row >> 7) * a.A.ld_s;
+            const float *pb = static_cast<const float *>(a.B.scales) +
+                              (per_row ? col : col >> 7) * a.B.ld_s;
+            uint64_t sum[64];   // pairs of columns
 #pragma unroll
-            for (int c = 0; c < BN; ++c) sum[c] = 0.0f;
-            float sa_next = load_scale(a.A, ra, 0), sb_next = load_scale(a.B, rb, 0);
+            for (int c = 0; c < 64; ++c) sum[c] = 0;
+            float sa_next = pa[0], sb_next = pb[0];
 #pragma unroll 1
             for (int kb = 0; kb < a.num_kb; ++kb) {
-                const float sa = sa_next;
-                float *sb = sbs + (kb & 1) * BN;
-                sb[et] = sb_next;
+                const float sa = sa_next, sb = sb_next;
                 if (kb + 1 < a.num_kb) {
-                    sa_next = load_scale(a.A, ra, kb + 1);
-                    sb_next = load_scale(a.B, rb, kb + 1);
+                    sa_next = pa[kb + 1];
+                    sb_next = pb[kb + 1];
                 }
-                // the other buffer is written only after this barrier of the next block
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const float *sbk = sbs + (kb & 1) * BN;
+                if (per_row) {
+                    sbs[(kb & 1) * BN + et] = sb;
+                    // a buffer is written again only after the next block's barrier
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                }
                 const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
                 if (!__all_sync(0xFFFFFFFFu, got)) {
                     if (lane == 0) raise_error(abort_flag);
-                    ok = false;
-                    // the barrier's other warps see the abort flag in their own wait
+                    ok = false;   // goes on to this tile's end, where all agree to stop
                 }
-                tc_fence_after();
                 if (ok) {
+                    tc_fence_after();
+                    const uint32_t t = t0 + acc * BN;
+                    uint32_t r[2][16];
+                    tmem_load_16cols(t, r[0]);
 #pragma unroll
-                    for (int h = 0; h < BN / 32; ++h) {
-                        uint32_t r[32];
-                        tmem_load_32cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                             acc * BN + h * 32,
-                                         r);
+                    for (int h = 0; h < 8; ++h) {
+                        tmem_wait_16cols(r[h & 1]);
+                        if (h < 7) {
+                            tmem_load_16cols(t + (h + 1) * 16, r[(h + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(mapa_shared(acce0 + 8 * acc, 0));
+                        }
+                        if (per_row) {
+                            const uint64_t sa2 = splat_f32x2(sa);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            sum[h * 32 + c] = __fmaf_rn(__uint_as_float(r[c]),
-                                                        __fmul_rn(sa, sb[h * 32 + c]),
-                                                        sum[h * 32 + c]);
+                            for (int c = 0; c < 4; ++c) {
+                                const ulonglong2 s2 = *reinterpret_cast<const ulonglong2 *>(
+                                    sbk + half * 128 + h * 16 + 4 * c);
+                                const uint64_t v0 = f32x2_pack(__uint_as_float(r[h & 1][4 * c]),
+                                                               __uint_as_float(r[h & 1][4 * c + 1]));
+                                const uint64_t v1 = f32x2_pack(__uint_as_float(r[h & 1][4 * c + 2]),
+                                                               __uint_as_float(r[h & 1][4 * c + 3]));
+                                sum[8 * h + 2 * c] =
+                                    f32x2_fma(v0, f32x2_mul(sa2, s2.x), sum[8 * h + 2 * c]);
+                                sum[8 * h + 2 * c + 1] =
+                                    f32x2_fma(v1, f32x2_mul(sa2, s2.y), sum[8 * h + 2 * c + 1]);
+                            }
+                        } else {
+                            const uint64_t s2 = splat_f32x2(__fmul_rn(sa, sb));
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                sum[8 * h + c] =
+                                    f32x2_fma(f32x2_pack(__uint_as_float(r[h & 1][2 * c]),
+                                                         __uint_as_float(r[h & 1][2 * c + 1])),
+                                              s2, sum[8 * h + c]);
+                        }
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(acce0 + 8 * acc);
                 }
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");   // all have read the last scales
-            if (ok && row < a.M) {
-                __nv_bfloat16 *d = a.D + row * a.ldd;
-                const int64_t c0 = static_cast<int64_t>(nb) * BN;
+            // all have read the last scales before the next tile's are written, and all
+            // go on or none: a warp alone in the next tile's barriers would stay there
+            ok = barrier_and(1, 256, ok);
+            if (ok) {
 #pragma unroll
-                for (int c = 0; c < BN; c += 8) {
-                    float v[8];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t packed[32];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = sum[c + i];
-                    if (c0 + c < a.N)
-                        store_row<__nv_bfloat16, 8>(d, c0 + c, a.N, a.vecd, v);
+                    for (int j = 0; j < 32; ++j) {
+                        float lo, hi;
+                        f32x2_unpack(sum[32 * c + j], lo, hi);
+                        packed[j] = pack2<__nv_bfloat16>(lo, hi);
+                    }
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+                    store_chunk(a, sbuf, row0, col0 + half * 128 + c * EPI_COLS, packed);
                 }
             }
         }
+        if (lane == 0) bulk_wait_group<0>();
+        __syncwarp();
+    }
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ----------------------------------------------------------------- few kernel --
+// A CTA computes 128 rows of B (weights) times NT rows of A (tokens) over its share
+// of the k-blocks; gridDim.x CTAs, a cluster, share a tile's k-blocks.  Warps: 0 TMA,
+// 1 MMA, 2-5 sums as in the f32 kernel (thread = weight row, one sum per token).
+// Shared memory allows two CTAs per SM, so one's start and end overlap the other's loads.
+
+template <int NT>
+struct Few {
+    static constexpr int STAGES = NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
+    static constexpr int X_STAGE = NT * BK;
+    static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+    static constexpr int TMEM = 2 * NT;   // columns, a power of two of at least 32
+    static constexpr size_t SMEM =
+        1024 + STAGES * (HALF + X_STAGE) + 2 * NT * 4 + NUM_BARS * 8 + 16;
+    static_assert(STAGES * (HALF + X_STAGE) >= NT * 128 * 4, "the sums fit where the tiles were");
+};
+
+struct FewArgs {
+    CUtensorMap mapW, mapX;   // B's rows (128 x 128 boxes) and A's (128 x NT)
+    BlockView W, X;
+    __nv_bfloat16 *D;
+    int64_t M, N, ldd;
+    int num_kb;
+    uint32_t idesc;
+};
+
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_constant__ FewArgs a) {
+    using C = Few<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    const uint32_t sW = smem_u32(smem), sX = sW + C::STAGES * HALF;
+    float *sxs = reinterpret_cast<float *>(smem + C::STAGES * (HALF + C::X_STAGE));   // [2][NT]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sxs + 2 * NT);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::NUM_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
+    const uint32_t accf0 = empty0 + 8 * C::STAGES, acce0 = accf0 + 16, drain = acce0 + 16;
+    const int splits = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(a.num_kb) * split / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(a.num_kb) * (split + 1) / splits);
+    const int32_t wrow0 = static_cast<int32_t>(blockIdx.y) * 128;
+    const int32_t xrow0 = static_cast<int32_t>(blockIdx.z) * NT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf0 + 8 * b, 1);
+            mbar_init(acce0 + 8 * b, 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&a.mapW);
+        prefetch_tmap(&a.mapX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    float sum[NT];
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
+                    raise_error(abort_flag);
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = full0 + 8 * stage;
+                mbar_arrive_expect_tx(fb, HALF + C::X_STAGE);
+                tma_load_2d(sW + stage * HALF, &a.mapW, fb, kb * BK, wrow0);
+                tma_load_2d(sX + stage * C::X_STAGE, &a.mapX, fb, kb * BK, xrow0);
+                ++issued;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                // let the copies already issued land before the CTA exits
+                for (int i = 0; i < C::STAGES && issued > 0; ++i, --issued) {
+                    stage = stage == 0 ? C::STAGES - 1 : stage - 1;
+                    if (stage == C::STAGES - 1) phase ^= 1u;
+                    mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool any = false;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) ||
+                    !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
+                    raise_error(abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k)
+                    mma_f8f6f4(tmem + acc * NT, smem_desc_sw128(sW + stage * HALF + 32 * k),
+                               smem_desc_sw128(sX + stage * C::X_STAGE + 32 * k), a.idesc, k != 0);
+                mma_commit(empty0 + 8 * stage);
+                mma_commit(accf0 + 8 * acc);
+                any = true;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+            if (!ok && any) {
+                mma_commit(drain);
+                mbar_wait(drain, 0, nullptr, 100000000ull);
+            }
+        }
+    } else {
+        const int q = warp & 3;
+        const int et = threadIdx.x - 64;
+        const int64_t w = min(static_cast<int64_t>(wrow0) + q * 32 + lane, a.N - 1);
+        const int64_t x = min(static_cast<int64_t>(xrow0) + et, a.M - 1);
+        const int64_t rw = a.W.block_rows == 1 ? w : w >> 7, rx = a.X.block_rows == 1 ? x : x >> 7;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+#pragma unroll
+        for (int c = 0; c < NT; ++c) sum[c] = 0.0f;
+        float sw_next = 0.0f, sx_next = 0.0f;
+        if (kb0 < kb1) {
+            sw_next = load_scale(a.W, rw, kb0);
+            if (et < NT) sx_next = load_scale(a.X, rx, kb0);
+        }
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const float sw = sw_next;
+            float *sx = sxs + ((kb - kb0) & 1) * NT;
+            if (et < NT) sx[et] = sx_next;
+            if (kb + 1 < kb1) {
+                sw_next = load_scale(a.W, rw, kb + 1);
+                if (et < NT) sx_next = load_scale(a.X, rx, kb + 1);
+            }
+            // a buffer is written again only after the next block's barrier
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;   // the others give up in the same wait
+            }
+            if (ok) {
+                tc_fence_after();
+                const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * NT;
+#pragma unroll
+                for (int h = 0; h < NT / 16; ++h) {
+                    uint32_t r[16];
+                    tmem_load_16cols(t + h * 16, r);
+                    tmem_wait_16cols(r);
+                    if (h == NT / 16 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(acce0 + 8 * acc);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        sum[16 * h + c] = __fmaf_rn(__uint_as_float(r[c]), __fmul_rn(sw, sx[16 * h + c]),
+                                                    sum[16 * h + c]);
+                }
+            }
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+    const int64_t tokens = a.M - xrow0 < NT ? a.M - xrow0 : NT;
+    const int64_t n = static_cast<int64_t>(wrow0) + (warp & 3) * 32 + lane;
+    __nv_bfloat16 *d = a.D + static_cast<int64_t>(xrow0) * a.ldd + n;
+    if (splits == 1) {
+        if (warp >= 2 && ok && n < a.N) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                if (c < tokens) d[c * a.ldd] = __float2bfloat16_rn(sum[c]);
+        }
+    } else {
+        // sums [token][weight row] in the shared memory that held the tiles: all MMAs
+        // that read it are done
+        float *red = reinterpret_cast<float *>(smem);
+        __syncthreads();
+        const int r = (warp & 3) * 32 + lane;
+        if (warp >= 2) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+                if (c < tokens) red[c * 128 + r] = sum[c];
+        }
+        __syncwarp();
+        cluster_sync();
+        // this CTA joins every splits-th token, in the order of the splits
+        if (warp >= 2 && n < a.N) {
+            for (int c = split; c < tokens; c += splits) {
+                const uint32_t at = smem_u32(red + c * 128 + r);
+                float s = 0.0f;
+                for (int k = 0; k < splits; ++k)
+                    s = __fadd_rn(s, ld_shared_cluster(mapa_shared(at, static_cast<uint32_t>(k))));
+                d[c * a.ldd] = __float2bfloat16_rn(s);
+            }
+        }
+        __syncwarp();
+        cluster_sync();   // the others have read this CTA's sums
     }
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc(tmem, C::TMEM);
     }
+}
+
+// --------------------------------------------------------------------- host --
+
+// attr must have room for two attributes: the cluster shape and PDL.
+cudaLaunchConfig_t cluster_config(dim3 grid, int threads, size_t smem, int cluster,
+                                  cudaLaunchAttribute *attr, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// The pair kernel's shared-memory limit is set and the number of CTA pairs that
+// can be resident at once is found on the first call.
+struct PairKernel {
+    void (*kernel)(PairArgs);
+    int threads;
+    size_t smem;
+    std::once_flag once;
+    cudaError_t err = cudaSuccess;
+    int slots = 0;
+
+    void init(int sm_count) {
+        std::call_once(once, [this, sm_count] {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+            if (err != cudaSuccess) return;
+            cudaLaunchAttribute attr[2];
+            cudaLaunchConfig_t cfg =
+                cluster_config(dim3(sm_count & ~1), threads, smem, 2, attr, nullptr);
+            cfg.numAttrs = 1;
+            err = cudaOccupancyMaxActiveClusters(&slots, kernel, &cfg);
+        });
+    }
+};
+PairKernel g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
+PairKernel g_f32{block_gemm_f32_kernel, FS_THREADS, FS_SMEM};
+
+template <int NT>
+cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D, int sm_count,
+                       cudaStream_t st, const char **what) {
+    using C = Few<NT>;
+    FewArgs a;
+    if (!encode_tmap_2d(&a.mapW, B.codes, false, B.cols, B.rows, BK, 128, true, B.ld) ||
+        !encode_tmap_2d(&a.mapX, A.codes, false, A.cols, A.rows, BK, NT, true, A.ld)) {
+        *what = "cuTensorMapEncodeTiled failed for an operand";
+        return cudaErrorInvalidValue;
+    }
+    a.W = B;
+    a.X = A;
+    a.D = static_cast<__nv_bfloat16 *>(D.data);
+    a.M = D.rows;
+    a.N = D.cols;
+    a.ldd = D.ld;
+    a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
+    a.idesc = idesc_f8(static_cast<uint32_t>(B.fmt), static_cast<uint32_t>(A.fmt), 128, NT);
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(block_gemm_few_kernel<NT>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(C::SMEM));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const int64_t tw = (D.cols + 127) / 128, tx = (D.rows + NT - 1) / NT;
+    // two CTAs per SM where the k-blocks allow it, at least two k-blocks each
+    int splits = 1;
+    while (splits < 8 && tw * tx * splits * 2 <= 2 * sm_count && a.num_kb >= splits * 4) splits *= 2;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg =
+        cluster_config(dim3(splits, static_cast<unsigned>(tw), static_cast<unsigned>(tx)), 192, C::SMEM,
+                       splits, attr, st);
+    return cudaLaunchKernelEx(&cfg, block_gemm_few_kernel<NT>, a);
 }
 
 }  // namespace
@@ -246,12 +954,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_gemm_kernel(const __grid
 cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatView &D,
                               int sm_count, cudaStream_t st, const char **what) {
     if (D.rows == 0 || D.cols == 0) return cudaSuccess;
-    if (A.cols == 0)
-        return cudaMemset2DAsync(D.data, D.ld * 2, 0, D.cols * 2, D.rows, st);
-    Args a;
+    if (A.cols == 0) return cudaMemset2DAsync(D.data, D.ld * 2, 0, D.cols * 2, D.rows, st);
+    const bool mx = A.scale_f32 == 0;
+    PairKernel &pk = mx ? g_mx : g_f32;
+    if (D.rows > 128) pk.init(sm_count);
+    if (D.rows <= 128 || pk.err != cudaSuccess || pk.slots < 1) {
+        if (pk.err != cudaSuccess) return pk.err;
+        if (D.rows <= 16) return launch_few<16>(A, B, D, sm_count, st, what);
+        if (D.rows <= 32) return launch_few<32>(A, B, D, sm_count, st, what);
+        if (D.rows <= 64) return launch_few<64>(A, B, D, sm_count, st, what);
+        return launch_few<128>(A, B, D, sm_count, st, what);
+    }
+    PairArgs a;
+    a.tma_d = (reinterpret_cast<uintptr_t>(D.data) & 15u) == 0 && D.ld % 8 == 0;
+    a.pairs_d = (reinterpret_cast<uintptr_t>(D.data) & 3u) == 0 && D.ld % 2 == 0;
     if (!encode_tmap_2d(&a.mapA, A.codes, false, A.cols, A.rows, BK, BM, true, A.ld) ||
-        !encode_tmap_2d(&a.mapB, B.codes, false, B.cols, B.rows, BK, BN, true, B.ld)) {
+        !encode_tmap_2d(&a.mapB, B.codes, false, B.cols, B.rows, BK, BN / 2, true, B.ld)) {
         *what = "cuTensorMapEncodeTiled failed for an operand";
+        return cudaErrorInvalidValue;
+    }
+    if (a.tma_d && !encode_tmap_2d(&a.mapD, D.data, true, D.cols, D.rows, EPI_COLS, 32, true, D.ld)) {
+        *what = "cuTensorMapEncodeTiled failed for the output";
         return cudaErrorInvalidValue;
     }
     a.A = A;
@@ -260,20 +983,17 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     a.M = D.rows;
     a.N = D.cols;
     a.ldd = D.ld;
-    a.vecd = (reinterpret_cast<uintptr_t>(D.data) & 15u) == 0 && D.ld % 8 == 0;
+    a.tiles_m = static_cast<int>((D.rows + 2 * BM - 1) / (2 * BM));
     a.tiles_n = static_cast<int>((D.cols + BN - 1) / BN);
-    a.num_tiles = static_cast<int>((D.rows + BM - 1) / BM) * a.tiles_n;
+    a.num_tiles = a.tiles_m * a.tiles_n;
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
-    a.idesc = idesc_f8(static_cast<uint32_t>(A.fmt), static_cast<uint32_t>(B.fmt), BM, BN);
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(block_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(SMEM));
-    });
-    if (attr != cudaSuccess) return attr;
-    const int grid = a.num_tiles < sm_count ? a.num_tiles : sm_count;
-    return launch_pdl(block_gemm_kernel, dim3(grid), dim3(NUM_THREADS), SMEM, st, a);
+    a.group_m = raster_group(D.rows * A.cols, D.cols * A.cols, a.tiles_m);
+    const uint32_t fa = static_cast<uint32_t>(A.fmt), fb = static_cast<uint32_t>(B.fmt);
+    a.idesc = mx ? idesc_mxf8(fa, fb, 2 * BM, BN, 0) : idesc_f8(fa, fb, 2 * BM, BN);
+    const int units = a.num_tiles < pk.slots ? a.num_tiles : pk.slots;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), pk.threads, pk.smem, 2, attr, st);
+    return cudaLaunchKernelEx(&cfg, pk.kernel, a);
 }
 
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags) {

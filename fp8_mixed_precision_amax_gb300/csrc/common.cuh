@@ -251,6 +251,42 @@ __device__ __forceinline__ void tmem_load_32cols(uint32_t taddr, uint32_t (&r)[3
     asm volatile("tcgen05.wait::ld.sync.aligned;" : FP8K_R32(r) : : "memory");
 }
 
+// 16 consecutive fp32 columns of this thread's TMEM lane, without the wait: the
+// registers are tied to the wait (tmem_wait_16cols) that has to follow.
+#define FP8K_R16(r)                                                                              \
+    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),       \
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), \
+        "+r"(r[14]), "+r"(r[15])
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : FP8K_R16(r)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_16cols(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : FP8K_R16(r) : : "memory");
+}
+
+// Store 4 or 8 consecutive 32-bit columns of this thread's TMEM lane, and the
+// wait for this thread's stores.
+__device__ __forceinline__ void tmem_store_4cols(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c,
+                                                 uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // ------------------------------------------- CTA pairs (cta_group::2) --
 // A cluster of two CTAs on two SMs computes one 256-row tile: each CTA
 // TMA-loads its own operand halves into its own shared memory (no
@@ -317,6 +353,28 @@ __device__ __forceinline__ void mma_f8f6f4_pair(uint32_t d_tmem, uint64_t a_desc
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// The same with one E8M0 scale per row of A and of B for the instruction's 32
+// columns (kind::mxf8f6f4), read from tensor memory at sfa and sfb of both CTAs.
+__device__ __forceinline__ void mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::mxf8f6f4: A / B formats (0 = E4M3, 1 = E5M2),
+// both K-major, E8M0 scales in byte `sf` of their tensor-memory words, shape M x N.
+__host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t fa, uint32_t fb, uint32_t m, uint32_t n,
+                                                  uint32_t sf) {
+    return (sf << 4) | (fa << 7) | (fb << 10) | ((n >> 3) << 17) | (1u << 23) | ((m >> 7) << 27) |
+           (sf << 29);
 }
 
 // Arrive once on the mbarrier at the same shared-memory offset in every CTA of
