@@ -36,6 +36,63 @@ __device__ __forceinline__ void raise_error(volatile int *abort_flag) {
     *abort_flag = 1;
 }
 
+// One row's scales along K, fetched four k-blocks ahead: a word of E8M0 bytes or four
+// floats at a time.  (Fetched one block ahead, each block waited for L2: 3500 cycles
+// per block of the f32 kernel instead of the 512 of its MMAs.)
+template <bool MAY_E8M0>
+struct ScaleStream {
+    const uint8_t *row;
+    int num_kb;
+    bool f32, vec;      // vec: four floats are one 16-byte load
+    uint32_t raw[4];    // the next group
+    float cur[4];       // scales from the current k-block on
+
+    __device__ __forceinline__ void fetch(int group) {
+        const int kb = 4 * group;
+        if (kb >= num_kb) return;
+        if (MAY_E8M0 && !f32) {
+            raw[0] = *reinterpret_cast<const uint32_t *>(row + kb);
+        } else if (vec) {
+            const uint4 u = reinterpret_cast<const uint4 *>(row)[group];
+            raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                raw[i] = kb + i < num_kb ? reinterpret_cast<const uint32_t *>(row)[kb + i] : 0u;
+        }
+    }
+    __device__ __forceinline__ void decode() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            cur[i] = MAY_E8M0 && !f32 ? scale_value(raw[0] >> (8 * i) & 0xFFu) : __uint_as_float(raw[i]);
+    }
+    // from k-block kb0 on (rows of E8M0 scales are 4-byte aligned and whole words)
+    __device__ __forceinline__ void start(const BlockView &v, int64_t r, int kb0, int blocks) {
+        const int64_t at = (v.block_rows == 1 ? r : r >> 7) * v.ld_s;
+        f32 = !MAY_E8M0 || v.scale_f32 != 0;
+        row = static_cast<const uint8_t *>(v.scales) + (f32 ? 4 * at : at);
+        vec = ((reinterpret_cast<uintptr_t>(v.scales) | static_cast<uintptr_t>(4 * v.ld_s)) & 15u) == 0;
+        num_kb = blocks;
+        fetch(kb0 >> 2);
+        if (kb0 & 3) {
+            decode();
+            for (int i = 0; i < (kb0 & 3); ++i) shift();
+            fetch((kb0 >> 2) + 1);
+        }
+    }
+    __device__ __forceinline__ void shift() { cur[0] = cur[1], cur[1] = cur[2], cur[2] = cur[3]; }
+    // the scale of k-block kb; called for each in turn
+    __device__ __forceinline__ float next(int kb) {
+        if ((kb & 3) == 0) {
+            decode();
+            fetch((kb >> 2) + 1);
+        }
+        const float s = cur[0];
+        shift();
+        return s;
+    }
+};
+
 // ------------------------------------------------------- pair kernels: common --
 // Two CTAs on two SMs (a cluster) share each 256 x 256 tile (cta_group::2): each
 // loads its own 128 rows of A and 128 of the 256 rows of B, and the even CTA
@@ -104,17 +161,13 @@ __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int un
     }
 }
 
-// A warp's 32 rows x 64 columns of BF16 (lane = row, packed[j] = columns 2j, 2j + 1)
-// to D at (row0, col0) by way of its staging buffer, where 16-byte chunk j of row r
-// sits at j ^ (r mod 8): the 128-byte swizzle of D's tensor map.  Rows of D that TMA
-// cannot address go out with each warp instruction along one row.
+// A warp's 32 rows x 64 columns of BF16 to D at (row0, col0) from its staging buffer,
+// where 16-byte chunk j of row r sits at j ^ (r mod 8): the 128-byte swizzle of D's
+// tensor map.  Rows of D that TMA cannot address go out with each warp instruction
+// along one row.
 __device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, int64_t row0,
-                                            int64_t col0, const uint32_t (&packed)[32]) {
+                                            int64_t col0) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        st_shared_v4(sbuf + lane * 128 + ((j ^ (lane & 7)) << 4), packed[4 * j], packed[4 * j + 1],
-                     packed[4 * j + 2], packed[4 * j + 3]);
     // a TMA store clips at 16-byte steps: a chunk that ends inside one goes the other way
     if (a.tma_d && (col0 + EPI_COLS <= a.N || a.N % 8 == 0)) {
         fence_proxy_async_smem();
@@ -371,8 +424,12 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 // this buffer's previous store (two chunks back) has read it
                 if (lane == 0) bulk_wait_group_read<1>();
                 __syncwarp();
-                store_chunk(a, sD + (q * 2 + (chunk & 1)) * EPI_BUF, row0,
-                            static_cast<int64_t>(nb) * BN + c * EPI_COLS, packed);
+                const uint32_t sbuf = sD + (q * 2 + (chunk & 1)) * EPI_BUF;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    st_shared_v4(sbuf + lane * 128 + ((j ^ (lane & 7)) << 4), packed[4 * j],
+                                 packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
+                store_chunk(a, sbuf, row0, static_cast<int64_t>(nb) * BN + c * EPI_COLS);
                 ++chunk;
             }
         }
@@ -406,23 +463,37 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool pred) {
 // half (w - 4) / 4 of the tile's columns, 128 sums per thread.  Each k-block's MMAs
 // start a fresh accumulator in one of two TMEM buffers; while one is summed the other
 // is computed.  Of the launch's 384 x 168 registers the first four warps hand back
-// 80 each per thread and the eight summing warps take 40 more: 128 x 88 + 256 x 208.
+// 96 each per thread and the eight summing warps take 48 more: 128 x 72 + 256 x 216.
+//
+// The scales of four k-blocks at a time go through shared memory.  A thread reads the
+// accumulator as 16 lanes x 256 bits: it holds 4 rows and 32 columns of the warp's
+// 32 x 128, so that it needs 4 scales of A and 32 of B.  (With one row per thread,
+// it needs 128 of B, and their 128 x 32 lanes x 4 bytes from shared memory took twice
+// the MMAs' time.)  PER_ROW: B has one scale per row; otherwise the 128 columns of a
+// warp share one.
 
 constexpr int FS_STAGES = 5;
 constexpr int FS_THREADS = 384;
-constexpr int FS_REGS_CONTROL = 88, FS_REGS_SUMS = 208;
+constexpr int FS_REGS_CONTROL = 72, FS_REGS_SUMS = 216;
 static_assert(128 * FS_REGS_CONTROL + 256 * FS_REGS_SUMS <= FS_THREADS * 168, "register split");
 constexpr int FS_BARS = 2 * FS_STAGES + 4 + 1;
-constexpr size_t FS_SMEM = 1024 + FS_STAGES * 2 * HALF + 8 * EPI_BUF + 2 * BN * 4 + FS_BARS * 8 + 16;
+// B's scales of a k-block: per half of the columns and lane class (columns 8 j + 2 c,
+// + 1 of class c) 32 floats, padded by 16 bytes so that the four classes' reads fall
+// into different banks.
+constexpr int FS_CLASS = 36, FS_SB = 8 * FS_CLASS;
+constexpr size_t FS_SMEM = 1024 + FS_STAGES * 2 * HALF + 8 * EPI_BUF + 8 * (FS_SB + BM) * 4 +
+                           FS_BARS * 8 + 16;
 
+template <bool PER_ROW>
 __global__ void __launch_bounds__(FS_THREADS, 1)
     block_gemm_f32_kernel(const __grid_constant__ PairArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     const uint32_t sA = smem_u32(smem), sB = sA + FS_STAGES * HALF;
     const uint32_t sD = sB + FS_STAGES * HALF;
-    float *sbs = reinterpret_cast<float *>(smem + FS_STAGES * 2 * HALF + 8 * EPI_BUF);   // [2][BN]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sbs + 2 * BN);
+    float *sbs = reinterpret_cast<float *>(smem + FS_STAGES * 2 * HALF + 8 * EPI_BUF);   // [8][FS_SB]
+    float *sas = sbs + 8 * FS_SB;                                                        // [8][BM]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sas + 8 * BM);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + FS_BARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -503,42 +574,53 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FS_REGS_SUMS));
         const int q = warp & 3, half = (warp - 4) >> 2;
-        const int et = threadIdx.x - 128;   // 0..255: the column whose scale this thread fetches
+        const int et = threadIdx.x - 128;   // 0..255: the column (and row) whose scales it fetches
         const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
         const uint32_t sbuf = sD + (warp - 4) * EPI_BUF;
-        const bool per_row = a.B.block_rows == 1;   // otherwise one scale of B per half
+        const int own_col = (et >> 7) * 4 * FS_CLASS + ((et >> 1) & 3) * FS_CLASS +
+                            ((et >> 3) & 15) * 2 + (et & 1);
+        const int my_cols = half * 4 * FS_CLASS + (lane & 3) * FS_CLASS;
+        const int my_row = q * 32 + (lane >> 2);
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
             int mb, nb;
             tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
-            const int64_t row0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32;
+            const int64_t crow0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM;
             const int64_t col0 = static_cast<int64_t>(nb) * BN;
             // rows and columns past the end repeat the last one
-            const int64_t row = min(row0 + lane, a.M - 1);
-            const int64_t col = min(col0 + (per_row ? et : half * 128), a.N - 1);
-            const float *pa = static_cast<const float *>(a.A.scales) +
-                              (a.A.block_rows == 1 ? row : row >> 7) * a.A.ld_s;
-            const float *pb = static_cast<const float *>(a.B.scales) +
-                              (per_row ? col : col >> 7) * a.B.ld_s;
-            uint64_t sum[64];   // pairs of columns
+            ScaleStream<false> fa, fb;
+            if (et < BM) fa.start(a.A, min(crow0 + et, a.M - 1), 0, a.num_kb);
+            fb.start(a.B, min(col0 + et, a.N - 1), 0, a.num_kb);
+            uint64_t sum[4][16];   // [row lane / 4 + 8 i][columns 8 j + 2 (lane mod 4), + 1]
 #pragma unroll
-            for (int c = 0; c < 64; ++c) sum[c] = 0;
-            float sa_next = pa[0], sb_next = pb[0];
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[i][j] = 0;
 #pragma unroll 1
             for (int kb = 0; kb < a.num_kb; ++kb) {
-                const float sa = sa_next, sb = sb_next;
-                if (kb + 1 < a.num_kb) {
-                    sa_next = pa[kb + 1];
-                    sb_next = pb[kb + 1];
-                }
-                const float *sbk = sbs + (kb & 1) * BN;
-                if (per_row) {
-                    sbs[(kb & 1) * BN + et] = sb;
-                    // a buffer is written again only after the next block's barrier
+                if ((kb & 3) == 0) {
+                    // the scales of four k-blocks; they are written over eight blocks
+                    // later, with a barrier in between
+                    if (et < BM) {
+                        fa.decode();
+                        fa.fetch((kb >> 2) + 1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sas[((kb & 7) + i) * BM + et] = fa.cur[i];
+                    }
+                    fb.decode();
+                    fb.fetch((kb >> 2) + 1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sbs[((kb & 7) + i) * FS_SB + own_col] = fb.cur[i];
                     asm volatile("bar.sync 1, 256;" ::: "memory");
                 }
+                const float *sbk = sbs + (kb & 7) * FS_SB + my_cols;
+                const float *sak = sas + (kb & 7) * BM + my_row;
+                uint64_t sa2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sa2[i] = splat_f32x2(PER_ROW ? sak[8 * i] : __fmul_rn(sak[8 * i], sbk[0]));
                 const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
                 if (!__all_sync(0xFFFFFFFFu, got)) {
                     if (lane == 0) raise_error(abort_flag);
@@ -548,40 +630,41 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                     tc_fence_after();
                     const uint32_t t = t0 + acc * BN;
                     uint32_t r[2][16];
-                    tmem_load_16cols(t, r[0]);
+                    uint64_t sb2[4];
+                    tmem_load_16x256b_x4(t, r[0]);
 #pragma unroll
                     for (int h = 0; h < 8; ++h) {
-                        tmem_wait_16cols(r[h & 1]);
+                        // 32 columns (h / 2) of the quarter's lanes 16 (h mod 2) .. + 15
+                        uint32_t(&v)[16] = r[h & 1];
+                        tmem_wait_16cols(v);
                         if (h < 7) {
-                            tmem_load_16cols(t + (h + 1) * 16, r[(h + 1) & 1]);
+                            tmem_load_16x256b_x4(t + ((h + 1) >> 1) * 32 +
+                                                     (static_cast<uint32_t>((h + 1) & 1) << 20),
+                                                 r[(h + 1) & 1]);
                         } else {
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(mapa_shared(acce0 + 8 * acc, 0));
+                            if (lane == 0)
+                                mbar_arrive_cluster_relaxed(mapa_shared(acce0 + 8 * acc, 0));
                         }
-                        if (per_row) {
-                            const uint64_t sa2 = splat_f32x2(sa);
+                        if (PER_ROW && (h & 1) == 0) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const ulonglong2 s2 = *reinterpret_cast<const ulonglong2 *>(
-                                    sbk + half * 128 + h * 16 + 4 * c);
-                                const uint64_t v0 = f32x2_pack(__uint_as_float(r[h & 1][4 * c]),
-                                                               __uint_as_float(r[h & 1][4 * c + 1]));
-                                const uint64_t v1 = f32x2_pack(__uint_as_float(r[h & 1][4 * c + 2]),
-                                                               __uint_as_float(r[h & 1][4 * c + 3]));
-                                sum[8 * h + 2 * c] =
-                                    f32x2_fma(v0, f32x2_mul(sa2, s2.x), sum[8 * h + 2 * c]);
-                                sum[8 * h + 2 * c + 1] =
-                                    f32x2_fma(v1, f32x2_mul(sa2, s2.y), sum[8 * h + 2 * c + 1]);
+                            for (int j = 0; j < 2; ++j) {
+                                const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(
+                                    sbk + (h >> 1) * 8 + 4 * j);
+                                sb2[2 * j] = u.x, sb2[2 * j + 1] = u.y;
                             }
-                        } else {
-                            const uint64_t s2 = splat_f32x2(__fmul_rn(sa, sb));
+                        }
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                sum[8 * h + c] =
-                                    f32x2_fma(f32x2_pack(__uint_as_float(r[h & 1][2 * c]),
-                                                         __uint_as_float(r[h & 1][2 * c + 1])),
-                                              s2, sum[8 * h + c]);
+                        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint64_t x = f32x2_pack(__uint_as_float(v[4 * j + 2 * i]),
+                                                              __uint_as_float(v[4 * j + 2 * i + 1]));
+                                const uint64_t s1 = sa2[2 * (h & 1) + i];
+                                uint64_t &to = sum[2 * (h & 1) + i][4 * (h >> 1) + j];
+                                to = f32x2_fma(x, PER_ROW ? f32x2_mul(s1, sb2[j]) : s1, to);
+                            }
                         }
                     }
                 }
@@ -596,16 +679,22 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
             if (ok) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t packed[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float lo, hi;
-                        f32x2_unpack(sum[32 * c + j], lo, hi);
-                        packed[j] = pack2<__nv_bfloat16>(lo, hi);
-                    }
                     if (lane == 0) bulk_wait_group_read<0>();
                     __syncwarp();
-                    store_chunk(a, sbuf, row0, col0 + half * 128 + c * EPI_COLS, packed);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            float lo, hi;
+                            f32x2_unpack(sum[i][8 * c + j], lo, hi);
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(
+                                             sbuf + ((lane >> 2) + 8 * i) * 128 +
+                                             ((j ^ (lane >> 2)) << 4) + (lane & 3) * 4),
+                                         "r"(pack2<__nv_bfloat16>(lo, hi))
+                                         : "memory");
+                        }
+                    }
+                    store_chunk(a, sbuf, crow0 + q * 32, col0 + half * 128 + c * EPI_COLS);
                 }
             }
         }
@@ -771,25 +860,18 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
         const int et = threadIdx.x - 64;
         const int64_t w = min(static_cast<int64_t>(wrow0) + q * 32 + lane, a.N - 1);
         const int64_t x = min(static_cast<int64_t>(xrow0) + et, a.M - 1);
-        const int64_t rw = a.W.block_rows == 1 ? w : w >> 7, rx = a.X.block_rows == 1 ? x : x >> 7;
         int acc = 0;
         uint32_t acc_phase = 0;
 #pragma unroll
         for (int c = 0; c < NT; ++c) sum[c] = 0.0f;
-        float sw_next = 0.0f, sx_next = 0.0f;
-        if (kb0 < kb1) {
-            sw_next = load_scale(a.W, rw, kb0);
-            if (et < NT) sx_next = load_scale(a.X, rx, kb0);
-        }
+        ScaleStream<true> fw, fx;
+        fw.start(a.W, w, kb0, kb1);
+        fx.start(a.X, x, kb0, kb1);
 #pragma unroll 1
         for (int kb = kb0; kb < kb1; ++kb) {
-            const float sw = sw_next;
+            const float sw = fw.next(kb), sx_own = fx.next(kb);
             float *sx = sxs + ((kb - kb0) & 1) * NT;
-            if (et < NT) sx[et] = sx_next;
-            if (kb + 1 < kb1) {
-                sw_next = load_scale(a.W, rw, kb + 1);
-                if (et < NT) sx_next = load_scale(a.X, rx, kb + 1);
-            }
+            if (et < NT) sx[et] = sx_own;
             // a buffer is written again only after the next block's barrier
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
@@ -910,7 +992,8 @@ struct PairKernel {
     }
 };
 PairKernel g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
-PairKernel g_f32{block_gemm_f32_kernel, FS_THREADS, FS_SMEM};
+PairKernel g_f32_tiles{block_gemm_f32_kernel<false>, FS_THREADS, FS_SMEM};
+PairKernel g_f32_rows{block_gemm_f32_kernel<true>, FS_THREADS, FS_SMEM};
 
 template <int NT>
 cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D, int sm_count,
@@ -956,7 +1039,7 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     if (D.rows == 0 || D.cols == 0) return cudaSuccess;
     if (A.cols == 0) return cudaMemset2DAsync(D.data, D.ld * 2, 0, D.cols * 2, D.rows, st);
     const bool mx = A.scale_f32 == 0;
-    PairKernel &pk = mx ? g_mx : g_f32;
+    PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
     if (D.rows > 128) pk.init(sm_count);
     if (D.rows <= 128 || pk.err != cudaSuccess || pk.slots < 1) {
         if (pk.err != cudaSuccess) return pk.err;

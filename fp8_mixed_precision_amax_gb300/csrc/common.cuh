@@ -265,6 +265,17 @@ __device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[1
         : "r"(taddr)
         : "memory");
 }
+// The same of 16 lanes x 32 columns: lane t of the warp gets, for each 8 columns j,
+// r[4 j], r[4 j + 1] = row t / 4, columns 8 j + 2 (t mod 4), + 1, and r[4 j + 2],
+// r[4 j + 3] = the same columns of row t / 4 + 8.
+__device__ __forceinline__ void tmem_load_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : FP8K_R16(r)
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_16cols(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : FP8K_R16(r) : : "memory");
 }
@@ -314,6 +325,14 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // Arrive on an mbarrier of any CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
+// The same without the release of this thread's memory operations (which waits for
+// its loads in flight): for handing back tensor memory whose loads have been waited
+// for and fenced (tcgen05.fence::before_thread_sync).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
 }
 
