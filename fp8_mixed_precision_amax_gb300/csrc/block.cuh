@@ -228,28 +228,128 @@ __device__ __forceinline__ void store_code_word(uint8_t *p, uint32_t w, int64_t 
 
 // ----------------------------------------------------------- tile kernels --
 //
-// A CTA of 512 threads holds a 128 x 128 tile in fp32 registers: warp w has
-// rows 8 w .. 8 w + 7, lane l columns 4 l .. 4 l + 3, so v[r][j] is row
-// 8 w + r, column 4 l + j.  Elements outside the matrix are 0: they leave
-// every maximum as it is.  A row's maximum is one warp reduction; a column's
-// is taken over a thread's 8 rows and then over the 16 warps in shared memory.
+// Persistent CTAs of 512 threads hold one 128 x 128 tile at a time in fp32 registers:
+// warp w has rows 8 w .. 8 w + 7, lane l columns 4 l .. 4 l + 3 as two packed
+// pairs, so v[r][p] is row 8 w + r, columns 4 l + 2 p, + 1.  Elements outside the
+// matrix are 0: they leave every maximum as it is.  While a tile is worked on, each
+// warp's rows of the CTA's next tile are already on their way into shared memory
+// (cp.async, waited for by that warp alone).
+//
+// A row's maximum is one warp reduction.  A column's is taken over a thread's 8
+// rows, then over the 16 warps by one thread per column.  The transposed codes go
+// through shared memory and leave in rows of 128 bytes.
 
 constexpr int kTile = 128;
 constexpr int kTileThreads = 512;
 constexpr int kTileRows = 8;   // rows per warp
 
-struct TileSmem {
-    uint32_t colmax[16][kTile];   // per warp: a column's maximum over the warp's rows
-    uint8_t codes[kTile * kTile]; // transposed codes [column][row], swizzled (see tile_cols)
-};
+using TileValues = uint64_t[kTileRows][2];
 
-// The tile's own maximum (block_rows 128), the same in every thread.
-__device__ __forceinline__ uint32_t tile_max(const float (&v)[kTileRows][4], uint32_t *red) {
+// Tile t of a matrix of tiles_r x tiles_c: four rows of tiles are walked side by side,
+// column by column, so that the neighbours whose scales share a word (four tiles
+// down, four tiles across) and whose transposed rows continue each other are in
+// flight together.
+__device__ __forceinline__ void tile_origin(unsigned t, unsigned tiles_r, unsigned tiles_c,
+                                            int64_t &row0, int64_t &col0) {
+    const unsigned group = t / (4 * tiles_c), in = t - group * 4 * tiles_c;
+    const unsigned rows = min(4u, tiles_r - 4 * group);
+    row0 = static_cast<int64_t>(4 * group + in % rows) * kTile;
+    col0 = static_cast<int64_t>(in / rows) * kTile;
+}
+
+__host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// This warp's 8 rows x 128 columns of elements of `size` bytes at (row0, col0) into
+// its part of a stage (rows of 128 * size bytes); outside the matrix: zeros.  vec:
+// rows are 16-byte aligned; otherwise elements are copied one by one.
+template <int SIZE>
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const void *base, int64_t ld, int64_t rows,
+                                           int64_t cols, bool vec, int64_t row0, int64_t col0) {
+    constexpr int kPerRow = kTile * SIZE / 16;   // 16-byte chunks
+    constexpr int kElems = 16 / SIZE;
+    const int lane = threadIdx.x & 31;
+    const int64_t first = row0 + (threadIdx.x >> 5) * kTileRows;
+    const uint8_t *p = static_cast<const uint8_t *>(base);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < kTileRows * kPerRow / 32; ++i) {
+            const int idx = i * 32 + lane, r = idx / kPerRow, k = idx % kPerRow;
+            const int64_t c = col0 + k * kElems;
+            int64_t left = first + r < rows ? (cols - c) * SIZE : 0;
+            left = left < 0 ? 0 : left > 16 ? 16 : left;
+            const uint8_t *src = left ? p + ((first + r) * ld + c) * SIZE : p;
+            cp_async16(dst + r * kTile * SIZE + k * 16, src, static_cast<uint32_t>(left));
+        }
+    } else {
+        for (int idx = lane; idx < kTileRows * kTile; idx += 32) {
+            const int r = idx / kTile, k = idx % kTile;
+            const bool in = first + r < rows && col0 + k < cols;
+            const uint8_t *src = p + ((first + r) * ld + col0 + k) * SIZE;
+            const uint32_t at = dst + idx * SIZE;
+            if constexpr (SIZE == 4) {
+                const uint32_t w = in ? *reinterpret_cast<const uint32_t *>(src) : 0u;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+            } else {
+                const uint16_t w = in ? *reinterpret_cast<const uint16_t *>(src) : uint16_t(0);
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(w) : "memory");
+            }
+        }
+    }
+}
+
+// Row r's four elements of this lane from a warp's part of a stage.
+template <typename T>
+__device__ __forceinline__ void staged4(const uint8_t *part, int r, uint64_t (&v)[2]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (sizeof(T) == 4) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(part + r * 512 + lane * 16);
+        v[0] = u.x, v[1] = u.y;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2 *>(part + r * 256 + lane * 8);
+        const float2 a = unpack2<T>(u.x), b = unpack2<T>(u.y);
+        v[0] = f32x2_pack(a.x, a.y), v[1] = f32x2_pack(b.x, b.y);
+    }
+}
+// The same of FP8 codes, times the row's scale.
+__device__ __forceinline__ void staged_codes4(const uint8_t *part, int r, int fmt, float scale,
+                                              uint64_t (&v)[2]) {
+    float f[4];
+    decode4(*reinterpret_cast<const uint32_t *>(part + r * 128 + (threadIdx.x & 31) * 4), fmt, f);
+    const uint64_t s2 = splat_f32x2(scale);
+    v[0] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
+    v[1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
+}
+
+// max |x| over finite x, given the plain maximum (which skips NaN unless there is
+// nothing else): only an infinity or nothing but NaN takes the slow way.
+__device__ __forceinline__ uint32_t finite_max4(float a, float b, float c, float d) {
+    const float m = fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));
+    if (m < __uint_as_float(0x7F800000u)) return __float_as_uint(m);
+    return max(max(finite_abs_bits(a), finite_abs_bits(b)),
+               max(finite_abs_bits(c), finite_abs_bits(d)));
+}
+
+// The tile's own maximum (block_rows 128), the same in every thread.  One barrier;
+// red is not written again before another one.
+__device__ __forceinline__ uint32_t tile_max(const TileValues &v, uint32_t *red) {
     uint32_t m = 0;
 #pragma unroll
-    for (int r = 0; r < kTileRows; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, finite_abs_bits(v[r][j]));
+    for (int r = 0; r < kTileRows; ++r) {
+        float a, b, c, d;
+        f32x2_unpack(v[r][0], a, b);
+        f32x2_unpack(v[r][1], c, d);
+        m = max(m, finite_max4(a, b, c, d));
+    }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -260,79 +360,102 @@ __device__ __forceinline__ uint32_t tile_max(const float (&v)[kTileRows][4], uin
 // Row-major codes and scales of the tile at (row0, col0).  tile_byte < 0: one
 // scale per row; otherwise the whole tile's.
 template <int FMT>
-__device__ __forceinline__ void tile_rows(const float (&v)[kTileRows][4], const BlockView &q,
-                                          int64_t row0, int64_t col0, int tile_byte) {
+__device__ __forceinline__ void tile_rows(const TileValues &v, const BlockView &q, int64_t row0,
+                                          int64_t col0, int tile_byte) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = col0 + 4 * lane;
+    const int64_t first = row0 + warp * kTileRows, c = col0 + 4 * lane;
     if (tile_byte >= 0 && threadIdx.x == 0)
         store_scale(q, row0 / kTile, col0 / kTile, static_cast<uint32_t>(tile_byte));
+    uint32_t mine = 0;   // lane r: row r's scale
+    uint8_t *p = q.codes + first * q.ld + c;
 #pragma unroll
     for (int r = 0; r < kTileRows; ++r) {
-        const int64_t row = row0 + warp * kTileRows + r;
         uint32_t byte = static_cast<uint32_t>(tile_byte);
         if (tile_byte < 0) {
-            const uint32_t m = max(max(finite_abs_bits(v[r][0]), finite_abs_bits(v[r][1])),
-                                   max(finite_abs_bits(v[r][2]), finite_abs_bits(v[r][3])));
-            byte = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, m));
+            float x, y, z, w;
+            f32x2_unpack(v[r][0], x, y);
+            f32x2_unpack(v[r][1], z, w);
+            byte = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, finite_max4(x, y, z, w)));
+            if (lane == r) mine = byte;
         }
-        if (row >= q.rows) continue;   // the same for the whole warp
-        if (tile_byte < 0 && lane == 0) store_scale(q, row, col0 / kTile, byte);
-        const uint32_t w = encode4<FMT>(v[r][0], v[r][1], v[r][2], v[r][3], scale_inverse(byte));
-        if (c < q.cols) store_code_word(q.codes + row * q.ld + c, w, q.cols - c);
+        const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
+        float x, y, z, w;
+        f32x2_unpack(f32x2_mul(v[r][0], inv2), x, y);
+        f32x2_unpack(f32x2_mul(v[r][1], inv2), z, w);
+        const uint32_t code = cvt2_fp8<FMT>(x, y) | (cvt2_fp8<FMT>(z, w) << 16);
+        if (first + r < q.rows && c < q.cols) store_code_word(p, code, q.cols - c);
+        p += q.ld;
+    }
+    if (tile_byte < 0 && lane < kTileRows && first + lane < q.rows)
+        store_scale(q, first + lane, col0 / kTile, mine);
+}
+
+// Transposition, in steps with a barrier between each two:
+//   cols_max     per warp and column, the maximum over the warp's rows;
+//   cols_scale   one thread per column: its scale, to memory and, inverted, to inv;
+//   cols_codes   codes into `codes`: column c's 128 bytes are its row c, in
+//                chunks of 16 bytes (two warps' 8 rows each); chunk k is kept at place
+//                k ^ ((c >> 2) & 7), its halves swapped when bit 5 of c is set: the
+//                lanes of a warp write 8 bytes each to columns 4 apart, and half a warp
+//                then covers all banks once;
+//   cols_store   the tile's columns as rows of qt.
+struct ColsSmem {
+    uint32_t max[16][kTile];
+    float inv[kTile];
+    uint8_t codes[kTile * kTile];
+};
+
+__device__ __forceinline__ void cols_max(const TileValues &v, ColsSmem &sm) {
+    uint32_t m[4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        float lo[kTileRows], hi[kTileRows];
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r) f32x2_unpack(v[r][p], lo[r], hi[r]);
+        m[2 * p] = max(finite_max4(lo[0], lo[1], lo[2], lo[3]), finite_max4(lo[4], lo[5], lo[6], lo[7]));
+        m[2 * p + 1] =
+            max(finite_max4(hi[0], hi[1], hi[2], hi[3]), finite_max4(hi[4], hi[5], hi[6], hi[7]));
+    }
+    *reinterpret_cast<uint4 *>(&sm.max[threadIdx.x >> 5][4 * (threadIdx.x & 31)]) =
+        make_uint4(m[0], m[1], m[2], m[3]);
+}
+
+// thread c (0 .. 127) of the caller's choice
+template <int FMT>
+__device__ __forceinline__ void cols_scale(int c, ColsSmem &sm, const BlockView &qt, int64_t row0,
+                                           int64_t col0) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) m = max(m, sm.max[w][c]);
+    const uint32_t byte = scale_byte<FMT>(m);
+    sm.inv[c] = scale_inverse(byte);
+    if (col0 + c < qt.rows) store_scale(qt, col0 + c, row0 / kTile, byte);
+}
+
+template <int FMT>
+__device__ __forceinline__ void cols_codes(const TileValues &v, const ulonglong2 inv, ColsSmem &sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        float lo[kTileRows], hi[kTileRows];
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r)
+            f32x2_unpack(f32x2_mul(v[r][p], p ? inv.y : inv.x), lo[r], hi[r]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float(&x)[kTileRows] = j ? hi : lo;
+            const int c = 4 * lane + 2 * p + j;
+            const int at = c * kTile + (((warp >> 1) ^ ((c >> 2) & 7)) << 4) +
+                           (((warp & 1) ^ ((c >> 5) & 1)) << 3);
+            *reinterpret_cast<uint2 *>(&sm.codes[at]) =
+                make_uint2(cvt2_fp8<FMT>(x[0], x[1]) | (cvt2_fp8<FMT>(x[2], x[3]) << 16),
+                           cvt2_fp8<FMT>(x[4], x[5]) | (cvt2_fp8<FMT>(x[6], x[7]) << 16));
+        }
     }
 }
 
-// The transpose of the tile: qt's rows are the tile's columns.  The codes go
-// through shared memory: column c's 128 bytes are row c of `codes`, in chunks of
-// 16 bytes (two warps' 8 rows each).  Chunk k is kept at place
-// k ^ ((c >> 2) & 7), its halves swapped when bit 5 of c is set: the lanes of a
-// warp write 8 bytes each to columns 4 apart, and half a warp then covers all
-// banks once.  Called by all threads; begins with the caller's shared memory free.
-template <int FMT>
-__device__ __forceinline__ void tile_cols(const float (&v)[kTileRows][4], const BlockView &qt,
-                                          int64_t row0, int64_t col0, int tile_byte,
-                                          TileSmem &sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float inv[4];
-    if (tile_byte < 0) {
-        uint32_t m[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            m[j] = 0;
-#pragma unroll
-            for (int r = 0; r < kTileRows; ++r) m[j] = max(m[j], finite_abs_bits(v[r][j]));
-        }
-        *reinterpret_cast<uint4 *>(&sm.colmax[warp][4 * lane]) = make_uint4(m[0], m[1], m[2], m[3]);
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 16; ++w) {
-            const uint4 o = *reinterpret_cast<const uint4 *>(&sm.colmax[w][4 * lane]);
-            m[0] = max(m[0], o.x), m[1] = max(m[1], o.y), m[2] = max(m[2], o.z),
-            m[3] = max(m[3], o.w);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t byte = scale_byte<FMT>(m[j]);
-            inv[j] = scale_inverse(byte);
-            const int64_t c = col0 + 4 * lane + j;
-            if (warp == 0 && c < qt.rows) store_scale(qt, c, row0 / kTile, byte);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) inv[j] = scale_inverse(static_cast<uint32_t>(tile_byte));
-        if (threadIdx.x == 0)
-            store_scale(qt, col0 / kTile, row0 / kTile, static_cast<uint32_t>(tile_byte));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int c = 4 * lane + j;
-        const uint32_t lo = encode4<FMT>(v[0][j], v[1][j], v[2][j], v[3][j], inv[j]);
-        const uint32_t hi = encode4<FMT>(v[4][j], v[5][j], v[6][j], v[7][j], inv[j]);
-        const int at = c * kTile + (((warp >> 1) ^ ((c >> 2) & 7)) << 4) +
-                       (((warp & 1) ^ ((c >> 5) & 1)) << 3);
-        *reinterpret_cast<uint2 *>(&sm.codes[at]) = make_uint2(lo, hi);
-    }
-    __syncthreads();
+__device__ __forceinline__ void cols_store(const ColsSmem &sm, const BlockView &qt, int64_t row0,
+                                           int64_t col0) {
 #pragma unroll
     for (int i = 0; i < kTile * kTile / 16 / kTileThreads; ++i) {
         const int idx = threadIdx.x + i * kTileThreads;
@@ -351,6 +474,10 @@ __device__ __forceinline__ void tile_cols(const float (&v)[kTileRows][4], const 
             store_code_word(p + 12, u.w, qt.cols - r - 12);
         }
     }
+}
+
+__device__ __forceinline__ ulonglong2 cols_inv(const ColsSmem &sm) {
+    return *reinterpret_cast<const ulonglong2 *>(&sm.inv[4 * (threadIdx.x & 31)]);
 }
 
 }  // namespace fp8k

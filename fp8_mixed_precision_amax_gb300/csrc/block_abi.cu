@@ -127,7 +127,7 @@ fp8_status fp8_block_quantize(const fp8_matrix *x, const fp8_block_tensor *q,
     FP8_TRY(check_tiles(fn, vx.rows, vx.cols));
     int sms;
     FP8_TRY(current_device(&sms));
-    FP8_CUDA(fp8k::launch_block_quantize(vx, vq, vqt, static_cast<cudaStream_t>(stream)), fn);
+    FP8_CUDA(fp8k::launch_block_quantize(vx, vq, vqt, sms, static_cast<cudaStream_t>(stream)), fn);
     return FP8_OK;
 }
 
@@ -271,7 +271,7 @@ fp8_status fp8_layernorm_recompute(const fp8_block_tensor *x8, const void *gamma
     FP8_TRY(check_tiles(fn, vx8.rows, vx8.cols));
     int sms;
     FP8_TRY(current_device(&sms));
-    FP8_CUDA(fp8k::launch_ln_recompute(vx8, gamma, beta, wtype, mean, rstd, vyt,
+    FP8_CUDA(fp8k::launch_ln_recompute(vx8, gamma, beta, wtype, mean, rstd, vyt, sms,
                                        static_cast<cudaStream_t>(stream)),
              fn);
     return FP8_OK;
@@ -324,7 +324,7 @@ fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
     FP8_TRY(check_tiles(fn, M, F));
     int sms;
     FP8_TRY(current_device(&sms));
-    FP8_CUDA(fp8k::launch_swiglu_bwd(vda, vh8, vdh8, vdh8t, va8t,
+    FP8_CUDA(fp8k::launch_swiglu_bwd(vda, vh8, vdh8, vdh8t, va8t, sms,
                                      static_cast<cudaStream_t>(stream)),
              fn);
     return FP8_OK;

@@ -6,6 +6,7 @@
 // All are bound by HBM.  What has to be written transposed goes tile by tile
 // (128 x 128, one block wide both ways), the rest row by row.
 #include <cstdint>
+#include <mutex>
 
 #include "block.cuh"
 
@@ -13,41 +14,71 @@ namespace fp8k {
 
 namespace {
 
-// The CTA's tile: tiles are numbered along the rows of tiles.
-__device__ __forceinline__ void tile_origin(int64_t cols, int64_t &row0, int64_t &col0) {
-    const unsigned per_row = static_cast<unsigned>((cols + kTile - 1) / kTile);
-    row0 = static_cast<int64_t>(blockIdx.x / per_row) * kTile;
-    col0 = static_cast<int64_t>(blockIdx.x % per_row) * kTile;
-}
-
 // ----------------------------------------------------------- quantization --
 
+template <typename T>
+struct QuantSmem {
+    uint8_t in[2][kTile * kTile * sizeof(T)];
+    ColsSmem cols;
+    uint32_t red[2][16];
+};
+
+// Both ways or the transpose alone; also tiles row-major.
 template <typename T, int FMT, bool TILE>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 4 ? 1 : 2)
     block_quantize_kernel(const T *__restrict__ x, int64_t rows, int64_t cols, int64_t ld, bool vec,
-                          const BlockView q, const BlockView qt) {
-    __shared__ __align__(16) TileSmem sm;
-    __shared__ uint32_t red[16];
+                          const BlockView q, const BlockView qt, unsigned tiles_r,
+                          unsigned tiles_c) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    QuantSmem<T> &sm = *reinterpret_cast<QuantSmem<T> *>(smem_raw);
+    const int part = (threadIdx.x >> 5) * kTileRows * kTile * static_cast<int>(sizeof(T));
     pdl_wait();
     pdl_trigger();
+    const unsigned tiles = tiles_r * tiles_c;
     int64_t row0, col0;
-    tile_origin(cols, row0, col0);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float v[kTileRows][4];
-#pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-        const int64_t row = row0 + warp * kTileRows + r;
-        if (row < rows) {
-            load_row<T, 4>(x + row * ld, col0 + 4 * lane, cols, vec, v[r]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[r][j] = 0.0f;
+    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
+    fetch_rows<sizeof(T)>(smem_u32(sm.in[0]) + part, x, ld, rows, cols, vec, row0, col0);
+    cp_async_commit();
+    int stage = 0;
+    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, stage ^= 1) {
+        int64_t next_row0 = 0, next_col0 = 0;
+        __syncwarp();   // the warp has read this part of the other stage
+        if (t + gridDim.x < tiles) {
+            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+            fetch_rows<sizeof(T)>(smem_u32(sm.in[stage ^ 1]) + part, x, ld, rows, cols, vec,
+                                  next_row0, next_col0);
         }
+        cp_async_commit();
+        cp_async_wait<1>();
+        __syncwarp();
+        TileValues v;
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r) staged4<T>(sm.in[stage] + part, r, v[r]);
+        int byte = -1;
+        if constexpr (TILE) byte = static_cast<int>(scale_byte<FMT>(tile_max(v, sm.red[stage])));
+        if (qt.codes != nullptr) {
+            ulonglong2 inv;
+            if constexpr (TILE) {
+                if (threadIdx.x == 0) store_scale(qt, col0 / kTile, row0 / kTile, byte);
+                inv.x = inv.y = splat_f32x2(scale_inverse(byte));
+            } else {
+                cols_max(v, sm.cols);
+                __syncthreads();
+                if (threadIdx.x < kTile) cols_scale<FMT>(threadIdx.x, sm.cols, qt, row0, col0);
+                __syncthreads();
+                inv = cols_inv(sm.cols);
+            }
+            cols_codes<FMT>(v, inv, sm.cols);
+        }
+        if (q.codes != nullptr) tile_rows<FMT>(v, q, row0, col0, byte);
+        if (qt.codes != nullptr) {
+            __syncthreads();
+            cols_store(sm.cols, qt, row0, col0);
+            // with tiles, nothing else keeps the next codes from overtaking these reads
+            if constexpr (TILE) __syncthreads();
+        }
+        row0 = next_row0, col0 = next_col0;
     }
-    int byte = -1;
-    if constexpr (TILE) byte = static_cast<int>(scale_byte<FMT>(tile_max(v, red)));
-    if (q.codes != nullptr) tile_rows<FMT>(v, q, row0, col0, byte);
-    if (qt.codes != nullptr) tile_cols<FMT>(v, qt, row0, col0, byte, sm);
 }
 
 // One warp per 1024 columns of a row, 8 per lane and step of 256.
@@ -75,45 +106,78 @@ __global__ void __launch_bounds__(256) block_dequantize_kernel(const BlockView q
 
 // ------------------------------------------------ LayerNorm's output again --
 
+struct RecomputeSmem {
+    uint8_t in[2][kTile * kTile];
+    ColsSmem cols;
+};
+
+template <int FMT>
 __global__ void __launch_bounds__(kTileThreads, 2)
     ln_recompute_kernel(const BlockView x8, const void *__restrict__ gamma,
                         const void *__restrict__ beta, int wtype, const float *__restrict__ mean,
-                        const float *__restrict__ rstd, const BlockView yt) {
-    __shared__ __align__(16) TileSmem sm;
+                        const float *__restrict__ rstd, const BlockView yt, unsigned tiles_r,
+                        unsigned tiles_c) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    RecomputeSmem &sm = *reinterpret_cast<RecomputeSmem *>(smem_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp * kTileRows * kTile;
     pdl_wait();
     pdl_trigger();
+    const unsigned tiles = tiles_r * tiles_c;
     int64_t row0, col0;
-    tile_origin(x8.cols, row0, col0);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = col0 + 4 * lane;
-    float g[4], b[4], v[kTileRows][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const bool in = c + j < x8.cols;
-        g[j] = in ? load_any(gamma, wtype, c + j) : 0.0f;
-        b[j] = in ? load_any(beta, wtype, c + j) : 0.0f;
-    }
-#pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-        const int64_t row = row0 + warp * kTileRows + r;
-        if (row < x8.rows) {
-            load_codes<4>(x8.codes + row * x8.ld, c, x8.cols, x8.fmt,
-                          load_scale(x8, row, col0 / kTile), v[r]);
-            const float mu = mean[row], rs = rstd[row];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[r][j] = c + j < x8.cols
-                              ? __fadd_rn(__fmul_rn(__fmul_rn(__fsub_rn(v[r][j], mu), rs), g[j]), b[j])
-                              : 0.0f;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[r][j] = 0.0f;
+    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
+    fetch_rows<1>(smem_u32(sm.in[0]) + part, x8.codes, x8.ld, x8.rows, up16(x8.cols), true, row0, col0);
+    cp_async_commit();
+    int stage = 0;
+    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, stage ^= 1) {
+        int64_t next_row0 = 0, next_col0 = 0;
+        __syncwarp();
+        if (t + gridDim.x < tiles) {
+            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+            fetch_rows<1>(smem_u32(sm.in[stage ^ 1]) + part, x8.codes, x8.ld, x8.rows, up16(x8.cols),
+                          true, next_row0, next_col0);
         }
+        cp_async_commit();
+        // lane r: row r's scale and statistics; the lane's columns' gamma and beta
+        const int64_t row = row0 + warp * kTileRows + lane;
+        const bool there = lane < kTileRows && row < x8.rows;
+        const float sc = there ? load_scale(x8, row, col0 / kTile) : 0.0f;
+        const float mu = there ? mean[row] : 0.0f, rs = there ? rstd[row] : 0.0f;
+        const int64_t c = col0 + 4 * lane;
+        float g[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            g[j] = c + j < x8.cols ? load_any(gamma, wtype, c + j) : 0.0f;
+            b[j] = c + j < x8.cols ? load_any(beta, wtype, c + j) : 0.0f;
+        }
+        cp_async_wait<1>();
+        __syncwarp();
+        TileValues v;
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r) {
+            staged_codes4(sm.in[stage] + part, r, x8.fmt, __shfl_sync(0xFFFFFFFFu, sc, r), v[r]);
+            const float m = __shfl_sync(0xFFFFFFFFu, mu, r), s = __shfl_sync(0xFFFFFFFFu, rs, r);
+            const bool in = row0 + warp * kTileRows + r < x8.rows;
+            float x[4];
+            f32x2_unpack(v[r][0], x[0], x[1]);
+            f32x2_unpack(v[r][1], x[2], x[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y = __fadd_rn(__fmul_rn(__fmul_rn(__fsub_rn(x[j], m), s), g[j]), b[j]);
+                x[j] = in && c + j < x8.cols ? y : 0.0f;
+            }
+            v[r][0] = f32x2_pack(x[0], x[1]);
+            v[r][1] = f32x2_pack(x[2], x[3]);
+        }
+        cols_max(v, sm.cols);
+        __syncthreads();
+        if (threadIdx.x < kTile) cols_scale<FMT>(threadIdx.x, sm.cols, yt, row0, col0);
+        __syncthreads();
+        cols_codes<FMT>(v, cols_inv(sm.cols), sm.cols);
+        __syncthreads();
+        cols_store(sm.cols, yt, row0, col0);
+        row0 = next_row0, col0 = next_col0;
     }
-    if (yt.fmt == 0)
-        tile_cols<0>(v, yt, row0, col0, -1, sm);
-    else
-        tile_cols<1>(v, yt, row0, col0, -1, sm);
 }
 
 // ----------------------------------------------------------------- SwiGLU --
@@ -176,57 +240,121 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
     }
 }
 
-template <typename T, int FMT>
+template <typename T>
+struct SwigluSmem {
+    // two stages of float da would not fit beside the rest
+    static constexpr int kStages = sizeof(T) == 4 ? 1 : 2;
+    uint8_t da[kStages][kTile * kTile * sizeof(T)];
+    uint8_t gate[kStages][kTile * kTile], value[kStages][kTile * kTile];
+    ColsSmem cols[3];   // d gate, d value, the output
+};
+
+// The three results of a tile in registers at once: 192 KB of the SM's 256.
+template <typename T, int FMT, int AFMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_bwd_kernel(const T *__restrict__ da, int64_t M, int64_t F, int64_t ld, bool vec,
                       const BlockView h8, const BlockView dh8, const BlockView dh8t,
-                      const BlockView a8t) {
-    __shared__ __align__(16) TileSmem sm;
+                      const BlockView a8t, unsigned tiles_r, unsigned tiles_c) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SwigluSmem<T> &sm = *reinterpret_cast<SwigluSmem<T> *>(smem_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int part = warp * kTileRows * kTile;
+    constexpr int kSize = static_cast<int>(sizeof(T));
+    constexpr int kStages = SwigluSmem<T>::kStages;
     pdl_wait();
     pdl_trigger();
-    int64_t row0, col0;
-    tile_origin(F, row0, col0);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = col0 + 4 * lane;
-    float dg[kTileRows][4], du[kTileRows][4], a[kTileRows][4];
-#pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-        const int64_t row = row0 + warp * kTileRows + r;
-        if (row < M) {
-            float d[4], g[4], u[4];
-            load_row<T, 4>(da + row * ld, c, F, vec, d);
-            load_codes<4>(h8.codes + row * h8.ld, c, h8.cols, h8.fmt,
-                          load_scale(h8, row, col0 / kTile), g);
-            load_codes<4>(h8.codes + row * h8.ld, F + c, h8.cols, h8.fmt,
-                          load_scale(h8, row, (F + col0) / kTile), u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float s = sigmoid(g[j]), gs = __fmul_rn(g[j], s);
-                a[r][j] = __fmul_rn(gs, u[j]);
-                du[r][j] = __fmul_rn(d[j], gs);
-                dg[r][j] = __fmul_rn(__fmul_rn(__fmul_rn(d[j], u[j]), s),
-                                     __fmaf_rn(g[j], __fsub_rn(1.0f, s), 1.0f));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[r][j] = du[r][j] = dg[r][j] = 0.0f;
+    const unsigned tiles = tiles_r * tiles_c;
+    int64_t row0 = 0, col0 = 0;
+    auto fetch = [&](int stage, int64_t r0, int64_t c0) {
+        fetch_rows<kSize>(smem_u32(sm.da[stage]) + part * kSize, da, ld, M, F, vec, r0, c0);
+        fetch_rows<1>(smem_u32(sm.gate[stage]) + part, h8.codes, h8.ld, M, F, true, r0, c0);
+        fetch_rows<1>(smem_u32(sm.value[stage]) + part, h8.codes + F, h8.ld, M, F, true, r0, c0);
+    };
+    // lanes 0 .. 7: the rows' scales of gate; lanes 8 .. 15: of value
+    auto fetch_scale = [&](int64_t r0, int64_t c0) {
+        const int64_t row = r0 + warp * kTileRows + (lane & 7);
+        return lane < 16 && row < M ? load_scale(h8, row, (c0 + (lane < 8 ? 0 : F)) / kTile) : 0.0f;
+    };
+    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
+    fetch(0, row0, col0);
+    cp_async_commit();
+    float sc_next = fetch_scale(row0, col0);
+    int stage = 0;
+    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const float sc = sc_next;
+        int64_t next_row0 = 0, next_col0 = 0;
+        const bool more = t + gridDim.x < tiles;
+        if (more) {
+            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+            sc_next = fetch_scale(next_row0, next_col0);
         }
-    }
-    if (dh8.codes != nullptr) {
-        tile_rows<FMT>(dg, dh8, row0, col0, -1);
-        tile_rows<FMT>(du, dh8, row0, F + col0, -1);
-    }
-    if (dh8t.codes != nullptr) {
-        tile_cols<FMT>(dg, dh8t, row0, col0, -1, sm);
+        if constexpr (kStages == 2) {
+            __syncwarp();   // the warp has read its part of the other stage
+            if (more) fetch(stage ^ 1, next_row0, next_col0);
+            cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
+        __syncwarp();
+        TileValues dg, du, a;
+        const uint64_t one2 = splat_f32x2(1.0f);
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r) {
+            uint64_t d[2], g[2], u[2];
+            staged4<T>(sm.da[stage] + part * kSize, r, d);
+            staged_codes4(sm.gate[stage] + part, r, h8.fmt, __shfl_sync(0xFFFFFFFFu, sc, r), g);
+            staged_codes4(sm.value[stage] + part, r, h8.fmt, __shfl_sync(0xFFFFFFFFu, sc, r + 8), u);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float g0, g1;
+                f32x2_unpack(g[p], g0, g1);
+                const uint64_t s = f32x2_pack(sigmoid(g0), sigmoid(g1));
+                const uint64_t gs = f32x2_mul(g[p], s);
+                a[r][p] = f32x2_mul(gs, u[p]);
+                du[r][p] = f32x2_mul(d[p], gs);
+                dg[r][p] = f32x2_mul(f32x2_mul(f32x2_mul(d[p], u[p]), s),
+                                     f32x2_fma(g[p], f32x2_sub(one2, s), one2));
+            }
+        }
+        if constexpr (kStages == 1) {
+            __syncwarp();
+            if (more) fetch(0, next_row0, next_col0);
+            cp_async_commit();
+        }
+        const bool t_dh = dh8t.codes != nullptr, t_a = a8t.codes != nullptr;
+        if (t_dh) {
+            cols_max(dg, sm.cols[0]);
+            cols_max(du, sm.cols[1]);
+        }
+        if (t_a) cols_max(a, sm.cols[2]);
         __syncthreads();
-        tile_cols<FMT>(du, dh8t, row0, F + col0, -1, sm);
+        const int c = threadIdx.x & (kTile - 1);
+        if (threadIdx.x < kTile) {
+            if (t_dh) cols_scale<FMT>(c, sm.cols[0], dh8t, row0, col0);
+        } else if (threadIdx.x < 2 * kTile) {
+            if (t_dh) cols_scale<FMT>(c, sm.cols[1], dh8t, row0, F + col0);
+        } else if (threadIdx.x < 3 * kTile) {
+            if (t_a) cols_scale<AFMT>(c, sm.cols[2], a8t, row0, col0);
+        }
         __syncthreads();
-    }
-    if (a8t.codes != nullptr) {
-        if (a8t.fmt == 0)
-            tile_cols<0>(a, a8t, row0, col0, -1, sm);
-        else
-            tile_cols<1>(a, a8t, row0, col0, -1, sm);
+        if (t_dh) {
+            cols_codes<FMT>(dg, cols_inv(sm.cols[0]), sm.cols[0]);
+            cols_codes<FMT>(du, cols_inv(sm.cols[1]), sm.cols[1]);
+        }
+        if (t_a) cols_codes<AFMT>(a, cols_inv(sm.cols[2]), sm.cols[2]);
+        if (dh8.codes != nullptr) {
+            tile_rows<FMT>(dg, dh8, row0, col0, -1);
+            tile_rows<FMT>(du, dh8, row0, F + col0, -1);
+        }
+        __syncthreads();
+        if (t_dh) {
+            cols_store(sm.cols[0], dh8t, row0, col0);
+            cols_store(sm.cols[1], dh8t, row0, F + col0);
+        }
+        if (t_a) cols_store(sm.cols[2], a8t, row0, col0);
+        row0 = next_row0, col0 = next_col0;
+        if constexpr (kStages == 2) stage ^= 1;
     }
 }
 
@@ -238,33 +366,55 @@ bool rows_vec(const MatView &m, int n) {
            (m.ld * (m.type == kTypeF32 ? 4 : 2)) % al == 0;
 }
 
-dim3 tile_grid(int64_t rows, int64_t cols) {
-    return dim3(static_cast<unsigned>(((cols + kTile - 1) / kTile) * ((rows + kTile - 1) / kTile)));
+unsigned capped(int64_t n, int64_t cap) { return static_cast<unsigned>(n < cap ? n : cap); }
+
+unsigned tiles_of(int64_t n) { return static_cast<unsigned>((n + kTile - 1) / kTile); }
+
+// A persistent tile kernel with `per_sm` CTAs per SM, its shared-memory limit set on the
+// first launch.
+template <auto KERNEL, typename Smem, typename... Args>
+cudaError_t launch_tiles(int per_sm, int64_t rows, int64_t cols, int sm_count, cudaStream_t st,
+                         Args... args) {
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(sizeof(Smem)));
+    });
+    if (err != cudaSuccess) return err;
+    const unsigned r = tiles_of(rows), c = tiles_of(cols);
+    const dim3 grid(capped(static_cast<int64_t>(r) * c, static_cast<int64_t>(sm_count) * per_sm));
+    return launch_pdl(KERNEL, grid, dim3(kTileThreads), sizeof(Smem), st, args..., r, c);
+}
+
+template <typename T, int FMT, bool TILE>
+cudaError_t quantize_tiles(const MatView &x, const BlockView &q, const BlockView &qt, int sm_count,
+                           cudaStream_t st) {
+    return launch_tiles<block_quantize_kernel<T, FMT, TILE>, QuantSmem<T>>(
+        sizeof(T) == 4 ? 1 : 2, x.rows, x.cols, sm_count, st, static_cast<const T *>(x.data), x.rows,
+        x.cols, x.ld, rows_vec(x, static_cast<int>(16 / sizeof(T))), q, qt);
 }
 
 template <typename T>
 cudaError_t quantize_typed(const MatView &x, const BlockView &q, const BlockView &qt, int fmt,
-                           bool tile, cudaStream_t st) {
-    const dim3 grid = tile_grid(x.rows, x.cols), block(kTileThreads);
-    const T *p = static_cast<const T *>(x.data);
-    const bool vec = rows_vec(x, 4);
-    auto k = fmt == 0 ? (tile ? block_quantize_kernel<T, 0, true> : block_quantize_kernel<T, 0, false>)
-                      : (tile ? block_quantize_kernel<T, 1, true> : block_quantize_kernel<T, 1, false>);
-    return launch_pdl(k, grid, block, 0, st, p, x.rows, x.cols, x.ld, vec, q, qt);
+                           bool tile, int sm_count, cudaStream_t st) {
+    if (fmt == 0)
+        return tile ? quantize_tiles<T, 0, true>(x, q, qt, sm_count, st)
+                    : quantize_tiles<T, 0, false>(x, q, qt, sm_count, st);
+    return tile ? quantize_tiles<T, 1, true>(x, q, qt, sm_count, st)
+                : quantize_tiles<T, 1, false>(x, q, qt, sm_count, st);
 }
-
-unsigned capped(int64_t n, int64_t cap) { return static_cast<unsigned>(n < cap ? n : cap); }
 
 }  // namespace
 
 cudaError_t launch_block_quantize(const MatView &x, const BlockView &q, const BlockView &qt,
-                                  cudaStream_t st) {
+                                  int sm_count, cudaStream_t st) {
     if (x.rows == 0 || x.cols == 0) return cudaSuccess;
     const BlockView &any = q.codes != nullptr ? q : qt;
     const bool tile = any.block_rows != 1;
-    if (x.type == kTypeF32) return quantize_typed<float>(x, q, qt, any.fmt, tile, st);
-    if (x.type == kTypeBF16) return quantize_typed<__nv_bfloat16>(x, q, qt, any.fmt, tile, st);
-    return quantize_typed<__half>(x, q, qt, any.fmt, tile, st);
+    if (x.type == kTypeF32) return quantize_typed<float>(x, q, qt, any.fmt, tile, sm_count, st);
+    if (x.type == kTypeBF16) return quantize_typed<__nv_bfloat16>(x, q, qt, any.fmt, tile, sm_count, st);
+    return quantize_typed<__half>(x, q, qt, any.fmt, tile, sm_count, st);
 }
 
 cudaError_t launch_block_dequantize(const BlockView &q, const MatView &out, int sm_count,
@@ -285,10 +435,13 @@ cudaError_t launch_block_dequantize(const BlockView &q, const MatView &out, int 
 
 cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,
                                 const float *mean, const float *rstd, const BlockView &yt,
-                                cudaStream_t st) {
+                                int sm_count, cudaStream_t st) {
     if (x8.rows == 0 || x8.cols == 0) return cudaSuccess;
-    return launch_pdl(ln_recompute_kernel, tile_grid(x8.rows, x8.cols), dim3(kTileThreads), 0, st, x8,
-                      gamma, beta, wtype, mean, rstd, yt);
+    if (yt.fmt == 0)
+        return launch_tiles<ln_recompute_kernel<0>, RecomputeSmem>(2, x8.rows, x8.cols, sm_count, st,
+                                                                   x8, gamma, beta, wtype, mean, rstd, yt);
+    return launch_tiles<ln_recompute_kernel<1>, RecomputeSmem>(2, x8.rows, x8.cols, sm_count, st, x8,
+                                                               gamma, beta, wtype, mean, rstd, yt);
 }
 
 cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const BlockView &h8,
@@ -308,23 +461,37 @@ cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const Block
 }
 
 namespace {
+template <typename T, int FMT, int AFMT>
+cudaError_t swiglu_bwd_tiles(const MatView &da, const BlockView &h8, const BlockView &dh8,
+                             const BlockView &dh8t, const BlockView &a8t, int sm_count,
+                             cudaStream_t st) {
+    return launch_tiles<swiglu_bwd_kernel<T, FMT, AFMT>, SwigluSmem<T>>(
+        1, da.rows, da.cols, sm_count, st, static_cast<const T *>(da.data), da.rows, da.cols, da.ld,
+        rows_vec(da, static_cast<int>(16 / sizeof(T))), h8, dh8, dh8t, a8t);
+}
+
 template <typename T>
 cudaError_t swiglu_bwd_typed(const MatView &da, const BlockView &h8, const BlockView &dh8,
-                             const BlockView &dh8t, const BlockView &a8t, cudaStream_t st) {
+                             const BlockView &dh8t, const BlockView &a8t, int sm_count,
+                             cudaStream_t st) {
     const int fmt = dh8.codes != nullptr ? dh8.fmt : dh8t.fmt;
-    auto k = fmt == 0 ? swiglu_bwd_kernel<T, 0> : swiglu_bwd_kernel<T, 1>;
-    return launch_pdl(k, tile_grid(da.rows, da.cols), dim3(kTileThreads), 0, st,
-                      static_cast<const T *>(da.data), da.rows, da.cols, da.ld, rows_vec(da, 4), h8,
-                      dh8, dh8t, a8t);
+    const int afmt = a8t.codes != nullptr ? a8t.fmt : 0;
+    if (fmt == 0)
+        return afmt == 0 ? swiglu_bwd_tiles<T, 0, 0>(da, h8, dh8, dh8t, a8t, sm_count, st)
+                         : swiglu_bwd_tiles<T, 0, 1>(da, h8, dh8, dh8t, a8t, sm_count, st);
+    return afmt == 0 ? swiglu_bwd_tiles<T, 1, 0>(da, h8, dh8, dh8t, a8t, sm_count, st)
+                     : swiglu_bwd_tiles<T, 1, 1>(da, h8, dh8, dh8t, a8t, sm_count, st);
 }
 }  // namespace
 
 cudaError_t launch_swiglu_bwd(const MatView &da, const BlockView &h8, const BlockView &dh8,
-                              const BlockView &dh8t, const BlockView &a8t, cudaStream_t st) {
+                              const BlockView &dh8t, const BlockView &a8t, int sm_count,
+                              cudaStream_t st) {
     if (da.rows == 0 || da.cols == 0) return cudaSuccess;
-    if (da.type == kTypeF32) return swiglu_bwd_typed<float>(da, h8, dh8, dh8t, a8t, st);
-    if (da.type == kTypeBF16) return swiglu_bwd_typed<__nv_bfloat16>(da, h8, dh8, dh8t, a8t, st);
-    return swiglu_bwd_typed<__half>(da, h8, dh8, dh8t, a8t, st);
+    if (da.type == kTypeF32) return swiglu_bwd_typed<float>(da, h8, dh8, dh8t, a8t, sm_count, st);
+    if (da.type == kTypeBF16)
+        return swiglu_bwd_typed<__nv_bfloat16>(da, h8, dh8, dh8t, a8t, sm_count, st);
+    return swiglu_bwd_typed<__half>(da, h8, dh8, dh8t, a8t, sm_count, st);
 }
 
 }  // namespace fp8k

@@ -191,7 +191,7 @@ struct BlockView {
 
 // x into q and / or its transpose into qt (block_quant.cu).
 cudaError_t launch_block_quantize(const MatView &x, const BlockView &q, const BlockView &qt,
-                                  cudaStream_t st);
+                                  int sm_count, cudaStream_t st);
 cudaError_t launch_block_dequantize(const BlockView &q, const MatView &out, int sm_count,
                                     cudaStream_t st);
 // D [M][N] (BF16) = A [M][K] . B [N][K]^T (block_gemm.cu).
@@ -209,12 +209,13 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
 // yt = quantized transpose of LayerNorm(x8) (block_quant.cu).
 cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,
                                 const float *mean, const float *rstd, const BlockView &yt,
-                                cudaStream_t st);
+                                int sm_count, cudaStream_t st);
 // SwiGLU (block_quant.cu).
 cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const BlockView &h8,
                               int sm_count, cudaStream_t st);
 cudaError_t launch_swiglu_bwd(const MatView &da, const BlockView &h8, const BlockView &dh8,
-                              const BlockView &dh8t, const BlockView &a8t, cudaStream_t st);
+                              const BlockView &dh8t, const BlockView &a8t, int sm_count,
+                              cudaStream_t st);
 
 // Read and clear the block GEMM's device error flag (block_gemm.cu).
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags);
