@@ -166,7 +166,10 @@ def _check(status: int) -> None:
         raise Fp8Error(status, _lib.fp8_last_error().decode())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> "ctypes.c_void_p | int":
+    if stream is None and torch.cuda.is_initialized():
+        # the current device's current stream, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if stream is None:
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
@@ -765,28 +768,31 @@ class BlockFp8:
 def _block(q: BlockFp8 | None, name: str):
     if q is None:
         return None
-    codes, scales = q.codes, q.scales
+    codes, scales, cols, block_rows = q.codes, q.scales, q.cols, q.block_rows
     if not codes.is_cuda or not scales.is_cuda:
         raise ValueError(f"{name} must be in CUDA memory")
-    if not _fp8_view_ok(codes) or codes.dim() != 2:
+    if codes.dtype is not _U8 and not _fp8_view_ok(codes) or codes.dim() != 2:
         raise ValueError(f"{name}: codes must be a matrix of FP8 codes (uint8 / float8)")
-    if scales.dtype not in _SCALE_TYPES or scales.dim() != 2:
+    scale_type = _SCALE_TYPES.get(scales.dtype)
+    if scale_type is None or scales.dim() != 2:
         raise ValueError(f"{name}: scales must be a matrix of uint8 (E8M0) or float32")
     rows, pitch = codes.shape
-    if rows and (codes.stride(1) != 1 or pitch < -(-q.cols // 16) * 16):
-        raise ValueError(f"{name}: codes must be contiguous along the columns, {q.cols} of them "
+    ld, inner = codes.stride()
+    if rows and (inner != 1 or pitch < -(-cols // 16) * 16):
+        raise ValueError(f"{name}: codes must be contiguous along the columns, {cols} of them "
                          f"rounded up to a multiple of 16; got {tuple(codes.shape)}")
-    nb = -(-q.cols // 128)
     srows, spitch = scales.shape
-    if q.block_rows > 0 and (srows < -(-rows // q.block_rows) or spitch < nb
-                             or (srows and spitch and scales.stride(1) != 1)):
-        raise ValueError(f"{name}: scales must be [{-(-rows // q.block_rows)}, >= {nb}] and "
+    lds, sinner = scales.stride()
+    nb = -(-cols // 128)
+    if block_rows > 0 and (srows < -(-rows // block_rows) or spitch < nb
+                           or (srows and spitch and sinner != 1)):
+        raise ValueError(f"{name}: scales must be [{-(-rows // block_rows)}, >= {nb}] and "
                          f"contiguous along the columns; got {tuple(scales.shape)}")
-    if scales.dtype == torch.uint8 and spitch < -(-nb // 4) * 4:
+    if scale_type == SCALE_E8M0 and spitch < -(-nb // 4) * 4:
         raise ValueError(f"{name}: rows of E8M0 scales must hold whole words of 4; got {spitch}")
-    return fp8_block_tensor(codes.data_ptr(), rows, q.cols, codes.stride(0) if rows > 1 and pitch else pitch,
-                            scales.data_ptr(), scales.stride(0) if srows > 1 and spitch else spitch, q.fmt,
-                            q.block_rows, _SCALE_TYPES[scales.dtype])
+    return fp8_block_tensor(codes.data_ptr(), rows, cols, ld if rows > 1 and pitch else pitch,
+                            scales.data_ptr(), lds if srows > 1 and spitch else spitch, q.fmt,
+                            block_rows, scale_type)
 
 
 def _matrix(t: torch.Tensor | None, name: str):
@@ -794,29 +800,35 @@ def _matrix(t: torch.Tensor | None, name: str):
         return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES:
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {tuple(t.shape)}")
     rows, cols = t.shape
-    if cols > 1 and rows and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1 and rows:
         raise ValueError(f"{name} must be contiguous along its columns")
-    return fp8_matrix(t.data_ptr(), rows, cols, t.stride(0) if rows > 1 and cols else cols,
-                      _DTYPES[t.dtype])
+    return fp8_matrix(t.data_ptr(), rows, cols, ld if rows > 1 and cols else cols, dtype)
 
 
-def _param(t: torch.Tensor, n: int, name: str):
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return _ptr(t, None, name)
+def _vector(t: torch.Tensor, n: int, name: str, dtype=None) -> int:
+    """Address of n contiguous elements, float32 (dtype) or of any matrix type."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _DTYPES):
+        raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must have {n} contiguous elements")
+    return t.data_ptr()
 
 
-def _stat(t: torch.Tensor, n: int, name: str):
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements")
-    return _ptr(t, torch.float32, name)
+def _param(t: torch.Tensor, n: int, name: str) -> int:
+    return _vector(t, n, name)
+
+
+def _stat(t: torch.Tensor, n: int, name: str) -> int:
+    return _vector(t, n, name, torch.float32)
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:

@@ -126,6 +126,134 @@ __device__ __forceinline__ void store_row(T *row, int64_t c, int64_t cols, bool 
     }
 }
 
+// ------------------------------------------------- rows of any alignment --
+//
+// A thread's 8 elements of a row whose start has any alignment, by 16-byte accesses
+// alone.  Only 16-byte blocks that hold an element of the row are touched (such a
+// block never leaves the allocation, which starts and ends on wider boundaries).
+// A warp's lanes hold consecutive groups of 8, so that a store can hand the end of
+// one lane's group to the next lane, whose 16-byte blocks it completes.
+
+// Bytes [off, off + 4 N) of the words in w: off in 0 .. 15, even.
+template <int N, int WORDS>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[WORDS], uint32_t off, uint32_t (&out)[N]) {
+    static_assert(WORDS >= N + 4, "a whole block more than the result");
+    uint32_t a[N + 2], b[N + 1];
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) a[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) b[i] = off & 4u ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = off & 2u ? __funnelshift_r(b[i], b[i + 1], 16) : b[i];
+}
+
+template <typename T>
+struct RawRow8 {
+    static constexpr int kWords = 2 * static_cast<int>(sizeof(T));   // of 8 elements
+    uint32_t w[kWords + 4];
+
+    // the blocks that hold columns c .. c + 7 of the row
+    __device__ __forceinline__ void load(const T *row, int64_t c, int64_t cols) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(row + c);
+        const uintptr_t end = reinterpret_cast<uintptr_t>(row + cols), base = p & ~uintptr_t(15);
+#pragma unroll
+        for (int i = 0; i < kWords / 4 + 1; ++i) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (base + 16 * i < end && (i < kWords / 4 || base != p))
+                u = *reinterpret_cast<const uint4 *>(base + 16 * i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    }
+    // the 8 elements as packed pairs; columns from cols on are 0
+    __device__ __forceinline__ void get(const T *row, int64_t c, int64_t cols, uint64_t (&v)[4]) const {
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+        uint32_t x[kWords];
+        if (off == 0) {   // the same for the whole row: 8 elements are whole blocks
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) x[i] = w[i];
+        } else {
+            shift_words<kWords, kWords + 4>(w, off, x);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[i] = f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            } else {
+                const float2 f = unpack2<T>(x[i]);
+                v[i] = f32x2_pack(f.x, f.y);
+            }
+        }
+        if (c + 8 > cols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                f32x2_unpack(v[i], lo, hi);
+                v[i] = f32x2_pack(c + 2 * i < cols ? lo : 0.0f, c + 2 * i + 1 < cols ? hi : 0.0f);
+            }
+        }
+    }
+};
+
+// Stores the pairs to columns c .. c + 7 (those below cols).  All lanes of the warp
+// take part, lane l + 1 with the columns after lane l's.
+template <typename T>
+__device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t cols, const uint64_t (&v)[4]) {
+    constexpr int kWords = 2 * static_cast<int>(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    uint32_t w[kWords + 8];   // the lane before's last block, this lane's words, room to shift
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f32x2_unpack(v[i], lo, hi);
+        if constexpr (sizeof(T) == 4) {
+            w[4 + 2 * i] = __float_as_uint(lo), w[5 + 2 * i] = __float_as_uint(hi);
+        } else {
+            w[4 + i] = pack2<T>(lo, hi);
+        }
+    }
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+    uint8_t *p = reinterpret_cast<uint8_t *>(row + c);
+    const bool full = c + 8 <= cols;
+    if (off == 0) {
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4 *>(p)[i] =
+                    make_uint4(w[4 + 4 * i], w[5 + 4 * i], w[6 + 4 * i], w[7 + 4 * i]);
+            return;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __shfl_up_sync(0xFFFFFFFFu, w[kWords + i], 1);
+            w[kWords + 4 + i] = 0;
+        }
+        uint32_t x[kWords];
+        shift_words<kWords, kWords + 8>(w, 16u - off, x);
+        if (full) {
+            uint4 *blocks = reinterpret_cast<uint4 *>(p - off);
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)   // block 0 starts in the lane before
+                if (i > 0 || lane > 0)
+                    blocks[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+    }
+    // what no whole block covers: the first lane's beginning, the end that the next lane
+    // does not take, and a group that the row's end cuts
+    const int head = full && lane > 0 ? 0 : full ? static_cast<int>(16 - off) / static_cast<int>(sizeof(T)) : 8;
+    const int tail = full && (lane == 31 || c + 16 > cols) ? static_cast<int>(off) / static_cast<int>(sizeof(T)) : 0;
+    if (head == 0 && tail == 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if ((i < head || i >= 8 - tail) && c + i < cols) {
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t *>(p)[i] = w[4 + i];
+            else
+                reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(w[4 + i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
 // gamma or beta (type known at run time) at column c.
 __device__ __forceinline__ float load_any(const void *p, int type, int64_t c) {
     if (type == kTypeF32) return static_cast<const float *>(p)[c];

@@ -17,58 +17,93 @@ namespace fp8k {
 
 namespace {
 
-// Sum of a pair over the CTA, in a fixed order, the same in every thread.  The
-// caller alternates between two buffers: a buffer is written again only after
-// a barrier that follows its last read.
-template <int NT>
-__device__ __forceinline__ float2 cta_sum2(float a, float b, float2 (&buf)[NT / 32]) {
+// Who works on a row: a warp (rows of up to 32 x 8 x VPT columns; a CTA has kWarps rows
+// at a time) or the whole CTA.  Thread i of the team holds columns 8 (i + k team) .. + 7
+// for k < VPT, as packed pairs.  The row after the one in work is already being
+// loaded, into registers.
+constexpr int kWarps = 8;
+
+template <bool WARP>
+struct Team {
+    int id, size;        // this thread's place, threads per row
+    int64_t row, step;   // the first row, and from one to the next
+    __device__ __forceinline__ Team() {
+        if constexpr (WARP) {
+            id = threadIdx.x & 31, size = 32;
+            row = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+            step = static_cast<int64_t>(gridDim.x) * kWarps;
+        } else {
+            id = threadIdx.x, size = blockDim.x;
+            row = blockIdx.x, step = gridDim.x;
+        }
+    }
+};
+
+// Sum of a pair over the team, in a fixed order, the same in every thread.  A CTA's
+// calls alternate between two buffers: a buffer is written again only after a
+// barrier that follows its last read.
+template <bool WARP>
+__device__ __forceinline__ float2 team_sum2(float a, float b, float2 (&buf)[32]) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         a = __fadd_rn(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
         b = __fadd_rn(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
     }
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+    if constexpr (WARP) return make_float2(a, b);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    float2 s = buf[0];
+    const float2 s = lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : make_float2(0.0f, 0.0f);
+    a = s.x, b = s.y;
 #pragma unroll
-    for (int w = 1; w < NT / 32; ++w) {
-        s.x = __fadd_rn(s.x, buf[w].x);
-        s.y = __fadd_rn(s.y, buf[w].y);
+    for (int o = 16; o; o >>= 1) {
+        a = __fadd_rn(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        b = __fadd_rn(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
     }
-    return s;
+    return make_float2(a, b);
+}
+
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float lo, hi;
+    f32x2_unpack(v, lo, hi);
+    return __fadd_rn(lo, hi);
 }
 
 // Quantizes 8 consecutive columns per lane: 16 lanes hold a block of 128.  All
-// lanes of the warp take part; lanes past the row hold zeros.
-__device__ __forceinline__ void emit_block8(const float (&v)[8], const BlockView &q, int64_t row,
+// lanes of the warp take part; columns past the row are 0.
+template <int FMT>
+__device__ __forceinline__ void emit_block8(const uint64_t (&v)[4], const BlockView &q, int64_t row,
                                             int64_t c) {
-    uint32_t m = 0;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
+    for (int i = 0; i < 4; ++i) f32x2_unpack(v[i], x[2 * i], x[2 * i + 1]);
+    uint32_t m = max(finite_max4(x[0], x[1], x[2], x[3]), finite_max4(x[4], x[5], x[6], x[7]));
 #pragma unroll
     for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const uint32_t byte = q.fmt == 0 ? scale_byte<0>(m) : scale_byte<1>(m);
-    const float inv = scale_inverse(byte);
+    const uint32_t byte = scale_byte<FMT>(m);
     if (c >= q.cols) return;
     if ((threadIdx.x & 15) == 0) store_scale(q, row, c >> 7, byte);
-    uint2 w;
-    if (q.fmt == 0)
-        w = make_uint2(encode4<0>(v[0], v[1], v[2], v[3], inv), encode4<0>(v[4], v[5], v[6], v[7], inv));
-    else
-        w = make_uint2(encode4<1>(v[0], v[1], v[2], v[3], inv), encode4<1>(v[4], v[5], v[6], v[7], inv));
+    const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f32x2_unpack(f32x2_mul(v[i], inv2), lo, hi);
+        w[i] = cvt2_fp8<FMT>(lo, hi);
+    }
+    w[0] |= w[1] << 16, w[2] |= w[3] << 16;
     uint8_t *p = q.codes + row * q.ld + c;
     if (c + 8 <= q.cols) {
-        *reinterpret_cast<uint2 *>(p) = w;
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[2]);
     } else {
-        store_code_word(p, w.x, q.cols - c);
-        store_code_word(p + 4, w.y, q.cols - c - 4);
+        store_code_word(p, w[0], q.cols - c);
+        store_code_word(p + 4, w[2], q.cols - c - 4);
     }
 }
 
 struct LnFwdArgs {
     const void *x;
     int64_t rows, cols, ldx;
-    bool vecx, vecy;
     const void *gamma, *beta;
     int wtype;
     float eps;
@@ -78,67 +113,154 @@ struct LnFwdArgs {
     float *mean, *rstd;
 };
 
-// One row at a time per CTA; thread t holds columns 8 (t + NT k) .. + 7, k < VPT
-// (WIDE: k without a bound, x read again for each use).
-template <typename T, int NT, int VPT, bool WIDE>
-__global__ void __launch_bounds__(NT) ln_fwd_kernel(const LnFwdArgs a) {
-    __shared__ float2 buf[2][NT / 32];
+// The part of the forward that follows the statistics, for 8 columns.
+template <typename T>
+__device__ __forceinline__ void ln_finish(const LnFwdArgs &a, int64_t row, int64_t c, uint64_t nmu2,
+                                          uint64_t rs2, const uint64_t (&g)[4],
+                                          const uint64_t (&b)[4], const uint64_t (&x)[4]) {
+    if (a.x8.codes != nullptr) {
+        if (a.x8.fmt == 0)
+            emit_block8<0>(x, a.x8, row, c);
+        else
+            emit_block8<1>(x, a.x8, row, c);
+    }
+    if (a.y == nullptr && a.y8.codes == nullptr) return;
+    uint64_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = f32x2_fma(f32x2_mul(f32x2_add(x[i], nmu2), rs2), g[i], b[i]);
+    if (a.y != nullptr) store_row8<T>(static_cast<T *>(a.y) + row * a.ldy, c, a.cols, y);
+    if (a.y8.codes != nullptr) {
+        if (a.y8.fmt == 0)
+            emit_block8<0>(y, a.y8, row, c);
+        else
+            emit_block8<1>(y, a.y8, row, c);
+    }
+}
+
+__device__ __forceinline__ void load_param8(const void *p, int type, int64_t c, int64_t cols,
+                                            uint64_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = f32x2_pack(c + 2 * i < cols ? load_any(p, type, c + 2 * i) : 0.0f,
+                          c + 2 * i + 1 < cols ? load_any(p, type, c + 2 * i + 1) : 0.0f);
+}
+
+// sum of (x - mean)^2 over 8 columns; those past the row do not count
+__device__ __forceinline__ uint64_t deviations(const uint64_t (&x)[4], uint64_t nmu2, int64_t c,
+                                               int64_t cols, uint64_t s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t d = f32x2_add(x[i], nmu2);
+        if (c + 8 > cols) {
+            float lo, hi;
+            f32x2_unpack(d, lo, hi);
+            d = f32x2_pack(c + 2 * i < cols ? lo : 0.0f, c + 2 * i + 1 < cols ? hi : 0.0f);
+        }
+        s = f32x2_fma(d, d, s);
+    }
+    return s;
+}
+
+template <typename T, int VPT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const LnFwdArgs a) {
+    __shared__ float2 buf[2][32];
+    const Team<WARP> team;
     pdl_wait();
     pdl_trigger();
     const float n = static_cast<float>(a.cols);
-    const int64_t nk = WIDE ? (a.cols + 8 * NT - 1) / (8 * NT) : VPT;
+    RawRow8<T> raw[VPT];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            raw[k].load(static_cast<const T *>(a.x) + row * a.ldx, 8 * (team.id + k * team.size), a.cols);
+    };
+    if (team.row < a.rows) fetch(team.row);
+    // gamma and beta stay in registers where there is room for them
+    constexpr int kKept = VPT <= 2 ? VPT : 1;
+    uint64_t g[kKept][4], b[kKept][4];
+    auto params = [&](int k, int slot) {
+        load_param8(a.gamma, a.wtype, 8 * (team.id + k * team.size), a.cols, g[slot]);
+        load_param8(a.beta, a.wtype, 8 * (team.id + k * team.size), a.cols, b[slot]);
+    };
+    if constexpr (VPT <= 2) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) params(k, k);
+    }
+    for (int64_t row = team.row; row < a.rows; row += team.step) {
+        uint64_t x[VPT][4], s2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            raw[k].get(static_cast<const T *>(a.x) + row * a.ldx, 8 * (team.id + k * team.size), a.cols,
+                       x[k]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s2 = f32x2_add(s2, x[k][i]);
+        }
+        if (row + team.step < a.rows) fetch(row + team.step);
+        const float mu = __fdiv_rn(team_sum2<WARP>(sum2(s2), 0.0f, buf[0]).x, n);
+        const uint64_t nmu2 = splat_f32x2(-mu);
+        s2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            s2 = deviations(x[k], nmu2, 8 * (team.id + k * team.size), a.cols, s2);
+        const float var = __fdiv_rn(team_sum2<WARP>(sum2(s2), 0.0f, buf[1]).x, n);
+        const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+        if (team.id == 0) {
+            a.mean[row] = mu;
+            a.rstd[row] = rs;
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            if constexpr (VPT > 2) params(k, 0);
+            ln_finish<T>(a, row, 8 * (team.id + k * team.size), nmu2, splat_f32x2(rs), g[k % kKept],
+                         b[k % kKept], x[k]);
+        }
+    }
+}
+
+// Rows too long for a CTA's registers: x is read again for each use.
+template <typename T>
+__global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
+    __shared__ float2 buf[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const float n = static_cast<float>(a.cols);
+    // whole warps stay together: the exchanges between lanes need all of them
+    const int64_t warp0 = 8 * (threadIdx.x & ~31);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *xr = static_cast<const T *>(a.x) + row * a.ldx;
-        float v[VPT][8];
-        float s = 0.0f;
-        for (int64_t kk = 0; kk < nk; kk += VPT) {
+        RawRow8<T> raw;
+        uint64_t x[4], s2 = 0;
+        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+            const int64_t c = w + 8 * (threadIdx.x & 31);
+            raw.load(xr, c, a.cols);
+            raw.get(xr, c, a.cols, x);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                load_row<T, 8>(xr, 8 * (threadIdx.x + NT * (kk + k)), a.cols, a.vecx, v[k]);
-                float p = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) p = __fadd_rn(p, v[k][i]);
-                s = __fadd_rn(s, p);
-            }
+            for (int i = 0; i < 4; ++i) s2 = f32x2_add(s2, x[i]);
         }
-        const float mu = __fdiv_rn(cta_sum2<NT>(s, 0.0f, buf[0]).x, n);
-        float d2 = 0.0f;
-        for (int64_t kk = 0; kk < nk; kk += VPT) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t c = 8 * (threadIdx.x + NT * (kk + k));
-                if (WIDE) load_row<T, 8>(xr, c, a.cols, a.vecx, v[k]);
-                float p = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = c + i < a.cols ? __fsub_rn(v[k][i], mu) : 0.0f;
-                    p = __fmaf_rn(d, d, p);
-                }
-                d2 = __fadd_rn(d2, p);
-            }
+        const float mu = __fdiv_rn(team_sum2<false>(sum2(s2), 0.0f, buf[0]).x, n);
+        const uint64_t nmu2 = splat_f32x2(-mu);
+        s2 = 0;
+        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+            const int64_t c = w + 8 * (threadIdx.x & 31);
+            raw.load(xr, c, a.cols);
+            raw.get(xr, c, a.cols, x);
+            s2 = deviations(x, nmu2, c, a.cols, s2);
         }
-        const float var = __fdiv_rn(cta_sum2<NT>(d2, 0.0f, buf[1]).x, n);
+        const float var = __fdiv_rn(team_sum2<false>(sum2(s2), 0.0f, buf[1]).x, n);
         const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
         if (threadIdx.x == 0) {
             a.mean[row] = mu;
             a.rstd[row] = rs;
         }
-        for (int64_t kk = 0; kk < nk; kk += VPT) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t c = 8 * (threadIdx.x + NT * (kk + k));
-                if (WIDE) load_row<T, 8>(xr, c, a.cols, a.vecx, v[k]);
-                if (a.x8.codes != nullptr) emit_block8(v[k], a.x8, row, c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i < a.cols)
-                        v[k][i] = __fadd_rn(__fmul_rn(__fmul_rn(__fsub_rn(v[k][i], mu), rs),
-                                                      load_any(a.gamma, a.wtype, c + i)),
-                                            load_any(a.beta, a.wtype, c + i));
-                if (a.y != nullptr)
-                    store_row<T, 8>(static_cast<T *>(a.y) + row * a.ldy, c, a.cols, a.vecy, v[k]);
-                if (a.y8.codes != nullptr) emit_block8(v[k], a.y8, row, c);
-            }
+        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+            const int64_t c = w + 8 * (threadIdx.x & 31);
+            uint64_t g[4], b[4];
+            load_param8(a.gamma, a.wtype, c, a.cols, g);
+            load_param8(a.beta, a.wtype, c, a.cols, b);
+            raw.load(xr, c, a.cols);
+            raw.get(xr, c, a.cols, x);
+            ln_finish<T>(a, row, c, nmu2, splat_f32x2(rs), g, b, x);
         }
     }
 }
@@ -146,117 +268,183 @@ __global__ void __launch_bounds__(NT) ln_fwd_kernel(const LnFwdArgs a) {
 struct LnBwdArgs {
     const void *dy, *x;
     int64_t rows, cols, lddy, ldx, lddx;
-    bool vecdy, vecx, vecdx;
     BlockView x8;
     const void *gamma;
     int wtype;
     const float *mean, *rstd;
     void *dx;
     float *part;       // [gridDim.x][2][cols]: a CTA's sums of dy * xhat and dy
-    float2 *row_sums;  // WIDE: [rows] sums of u and u * xhat
+    float2 *row_sums;  // wide rows: [rows] sums of u and u * xhat
 };
 
+// 8 columns of x on their way: as they are, or codes with their block's scale.
 template <typename T, bool SAVED>
-__device__ __forceinline__ void load_pair(const LnBwdArgs &a, int64_t row, int64_t c, float mu,
-                                          float rs, float (&dy)[8], float (&xh)[8]) {
-    load_row<T, 8>(static_cast<const T *>(a.dy) + row * a.lddy, c, a.cols, a.vecdy, dy);
-    if constexpr (SAVED) {
-        const float s = c < a.cols ? load_scale(a.x8, row, c >> 7) : 0.0f;
-        load_codes<8>(a.x8.codes + row * a.x8.ld, c, a.cols, a.x8.fmt, s, xh);
-    } else {
-        load_row<T, 8>(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, a.vecx, xh);
+struct RawX8;
+template <typename T>
+struct RawX8<T, false> {
+    RawRow8<T> raw;
+    __device__ __forceinline__ void load(const LnBwdArgs &a, int64_t row, int64_t c) {
+        raw.load(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols);
     }
+    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t row, int64_t c, uint64_t (&v)[4]) const {
+        raw.get(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, v);
+    }
+};
+template <typename T>
+struct RawX8<T, true> {
+    uint2 codes;
+    float scale;
+    __device__ __forceinline__ void load(const LnBwdArgs &a, int64_t row, int64_t c) {
+        const bool in = c < a.cols;
+        codes = in ? *reinterpret_cast<const uint2 *>(a.x8.codes + row * a.x8.ld + c) : make_uint2(0, 0);
+        scale = in ? load_scale(a.x8, row, c >> 7) : 0.0f;
+    }
+    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t, int64_t c, uint64_t (&v)[4]) const {
+        float f[8];
+        decode4(codes.x, a.x8.fmt, *reinterpret_cast<float(*)[4]>(f));
+        decode4(codes.y, a.x8.fmt, *reinterpret_cast<float(*)[4]>(f + 4));
+        const uint64_t s2 = splat_f32x2(scale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        xh[i] = c + i < a.cols ? __fmul_rn(__fsub_rn(xh[i], mu), rs) : 0.0f;
+        for (int i = 0; i < 4; ++i)   // codes past the row may be anything
+            v[i] = f32x2_mul(f32x2_pack(c + 2 * i < a.cols ? f[2 * i] : 0.0f,
+                                        c + 2 * i + 1 < a.cols ? f[2 * i + 1] : 0.0f),
+                             s2);
+    }
+};
+
+// xhat in place of x, and u in place of dy; their sums for the row, and the column sums
+__device__ __forceinline__ void ln_bwd_accumulate(uint64_t nmu2, uint64_t rs2, const uint64_t (&g)[4],
+                                                  uint64_t (&dy)[4], uint64_t (&x)[4],
+                                                  uint64_t (&dg)[4], uint64_t (&db)[4], uint64_t &s1,
+                                                  uint64_t &s2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = f32x2_mul(f32x2_add(x[i], nmu2), rs2);
+        dg[i] = f32x2_fma(dy[i], x[i], dg[i]);
+        db[i] = f32x2_add(db[i], dy[i]);
+        dy[i] = f32x2_mul(dy[i], g[i]);
+        s1 = f32x2_add(s1, dy[i]);
+        s2 = f32x2_fma(dy[i], x[i], s2);
+    }
 }
 
-// WIDE rows: the two row sums, in a pass of their own.
-template <typename T, bool SAVED, int NT>
-__global__ void __launch_bounds__(NT) ln_bwd_sums_kernel(const LnBwdArgs a) {
-    __shared__ float2 buf[2][NT / 32];
+// Wide rows: the two row sums, in a pass of their own.
+template <typename T, bool SAVED>
+__global__ void __launch_bounds__(1024) ln_bwd_sums_kernel(const LnBwdArgs a) {
+    __shared__ float2 buf[2][32];
     pdl_wait();
     pdl_trigger();
     int flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        const float mu = a.mean[row], rs = a.rstd[row];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * NT) {
-            float dy[8], xh[8];
-            load_pair<T, SAVED>(a, row, c, mu, rs, dy, xh);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u =
-                    c + i < a.cols ? __fmul_rn(dy[i], load_any(a.gamma, a.wtype, c + i)) : 0.0f;
-                s1 = __fadd_rn(s1, u);
-                s2 = __fmaf_rn(u, xh[i], s2);
-            }
+        const uint64_t nmu2 = splat_f32x2(-a.mean[row]), rs2 = splat_f32x2(a.rstd[row]);
+        uint64_t s1 = 0, s2 = 0;
+        for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * 1024) {
+            const T *dyr = static_cast<const T *>(a.dy) + row * a.lddy;
+            RawRow8<T> rdy;
+            RawX8<T, SAVED> rx;
+            rdy.load(dyr, c, a.cols);
+            rx.load(a, row, c);
+            uint64_t dy[4], x[4], g[4], dg[4] = {}, db[4] = {};
+            load_param8(a.gamma, a.wtype, c, a.cols, g);
+            rdy.get(dyr, c, a.cols, dy);
+            rx.get(a, row, c, x);
+            ln_bwd_accumulate(nmu2, rs2, g, dy, x, dg, db, s1, s2);
         }
-        const float2 s = cta_sum2<NT>(s1, s2, buf[flip]);
+        const float2 s = team_sum2<false>(sum2(s1), sum2(s2), buf[flip]);
         if (threadIdx.x == 0) a.row_sums[row] = s;
     }
 }
 
-// Rows in turn; a thread keeps its columns (as in the forward) and their sums
-// over the CTA's rows.  WIDE: blockIdx.y is a slab of 8 NT VPT columns and the
-// rows' sums are already there.
-template <typename T, bool SAVED, int NT, int VPT, bool WIDE>
-__global__ void __launch_bounds__(NT) ln_bwd_kernel(const LnBwdArgs a) {
-    __shared__ float2 buf[2][NT / 32];
+// Rows in turn; a thread keeps its columns (as in the forward) and their sums over
+// the CTA's rows.  WIDE: blockIdx.y is a slab of 8 VPT blockDim.x columns and the rows'
+// sums are already there.
+template <typename T, bool SAVED, int VPT, bool WARP, bool WIDE>
+__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const LnBwdArgs a) {
+    __shared__ float2 buf[2][32];
+    const Team<WARP> team;
     pdl_wait();
     pdl_trigger();
     const float n = static_cast<float>(a.cols);
-    const int64_t base = WIDE ? static_cast<int64_t>(blockIdx.y) * 8 * NT * VPT : 0;
-    float dg[VPT][8] = {}, db[VPT][8] = {}, g[VPT][8];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int64_t c = base + 8 * (threadIdx.x + NT * k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            g[k][i] = c + i < a.cols ? load_any(a.gamma, a.wtype, c + i) : 0.0f;
-    }
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        const float mu = a.mean[row], rs = a.rstd[row];
-        float dy[VPT][8], xh[VPT][8];
-        float s1 = 0.0f, s2 = 0.0f;
+    const int64_t base = WIDE ? static_cast<int64_t>(blockIdx.y) * 8 * VPT * blockDim.x : 0;
+    auto col = [&](int k) { return base + 8 * (team.id + k * team.size); };
+    RawRow8<T> rdy[VPT];
+    RawX8<T, SAVED> rx[VPT];
+    float mu_next = 0.0f, rs_next = 0.0f;
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            load_pair<T, SAVED>(a, row, base + 8 * (threadIdx.x + NT * k), mu, rs, dy[k], xh[k]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dg[k][i] = __fmaf_rn(dy[k][i], xh[k][i], dg[k][i]);
-                db[k][i] = __fadd_rn(db[k][i], dy[k][i]);
-                const float u = __fmul_rn(dy[k][i], g[k][i]);
-                s1 = __fadd_rn(s1, u);
-                s2 = __fmaf_rn(u, xh[k][i], s2);
-            }
+            rdy[k].load(static_cast<const T *>(a.dy) + row * a.lddy, col(k), a.cols);
+            rx[k].load(a, row, col(k));
         }
+        mu_next = a.mean[row], rs_next = a.rstd[row];
+    };
+    if (team.row < a.rows) fetch(team.row);
+    uint64_t dg[VPT][4] = {}, db[VPT][4] = {}, g[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) load_param8(a.gamma, a.wtype, col(k), a.cols, g[k]);
+    int flip = 0;
+    for (int64_t row = team.row; row < a.rows; row += team.step, flip ^= 1) {
+        const uint64_t nmu2 = splat_f32x2(-mu_next), rs2 = splat_f32x2(rs_next);
+        uint64_t dy[VPT][4], x[VPT][4], s1 = 0, s2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            rdy[k].get(static_cast<const T *>(a.dy) + row * a.lddy, col(k), a.cols, dy[k]);
+            rx[k].get(a, row, col(k), x[k]);
+        }
+        if (row + team.step < a.rows) fetch(row + team.step);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            ln_bwd_accumulate(nmu2, rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
         float2 s;
         if constexpr (WIDE)
             s = a.row_sums[row];
         else
-            s = cta_sum2<NT>(s1, s2, buf[flip]);
-        const float m1 = __fdiv_rn(s.x, n), m2 = __fdiv_rn(s.y, n);
+            s = team_sum2<WARP>(sum2(s1), sum2(s2), buf[flip]);
+        const uint64_t nm1 = splat_f32x2(-__fdiv_rn(s.x, n)), nm2 = splat_f32x2(-__fdiv_rn(s.y, n));
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                dy[k][i] = __fmul_rn(rs, __fsub_rn(__fsub_rn(__fmul_rn(dy[k][i], g[k][i]), m1),
-                                                   __fmul_rn(xh[k][i], m2)));
-            store_row<T, 8>(static_cast<T *>(a.dx) + row * a.lddx,
-                            base + 8 * (threadIdx.x + NT * k), a.cols, a.vecdx, dy[k]);
+            for (int i = 0; i < 4; ++i)
+                dy[k][i] = f32x2_mul(f32x2_fma(x[k][i], nm2, f32x2_add(dy[k][i], nm1)), rs2);
+            store_row8<T>(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
         }
     }
     float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    if constexpr (WARP) {
+        // the warps add theirs one after the other
+        extern __shared__ float sums[];   // [2][cols]
+        for (int w = 0; w < kWarps; ++w) {
+            if (static_cast<int>(threadIdx.x >> 5) == w) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const int64_t c = base + 8 * (threadIdx.x + NT * k);
+                for (int k = 0; k < VPT; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (c + i < a.cols) {
-                part[c + i] = dg[k][i];
-                part[a.cols + c + i] = db[k][i];
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t c = col(k) + i;
+                        if (c >= a.cols) continue;
+                        float lo, hi, lo2, hi2;
+                        f32x2_unpack(dg[k][i / 2], lo, hi);
+                        f32x2_unpack(db[k][i / 2], lo2, hi2);
+                        const float p = i & 1 ? hi : lo, q = i & 1 ? hi2 : lo2;
+                        sums[c] = w ? __fadd_rn(sums[c], p) : p;
+                        sums[a.cols + c] = w ? __fadd_rn(sums[a.cols + c], q) : q;
+                    }
+            }
+            __syncthreads();
+        }
+        for (int64_t c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = sums[c];
+    } else {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = col(k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                f32x2_unpack(dg[k][i], lo, hi);
+                if (c + 2 * i < a.cols) part[c + 2 * i] = lo;
+                if (c + 2 * i + 1 < a.cols) part[c + 2 * i + 1] = hi;
+                f32x2_unpack(db[k][i], lo, hi);
+                if (c + 2 * i < a.cols) part[a.cols + c + 2 * i] = lo;
+                if (c + 2 * i + 1 < a.cols) part[a.cols + c + 2 * i + 1] = hi;
             }
         }
     }
@@ -290,45 +478,66 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float *__rest
     }
 }
 
-bool rows_vec8(const void *p, int64_t ld, int type) {
-    const int64_t size = type == kTypeF32 ? 4 : 2;
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16 == 0;
+// Threads of a CTA that shares a row: whole warps, 8 VPT columns each.
+unsigned row_threads(int64_t cols, int vpt) {
+    return static_cast<unsigned>((cols + 256 * vpt - 1) / (256 * vpt) * 32);
+}
+
+unsigned capped(int64_t n, int64_t cap) { return static_cast<unsigned>(n < cap ? n : cap); }
+
+template <typename T, int VPT, bool WARP>
+cudaError_t ln_fwd_rows(const LnFwdArgs &a, int sms, cudaStream_t st) {
+    const unsigned threads = WARP ? 32 * kWarps : row_threads(a.cols, VPT);
+    // CTAs that the registers allow at once
+    const int64_t resident = static_cast<int64_t>(sms) * (threads < 640 ? 640 / threads : 1);
+    const unsigned grid = capped(WARP ? (a.rows + kWarps - 1) / kWarps : a.rows, resident);
+    return launch_pdl(ln_fwd_kernel<T, VPT, WARP>, dim3(grid), dim3(threads), 0, st, a);
 }
 
 template <typename T>
 cudaError_t ln_fwd_typed(const LnFwdArgs &a, int sms, cudaStream_t st) {
-    const int64_t cap = static_cast<int64_t>(sms) * 16;
-    const dim3 grid(static_cast<unsigned>(a.rows < cap ? a.rows : cap));
-    if (a.cols <= 1024) return launch_pdl(ln_fwd_kernel<T, 128, 1, false>, grid, dim3(128), 0, st, a);
-    if (a.cols <= 4096) return launch_pdl(ln_fwd_kernel<T, 256, 2, false>, grid, dim3(256), 0, st, a);
-    if (a.cols <= 8192) return launch_pdl(ln_fwd_kernel<T, 512, 2, false>, grid, dim3(512), 0, st, a);
-    if (a.cols <= 16384) return launch_pdl(ln_fwd_kernel<T, 512, 4, false>, grid, dim3(512), 0, st, a);
-    return launch_pdl(ln_fwd_kernel<T, 1024, 2, true>, grid, dim3(1024), 0, st, a);
+    if (a.cols <= 256) return ln_fwd_rows<T, 1, true>(a, sms, st);
+    if (a.cols <= 512) return ln_fwd_rows<T, 2, true>(a, sms, st);
+    if (a.cols <= 8192) return ln_fwd_rows<T, 2, false>(a, sms, st);
+    if (a.cols <= 16384) return ln_fwd_rows<T, 4, false>(a, sms, st);
+    return launch_pdl(ln_fwd_wide_kernel<T>, dim3(capped(a.rows, 2 * sms)), dim3(1024), 0, st, a);
 }
 
-constexpr int kBwdCtas = 304;       // most CTAs that keep sums of their own
-constexpr int64_t kBwdWide = 16384; // rows up to this are held in registers
+constexpr int64_t kBwdNarrow = 512;   // rows up to this belong to one warp
+constexpr int64_t kBwdWide = 8192;    // rows up to this are held in a CTA's registers
+constexpr int kBwdVpt = 2;
+constexpr int64_t kBwdSlab = 8 * kBwdVpt * 256;   // columns of a wide row's slab
+
+// CTAs that keep column sums of their own, at most: as many as the registers (128 per
+// thread) allow at once on 152 SMs; one per SM and slab of a wide row.
+int64_t bwd_ctas(int64_t rows, int64_t cols) {
+    constexpr int64_t sms = 152;
+    if (cols <= kBwdNarrow) return capped((rows + kWarps - 1) / kWarps, 2 * sms);
+    if (cols > kBwdWide) return capped(rows, sms);
+    const unsigned threads = row_threads(cols, kBwdVpt);
+    return capped(rows, sms * (threads < 512 ? 512 / threads : 1));
+}
 
 template <typename T, bool SAVED>
 cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
-    const int g = static_cast<int>(a.rows < kBwdCtas ? a.rows : kBwdCtas);
+    const int g = static_cast<int>(bwd_ctas(a.rows, a.cols));
     a.part = static_cast<float *>(ws);
     const dim3 grid(g);
+    const size_t sums = static_cast<size_t>(2 * a.cols * 4);
     cudaError_t e;
-    if (a.cols <= 1024)
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, 128, 1, false>, grid, dim3(128), 0, st, a);
-    else if (a.cols <= 4096)
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, 256, 2, false>, grid, dim3(256), 0, st, a);
-    else if (a.cols <= 8192)
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, 512, 2, false>, grid, dim3(512), 0, st, a);
-    else if (a.cols <= kBwdWide)
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, 1024, 2, false>, grid, dim3(1024), 0, st, a);
-    else {
+    if (a.cols <= 256) {
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, 1, true, false>, grid, dim3(32 * kWarps), sums, st, a);
+    } else if (a.cols <= kBwdNarrow) {
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, 2, true, false>, grid, dim3(32 * kWarps), sums, st, a);
+    } else if (a.cols <= kBwdWide) {
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, kBwdVpt, false, false>, grid,
+                       dim3(row_threads(a.cols, kBwdVpt)), 0, st, a);
+    } else {
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * a.cols);
-        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED, 1024>, dim3(static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048)), dim3(1024), 0, st, a);
+        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 2 * 152)), dim3(1024), 0, st, a);
         if (e != cudaSuccess) return e;
-        const dim3 slabs(g, static_cast<unsigned>((a.cols + 4095) / 4096));
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, 256, 2, true>, slabs, dim3(256), 0, st, a);
+        const dim3 slabs(g, static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab));
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, kBwdVpt, false, true>, slabs, dim3(256), 0, st, a);
     }
     if (e != cudaSuccess) return e;
     return launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32)),
@@ -342,17 +551,15 @@ cudaError_t launch_ln_fwd(const MatView &x, const void *gamma, const void *beta,
                           float eps, const MatView &y, const BlockView &y8, const BlockView &x8,
                           float *mean, float *rstd, int sm_count, cudaStream_t st) {
     if (x.rows == 0) return cudaSuccess;
-    const LnFwdArgs a{x.data, x.rows, x.cols, x.ld, rows_vec8(x.data, x.ld, x.type),
-                      rows_vec8(y.data, y.ld, x.type), gamma, beta, wtype, eps, y.data, y.ld, y8,
-                      x8, mean, rstd};
+    const LnFwdArgs a{x.data, x.rows, x.cols, x.ld, gamma, beta, wtype, eps, y.data, y.ld, y8, x8,
+                      mean,   rstd};
     if (x.type == kTypeF32) return ln_fwd_typed<float>(a, sm_count, st);
     if (x.type == kTypeBF16) return ln_fwd_typed<__nv_bfloat16>(a, sm_count, st);
     return ln_fwd_typed<__half>(a, sm_count, st);
 }
 
 int64_t ln_bwd_workspace(int64_t rows, int64_t cols) {
-    const int64_t g = rows < kBwdCtas ? rows : kBwdCtas;
-    return g * 2 * cols * 4 + (cols > kBwdWide ? rows * 8 : 0);
+    return bwd_ctas(rows, cols) * 2 * cols * 4 + (cols > kBwdWide ? rows * 8 : 0);
 }
 
 cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
@@ -364,10 +571,8 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
         if (e != cudaSuccess) return e;
         return cudaMemsetAsync(dbeta, 0, dy.cols * 4, st);
     }
-    const LnBwdArgs a{dy.data, x.data, dy.rows, dy.cols, dy.ld, x.ld, dx.ld,
-                      rows_vec8(dy.data, dy.ld, dy.type), rows_vec8(x.data, x.ld, dy.type),
-                      rows_vec8(dx.data, dx.ld, dy.type), x8, gamma, wtype, mean, rstd, dx.data,
-                      nullptr, nullptr};
+    const LnBwdArgs a{dy.data, x.data, dy.rows, dy.cols, dy.ld, x.ld, dx.ld, x8,
+                      gamma,   wtype,  mean,    rstd,    dx.data, nullptr, nullptr};
     const bool saved = x8.codes != nullptr;
 #define FP8K_LN_BWD(T)                                                            \
     (saved ? ln_bwd_typed<T, true>(a, dgamma, dbeta, ws, st)                      \
