@@ -263,21 +263,14 @@ __device__ __forceinline__ float load_any(const void *p, int type, int64_t c) {
 
 // ------------------------------------------------------------ block scales --
 
-// |x| as bits, 0 for infinities and NaN: the unsigned maximum of these is the
-// largest finite magnitude.
-__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
-    const uint32_t a = __float_as_uint(x) & 0x7FFFFFFFu;
-    return a < 0x7F800000u ? a : 0u;
-}
-
 // E8M0 byte of a block: e + 127 for the smallest e >= -127 with amax <= fmax 2^e.
 // Both formats' fmax is 1.75 2^t (t = 8 or 15).  With amax = f 2^p, 1 <= f < 2, e is
 // p - t if f <= 1.75 and p - t + 1 otherwise, and the biased exponent field of
 // amax is p + 127.  A subnormal amax (field 0) gives byte 0, as it should.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-    const int e = static_cast<int>(amax_bits >> 23) - (FMT == 0 ? 8 : 15) +
-                  ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    // adding 0x1FFFFF carries into the exponent exactly when the fraction is above .75
+    const int e = static_cast<int>((amax_bits + 0x1FFFFFu) >> 23) - (FMT == 0 ? 8 : 15);
     return static_cast<uint32_t>(max(e, 0));
 }
 // 2^-(byte - 127) for a byte of scale_byte (at most 247, so never subnormal)
@@ -339,10 +332,42 @@ __device__ __forceinline__ void load_codes(const uint8_t *row, int64_t c, int64_
     }
 }
 
+// Four values (two packed pairs) to a word of four codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-    return cvt2_fp8<FMT>(__fmul_rn(a, inv), __fmul_rn(b, inv)) |
-           (cvt2_fp8<FMT>(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16);
+__device__ __forceinline__ uint32_t encode4(uint64_t ab, uint64_t cd) {
+    float a, b, c, d;
+    f32x2_unpack(ab, a, b);
+    f32x2_unpack(cd, c, d);
+    uint32_t w;
+    if constexpr (FMT == 0)
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(w) : "f"(a), "f"(b), "f"(c), "f"(d));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+            "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(w) : "f"(a), "f"(b), "f"(c), "f"(d));
+    return w;
+}
+
+// max(m, |a|, |b|) in one instruction; NaN does not count.  m is not NaN.
+__device__ __forceinline__ float absmax3(float m, float a, float b) {
+    float d;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float absmax3(float m, uint64_t ab) {
+    float a, b;
+    f32x2_unpack(ab, a, b);
+    return absmax3(m, a, b);
+}
+__device__ __forceinline__ bool is_inf(float m) { return m == __uint_as_float(0x7F800000u); }
+// the pair with 0 in place of infinities: what a maximum that came out infinite is
+// taken over again
+__device__ __forceinline__ uint64_t without_inf(uint64_t ab) {
+    float a, b;
+    f32x2_unpack(ab, a, b);
+    return f32x2_pack(is_inf(fabsf(a)) ? 0.0f : a, is_inf(fabsf(b)) ? 0.0f : b);
 }
 
 // bytes [0, n) of a word of codes to p (4-byte aligned)
@@ -353,6 +378,65 @@ __device__ __forceinline__ void store_code_word(uint8_t *p, uint32_t w, int64_t 
         for (int i = 0; i < n; ++i) p[i] = static_cast<uint8_t>(w >> (8 * i));
     }
 }
+
+// One row's block-scaled output by lanes that hold 8 consecutive columns each: 16 lanes
+// hold a block of 128.  Addresses are kept for this thread's columns and moved from
+// row to row.
+struct RowWriter {
+    uint8_t *code;     // of this thread's first column
+    uint8_t *scale;
+    int64_t code_step, scale_step;   // bytes from one of the team's rows to the next
+    bool e5m2, f32;
+
+    __device__ __forceinline__ void start(const BlockView &q, int64_t row, int64_t rows_step, int64_t c) {
+        e5m2 = q.fmt != 0;
+        f32 = q.scale_f32 != 0;
+        const int64_t size = f32 ? 4 : 1;
+        code = q.codes + row * q.ld + c;
+        scale = static_cast<uint8_t *>(q.scales) + (row * q.ld_s + (c >> 7)) * size;
+        code_step = rows_step * q.ld;
+        scale_step = rows_step * q.ld_s * size;
+    }
+    __device__ __forceinline__ void next_row() {
+        code += code_step;
+        scale += scale_step;
+    }
+    // All lanes of the warp take part; `left` columns of the row are from this thread's
+    // first on (0 or less: none; the values there are 0).  at: columns past it.
+    __device__ __forceinline__ void put(const uint64_t (&v)[4], int at, int left) const {
+        if (e5m2)
+            put_as<1>(v, at, left);
+        else
+            put_as<0>(v, at, left);
+    }
+    template <int FMT>
+    __device__ __forceinline__ void put_as(const uint64_t (&v)[4], int at, int left) const {
+        float m = absmax3(absmax3(absmax3(absmax3(0.0f, v[0]), v[1]), v[2]), v[3]);
+        if (is_inf(m))
+            m = absmax3(absmax3(absmax3(absmax3(0.0f, without_inf(v[0])), without_inf(v[1])),
+                                without_inf(v[2])),
+                        without_inf(v[3]));
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const uint32_t byte = scale_byte<FMT>(__float_as_uint(m));
+        const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
+        const uint32_t w0 = encode4<FMT>(f32x2_mul(v[0], inv2), f32x2_mul(v[1], inv2));
+        const uint32_t w1 = encode4<FMT>(f32x2_mul(v[2], inv2), f32x2_mul(v[3], inv2));
+        if (left <= 0) return;
+        if ((threadIdx.x & 15) == 0) {
+            if (f32)
+                *reinterpret_cast<float *>(scale + (at >> 7) * 4) = scale_value(byte);
+            else
+                scale[at >> 7] = static_cast<uint8_t>(byte);
+        }
+        if (left >= 8) {
+            *reinterpret_cast<uint2 *>(code + at) = make_uint2(w0, w1);
+        } else {
+            store_code_word(code + at, w0, left);
+            store_code_word(code + at + 4, w1, left - 4);
+        }
+    }
+};
 
 // ----------------------------------------------------------- tile kernels --
 //
@@ -397,26 +481,35 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// This warp's 8 rows x 128 columns of elements of `size` bytes at (row0, col0) into
-// its part of a stage (rows of 128 * size bytes); outside the matrix: zeros.  vec:
+// This warp's 8 rows x 128 columns of elements of SIZE bytes at (row0, col0) into
+// its part of a stage (rows of 128 * SIZE bytes); outside the matrix: zeros.  vec:
 // rows are 16-byte aligned; otherwise elements are copied one by one.
 template <int SIZE>
 __device__ __forceinline__ void fetch_rows(uint32_t dst, const void *base, int64_t ld, int64_t rows,
                                            int64_t cols, bool vec, int64_t row0, int64_t col0) {
     constexpr int kPerRow = kTile * SIZE / 16;   // 16-byte chunks
     constexpr int kElems = 16 / SIZE;
+    constexpr int kStep = 32 / kPerRow;          // rows per instruction of the warp
     const int lane = threadIdx.x & 31;
     const int64_t first = row0 + (threadIdx.x >> 5) * kTileRows;
     const uint8_t *p = static_cast<const uint8_t *>(base);
     if (vec) {
+        const int r0 = lane / kPerRow, k = lane % kPerRow;
+        const int64_t c = col0 + k * kElems;
+        const uint8_t *src = p + ((first + r0) * ld + c) * SIZE;
+        const uint32_t to = dst + r0 * kTile * SIZE + k * 16;
+        if (row0 + kTile <= rows && col0 + kTile <= cols) {
 #pragma unroll
-        for (int i = 0; i < kTileRows * kPerRow / 32; ++i) {
-            const int idx = i * 32 + lane, r = idx / kPerRow, k = idx % kPerRow;
-            const int64_t c = col0 + k * kElems;
-            int64_t left = first + r < rows ? (cols - c) * SIZE : 0;
-            left = left < 0 ? 0 : left > 16 ? 16 : left;
-            const uint8_t *src = left ? p + ((first + r) * ld + c) * SIZE : p;
-            cp_async16(dst + r * kTile * SIZE + k * 16, src, static_cast<uint32_t>(left));
+            for (int i = 0; i < kTileRows / kStep; ++i, src += kStep * ld * SIZE)
+                cp_async16(to + i * kStep * kTile * SIZE, src, 16);
+        } else {
+            const int64_t left = (cols - c) * SIZE;
+            const uint32_t bytes = left <= 0 ? 0u : left < 16 ? static_cast<uint32_t>(left) : 16u;
+#pragma unroll
+            for (int i = 0; i < kTileRows / kStep; ++i, src += kStep * ld * SIZE) {
+                const uint32_t n = first + r0 + i * kStep < rows ? bytes : 0u;
+                cp_async16(to + i * kStep * kTile * SIZE, n ? src : p, n);
+            }
         }
     } else {
         for (int idx = lane; idx < kTileRows * kTile; idx += 32) {
@@ -458,31 +551,37 @@ __device__ __forceinline__ void staged_codes4(const uint8_t *part, int r, int fm
     v[1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
 }
 
-// max |x| over finite x, given the plain maximum (which skips NaN unless there is
-// nothing else): only an infinity or nothing but NaN takes the slow way.
-__device__ __forceinline__ uint32_t finite_max4(float a, float b, float c, float d) {
-    const float m = fmaxf(fmaxf(fabsf(a), fabsf(b)), fmaxf(fabsf(c), fabsf(d)));
-    if (m < __uint_as_float(0x7F800000u)) return __float_as_uint(m);
-    return max(max(finite_abs_bits(a), finite_abs_bits(b)),
-               max(finite_abs_bits(c), finite_abs_bits(d)));
+// Lane r (0 .. 7): the bits of row r's largest finite magnitude.
+__device__ __forceinline__ uint32_t row_maxima(const TileValues &v) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int r = 0; r < kTileRows; ++r) {
+        const float m = absmax3(absmax3(0.0f, v[r][0]), v[r][1]);
+        const uint32_t row = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+        if (lane == r) mine = row;
+    }
+    if (__any_sync(0xFFFFFFFFu, mine == 0x7F800000u)) {
+#pragma unroll 1
+        for (int r = 0; r < kTileRows; ++r) {
+            float m = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kTileRows; ++k)
+                if (k == r) m = absmax3(absmax3(0.0f, without_inf(v[k][0])), without_inf(v[k][1]));
+            const uint32_t row = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
+            if (lane == r) mine = row;
+        }
+    }
+    return mine;
 }
 
 // The tile's own maximum (block_rows 128), the same in every thread.  One barrier;
 // red is not written again before another one.
 __device__ __forceinline__ uint32_t tile_max(const TileValues &v, uint32_t *red) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-        float a, b, c, d;
-        f32x2_unpack(v[r][0], a, b);
-        f32x2_unpack(v[r][1], c, d);
-        m = max(m, finite_max4(a, b, c, d));
-    }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, row_maxima(v));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = red[threadIdx.x & 15];
-    return __reduce_max_sync(0xFFFFFFFFu, m);
+    return __reduce_max_sync(0xFFFFFFFFu, red[threadIdx.x & 15]);
 }
 
 // Row-major codes and scales of the tile at (row0, col0).  tile_byte < 0: one
@@ -492,30 +591,25 @@ __device__ __forceinline__ void tile_rows(const TileValues &v, const BlockView &
                                           int64_t col0, int tile_byte) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t first = row0 + warp * kTileRows, c = col0 + 4 * lane;
-    if (tile_byte >= 0 && threadIdx.x == 0)
-        store_scale(q, row0 / kTile, col0 / kTile, static_cast<uint32_t>(tile_byte));
-    uint32_t mine = 0;   // lane r: row r's scale
+    uint32_t byte = static_cast<uint32_t>(tile_byte);   // lane r: of row r
+    if (tile_byte < 0) {
+        byte = scale_byte<FMT>(row_maxima(v));
+        if (lane < kTileRows && first + lane < q.rows) store_scale(q, first + lane, col0 / kTile, byte);
+    } else if (threadIdx.x == 0) {
+        store_scale(q, row0 / kTile, col0 / kTile, byte);
+    }
+    const float inv = scale_inverse(byte);
+    const bool whole = row0 + kTile <= q.rows && col0 + kTile <= q.cols;
     uint8_t *p = q.codes + first * q.ld + c;
 #pragma unroll
-    for (int r = 0; r < kTileRows; ++r) {
-        uint32_t byte = static_cast<uint32_t>(tile_byte);
-        if (tile_byte < 0) {
-            float x, y, z, w;
-            f32x2_unpack(v[r][0], x, y);
-            f32x2_unpack(v[r][1], z, w);
-            byte = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, finite_max4(x, y, z, w)));
-            if (lane == r) mine = byte;
-        }
-        const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
-        float x, y, z, w;
-        f32x2_unpack(f32x2_mul(v[r][0], inv2), x, y);
-        f32x2_unpack(f32x2_mul(v[r][1], inv2), z, w);
-        const uint32_t code = cvt2_fp8<FMT>(x, y) | (cvt2_fp8<FMT>(z, w) << 16);
-        if (first + r < q.rows && c < q.cols) store_code_word(p, code, q.cols - c);
-        p += q.ld;
+    for (int r = 0; r < kTileRows; ++r, p += q.ld) {
+        const uint64_t inv2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, inv, r));
+        const uint32_t code = encode4<FMT>(f32x2_mul(v[r][0], inv2), f32x2_mul(v[r][1], inv2));
+        if (whole)
+            *reinterpret_cast<uint32_t *>(p) = code;
+        else if (first + r < q.rows && c < q.cols)
+            store_code_word(p, code, q.cols - c);
     }
-    if (tile_byte < 0 && lane < kTileRows && first + lane < q.rows)
-        store_scale(q, first + lane, col0 / kTile, mine);
 }
 
 // Transposition, in steps with a barrier between each two:
@@ -534,18 +628,29 @@ struct ColsSmem {
 };
 
 __device__ __forceinline__ void cols_max(const TileValues &v, ColsSmem &sm) {
-    uint32_t m[4];
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto take = [&](int r, uint64_t a0, uint64_t a1, uint64_t b0, uint64_t b1) {
+        float x, y, z, w;
+        f32x2_unpack(a0, x, y);
+        f32x2_unpack(b0, z, w);
+        m[0] = absmax3(m[0], x, z);
+        m[1] = absmax3(m[1], y, w);
+        f32x2_unpack(a1, x, y);
+        f32x2_unpack(b1, z, w);
+        m[2] = absmax3(m[2], x, z);
+        m[3] = absmax3(m[3], y, w);
+    };
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        float lo[kTileRows], hi[kTileRows];
+    for (int r = 0; r < kTileRows; r += 2) take(r, v[r][0], v[r][1], v[r + 1][0], v[r + 1][1]);
+    if (is_inf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])))) {
+        m[0] = m[1] = m[2] = m[3] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kTileRows; ++r) f32x2_unpack(v[r][p], lo[r], hi[r]);
-        m[2 * p] = max(finite_max4(lo[0], lo[1], lo[2], lo[3]), finite_max4(lo[4], lo[5], lo[6], lo[7]));
-        m[2 * p + 1] =
-            max(finite_max4(hi[0], hi[1], hi[2], hi[3]), finite_max4(hi[4], hi[5], hi[6], hi[7]));
+        for (int r = 0; r < kTileRows; r += 2)
+            take(r, without_inf(v[r][0]), without_inf(v[r][1]), without_inf(v[r + 1][0]),
+                 without_inf(v[r + 1][1]));
     }
-    *reinterpret_cast<uint4 *>(&sm.max[threadIdx.x >> 5][4 * (threadIdx.x & 31)]) =
-        make_uint4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<float4 *>(&sm.max[threadIdx.x >> 5][4 * (threadIdx.x & 31)]) =
+        make_float4(m[0], m[1], m[2], m[3]);
 }
 
 // thread c (0 .. 127) of the caller's choice
@@ -576,26 +681,26 @@ __device__ __forceinline__ void cols_codes(const TileValues &v, const ulonglong2
             const int at = c * kTile + (((warp >> 1) ^ ((c >> 2) & 7)) << 4) +
                            (((warp & 1) ^ ((c >> 5) & 1)) << 3);
             *reinterpret_cast<uint2 *>(&sm.codes[at]) =
-                make_uint2(cvt2_fp8<FMT>(x[0], x[1]) | (cvt2_fp8<FMT>(x[2], x[3]) << 16),
-                           cvt2_fp8<FMT>(x[4], x[5]) | (cvt2_fp8<FMT>(x[6], x[7]) << 16));
+                make_uint2(encode4<FMT>(f32x2_pack(x[0], x[1]), f32x2_pack(x[2], x[3])),
+                           encode4<FMT>(f32x2_pack(x[4], x[5]), f32x2_pack(x[6], x[7])));
         }
     }
 }
 
 __device__ __forceinline__ void cols_store(const ColsSmem &sm, const BlockView &qt, int64_t row0,
                                            int64_t col0) {
+    const int c0 = threadIdx.x >> 3, k = threadIdx.x & 7;
+    const int64_t r = row0 + 16 * k;
+    uint8_t *p = qt.codes + (col0 + c0) * qt.ld + r;
+    const bool whole = col0 + kTile <= qt.rows && row0 + kTile <= qt.cols;
 #pragma unroll
-    for (int i = 0; i < kTile * kTile / 16 / kTileThreads; ++i) {
-        const int idx = threadIdx.x + i * kTileThreads;
-        const int c = idx >> 3, k = idx & 7;
-        if (col0 + c >= qt.rows) continue;
+    for (int i = 0; i < kTile * 8 / kTileThreads; ++i, p += kTileThreads / 8 * qt.ld) {
+        const int c = c0 + i * (kTileThreads / 8);
         uint4 u = *reinterpret_cast<const uint4 *>(&sm.codes[c * kTile + ((k ^ ((c >> 2) & 7)) << 4)]);
         if ((c >> 5) & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-        const int64_t r = row0 + 16 * k;
-        uint8_t *p = qt.codes + (col0 + c) * qt.ld + r;
-        if (r + 16 <= qt.cols) {
+        if (whole || (col0 + c < qt.rows && r + 16 <= qt.cols)) {
             *reinterpret_cast<uint4 *>(p) = u;
-        } else {
+        } else if (col0 + c < qt.rows) {
             store_code_word(p, u.x, qt.cols - r);
             store_code_word(p + 4, u.y, qt.cols - r - 4);
             store_code_word(p + 8, u.z, qt.cols - r - 8);

@@ -187,23 +187,6 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x)));
 }
 
-// Quantizes 8 consecutive columns per lane; 16 lanes hold a block of 128.
-template <int FMT>
-__device__ __forceinline__ void emit_full8(const float (&v)[8], const BlockView &q, int64_t row,
-                                           int64_t c) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[i]));
-#pragma unroll
-    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const uint32_t byte = scale_byte<FMT>(m);
-    const float inv = scale_inverse(byte);
-    if ((threadIdx.x & 15) == 0) store_scale(q, row, c >> 7, byte);
-    *reinterpret_cast<uint2 *>(q.codes + row * q.ld + c) =
-        make_uint2(encode4<FMT>(v[0], v[1], v[2], v[3], inv),
-                   encode4<FMT>(v[4], v[5], v[6], v[7], inv));
-}
-
 // 16 lanes per block of 128 columns of a row, two blocks per warp.
 template <typename T>
 __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h, int64_t M, int64_t F,
@@ -211,31 +194,33 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
                                                          const BlockView h8) {
     pdl_wait();
     pdl_trigger();
-    const int64_t per_row = F / 128, total = M * per_row;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 16;
+    const unsigned per_row = static_cast<unsigned>(F / 128);
+    const int64_t total = M * per_row, step = static_cast<int64_t>(gridDim.x) * 16;
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; w < total;
          w += step) {
         // the warp's second half may be past the end: it repeats the first half's block
         int64_t blk = w + ((threadIdx.x >> 4) & 1);
         if (blk >= total) blk = w;
-        const int64_t row = blk / per_row, c = (blk % per_row) * 128 + 8 * (threadIdx.x & 15);
-        float g[8], u[8], a[8];
+        const int64_t row = blk / per_row, c = (blk - row * per_row) * 128 + 8 * (threadIdx.x & 15);
+        float g[8], u[8];
         load_row<T, 8>(h + row * ld, c, 2 * F, vec, g);
         load_row<T, 8>(h + row * ld, F + c, 2 * F, vec, u);
+        uint64_t g2[4], u2[4], a2[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = __fmul_rn(__fmul_rn(g[i], sigmoid(g[i])), u[i]);
-        if (a8.fmt == 0)
-            emit_full8<0>(a, a8, row, c);
-        else
-            emit_full8<1>(a, a8, row, c);
+        for (int i = 0; i < 4; ++i) {
+            g2[i] = f32x2_pack(g[2 * i], g[2 * i + 1]);
+            u2[i] = f32x2_pack(u[2 * i], u[2 * i + 1]);
+            const uint64_t s = f32x2_pack(sigmoid(g[2 * i]), sigmoid(g[2 * i + 1]));
+            a2[i] = f32x2_mul(f32x2_mul(g2[i], s), u2[i]);
+        }
+        RowWriter out;
+        out.start(a8, row, 0, c);
+        out.put(a2, 0, 8);
         if (h8.codes != nullptr) {
-            if (h8.fmt == 0) {
-                emit_full8<0>(g, h8, row, c);
-                emit_full8<0>(u, h8, row, F + c);
-            } else {
-                emit_full8<1>(g, h8, row, c);
-                emit_full8<1>(u, h8, row, F + c);
-            }
+            out.start(h8, row, 0, c);
+            out.put(g2, 0, 8);
+            out.start(h8, row, 0, F + c);
+            out.put(u2, 0, 8);
         }
     }
 }

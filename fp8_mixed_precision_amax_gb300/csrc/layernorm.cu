@@ -69,38 +69,6 @@ __device__ __forceinline__ float sum2(uint64_t v) {
     return __fadd_rn(lo, hi);
 }
 
-// Quantizes 8 consecutive columns per lane: 16 lanes hold a block of 128.  All
-// lanes of the warp take part; columns past the row are 0.
-template <int FMT>
-__device__ __forceinline__ void emit_block8(const uint64_t (&v)[4], const BlockView &q, int64_t row,
-                                            int64_t c) {
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f32x2_unpack(v[i], x[2 * i], x[2 * i + 1]);
-    uint32_t m = max(finite_max4(x[0], x[1], x[2], x[3]), finite_max4(x[4], x[5], x[6], x[7]));
-#pragma unroll
-    for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const uint32_t byte = scale_byte<FMT>(m);
-    if (c >= q.cols) return;
-    if ((threadIdx.x & 15) == 0) store_scale(q, row, c >> 7, byte);
-    const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        f32x2_unpack(f32x2_mul(v[i], inv2), lo, hi);
-        w[i] = cvt2_fp8<FMT>(lo, hi);
-    }
-    w[0] |= w[1] << 16, w[2] |= w[3] << 16;
-    uint8_t *p = q.codes + row * q.ld + c;
-    if (c + 8 <= q.cols) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[2]);
-    } else {
-        store_code_word(p, w[0], q.cols - c);
-        store_code_word(p + 4, w[2], q.cols - c - 4);
-    }
-}
-
 struct LnFwdArgs {
     const void *x;
     int64_t rows, cols, ldx;
@@ -113,29 +81,21 @@ struct LnFwdArgs {
     float *mean, *rstd;
 };
 
-// The part of the forward that follows the statistics, for 8 columns.
+// The part of the forward that follows the statistics, for 8 columns: `at` columns past
+// the writers' first, `left` columns before the row's end.
 template <typename T>
-__device__ __forceinline__ void ln_finish(const LnFwdArgs &a, int64_t row, int64_t c, uint64_t nmu2,
-                                          uint64_t rs2, const uint64_t (&g)[4],
+__device__ __forceinline__ void ln_finish(const LnFwdArgs &a, T *yr, const RowWriter &wy,
+                                          const RowWriter &wx, int64_t c, int at, int left,
+                                          uint64_t nmu2, uint64_t rs2, const uint64_t (&g)[4],
                                           const uint64_t (&b)[4], const uint64_t (&x)[4]) {
-    if (a.x8.codes != nullptr) {
-        if (a.x8.fmt == 0)
-            emit_block8<0>(x, a.x8, row, c);
-        else
-            emit_block8<1>(x, a.x8, row, c);
-    }
+    if (a.x8.codes != nullptr) wx.put(x, at, left);
     if (a.y == nullptr && a.y8.codes == nullptr) return;
     uint64_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         y[i] = f32x2_fma(f32x2_mul(f32x2_add(x[i], nmu2), rs2), g[i], b[i]);
-    if (a.y != nullptr) store_row8<T>(static_cast<T *>(a.y) + row * a.ldy, c, a.cols, y);
-    if (a.y8.codes != nullptr) {
-        if (a.y8.fmt == 0)
-            emit_block8<0>(y, a.y8, row, c);
-        else
-            emit_block8<1>(y, a.y8, row, c);
-    }
+    if (a.y != nullptr) store_row8<T>(yr, c, a.cols, y);
+    if (a.y8.codes != nullptr) wy.put(y, at, left);
 }
 
 __device__ __forceinline__ void load_param8(const void *p, int type, int64_t c, int64_t cols,
@@ -169,6 +129,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
     pdl_wait();
     pdl_trigger();
     const float n = static_cast<float>(a.cols);
+    const int left0 = static_cast<int>(a.cols) - 8 * team.id;
+    RowWriter wx, wy;
+    wx.start(a.x8, team.row, team.step, 8 * team.id);
+    wy.start(a.y8, team.row, team.step, 8 * team.id);
     RawRow8<T> raw[VPT];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -212,9 +176,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             if constexpr (VPT > 2) params(k, 0);
-            ln_finish<T>(a, row, 8 * (team.id + k * team.size), nmu2, splat_f32x2(rs), g[k % kKept],
-                         b[k % kKept], x[k]);
+            const int at = 8 * k * team.size;
+            ln_finish<T>(a, static_cast<T *>(a.y) + row * a.ldy, wy, wx, 8 * team.id + at, at, left0 - at,
+                         nmu2, splat_f32x2(rs), g[k % kKept], b[k % kKept], x[k]);
         }
+        wx.next_row();
+        wy.next_row();
     }
 }
 
@@ -227,6 +194,9 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
     const float n = static_cast<float>(a.cols);
     // whole warps stay together: the exchanges between lanes need all of them
     const int64_t warp0 = 8 * (threadIdx.x & ~31);
+    RowWriter wx, wy;
+    wx.start(a.x8, blockIdx.x, gridDim.x, 8 * threadIdx.x);
+    wy.start(a.y8, blockIdx.x, gridDim.x, 8 * threadIdx.x);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *xr = static_cast<const T *>(a.x) + row * a.ldx;
         RawRow8<T> raw;
@@ -260,8 +230,11 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
             load_param8(a.beta, a.wtype, c, a.cols, b);
             raw.load(xr, c, a.cols);
             raw.get(xr, c, a.cols, x);
-            ln_finish<T>(a, row, c, nmu2, splat_f32x2(rs), g, b, x);
+            ln_finish<T>(a, static_cast<T *>(a.y) + row * a.ldy, wy, wx, c, static_cast<int>(w - warp0),
+                         static_cast<int>(a.cols - c), nmu2, splat_f32x2(rs), g, b, x);
         }
+        wx.next_row();
+        wy.next_row();
     }
 }
 
