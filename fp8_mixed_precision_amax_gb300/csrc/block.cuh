@@ -194,6 +194,60 @@ struct RawRow8 {
     }
 };
 
+// N (8 or 16) elements of a row that starts on a 16-byte boundary and is a multiple of N
+// elements long.
+template <typename T, int N>
+struct RawVec {
+    static constexpr int kBlocks = N * static_cast<int>(sizeof(T)) / 16;
+    uint4 u[kBlocks];
+
+    __device__ __forceinline__ void load(const T *row, int64_t c, int64_t cols) {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+            u[i] = c < cols ? reinterpret_cast<const uint4 *>(row + c)[i] : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(const T *, int64_t, int64_t, uint64_t (&v)[N / 2]) const {
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[2 * i] = f32x2_pack(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+                v[2 * i + 1] = f32x2_pack(__uint_as_float(u[i].z), __uint_as_float(u[i].w));
+            } else {
+                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack2<T>(w[k]);
+                    v[4 * i + k] = f32x2_pack(f.x, f.y);
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T *row, int64_t c, int64_t cols,
+                                                 const uint64_t (&v)[N / 2]) {
+        if (c >= cols) return;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            uint4 q;
+            float a, b, d, e;
+            if constexpr (sizeof(T) == 4) {
+                f32x2_unpack(v[2 * i], a, b);
+                f32x2_unpack(v[2 * i + 1], d, e);
+                q = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(d),
+                               __float_as_uint(e));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f32x2_unpack(v[4 * i + k], a, b);
+                    w[k] = pack2<T>(a, b);
+                }
+                q = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            reinterpret_cast<uint4 *>(row + c)[i] = q;
+        }
+    }
+};
+
 // Stores the pairs to columns c .. c + 7 (those below cols).  All lanes of the warp
 // take part, lane l + 1 with the columns after lane l's.
 template <typename T>
@@ -379,9 +433,9 @@ __device__ __forceinline__ void store_code_word(uint8_t *p, uint32_t w, int64_t 
     }
 }
 
-// One row's block-scaled output by lanes that hold 8 consecutive columns each: 16 lanes
-// hold a block of 128.  Addresses are kept for this thread's columns and moved from
-// row to row.
+// One row's block-scaled output by lanes that hold 2 P = 8 or 16 consecutive columns
+// each: 64 / P lanes hold a block of 128.  Addresses are kept for this thread's columns
+// and moved from row to row.
 struct RowWriter {
     uint8_t *code;     // of this thread's first column
     uint8_t *scale;
@@ -401,39 +455,49 @@ struct RowWriter {
         code += code_step;
         scale += scale_step;
     }
-    // All lanes of the warp take part; `left` columns of the row are from this thread's
-    // first on (0 or less: none; the values there are 0).  at: columns past it.
-    __device__ __forceinline__ void put(const uint64_t (&v)[4], int at, int left) const {
+    // All lanes of the warp take part; `left` columns of the row are from the values'
+    // first on (0 or less: none; the values there are 0).  at: columns past the
+    // thread's first.
+    template <int P>
+    __device__ __forceinline__ void put(const uint64_t (&v)[P], int at, int left) const {
         if (e5m2)
             put_as<1>(v, at, left);
         else
             put_as<0>(v, at, left);
     }
-    template <int FMT>
-    __device__ __forceinline__ void put_as(const uint64_t (&v)[4], int at, int left) const {
-        float m = absmax3(absmax3(absmax3(absmax3(0.0f, v[0]), v[1]), v[2]), v[3]);
-        if (is_inf(m))
-            m = absmax3(absmax3(absmax3(absmax3(0.0f, without_inf(v[0])), without_inf(v[1])),
-                                without_inf(v[2])),
-                        without_inf(v[3]));
+    template <int FMT, int P>
+    __device__ __forceinline__ void put_as(const uint64_t (&v)[P], int at, int left) const {
+        float m = 0.0f;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int i = 0; i < P; ++i) m = absmax3(m, v[i]);
+        if (is_inf(m)) {
+            m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) m = absmax3(m, without_inf(v[i]));
+        }
+#pragma unroll
+        for (int o = 32 / P; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const uint32_t byte = scale_byte<FMT>(__float_as_uint(m));
         const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
-        const uint32_t w0 = encode4<FMT>(f32x2_mul(v[0], inv2), f32x2_mul(v[1], inv2));
-        const uint32_t w1 = encode4<FMT>(f32x2_mul(v[2], inv2), f32x2_mul(v[3], inv2));
+        uint32_t w[P / 2];
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i)
+            w[i] = encode4<FMT>(f32x2_mul(v[2 * i], inv2), f32x2_mul(v[2 * i + 1], inv2));
         if (left <= 0) return;
-        if ((threadIdx.x & 15) == 0) {
+        if ((threadIdx.x & (64 / P - 1)) == 0) {
             if (f32)
                 *reinterpret_cast<float *>(scale + (at >> 7) * 4) = scale_value(byte);
             else
                 scale[at >> 7] = static_cast<uint8_t>(byte);
         }
-        if (left >= 8) {
-            *reinterpret_cast<uint2 *>(code + at) = make_uint2(w0, w1);
+        if (left >= 2 * P) {
+            if constexpr (P == 8)
+                *reinterpret_cast<uint4 *>(code + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            else
+                *reinterpret_cast<uint2 *>(code + at) = make_uint2(w[0], w[1]);
         } else {
-            store_code_word(code + at, w0, left);
-            store_code_word(code + at + 4, w1, left - 4);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) store_code_word(code + at + 4 * i, w[i], left - 4 * i);
         }
     }
 };
