@@ -139,12 +139,13 @@ template <int N, int WORDS>
 __device__ __forceinline__ void shift_words(const uint32_t (&w)[WORDS], uint32_t off, uint32_t (&out)[N]) {
     static_assert(WORDS >= N + 4, "a whole block more than the result");
     uint32_t a[N + 2], b[N + 1];
+    const uint32_t pick = off & 2u ? 0x5432u : 0x3210u;
 #pragma unroll
     for (int i = 0; i < N + 2; ++i) a[i] = off & 8u ? w[i + 2] : w[i];
 #pragma unroll
     for (int i = 0; i < N + 1; ++i) b[i] = off & 4u ? a[i + 1] : a[i];
 #pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = off & 2u ? __funnelshift_r(b[i], b[i + 1], 16) : b[i];
+    for (int i = 0; i < N; ++i) out[i] = __byte_perm(b[i], b[i + 1], pick);
 }
 
 template <typename T>
@@ -164,9 +165,21 @@ struct RawRow8 {
             w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
         }
     }
+    // the same blocks from a copy in shared memory: `at` is the first one's address
+    __device__ __forceinline__ void load_shared(const uint8_t *at, bool more) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4 + 1; ++i) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (i < kWords / 4 || more) u = *reinterpret_cast<const uint4 *>(at + 16 * i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    }
     // the 8 elements as packed pairs; columns from cols on are 0
     __device__ __forceinline__ void get(const T *row, int64_t c, int64_t cols, uint64_t (&v)[4]) const {
-        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u);
+        get(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15u), static_cast<int>(cols - c), v);
+    }
+    // off: the row start's distance from a 16-byte boundary; left: columns from the first on
+    __device__ __forceinline__ void get(uint32_t off, int left, uint64_t (&v)[4]) const {
         uint32_t x[kWords];
         if (off == 0) {   // the same for the whole row: 8 elements are whole blocks
 #pragma unroll
@@ -183,12 +196,12 @@ struct RawRow8 {
                 v[i] = f32x2_pack(f.x, f.y);
             }
         }
-        if (c + 8 > cols) {
+        if (left < 8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float lo, hi;
                 f32x2_unpack(v[i], lo, hi);
-                v[i] = f32x2_pack(c + 2 * i < cols ? lo : 0.0f, c + 2 * i + 1 < cols ? hi : 0.0f);
+                v[i] = f32x2_pack(2 * i < left ? lo : 0.0f, 2 * i + 1 < left ? hi : 0.0f);
             }
         }
     }

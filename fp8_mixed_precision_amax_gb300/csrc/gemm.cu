@@ -573,6 +573,10 @@ cudaError_t read_and_clear_error_flag(unsigned *flags, cudaStream_t st) {
     unsigned block_flags = 0;
     e = read_and_clear_block_gemm_error_flag(&block_flags);
     *flags |= block_flags;
+    if (e != cudaSuccess) return e;
+    unsigned ln_flags = 0;
+    e = read_and_clear_ln_error_flag(&ln_flags);
+    *flags |= ln_flags;
     return e;
 }
 

@@ -217,8 +217,10 @@ cudaError_t launch_swiglu_bwd(const MatView &da, const BlockView &h8, const Bloc
                               const BlockView &dh8t, const BlockView &a8t, int sm_count,
                               cudaStream_t st);
 
-// Read and clear the block GEMM's device error flag (block_gemm.cu).
+// Read and clear the device error flags of the block GEMM (block_gemm.cu) and of
+// LayerNorm's backward (layernorm.cu).
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags);
+cudaError_t read_and_clear_ln_error_flag(unsigned *flags);
 
 // Diagnostic: while acc is not null, the first CTA of every GEMM launch adds
 // its SM clock cycles to acc[0] and its nanoseconds to acc[1] (gemm.cu).

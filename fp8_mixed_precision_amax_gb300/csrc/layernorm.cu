@@ -10,12 +10,15 @@
 // Both are bound by HBM: each value is read and written once, and a row stays
 // in its CTA's registers between the sums and the use of the sums.
 #include <cstdint>
+#include <mutex>
 
 #include "block.cuh"
 
 namespace fp8k {
 
 namespace {
+
+__device__ unsigned g_ln_error_flags = 0;
 
 // Who works on a row: a warp (narrow rows; a CTA has kWarps of them at a time) or the
 // whole CTA.  Thread i of the team holds columns E (i + k team) .. + E - 1 for k < VPT,
@@ -292,6 +295,22 @@ struct LnBwdArgs {
     float2 *row_sums;  // wide rows: [rows] sums of u and u * xhat
 };
 
+// 8 codes times their scale; `left` of them belong to the row, the others may be anything.
+__device__ __forceinline__ void codes8(uint2 w, int fmt, float scale, int left, uint64_t (&v)[4]) {
+    const uint64_t s2 = splat_f32x2(scale);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float f[4];
+        decode4(i ? w.y : w.x, fmt, f);
+        if (left < 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = 4 * i + k < left ? f[k] : 0.0f;
+        }
+        v[2 * i] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
+        v[2 * i + 1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
+    }
+}
+
 // Columns of x on their way: as they are, or codes with their block's scale.
 template <typename T, bool SAVED, int VEC>
 struct RawX {
@@ -323,18 +342,7 @@ struct RawX<T, true, VEC> {
         }
     }
     __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t, int64_t c, uint64_t (&v)[P]) const {
-        const uint64_t s2 = splat_f32x2(scale);
-#pragma unroll
-        for (int i = 0; i < P / 2; ++i) {
-            float f[4];
-            decode4(w[i], a.x8.fmt, f);
-            if (VEC == 0 && c + 8 > a.cols) {   // codes past the row may be anything
-#pragma unroll
-                for (int k = 0; k < 4; ++k) f[k] = c + 4 * i + k < a.cols ? f[k] : 0.0f;
-            }
-            v[2 * i] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
-            v[2 * i + 1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
-        }
+        codes8(make_uint2(w[0], w[1]), a.x8.fmt, scale, VEC ? 8 : static_cast<int>(a.cols - c), v);
     }
 };
 
@@ -382,7 +390,151 @@ __global__ void __launch_bounds__(1024) ln_bwd_sums_kernel(const LnBwdArgs a) {
     }
 }
 
-// Rows in turn; a thread keeps its columns (as in the forward) and their sums over
+// A CTA's sums over its rows, to its part of the workspace.
+template <int VPT, int P, typename Col>
+__device__ __forceinline__ void store_part(const LnBwdArgs &a, Col col, const uint64_t (&dg)[VPT][P],
+                                           const uint64_t (&db)[VPT][P]) {
+    float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int64_t c = col(k);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            f32x2_unpack(dg[k][i], lo, hi);
+            if (c + 2 * i < a.cols) part[c + 2 * i] = lo;
+            if (c + 2 * i + 1 < a.cols) part[c + 2 * i + 1] = hi;
+            f32x2_unpack(db[k][i], lo, hi);
+            if (c + 2 * i < a.cols) part[a.cols + c + 2 * i] = lo;
+            if (c + 2 * i + 1 < a.cols) part[a.cols + c + 2 * i + 1] = hi;
+        }
+    }
+}
+
+// Rows of 513 .. 8192 columns, one at a time per CTA: thread t has columns
+// 8 (t + k threads) .. + 7, k < 2, and their sums over the CTA's rows.  The next rows of
+// dy and x are on their way into a ring in shared memory by bulk copies of the 16-byte
+// blocks that hold them, whatever their alignment; the barrier of a row's sums
+// also tells that its place in the ring may be filled again.  (With the next row in
+// registers instead, one row's loads were in flight per CTA: 91 us at 8192 x 8192.)
+constexpr int kRing = 8;   // most rows in flight
+
+struct RingArgs {
+    LnBwdArgs a;
+    int stages;
+    uint32_t dy_span, x_span;   // bytes of a row's place: dy, then x or its codes
+};
+
+template <typename T, bool SAVED>
+__global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const RingArgs r) {
+    constexpr int VPT = 2, kSize = static_cast<int>(sizeof(T));
+    const LnBwdArgs &a = r.a;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t buf[2][32];
+    __shared__ uint64_t bars[kRing];
+    __shared__ int gave_up;
+    const uint32_t bar0 = smem_u32(bars), stage_bytes = r.dy_span + r.x_span;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < r.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+        gave_up = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const uint8_t *dy0 = static_cast<const uint8_t *>(a.dy), *x0 = static_cast<const uint8_t *>(a.x);
+    const int cols = static_cast<int>(a.cols);
+    auto issue = [&](int64_t row, int s) {
+        const uintptr_t d = reinterpret_cast<uintptr_t>(dy0 + row * a.lddy * kSize);
+        const uintptr_t x = SAVED ? reinterpret_cast<uintptr_t>(a.x8.codes + row * a.x8.ld)
+                                  : reinterpret_cast<uintptr_t>(x0 + row * a.ldx * kSize);
+        const uint32_t dn = (static_cast<uint32_t>(d & 15) + cols * kSize + 15) & ~15u;
+        const uint32_t xn = (static_cast<uint32_t>(x & 15) + cols * (SAVED ? 1 : kSize) + 15) & ~15u;
+        const uint32_t to = smem_u32(ring) + s * stage_bytes;
+        mbar_arrive_expect_tx(bar0 + 8 * s, dn + xn);
+        bulk_load_1d(to, reinterpret_cast<const void *>(d & ~uintptr_t(15)), dn, bar0 + 8 * s);
+        bulk_load_1d(to + r.dy_span, reinterpret_cast<const void *>(x & ~uintptr_t(15)), xn, bar0 + 8 * s);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < r.stages; ++s)
+            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < a.rows)
+                issue(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+    const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
+    auto col = [&](int k) { return static_cast<int>(8 * (threadIdx.x + k * blockDim.x)); };
+    uint64_t dg[VPT][4] = {}, db[VPT][4] = {}, g[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) load_param(a.gamma, a.wtype, col(k), a.cols, g[k]);
+    // what does not go through the ring is fetched a row ahead
+    float mu_next = 0.0f, rs_next = 0.0f, sc_next[VPT] = {};
+    auto fetch = [&](int64_t row) {
+        mu_next = a.mean[row], rs_next = a.rstd[row];
+        if constexpr (SAVED) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k)
+                if (col(k) < cols) sc_next[k] = load_scale(a.x8, row, col(k) >> 7);
+        }
+    };
+    if (blockIdx.x < a.rows) fetch(blockIdx.x);
+    int s = 0, flip = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const uint64_t nmu2 = splat_f32x2(-mu_next), rs2 = splat_f32x2(rs_next);
+        float sc[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) sc[k] = sc_next[k];
+        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (!mbar_wait(bar0 + 8 * s, phase, &gave_up)) {
+            // goes on with what is there, so that every thread still meets every barrier
+            atomicOr(&g_ln_error_flags, kErrWaitTimeout);
+            *static_cast<volatile int *>(&gave_up) = 1;
+        }
+        const uint8_t *stage = ring + s * stage_bytes;
+        const uint32_t doff = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dy0 + row * a.lddy * kSize) & 15);
+        const uint32_t xoff =
+            SAVED ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x0 + row * a.ldx * kSize) & 15);
+        uint64_t dy[VPT][4], x[VPT][4], s1 = 0, s2 = 0;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int left = cols - col(k);
+            if (left > 0) {
+                RawRow8<T> raw;
+                raw.load_shared(stage + col(k) * kSize, doff != 0);
+                raw.get(doff, left, dy[k]);
+                if constexpr (SAVED) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(stage + r.dy_span + col(k));
+                    codes8(w, a.x8.fmt, sc[k], left, x[k]);
+                } else {
+                    raw.load_shared(stage + r.dy_span + col(k) * kSize, xoff != 0);
+                    raw.get(xoff, left, x[k]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dy[k][i] = x[k][i] = 0;
+            }
+            ln_bwd_accumulate(nmu2, rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
+        }
+        const float2 sum = team_sum2<false>(sum2(s1), sum2(s2), buf[flip]);
+        if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
+            issue(row + static_cast<int64_t>(r.stages) * gridDim.x, s);
+        const uint64_t nm1 = splat_f32x2(__fmul_rn(sum.x, ninv_n)), nm2 = splat_f32x2(__fmul_rn(sum.y, ninv_n));
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dy[k][i] = f32x2_mul(f32x2_fma(x[k][i], nm2, f32x2_add(dy[k][i], nm1)), rs2);
+            store_row8<T>(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
+        }
+        if (++s == r.stages) s = 0, phase ^= 1u;
+    }
+    store_part(a, col, dg, db);
+    if (gave_up && threadIdx.x == 0)   // copies still in flight land (bounded) before the CTA exits
+        for (int i = 0; i < r.stages; ++i) {
+            mbar_wait(bar0 + 8 * s, phase, nullptr, 100000000ull);
+            if (++s == r.stages) s = 0, phase ^= 1u;
+        }
+}
+
+// Narrow rows (WARP) and wide ones.  Rows in turn; a thread keeps its columns (as in the forward) and their sums over
 // the CTA's rows.  WIDE: blockIdx.y is a slab of 8 VPT blockDim.x columns and the rows'
 // sums are already there.
 template <typename T, bool SAVED, int VPT, bool WARP, bool WIDE, int VEC>
@@ -462,20 +614,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const 
         }
         for (int64_t c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = sums[c];
     } else {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int64_t c = col(k);
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                float lo, hi;
-                f32x2_unpack(dg[k][i], lo, hi);
-                if (c + 2 * i < a.cols) part[c + 2 * i] = lo;
-                if (c + 2 * i + 1 < a.cols) part[c + 2 * i + 1] = hi;
-                f32x2_unpack(db[k][i], lo, hi);
-                if (c + 2 * i < a.cols) part[a.cols + c + 2 * i] = lo;
-                if (c + 2 * i + 1 < a.cols) part[a.cols + c + 2 * i + 1] = hi;
-            }
-        }
+        store_part(a, col, dg, db);
     }
 }
 
@@ -555,6 +694,28 @@ int64_t bwd_ctas(int64_t rows, int64_t cols) {
     return capped(rows, sms * (threads < 512 ? 512 / threads : 1));
 }
 
+// As many rows in flight as the CTAs of an SM have shared memory for.
+template <typename T, bool SAVED>
+cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
+    constexpr int64_t kSize = sizeof(T), kBytes = 200 << 10;
+    const unsigned threads = row_threads(a.cols, 16);
+    RingArgs r{a, 0, 0, 0};
+    r.dy_span = static_cast<uint32_t>((a.cols * kSize + 15 + 127) / 128 * 128 + 128);
+    r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
+    const int64_t per_sm = threads < 512 ? 512 / threads : 1;
+    const int64_t fit = kBytes / per_sm / (r.dy_span + r.x_span);
+    r.stages = static_cast<int>(fit < kRing ? fit : kRing);
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes));
+    });
+    if (err != cudaSuccess) return err;
+    return launch_pdl(ln_bwd_ring_kernel<T, SAVED>, dim3(grid), dim3(threads),
+                      static_cast<size_t>(r.stages) * (r.dy_span + r.x_span), st, r);
+}
+
 template <typename T, bool SAVED, int VEC>
 cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
     constexpr int VPT = 2;   // 16 columns per thread
@@ -566,8 +727,7 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
         e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, true, false, VEC>, grid, dim3(32 * kWarps),
                        static_cast<size_t>(2 * a.cols * 4), st, a);
     } else if (a.cols <= kBwdWide) {
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, false, false, VEC>, grid,
-                       dim3(row_threads(a.cols, 16)), 0, st, a);
+        e = ln_bwd_ring<T, SAVED>(a, g, st);
     } else {
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * a.cols);
         e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 2 * 152)), dim3(1024), 0, st, a);
@@ -623,6 +783,13 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
     if (dy.type == kTypeBF16) return FP8K_LN_BWD(__nv_bfloat16);
     return FP8K_LN_BWD(__half);
 #undef FP8K_LN_BWD
+}
+
+cudaError_t read_and_clear_ln_error_flag(unsigned *flags) {
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_ln_error_flags, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_ln_error_flags, &zero, sizeof(unsigned));
 }
 
 }  // namespace fp8k
