@@ -350,16 +350,21 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
                         : byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u);
 }
 
+// Scale of row-block rb, column-block cb (rb and the row stride below 2^31).
+__device__ __forceinline__ int64_t scale_at(const BlockView &q, int64_t rb, int64_t cb) {
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(rb)) *
+                                static_cast<uint32_t>(q.ld_s)) + cb;
+}
 __device__ __forceinline__ void store_scale(const BlockView &q, int64_t rb, int64_t cb,
                                             uint32_t byte) {
     if (q.scale_f32)
-        static_cast<float *>(q.scales)[rb * q.ld_s + cb] = scale_value(byte);
+        static_cast<float *>(q.scales)[scale_at(q, rb, cb)] = scale_value(byte);
     else
-        static_cast<uint8_t *>(q.scales)[rb * q.ld_s + cb] = static_cast<uint8_t>(byte);
+        static_cast<uint8_t *>(q.scales)[scale_at(q, rb, cb)] = static_cast<uint8_t>(byte);
 }
 __device__ __forceinline__ float load_scale(const BlockView &q, int64_t rb, int64_t cb) {
-    if (q.scale_f32) return static_cast<const float *>(q.scales)[rb * q.ld_s + cb];
-    return scale_value(static_cast<const uint8_t *>(q.scales)[rb * q.ld_s + cb]);
+    if (q.scale_f32) return static_cast<const float *>(q.scales)[scale_at(q, rb, cb)];
+    return scale_value(static_cast<const uint8_t *>(q.scales)[scale_at(q, rb, cb)]);
 }
 
 // Four FP8 codes (a word) to fp32, exactly (by way of FP16, which holds both formats).
@@ -534,16 +539,36 @@ constexpr int kTileRows = 8;   // rows per warp
 
 using TileValues = uint64_t[kTileRows][2];
 
-// Tile t of a matrix of tiles_r x tiles_c: four rows of tiles are walked side by side,
-// column by column, so that the neighbours whose scales share a word (four tiles
-// down, four tiles across) and whose transposed rows continue each other are in
-// flight together.
-__device__ __forceinline__ void tile_origin(unsigned t, unsigned tiles_r, unsigned tiles_c,
-                                            int64_t &row0, int64_t &col0) {
-    const unsigned group = t / (4 * tiles_c), in = t - group * 4 * tiles_c;
-    const unsigned rows = min(4u, tiles_r - 4 * group);
-    row0 = static_cast<int64_t>(4 * group + in % rows) * kTile;
-    col0 = static_cast<int64_t>(in / rows) * kTile;
+// A CTA's walk over the tiles of a matrix of tiles_r x tiles_c, gridDim.x apart.  Four
+// rows of tiles are walked side by side, column by column, so that the neighbours whose
+// scales share a word (four tiles down, four tiles across) and whose transposed rows
+// continue each other are in flight together.
+struct TileWalk {
+    unsigned t, tiles, group, in, tiles_r, per_group;
+
+    __device__ __forceinline__ TileWalk(unsigned rows, unsigned cols)
+        : t(blockIdx.x), tiles(rows * cols), group(0), in(blockIdx.x), tiles_r(rows), per_group(4 * cols) {
+        wrap();
+    }
+    __device__ __forceinline__ void wrap() {
+        while (in >= per_group) in -= per_group, ++group;
+    }
+    __device__ __forceinline__ bool there() const { return t < tiles; }
+    __device__ __forceinline__ void next() {
+        t += gridDim.x, in += gridDim.x;
+        wrap();
+    }
+    __device__ __forceinline__ void origin(unsigned &row0, unsigned &col0) const {
+        const unsigned rows = min(4u, tiles_r - 4 * group);
+        const unsigned r = rows == 4 ? in & 3 : in % rows, c = rows == 4 ? in >> 2 : in / rows;
+        row0 = (4 * group + r) * kTile;
+        col0 = c * kTile;
+    }
+};
+
+// row * ld, both below 2^31, in one instruction
+__device__ __forceinline__ int64_t row_at(unsigned row, int64_t ld) {
+    return static_cast<int64_t>(static_cast<uint64_t>(row) * static_cast<uint32_t>(ld));
 }
 
 __host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -563,24 +588,24 @@ __device__ __forceinline__ void cp_async_wait() {
 // rows are 16-byte aligned; otherwise elements are copied one by one.
 template <int SIZE>
 __device__ __forceinline__ void fetch_rows(uint32_t dst, const void *base, int64_t ld, int64_t rows,
-                                           int64_t cols, bool vec, int64_t row0, int64_t col0) {
+                                           int64_t cols, bool vec, unsigned row0, unsigned col0) {
     constexpr int kPerRow = kTile * SIZE / 16;   // 16-byte chunks
     constexpr int kElems = 16 / SIZE;
     constexpr int kStep = 32 / kPerRow;          // rows per instruction of the warp
     const int lane = threadIdx.x & 31;
-    const int64_t first = row0 + (threadIdx.x >> 5) * kTileRows;
+    const unsigned first = row0 + (threadIdx.x >> 5) * kTileRows;
     const uint8_t *p = static_cast<const uint8_t *>(base);
     if (vec) {
         const int r0 = lane / kPerRow, k = lane % kPerRow;
-        const int64_t c = col0 + k * kElems;
-        const uint8_t *src = p + ((first + r0) * ld + c) * SIZE;
+        const unsigned c = col0 + k * kElems;
+        const uint8_t *src = p + (row_at(first + r0, ld) + c) * SIZE;
         const uint32_t to = dst + r0 * kTile * SIZE + k * 16;
         if (row0 + kTile <= rows && col0 + kTile <= cols) {
 #pragma unroll
             for (int i = 0; i < kTileRows / kStep; ++i, src += kStep * ld * SIZE)
                 cp_async16(to + i * kStep * kTile * SIZE, src, 16);
         } else {
-            const int64_t left = (cols - c) * SIZE;
+            const int64_t left = (cols - static_cast<int64_t>(c)) * SIZE;
             const uint32_t bytes = left <= 0 ? 0u : left < 16 ? static_cast<uint32_t>(left) : 16u;
 #pragma unroll
             for (int i = 0; i < kTileRows / kStep; ++i, src += kStep * ld * SIZE) {
@@ -592,7 +617,7 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const void *base, int64
         for (int idx = lane; idx < kTileRows * kTile; idx += 32) {
             const int r = idx / kTile, k = idx % kTile;
             const bool in = first + r < rows && col0 + k < cols;
-            const uint8_t *src = p + ((first + r) * ld + col0 + k) * SIZE;
+            const uint8_t *src = p + (row_at(first + r, ld) + col0 + k) * SIZE;
             const uint32_t at = dst + idx * SIZE;
             if constexpr (SIZE == 4) {
                 const uint32_t w = in ? *reinterpret_cast<const uint32_t *>(src) : 0u;
@@ -664,10 +689,10 @@ __device__ __forceinline__ uint32_t tile_max(const TileValues &v, uint32_t *red)
 // Row-major codes and scales of the tile at (row0, col0).  tile_byte < 0: one
 // scale per row; otherwise the whole tile's.
 template <int FMT>
-__device__ __forceinline__ void tile_rows(const TileValues &v, const BlockView &q, int64_t row0,
-                                          int64_t col0, int tile_byte) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t first = row0 + warp * kTileRows, c = col0 + 4 * lane;
+__device__ __forceinline__ void tile_rows(const TileValues &v, const BlockView &q, unsigned row0,
+                                          unsigned col0, int tile_byte) {
+    const int lane = threadIdx.x & 31;
+    const unsigned first = row0 + (threadIdx.x >> 5) * kTileRows, c = col0 + 4 * lane;
     uint32_t byte = static_cast<uint32_t>(tile_byte);   // lane r: of row r
     if (tile_byte < 0) {
         byte = scale_byte<FMT>(row_maxima(v));
@@ -676,16 +701,21 @@ __device__ __forceinline__ void tile_rows(const TileValues &v, const BlockView &
         store_scale(q, row0 / kTile, col0 / kTile, byte);
     }
     const float inv = scale_inverse(byte);
-    const bool whole = row0 + kTile <= q.rows && col0 + kTile <= q.cols;
-    uint8_t *p = q.codes + first * q.ld + c;
+    uint8_t *p = q.codes + row_at(first, q.ld) + c;
+    if (row0 + kTile <= q.rows && col0 + kTile <= q.cols) {
 #pragma unroll
-    for (int r = 0; r < kTileRows; ++r, p += q.ld) {
-        const uint64_t inv2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, inv, r));
-        const uint32_t code = encode4<FMT>(f32x2_mul(v[r][0], inv2), f32x2_mul(v[r][1], inv2));
-        if (whole)
-            *reinterpret_cast<uint32_t *>(p) = code;
-        else if (first + r < q.rows && c < q.cols)
-            store_code_word(p, code, q.cols - c);
+        for (int r = 0; r < kTileRows; ++r, p += q.ld) {
+            const uint64_t inv2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, inv, r));
+            *reinterpret_cast<uint32_t *>(p) =
+                encode4<FMT>(f32x2_mul(v[r][0], inv2), f32x2_mul(v[r][1], inv2));
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < kTileRows; ++r, p += q.ld) {
+            const uint64_t inv2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, inv, r));
+            const uint32_t code = encode4<FMT>(f32x2_mul(v[r][0], inv2), f32x2_mul(v[r][1], inv2));
+            if (first + r < q.rows && c < q.cols) store_code_word(p, code, q.cols - c);
+        }
     }
 }
 
@@ -732,8 +762,8 @@ __device__ __forceinline__ void cols_max(const TileValues &v, ColsSmem &sm) {
 
 // thread c (0 .. 127) of the caller's choice
 template <int FMT>
-__device__ __forceinline__ void cols_scale(int c, ColsSmem &sm, const BlockView &qt, int64_t row0,
-                                           int64_t col0) {
+__device__ __forceinline__ void cols_scale(int c, ColsSmem &sm, const BlockView &qt, unsigned row0,
+                                           unsigned col0) {
     uint32_t m = 0;
 #pragma unroll
     for (int w = 0; w < 16; ++w) m = max(m, sm.max[w][c]);
@@ -764,24 +794,30 @@ __device__ __forceinline__ void cols_codes(const TileValues &v, const ulonglong2
     }
 }
 
-__device__ __forceinline__ void cols_store(const ColsSmem &sm, const BlockView &qt, int64_t row0,
-                                           int64_t col0) {
+__device__ __forceinline__ void cols_store(const ColsSmem &sm, const BlockView &qt, unsigned row0,
+                                           unsigned col0) {
+    constexpr int kRows = kTileThreads / 8;   // of qt per step
     const int c0 = threadIdx.x >> 3, k = threadIdx.x & 7;
-    const int64_t r = row0 + 16 * k;
-    uint8_t *p = qt.codes + (col0 + c0) * qt.ld + r;
+    const unsigned r = row0 + 16 * k;
+    uint8_t *p = qt.codes + row_at(col0 + c0, qt.ld) + r;
+    // steps keep c >> 2 modulo 8 and bit 5 of c as they are
+    static_assert(kRows % 64 == 0, "the swizzle is the same in every step");
+    const uint8_t *from = &sm.codes[c0 * kTile + ((k ^ ((c0 >> 2) & 7)) << 4)];
+    const bool swap = (c0 >> 5) & 1;
     const bool whole = col0 + kTile <= qt.rows && row0 + kTile <= qt.cols;
 #pragma unroll
-    for (int i = 0; i < kTile * 8 / kTileThreads; ++i, p += kTileThreads / 8 * qt.ld) {
-        const int c = c0 + i * (kTileThreads / 8);
-        uint4 u = *reinterpret_cast<const uint4 *>(&sm.codes[c * kTile + ((k ^ ((c >> 2) & 7)) << 4)]);
-        if ((c >> 5) & 1) u = make_uint4(u.z, u.w, u.x, u.y);
-        if (whole || (col0 + c < qt.rows && r + 16 <= qt.cols)) {
+    for (int i = 0; i < kTile / kRows; ++i, p += kRows * qt.ld) {
+        uint4 u = *reinterpret_cast<const uint4 *>(from + i * kRows * kTile);
+        if (swap) u = make_uint4(u.z, u.w, u.x, u.y);
+        const unsigned c = col0 + c0 + i * kRows;
+        if (whole || (c < qt.rows && r + 16 <= qt.cols)) {
             *reinterpret_cast<uint4 *>(p) = u;
-        } else if (col0 + c < qt.rows) {
-            store_code_word(p, u.x, qt.cols - r);
-            store_code_word(p + 4, u.y, qt.cols - r - 4);
-            store_code_word(p + 8, u.z, qt.cols - r - 8);
-            store_code_word(p + 12, u.w, qt.cols - r - 12);
+        } else if (c < qt.rows) {
+            const int64_t left = qt.cols - static_cast<int64_t>(r);
+            store_code_word(p, u.x, left);
+            store_code_word(p + 4, u.y, left - 4);
+            store_code_word(p + 8, u.z, left - 8);
+            store_code_word(p + 12, u.w, left - 12);
         }
     }
 }

@@ -26,7 +26,7 @@ fp8_status view(const char *fn, const fp8_matrix *m, const char *name, bool opti
     if (m->rows < 0 || m->cols < 0 || m->rows >= kMaxDim || m->cols >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: %s: bad size %lld x %lld", fn, name,
                     static_cast<long long>(m->rows), static_cast<long long>(m->cols));
-    if (m->ld < m->cols || m->ld >= (int64_t(1) << 40))
+    if (m->ld < m->cols || m->ld >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: %s: row stride %lld for %lld columns", fn, name,
                     static_cast<long long>(m->ld), static_cast<long long>(m->cols));
     const uintptr_t size = m->dtype == FP8_DTYPE_F32 ? 4 : 2;
@@ -55,10 +55,10 @@ fp8_status view(const char *fn, const fp8_block_tensor *q, const char *name, boo
     if (q->rows < 0 || q->cols < 0 || q->rows >= kMaxDim || q->cols >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: %s: bad size %lld x %lld", fn, name,
                     static_cast<long long>(q->rows), static_cast<long long>(q->cols));
-    if (q->ld < q->cols || q->ld >= (int64_t(1) << 40))
+    if (q->ld < q->cols || q->ld >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: %s: row stride %lld for %lld columns", fn, name,
                     static_cast<long long>(q->ld), static_cast<long long>(q->cols));
-    if (q->ld_scales < (q->cols + 127) / 128 || q->ld_scales >= (int64_t(1) << 33))
+    if (q->ld_scales < (q->cols + 127) / 128 || q->ld_scales >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: %s: %lld scales per row for %lld columns", fn, name,
                     static_cast<long long>(q->ld_scales), static_cast<long long>(q->cols));
     const bool empty = q->rows == 0 || q->cols == 0;

@@ -34,17 +34,19 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 4 ? 1 : 2)
     const int part = (threadIdx.x >> 5) * kTileRows * kTile * static_cast<int>(sizeof(T));
     pdl_wait();
     pdl_trigger();
-    const unsigned tiles = tiles_r * tiles_c;
-    int64_t row0, col0;
-    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
+    TileWalk walk(tiles_r, tiles_c);
+    unsigned row0, col0;
+    walk.origin(row0, col0);
     fetch_rows<sizeof(T)>(smem_u32(sm.in[0]) + part, x, ld, rows, cols, vec, row0, col0);
     cp_async_commit();
     int stage = 0;
-    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, stage ^= 1) {
-        int64_t next_row0 = 0, next_col0 = 0;
+    for (bool more = true; more; stage ^= 1) {
+        unsigned next_row0 = 0, next_col0 = 0;
+        walk.next();
+        more = walk.there();
         __syncwarp();   // the warp has read this part of the other stage
-        if (t + gridDim.x < tiles) {
-            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+        if (more) {
+            walk.origin(next_row0, next_col0);
             fetch_rows<sizeof(T)>(smem_u32(sm.in[stage ^ 1]) + part, x, ld, rows, cols, vec,
                                   next_row0, next_col0);
         }
@@ -123,23 +125,25 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     const int part = warp * kTileRows * kTile;
     pdl_wait();
     pdl_trigger();
-    const unsigned tiles = tiles_r * tiles_c;
-    int64_t row0, col0;
-    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
+    TileWalk walk(tiles_r, tiles_c);
+    unsigned row0, col0;
+    walk.origin(row0, col0);
     fetch_rows<1>(smem_u32(sm.in[0]) + part, x8.codes, x8.ld, x8.rows, up16(x8.cols), true, row0, col0);
     cp_async_commit();
     int stage = 0;
-    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x, stage ^= 1) {
-        int64_t next_row0 = 0, next_col0 = 0;
+    for (bool more = true; more; stage ^= 1) {
+        unsigned next_row0 = 0, next_col0 = 0;
+        walk.next();
+        more = walk.there();
         __syncwarp();
-        if (t + gridDim.x < tiles) {
-            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+        if (more) {
+            walk.origin(next_row0, next_col0);
             fetch_rows<1>(smem_u32(sm.in[stage ^ 1]) + part, x8.codes, x8.ld, x8.rows, up16(x8.cols),
                           true, next_row0, next_col0);
         }
         cp_async_commit();
         // lane r: row r's scale and statistics; the lane's columns' gamma and beta
-        const int64_t row = row0 + warp * kTileRows + lane;
+        const unsigned row = row0 + warp * kTileRows + lane;
         const bool there = lane < kTileRows && row < x8.rows;
         const float sc = there ? load_scale(x8, row, col0 / kTile) : 0.0f;
         const float mu = there ? mean[row] : 0.0f, rs = there ? rstd[row] : 0.0f;
@@ -182,9 +186,15 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 
 // ----------------------------------------------------------------- SwiGLU --
 
-// 1 / (1 + exp(-x)) to a few units in the last place: 0 for -inf, 1 for +inf.
+// 1 / (1 + exp(-x)) to a few units in the last place and |x| 2^-24: 0 for -inf, 1 for
+// +inf.  The instructions that flush subnormal numbers serve here: exp(-x) below 2^-126
+// is nothing beside 1, and a result below 2^-126 is far below any 8-bit step.  (The
+// general ones come with 7 more instructions per value.)
 __device__ __forceinline__ float sigmoid(float x) {
-    return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x)));
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x, -1.44269504f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
+    return s;
 }
 
 // 16 lanes per block of 128 columns of a row, two blocks per warp.
@@ -248,29 +258,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kStages = SwigluSmem<T>::kStages;
     pdl_wait();
     pdl_trigger();
-    const unsigned tiles = tiles_r * tiles_c;
-    int64_t row0 = 0, col0 = 0;
-    auto fetch = [&](int stage, int64_t r0, int64_t c0) {
+    TileWalk walk(tiles_r, tiles_c);
+    unsigned row0, col0;
+    walk.origin(row0, col0);
+    auto fetch = [&](int stage, unsigned r0, unsigned c0) {
         fetch_rows<kSize>(smem_u32(sm.da[stage]) + part * kSize, da, ld, M, F, vec, r0, c0);
         fetch_rows<1>(smem_u32(sm.gate[stage]) + part, h8.codes, h8.ld, M, F, true, r0, c0);
         fetch_rows<1>(smem_u32(sm.value[stage]) + part, h8.codes + F, h8.ld, M, F, true, r0, c0);
     };
     // lanes 0 .. 7: the rows' scales of gate; lanes 8 .. 15: of value
-    auto fetch_scale = [&](int64_t r0, int64_t c0) {
-        const int64_t row = r0 + warp * kTileRows + (lane & 7);
+    auto fetch_scale = [&](unsigned r0, unsigned c0) {
+        const unsigned row = r0 + warp * kTileRows + (lane & 7);
         return lane < 16 && row < M ? load_scale(h8, row, (c0 + (lane < 8 ? 0 : F)) / kTile) : 0.0f;
     };
-    tile_origin(blockIdx.x, tiles_r, tiles_c, row0, col0);
     fetch(0, row0, col0);
     cp_async_commit();
     float sc_next = fetch_scale(row0, col0);
     int stage = 0;
-    for (unsigned t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (bool more = true; more;) {
         const float sc = sc_next;
-        int64_t next_row0 = 0, next_col0 = 0;
-        const bool more = t + gridDim.x < tiles;
+        unsigned next_row0 = 0, next_col0 = 0;
+        walk.next();
+        more = walk.there();
         if (more) {
-            tile_origin(t + gridDim.x, tiles_r, tiles_c, next_row0, next_col0);
+            walk.origin(next_row0, next_col0);
             sc_next = fetch_scale(next_row0, next_col0);
         }
         if constexpr (kStages == 2) {
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (threadIdx.x < kTile) {
             if (t_dh) cols_scale<FMT>(c, sm.cols[0], dh8t, row0, col0);
         } else if (threadIdx.x < 2 * kTile) {
-            if (t_dh) cols_scale<FMT>(c, sm.cols[1], dh8t, row0, F + col0);
+            if (t_dh) cols_scale<FMT>(c, sm.cols[1], dh8t, row0, static_cast<unsigned>(F) + col0);
         } else if (threadIdx.x < 3 * kTile) {
             if (t_a) cols_scale<AFMT>(c, sm.cols[2], a8t, row0, col0);
         }
@@ -330,12 +341,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (t_a) cols_codes<AFMT>(a, cols_inv(sm.cols[2]), sm.cols[2]);
         if (dh8.codes != nullptr) {
             tile_rows<FMT>(dg, dh8, row0, col0, -1);
-            tile_rows<FMT>(du, dh8, row0, F + col0, -1);
+            tile_rows<FMT>(du, dh8, row0, static_cast<unsigned>(F) + col0, -1);
         }
         __syncthreads();
         if (t_dh) {
             cols_store(sm.cols[0], dh8t, row0, col0);
-            cols_store(sm.cols[1], dh8t, row0, F + col0);
+            cols_store(sm.cols[1], dh8t, row0, static_cast<unsigned>(F) + col0);
         }
         if (t_a) cols_store(sm.cols[2], a8t, row0, col0);
         row0 = next_row0, col0 = next_col0;

@@ -472,7 +472,7 @@ fp8_status fp8_linear_bwd_noalloc(const void *dY, int64_t M, int64_t N, int64_t 
  *           saturate to +-fmax, NaN stays NaN, the sign of zero is kept.
  * Sizes are free (odd ones too; 0 rows or columns: nothing is done).
  * Everything is dense along the columns; `ld` is the distance between rows
- * in elements. */
+ * in elements.  Rows, columns and strides are below 2^31. */
 
 typedef enum { FP8_DTYPE_F32 = 0, FP8_DTYPE_BF16 = 1, FP8_DTYPE_F16 = 2 } fp8_dtype;
 
