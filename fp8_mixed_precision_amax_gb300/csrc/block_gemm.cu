@@ -36,55 +36,47 @@ __device__ __forceinline__ void raise_error(volatile int *abort_flag) {
     *abort_flag = 1;
 }
 
-// One row's scales along K, fetched four k-blocks ahead: a word of E8M0 bytes or four
-// floats at a time.  (Fetched one block ahead, each block waited for L2: 3500 cycles
-// per block of the f32 kernel instead of the 512 of its MMAs.)
-template <bool MAY_E8M0>
+// One row's float scales along K, fetched four k-blocks ahead, four at a time.
+// (Fetched one block ahead, each block waited for L2.)
 struct ScaleStream {
-    const uint8_t *row;
+    const float *row;
     int num_kb;
-    bool f32, vec;      // vec: four floats are one 16-byte load
-    uint32_t raw[4];    // the next group
-    float cur[4];       // scales from the current k-block on
+    bool vec;        // four floats are one 16-byte load
+    float ahead[4];  // the next group
+    float cur[4];    // scales from the current k-block on
 
     __device__ __forceinline__ void fetch(int group) {
         const int kb = 4 * group;
         if (kb >= num_kb) return;
-        if (MAY_E8M0 && !f32) {
-            raw[0] = *reinterpret_cast<const uint32_t *>(row + kb);
-        } else if (vec) {
-            const uint4 u = reinterpret_cast<const uint4 *>(row)[group];
-            raw[0] = u.x, raw[1] = u.y, raw[2] = u.z, raw[3] = u.w;
+        if (vec) {
+            const float4 u = reinterpret_cast<const float4 *>(row)[group];
+            ahead[0] = u.x, ahead[1] = u.y, ahead[2] = u.z, ahead[3] = u.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                raw[i] = kb + i < num_kb ? reinterpret_cast<const uint32_t *>(row)[kb + i] : 0u;
+            for (int i = 0; i < 4; ++i) ahead[i] = kb + i < num_kb ? row[kb + i] : 0.0f;
         }
     }
-    __device__ __forceinline__ void decode() {
+    __device__ __forceinline__ void take() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            cur[i] = MAY_E8M0 && !f32 ? scale_value(raw[0] >> (8 * i) & 0xFFu) : __uint_as_float(raw[i]);
+        for (int i = 0; i < 4; ++i) cur[i] = ahead[i];
     }
-    // from k-block kb0 on (rows of E8M0 scales are 4-byte aligned and whole words)
+    __device__ __forceinline__ void shift() { cur[0] = cur[1], cur[1] = cur[2], cur[2] = cur[3]; }
+    // from k-block kb0 on, up to `blocks`
     __device__ __forceinline__ void start(const BlockView &v, int64_t r, int kb0, int blocks) {
-        const int64_t at = (v.block_rows == 1 ? r : r >> 7) * v.ld_s;
-        f32 = !MAY_E8M0 || v.scale_f32 != 0;
-        row = static_cast<const uint8_t *>(v.scales) + (f32 ? 4 * at : at);
+        row = static_cast<const float *>(v.scales) + (v.block_rows == 1 ? r : r >> 7) * v.ld_s;
         vec = ((reinterpret_cast<uintptr_t>(v.scales) | static_cast<uintptr_t>(4 * v.ld_s)) & 15u) == 0;
         num_kb = blocks;
         fetch(kb0 >> 2);
         if (kb0 & 3) {
-            decode();
+            take();
             for (int i = 0; i < (kb0 & 3); ++i) shift();
             fetch((kb0 >> 2) + 1);
         }
     }
-    __device__ __forceinline__ void shift() { cur[0] = cur[1], cur[1] = cur[2], cur[2] = cur[3]; }
     // the scale of k-block kb; called for each in turn
     __device__ __forceinline__ float next(int kb) {
         if ((kb & 3) == 0) {
-            decode();
+            take();
             fetch((kb >> 2) + 1);
         }
         const float s = cur[0];
@@ -590,7 +582,7 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
             const int64_t crow0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM;
             const int64_t col0 = static_cast<int64_t>(nb) * BN;
             // rows and columns past the end repeat the last one
-            ScaleStream<false> fa, fb;
+            ScaleStream fa, fb;
             if (et < BM) fa.start(a.A, min(crow0 + et, a.M - 1), 0, a.num_kb);
             fb.start(a.B, min(col0 + et, a.N - 1), 0, a.num_kb);
             uint64_t sum[4][16];   // [row lane / 4 + 8 i][columns 8 j + 2 (lane mod 4), + 1]
@@ -604,12 +596,12 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                     // the scales of four k-blocks; they are written over eight blocks
                     // later, with a barrier in between
                     if (et < BM) {
-                        fa.decode();
+                        fa.take();
                         fa.fetch((kb >> 2) + 1);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sas[((kb & 7) + i) * BM + et] = fa.cur[i];
                     }
-                    fb.decode();
+                    fb.take();
                     fb.fetch((kb >> 2) + 1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sbs[((kb & 7) + i) * FS_SB + own_col] = fb.cur[i];
@@ -714,18 +706,30 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
 // ----------------------------------------------------------------- few kernel --
 // A CTA computes 128 rows of B (weights) times NT rows of A (tokens) over its share
 // of the k-blocks; gridDim.x CTAs, a cluster, share a tile's k-blocks.  Warps: 0 TMA,
-// 1 MMA, 2-5 sums as in the f32 kernel (thread = weight row, one sum per token).
+// 1 MMA, the others (thread = weight row) by the scales' type:
+//   E8M0 (MX): four warps bring the scales to TMEM as in the mx kernel, and the sums
+//        back from it at the end;
+//   float: as in the f32 kernel, each warp with one lane quarter and, of eight warps,
+//        half of the tokens (16 tokens: four warps and all of them).  The accumulators
+//        take half the TMEM, so that the MMAs run ahead of the sums.
 // Shared memory allows two CTAs per SM, so one's start and end overlap the other's loads.
 
-template <int NT>
+template <int NT, bool MX>
 struct Few {
     static constexpr int STAGES = NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
     static constexpr int X_STAGE = NT * BK;
-    static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
-    static constexpr int TMEM = 2 * NT;   // columns, a power of two of at least 32
+    static constexpr int ACCS = MX ? 1 : NT <= 32 ? 8 : 256 / NT;
+    static constexpr int WARPS = MX || NT <= 16 ? 4 : 8;   // beside TMA and MMA
+    static constexpr int THREADS = 64 + 32 * WARPS;
+    static constexpr int COLS = NT * 4 / WARPS;            // tokens per warp
+    static constexpr int SF = NT;                          // MX: first TMEM column of the scales,
+    static constexpr int SF_STRIDE = 8;                    // per stage 4 for weights, 4 for tokens
+    static constexpr int TMEM = MX ? 2 * NT : ACCS * NT;   // columns, a power of two of at least 32
+    static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 4 + 1;
     static constexpr size_t SMEM =
         1024 + STAGES * (HALF + X_STAGE) + 2 * NT * 4 + NUM_BARS * 8 + 16;
     static_assert(STAGES * (HALF + X_STAGE) >= NT * 128 * 4, "the sums fit where the tiles were");
+    static_assert(!MX || SF + 2 * SF_STRIDE <= TMEM, "the scales fit");
 };
 
 struct FewArgs {
@@ -743,9 +747,10 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
     return v;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_constant__ FewArgs a) {
-    using C = Few<NT>;
+template <int NT, bool MX>
+__global__ void __launch_bounds__(Few<NT, MX>::THREADS)
+    block_gemm_few_kernel(const __grid_constant__ FewArgs a) {
+    using C = Few<NT, MX>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
     const uint32_t sW = smem_u32(smem), sX = sW + C::STAGES * HALF;
@@ -756,7 +761,8 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
-    const uint32_t accf0 = empty0 + 8 * C::STAGES, acce0 = accf0 + 16, drain = acce0 + 16;
+    const uint32_t accf0 = empty0 + 8 * C::STAGES, acce0 = accf0 + 8 * C::ACCS;
+    const uint32_t sff0 = acce0 + 8 * C::ACCS, sfe0 = sff0 + 16, drain = sfe0 + 16;
     const int splits = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
     const int kb0 = static_cast<int>(static_cast<int64_t>(a.num_kb) * split / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(a.num_kb) * (split + 1) / splits);
@@ -768,9 +774,13 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < C::ACCS; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, 4);
+            mbar_init(acce0 + 8 * b, C::WARPS);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sff0 + 8 * b, 4);
+            mbar_init(sfe0 + 8 * b, 1);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -789,7 +799,8 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
     pdl_wait();
     pdl_trigger();
 
-    float sum[NT];
+    const int q = warp & 3, part = (warp - 2) >> 2;   // lane quarter, share of the tokens
+    uint64_t sum[C::COLS / 2] = {};                   // pairs of tokens
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
@@ -823,11 +834,14 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
+            int stage = 0, acc = 0, sf = 0;
+            uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
             bool any = false;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) ||
+                // MX: a stage of scales holds those of four k-blocks, from a multiple of 4 on
+                const bool first = MX ? kb == kb0 || (kb & 3) == 0 : true;
+                const uint32_t ready = MX ? sff0 + 8 * sf : acce0 + 8 * acc;
+                if ((first && !mbar_wait(ready, MX ? sf_phase : acc_phase ^ 1u, abort_flag)) ||
                     !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
                     raise_error(abort_flag);
                     ok = false;
@@ -835,36 +849,115 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
                 }
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < BK / 32; ++k)
-                    mma_f8f6f4(tmem + acc * NT, smem_desc_sw128(sW + stage * HALF + 32 * k),
-                               smem_desc_sw128(sX + stage * C::X_STAGE + 32 * k), a.idesc, k != 0);
+                for (int k = 0; k < BK / 32; ++k) {
+                    const uint64_t wd = smem_desc_sw128(sW + stage * HALF + 32 * k);
+                    const uint64_t xd = smem_desc_sw128(sX + stage * C::X_STAGE + 32 * k);
+                    if constexpr (MX) {
+                        const uint32_t id = static_cast<uint32_t>(kb & 3);
+                        mma_mxf8(tmem, wd, xd, a.idesc | id << 4 | id << 29,
+                                 tmem + C::SF + sf * C::SF_STRIDE, tmem + C::SF + sf * C::SF_STRIDE + 4,
+                                 kb != kb0 || k != 0);
+                    } else {
+                        mma_f8f6f4(tmem + acc * NT, wd, xd, a.idesc, k != 0);
+                    }
+                }
                 mma_commit(empty0 + 8 * stage);
-                mma_commit(accf0 + 8 * acc);
                 any = true;
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
+                if constexpr (MX) {
+                    if ((kb & 3) == 3) {
+                        mma_commit(sfe0 + 8 * sf);
+                        if (++sf == 2) {
+                            sf = 0;
+                            sf_phase ^= 1u;
+                        }
+                    }
+                } else {
+                    mma_commit(accf0 + 8 * acc);
+                    if (++acc == C::ACCS) {
+                        acc = 0;
+                        acc_phase ^= 1u;
+                    }
                 }
             }
+            if (MX && ok) mma_commit(accf0);
             if (!ok && any) {
                 mma_commit(drain);
                 mbar_wait(drain, 0, nullptr, 100000000ull);
             }
         }
+    } else if constexpr (MX) {
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        // rows past the end repeat the last one
+        const uint8_t *pw[4], *px[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t w = min(static_cast<int64_t>(wrow0) + 32 * j + lane, a.N - 1);
+            const int64_t x = min(static_cast<int64_t>(xrow0) + 32 * j + lane, a.M - 1);
+            pw[j] = static_cast<const uint8_t *>(a.W.scales) + (a.W.block_rows == 1 ? w : w >> 7) * a.W.ld_s;
+            px[j] = static_cast<const uint8_t *>(a.X.scales) + (a.X.block_rows == 1 ? x : x >> 7) * a.X.ld_s;
+        }
+        uint32_t ww[4], wx[4] = {0, 0, 0, 0};
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ww[j] = *reinterpret_cast<const uint32_t *>(pw[j] + kb);
+                if (32 * j < NT) wx[j] = *reinterpret_cast<const uint32_t *>(px[j] + kb);
+            }
+        };
+        int sf = 0;
+        uint32_t sf_phase = 0;
+        if (kb0 < kb1) fetch(kb0 & ~3);
+        for (int kb = kb0 & ~3; kb < kb1; kb += 4) {
+            const uint32_t sw[4] = {ww[0], ww[1], ww[2], ww[3]}, sx[4] = {wx[0], wx[1], wx[2], wx[3]};
+            if (kb + 4 < kb1) fetch(kb + 4);
+            const bool got = mbar_wait(sfe0 + 8 * sf, sf_phase ^ 1u, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t at = lanes + C::SF + sf * C::SF_STRIDE;
+            tmem_store_4cols(at, sw[0], sw[1], sw[2], sw[3]);
+            tmem_store_4cols(at + 4, sx[0], sx[1], sx[2], sx[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sff0 + 8 * sf);
+            if (++sf == 2) {
+                sf = 0;
+                sf_phase ^= 1u;
+            }
+        }
+        const bool got = kb0 < kb1 && ok && mbar_wait(accf0, 0, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+            if (lane == 0 && kb0 < kb1) raise_error(abort_flag);
+            ok = false;
+        }
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < NT / 16; ++h) {
+                uint32_t r[16];
+                tmem_load_16cols(lanes + h * 16, r);
+                tmem_wait_16cols(r);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    sum[8 * h + c] = f32x2_pack(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+            }
+            tc_fence_before();
+        }
     } else {
-        const int q = warp & 3;
         const int et = threadIdx.x - 64;
         const int64_t w = min(static_cast<int64_t>(wrow0) + q * 32 + lane, a.N - 1);
         const int64_t x = min(static_cast<int64_t>(xrow0) + et, a.M - 1);
         int acc = 0;
         uint32_t acc_phase = 0;
-#pragma unroll
-        for (int c = 0; c < NT; ++c) sum[c] = 0.0f;
-        ScaleStream<true> fw, fx;
+        ScaleStream fw, fx;
         fw.start(a.W, w, kb0, kb1);
         fx.start(a.X, x, kb0, kb1);
 #pragma unroll 1
@@ -873,7 +966,7 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
             float *sx = sxs + ((kb - kb0) & 1) * NT;
             if (et < NT) sx[et] = sx_own;
             // a buffer is written again only after the next block's barrier
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * C::WARPS) : "memory");
             const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got)) {
                 if (lane == 0) raise_error(abort_flag);
@@ -881,59 +974,94 @@ __global__ void __launch_bounds__(192) block_gemm_few_kernel(const __grid_consta
             }
             if (ok) {
                 tc_fence_after();
-                const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * NT;
+                const uint32_t t =
+                    tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + part * C::COLS;
+                uint32_t r[2][16];
+                tmem_load_16cols(t, r[0]);
+                const uint64_t sw2 = splat_f32x2(sw);
 #pragma unroll
-                for (int h = 0; h < NT / 16; ++h) {
-                    uint32_t r[16];
-                    tmem_load_16cols(t + h * 16, r);
-                    tmem_wait_16cols(r);
-                    if (h == NT / 16 - 1) {
+                for (int h = 0; h < C::COLS / 16; ++h) {
+                    tmem_wait_16cols(r[h & 1]);
+                    if (h < C::COLS / 16 - 1) {
+                        tmem_load_16cols(t + (h + 1) * 16, r[(h + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(acce0 + 8 * acc);
                     }
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        sum[16 * h + c] = __fmaf_rn(__uint_as_float(r[c]), __fmul_rn(sw, sx[16 * h + c]),
-                                                    sum[16 * h + c]);
+                    for (int c = 0; c < 4; ++c) {
+                        const ulonglong2 s2 = *reinterpret_cast<const ulonglong2 *>(
+                            sx + part * C::COLS + 16 * h + 4 * c);
+                        const uint32_t *v = r[h & 1] + 4 * c;
+                        uint64_t *to = sum + 8 * h + 2 * c;
+                        to[0] = f32x2_fma(f32x2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                          f32x2_mul(sw2, s2.x), to[0]);
+                        to[1] = f32x2_fma(f32x2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                          f32x2_mul(sw2, s2.y), to[1]);
+                    }
                 }
             }
-            if (++acc == 2) {
+            if (++acc == C::ACCS) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
         }
     }
-    const int64_t tokens = a.M - xrow0 < NT ? a.M - xrow0 : NT;
-    const int64_t n = static_cast<int64_t>(wrow0) + (warp & 3) * 32 + lane;
+    const int tokens = a.M - xrow0 < NT ? static_cast<int>(a.M - xrow0) : NT;
+    const int r = q * 32 + lane;
+    const int64_t n = static_cast<int64_t>(wrow0) + r;
     __nv_bfloat16 *d = a.D + static_cast<int64_t>(xrow0) * a.ldd + n;
     if (splits == 1) {
         if (warp >= 2 && ok && n < a.N) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-                if (c < tokens) d[c * a.ldd] = __float2bfloat16_rn(sum[c]);
+            for (int c = 0; c < C::COLS / 2; ++c) {
+                const int token = part * C::COLS + 2 * c;
+                float lo, hi;
+                f32x2_unpack(sum[c], lo, hi);
+                if (token < tokens) d[token * a.ldd] = __float2bfloat16_rn(lo);
+                if (token + 1 < tokens) d[(token + 1) * a.ldd] = __float2bfloat16_rn(hi);
+            }
         }
     } else {
         // sums [token][weight row] in the shared memory that held the tiles: all MMAs
         // that read it are done
         float *red = reinterpret_cast<float *>(smem);
         __syncthreads();
-        const int r = (warp & 3) * 32 + lane;
         if (warp >= 2) {
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-                if (c < tokens) red[c * 128 + r] = sum[c];
+            for (int c = 0; c < C::COLS / 2; ++c) {
+                const int token = part * C::COLS + 2 * c;
+                float lo, hi;
+                f32x2_unpack(sum[c], lo, hi);
+                if (token < tokens) red[token * 128 + r] = lo;
+                if (token + 1 < tokens) red[(token + 1) * 128 + r] = hi;
+            }
         }
         __syncwarp();
         cluster_sync();
-        // this CTA joins every splits-th token, in the order of the splits
+        // this CTA joins every splits-th token, in the order of the splits; eight at a
+        // time, so that their reads from the other SMs are under way together
         if (warp >= 2 && n < a.N) {
-            for (int c = split; c < tokens; c += splits) {
-                const uint32_t at = smem_u32(red + c * 128 + r);
-                float s = 0.0f;
-                for (int k = 0; k < splits; ++k)
-                    s = __fadd_rn(s, ld_shared_cluster(mapa_shared(at, static_cast<uint32_t>(k))));
-                d[c * a.ldd] = __float2bfloat16_rn(s);
+            constexpr int U = 8;
+            const int step = splits * (C::WARPS / 4);
+            for (int c0 = split + part * splits; c0 < tokens; c0 += U * step) {
+                float s[U] = {};
+                for (int k = 0; k < splits; ++k) {
+                    float v[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        v[u] = c0 + u * step < tokens
+                                   ? ld_shared_cluster(mapa_shared(
+                                         smem_u32(red + (c0 + u * step) * 128 + r), static_cast<uint32_t>(k)))
+                                   : 0.0f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) s[u] = __fadd_rn(s[u], v[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * step < tokens)
+                        d[(c0 + u * step) * a.ldd] = __float2bfloat16_rn(s[u]);
             }
         }
         __syncwarp();
@@ -995,10 +1123,10 @@ PairKernel g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
 PairKernel g_f32_tiles{block_gemm_f32_kernel<false>, FS_THREADS, FS_SMEM};
 PairKernel g_f32_rows{block_gemm_f32_kernel<true>, FS_THREADS, FS_SMEM};
 
-template <int NT>
+template <int NT, bool MX>
 cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D, int sm_count,
                        cudaStream_t st, const char **what) {
-    using C = Few<NT>;
+    using C = Few<NT, MX>;
     FewArgs a;
     if (!encode_tmap_2d(&a.mapW, B.codes, false, B.cols, B.rows, BK, 128, true, B.ld) ||
         !encode_tmap_2d(&a.mapX, A.codes, false, A.cols, A.rows, BK, NT, true, A.ld)) {
@@ -1012,25 +1140,41 @@ cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D,
     a.N = D.cols;
     a.ldd = D.ld;
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
-    a.idesc = idesc_f8(static_cast<uint32_t>(B.fmt), static_cast<uint32_t>(A.fmt), 128, NT);
+    const uint32_t fw = static_cast<uint32_t>(B.fmt), fx = static_cast<uint32_t>(A.fmt);
+    a.idesc = MX ? idesc_mxf8(fw, fx, 128, NT, 0) : idesc_f8(fw, fx, 128, NT);
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(block_gemm_few_kernel<NT>,
+        attr_err = cudaFuncSetAttribute(block_gemm_few_kernel<NT, MX>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(C::SMEM));
     });
     if (attr_err != cudaSuccess) return attr_err;
     const int64_t tw = (D.cols + 127) / 128, tx = (D.rows + NT - 1) / NT;
-    // two CTAs per SM where the k-blocks allow it, at least two k-blocks each
-    int splits = 1;
-    while (splits < 8 && tw * tx * splits * 2 <= 2 * sm_count && a.num_kb >= splits * 4) splits *= 2;
+    // as many CTAs as run at once, two per SM, with at least two k-blocks each
+    int64_t splits = 2 * sm_count / (tw * tx);
+    if (splits > a.num_kb / 2) splits = a.num_kb / 2;
+    if (splits > 8) splits = 8;
+    if (splits < 1) splits = 1;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg =
-        cluster_config(dim3(splits, static_cast<unsigned>(tw), static_cast<unsigned>(tx)), 192, C::SMEM,
-                       splits, attr, st);
-    return cudaLaunchKernelEx(&cfg, block_gemm_few_kernel<NT>, a);
+        cluster_config(dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tw), static_cast<unsigned>(tx)),
+                       C::THREADS, C::SMEM,
+                       static_cast<int>(splits), attr, st);
+    return cudaLaunchKernelEx(&cfg, block_gemm_few_kernel<NT, MX>, a);
 }
+
+template <bool MX>
+cudaError_t launch_few_any(const BlockView &A, const BlockView &B, const MatView &D, int sm_count,
+                           cudaStream_t st, const char **what) {
+    if (D.rows <= 16) return launch_few<16, MX>(A, B, D, sm_count, st, what);
+    if (D.rows <= 32) return launch_few<32, MX>(A, B, D, sm_count, st, what);
+    if (D.rows <= 64) return launch_few<64, MX>(A, B, D, sm_count, st, what);
+    return launch_few<128, MX>(A, B, D, sm_count, st, what);
+}
+
+constexpr int64_t kFewRows = 128;   // the few kernel up to this many rows of A,
+constexpr int64_t kFewTiles = 38;   // or up to this many 256 x 256 tiles
 
 }  // namespace
 
@@ -1040,14 +1184,12 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     if (A.cols == 0) return cudaMemset2DAsync(D.data, D.ld * 2, 0, D.cols * 2, D.rows, st);
     const bool mx = A.scale_f32 == 0;
     PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
-    if (D.rows > 128) pk.init(sm_count);
-    if (D.rows <= 128 || pk.err != cudaSuccess || pk.slots < 1) {
-        if (pk.err != cudaSuccess) return pk.err;
-        if (D.rows <= 16) return launch_few<16>(A, B, D, sm_count, st, what);
-        if (D.rows <= 32) return launch_few<32>(A, B, D, sm_count, st, what);
-        if (D.rows <= 64) return launch_few<64>(A, B, D, sm_count, st, what);
-        return launch_few<128>(A, B, D, sm_count, st, what);
-    }
+    const int64_t pair_tiles = ((D.rows + 255) / 256) * ((D.cols + 255) / 256);
+    if (D.rows > kFewRows && pair_tiles > kFewTiles) pk.init(sm_count);
+    if (pk.err != cudaSuccess) return pk.err;
+    if (D.rows <= kFewRows || pair_tiles <= kFewTiles || pk.slots < 1)
+        return mx ? launch_few_any<true>(A, B, D, sm_count, st, what)
+                  : launch_few_any<false>(A, B, D, sm_count, st, what);
     PairArgs a;
     a.tma_d = (reinterpret_cast<uintptr_t>(D.data) & 15u) == 0 && D.ld % 8 == 0;
     a.pairs_d = (reinterpret_cast<uintptr_t>(D.data) & 3u) == 0 && D.ld % 2 == 0;
