@@ -710,15 +710,20 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
 //   E8M0 (MX): four warps bring the scales to TMEM as in the mx kernel, and the sums
 //        back from it at the end;
 //   float: as in the f32 kernel, each warp with one lane quarter and, of eight warps,
-//        half of the tokens (16 tokens: four warps and all of them).  The accumulators
-//        take half the TMEM, so that the MMAs run ahead of the sums.
-// Shared memory allows two CTAs per SM, so one's start and end overlap the other's loads.
+//        half of the tokens (16 tokens: four warps and all of them), with several
+//        accumulators, so that the MMAs run ahead of the sums.
+// Shared memory and TMEM allow two CTAs per SM, so that one's start and end overlap the
+// other's loads.  One SM alone reads some 65 GB/s whatever its ring holds, so K is split
+// until all SMs read: 1 x 4096 x 4096 takes 13.4 us unsplit and 6.8 in 8 parts.  The
+// join costs more with more tokens: 128 x 11008 x 4096 takes 18.9 us unsplit and
+// 19.1 in 3 parts, and a tile of 128 tokens is not split.
 
 template <int NT, bool MX>
 struct Few {
-    static constexpr int STAGES = NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
     static constexpr int X_STAGE = NT * BK;
+    static constexpr int STAGES = NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
     static constexpr int ACCS = MX ? 1 : NT <= 32 ? 8 : 256 / NT;
+    static constexpr int MOST_SPLITS = 8;
     static constexpr int WARPS = MX || NT <= 16 ? 4 : 8;   // beside TMA and MMA
     static constexpr int THREADS = 64 + 32 * WARPS;
     static constexpr int COLS = NT * 4 / WARPS;            // tokens per warp
@@ -748,7 +753,7 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
 }
 
 template <int NT, bool MX>
-__global__ void __launch_bounds__(Few<NT, MX>::THREADS)
+__global__ void __launch_bounds__(Few<NT, MX>::THREADS, NT <= 64 ? 2 : 1)
     block_gemm_few_kernel(const __grid_constant__ FewArgs a) {
     using C = Few<NT, MX>;
     extern __shared__ uint8_t smem_raw[];
@@ -803,91 +808,89 @@ __global__ void __launch_bounds__(Few<NT, MX>::THREADS)
     uint64_t sum[C::COLS / 2] = {};                   // pairs of tokens
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
-                    raise_error(abort_flag);
-                    ok = false;
-                    break;
-                }
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag))) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
                 const uint32_t fb = full0 + 8 * stage;
                 mbar_arrive_expect_tx(fb, HALF + C::X_STAGE);
                 tma_load_2d(sW + stage * HALF, &a.mapW, fb, kb * BK, wrow0);
                 tma_load_2d(sX + stage * C::X_STAGE, &a.mapX, fb, kb * BK, xrow0);
-                ++issued;
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
-            if (!ok) {
-                // let the copies already issued land before the CTA exits
-                for (int i = 0; i < C::STAGES && issued > 0; ++i, --issued) {
-                    stage = stage == 0 ? C::STAGES - 1 : stage - 1;
-                    if (stage == C::STAGES - 1) phase ^= 1u;
-                    mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
-                }
+            __syncwarp();
+            ++issued;
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {
+            // let the copies already issued land before the CTA exits
+            for (int i = 0; i < C::STAGES && issued > 0; ++i, --issued) {
+                stage = stage == 0 ? C::STAGES - 1 : stage - 1;
+                if (stage == C::STAGES - 1) phase ^= 1u;
+                mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0, acc = 0, sf = 0;
-            uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
-            bool any = false;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                // MX: a stage of scales holds those of four k-blocks, from a multiple of 4 on
-                const bool first = MX ? kb == kb0 || (kb & 3) == 0 : true;
-                const uint32_t ready = MX ? sff0 + 8 * sf : acce0 + 8 * acc;
-                if ((first && !mbar_wait(ready, MX ? sf_phase : acc_phase ^ 1u, abort_flag)) ||
-                    !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
-                    raise_error(abort_flag);
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        int stage = 0, acc = 0, sf = 0;
+        uint32_t phase = 0, acc_phase = 0, sf_phase = 0;
+        bool any = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            // MX: a stage of scales holds those of four k-blocks, from a multiple of 4 on
+            const bool first = MX ? kb == kb0 || (kb & 3) == 0 : true;
+            const uint32_t ready = MX ? sff0 + 8 * sf : acce0 + 8 * acc;
+            const bool go = (!first || mbar_wait(ready, MX ? sf_phase : acc_phase ^ 1u, abort_flag)) &&
+                            mbar_wait(full0 + 8 * stage, phase, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, go)) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t wd = smem_desc_sw128(sW + stage * HALF);
+                const uint64_t xd = smem_desc_sw128(sX + stage * C::X_STAGE);
 #pragma unroll
-                for (int k = 0; k < BK / 32; ++k) {
-                    const uint64_t wd = smem_desc_sw128(sW + stage * HALF + 32 * k);
-                    const uint64_t xd = smem_desc_sw128(sX + stage * C::X_STAGE + 32 * k);
+                for (int k = 0; k < BK / 32; ++k) {   // 32 bytes on: 2 in the descriptors' unit
                     if constexpr (MX) {
                         const uint32_t id = static_cast<uint32_t>(kb & 3);
-                        mma_mxf8(tmem, wd, xd, a.idesc | id << 4 | id << 29,
+                        mma_mxf8(tmem, wd + 2 * k, xd + 2 * k, a.idesc | id << 4 | id << 29,
                                  tmem + C::SF + sf * C::SF_STRIDE, tmem + C::SF + sf * C::SF_STRIDE + 4,
                                  kb != kb0 || k != 0);
                     } else {
-                        mma_f8f6f4(tmem + acc * NT, wd, xd, a.idesc, k != 0);
+                        mma_f8f6f4(tmem + acc * NT, wd + 2 * k, xd + 2 * k, a.idesc, k != 0);
                     }
                 }
                 mma_commit(empty0 + 8 * stage);
-                any = true;
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                if constexpr (MX) {
-                    if ((kb & 3) == 3) {
-                        mma_commit(sfe0 + 8 * sf);
-                        if (++sf == 2) {
-                            sf = 0;
-                            sf_phase ^= 1u;
-                        }
-                    }
-                } else {
-                    mma_commit(accf0 + 8 * acc);
-                    if (++acc == C::ACCS) {
-                        acc = 0;
-                        acc_phase ^= 1u;
-                    }
-                }
+                if (MX && (kb & 3) == 3) mma_commit(sfe0 + 8 * sf);
+                if (!MX) mma_commit(accf0 + 8 * acc);
+                if (MX && kb == kb1 - 1) mma_commit(accf0);
             }
-            if (MX && ok) mma_commit(accf0);
-            if (!ok && any) {
-                mma_commit(drain);
-                mbar_wait(drain, 0, nullptr, 100000000ull);
+            __syncwarp();
+            any = true;
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
             }
+            if (MX && (kb & 3) == 3 && ++sf == 2) {
+                sf = 0;
+                sf_phase ^= 1u;
+            }
+            if (!MX && ++acc == C::ACCS) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (!ok && any) {
+            if (elect_one()) mma_commit(drain);
+            __syncwarp();
+            mbar_wait(drain, 0, nullptr, 100000000ull);
         }
     } else if constexpr (MX) {
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
@@ -1040,28 +1043,31 @@ __global__ void __launch_bounds__(Few<NT, MX>::THREADS)
         }
         __syncwarp();
         cluster_sync();
-        // this CTA joins every splits-th token, in the order of the splits; eight at a
-        // time, so that their reads from the other SMs are under way together
+        // CTA k of the cluster joins tokens k, k + splits, ...  A read from another SM
+        // takes about a microsecond, so those of four tokens and all splits go out
+        // together.  (Writing the sums to the joining SM's memory instead is as fast for
+        // 16 tokens and slower for more; bulk copies are slower throughout.)
         if (warp >= 2 && n < a.N) {
-            constexpr int U = 8;
+            constexpr int U = 4;
             const int step = splits * (C::WARPS / 4);
             for (int c0 = split + part * splits; c0 < tokens; c0 += U * step) {
-                float s[U] = {};
-                for (int k = 0; k < splits; ++k) {
-                    float v[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        v[u] = c0 + u * step < tokens
-                                   ? ld_shared_cluster(mapa_shared(
-                                         smem_u32(red + (c0 + u * step) * 128 + r), static_cast<uint32_t>(k)))
-                                   : 0.0f;
-#pragma unroll
-                    for (int u = 0; u < U; ++u) s[u] = __fadd_rn(s[u], v[u]);
-                }
+                float v[U][C::MOST_SPLITS];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (c0 + u * step < tokens)
-                        d[(c0 + u * step) * a.ldd] = __float2bfloat16_rn(s[u]);
+#pragma unroll
+                    for (int k = 0; k < C::MOST_SPLITS; ++k)
+                        v[u][k] = k < splits && c0 + u * step < tokens
+                                      ? ld_shared_cluster(mapa_shared(
+                                            smem_u32(red + (c0 + u * step) * 128 + r),
+                                            static_cast<uint32_t>(k)))
+                                      : 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float s = 0.0f;   // in the order of the splits
+#pragma unroll
+                    for (int k = 0; k < C::MOST_SPLITS; ++k) s = __fadd_rn(s, v[u][k]);
+                    if (c0 + u * step < tokens) d[(c0 + u * step) * a.ldd] = __float2bfloat16_rn(s);
+                }
             }
         }
         __syncwarp();
@@ -1153,8 +1159,9 @@ cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D,
     const int64_t tw = (D.cols + 127) / 128, tx = (D.rows + NT - 1) / NT;
     // as many CTAs as run at once, two per SM, with at least two k-blocks each
     int64_t splits = 2 * sm_count / (tw * tx);
+    if (NT > 64 && tw * tx > sm_count / 2) splits = 1;   // the join costs more than it saves
     if (splits > a.num_kb / 2) splits = a.num_kb / 2;
-    if (splits > 8) splits = 8;
+    if (splits > C::MOST_SPLITS) splits = C::MOST_SPLITS;
     if (splits < 1) splits = 1;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg =

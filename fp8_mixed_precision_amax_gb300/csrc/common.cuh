@@ -192,6 +192,17 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// True in one lane of the warp, always the same one.  A warp that walks its loop whole and
+// lets this lane issue keeps addresses and descriptors in uniform registers, which
+// tcgen05 instructions take; in a branch on the lane number each issue first moves them
+// there.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(r));
+    return r != 0;
+}
+
 // D(tmem) (+)= A(smem) * B(smem)^T, one 128 x N x 32 FP8 MMA issued by one thread.
 __device__ __forceinline__ void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
