@@ -101,7 +101,7 @@ struct PairArgs {
     uint32_t idesc;
 };
 
-// The producer warp's lane 0: A and B slices of every k-block of the pair's tiles.
+// The producer warp: A and B slices of every k-block of the pair's tiles.
 template <int STAGES>
 __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int unit, int num_units,
                                         uint32_t sA, uint32_t sB, uint32_t full0, uint32_t empty0,
@@ -116,16 +116,19 @@ __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int un
         const int32_t arow = mb * 2 * BM + static_cast<int32_t>(rank) * BM;
         const int32_t brow = nb * BN + static_cast<int32_t>(rank) * (BN / 2);
         for (int kb = 0; kb < a.num_kb; ++kb) {
-            if (!mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag)) {
-                raise_error(abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag))) {
+                if ((threadIdx.x & 31) == 0) raise_error(abort_flag);
                 ok = false;
                 break;
             }
-            // both CTAs' halves complete on the even CTA's barrier
-            const uint32_t fb = full0 + 8 * stage, fb0 = mapa_shared(fb, 0);
-            if (rank == 0) mbar_arrive_expect_tx(fb, 4 * HALF);
-            tma_load_2d_pair(sA + stage * HALF, &a.mapA, fb0, kb * BK, arow);
-            tma_load_2d_pair(sB + stage * HALF, &a.mapB, fb0, kb * BK, brow);
+            if (elect_one()) {
+                // both CTAs' halves complete on the even CTA's barrier
+                const uint32_t fb = full0 + 8 * stage, fb0 = mapa_shared(fb, 0);
+                if (rank == 0) mbar_arrive_expect_tx(fb, 4 * HALF);
+                tma_load_2d_pair(sA + stage * HALF, &a.mapA, fb0, kb * BK, arow);
+                tma_load_2d_pair(sB + stage * HALF, &a.mapB, fb0, kb * BK, brow);
+            }
+            __syncwarp();
             ++issued;
             if (++stage == STAGES) {
                 stage = 0;
@@ -268,58 +271,62 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0)
-            produce<MX_STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
+        produce<MX_STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0, sf = 0, it = 0;
             uint32_t phase = 0, sf_phase = 0;
             bool ok = true, any = false;
             for (int tile = unit; ok && tile < a.num_tiles; tile += num_units, ++it) {
                 // the previous tile's epilogue has read the columns the two share
-                if (it > 0 && !mbar_wait(acce, static_cast<uint32_t>(it - 1) & 1u, abort_flag)) {
-                    raise_error(abort_flag);
+                const bool freed =
+                    it == 0 || mbar_wait(acce, static_cast<uint32_t>(it - 1) & 1u, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, freed)) {
+                    if (lane == 0) raise_error(abort_flag);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + ((it & 1) ? MX_ACC1 : 0);
                 for (int kb = 0; kb < a.num_kb; ++kb) {
-                    if (((kb & 3) == 0 && !mbar_wait(sff0 + 8 * sf, sf_phase, abort_flag)) ||
-                        !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
-                        raise_error(abort_flag);
+                    const bool last = kb == a.num_kb - 1;
+                    const bool go = ((kb & 3) != 0 || mbar_wait(sff0 + 8 * sf, sf_phase, abort_flag)) &&
+                                    mbar_wait(full0 + 8 * stage, phase, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, go)) {
+                        if (lane == 0) raise_error(abort_flag);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sfa = tmem + MX_SF + sf * MX_SF_STRIDE, sfb = sfa + 4;
-                    const uint32_t idesc = a.idesc | static_cast<uint32_t>(kb & 3) << 4 |
-                                           static_cast<uint32_t>(kb & 3) << 29;
+                    if (elect_one()) {
+                        const uint32_t sfa = tmem + MX_SF + sf * MX_SF_STRIDE, sfb = sfa + 4;
+                        const uint32_t idesc = a.idesc | static_cast<uint32_t>(kb & 3) << 4 |
+                                               static_cast<uint32_t>(kb & 3) << 29;
+                        const uint64_t ad = smem_desc_sw128(sA + stage * HALF);
+                        const uint64_t bd = smem_desc_sw128(sB + stage * HALF);
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        mma_mxf8_pair(d, smem_desc_sw128(sA + stage * HALF + 32 * k),
-                                      smem_desc_sw128(sB + stage * HALF + 32 * k), idesc, sfa, sfb,
-                                      (kb | k) != 0);
-                    mma_commit_pair(empty0 + 8 * stage, 0x3);
+                        for (int k = 0; k < BK / 32; ++k)   // 32 bytes on: 2 in the descriptors' unit
+                            mma_mxf8_pair(d, ad + 2 * k, bd + 2 * k, idesc, sfa, sfb, (kb | k) != 0);
+                        mma_commit_pair(empty0 + 8 * stage, 0x3);
+                        if ((kb & 3) == 3 || last) mma_commit_pair(sfe0 + 8 * sf, 0x3);
+                        if (last) mma_commit_pair(accf0 + 8 * (it & 1), 0x3);
+                    }
+                    __syncwarp();
                     any = true;
                     if (++stage == MX_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if ((kb & 3) == 3 || kb == a.num_kb - 1) {
-                        mma_commit_pair(sfe0 + 8 * sf, 0x3);
-                        if (++sf == 2) {
-                            sf = 0;
-                            sf_phase ^= 1u;
-                        }
+                    if (((kb & 3) == 3 || last) && ++sf == 2) {
+                        sf = 0;
+                        sf_phase ^= 1u;
                     }
                 }
-                if (!ok) break;
-                mma_commit_pair(accf0 + 8 * (it & 1), 0x3);
             }
             if (!ok && any) {
                 // wait (bounded) for the MMAs in flight before TMEM is freed
-                mma_commit_pair(drain, 0x1);
+                if (elect_one()) mma_commit_pair(drain, 0x1);
+                __syncwarp();
                 mbar_wait(drain, 0, nullptr, 100000000ull);
             }
         }
@@ -526,27 +533,32 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FS_REGS_CONTROL));
-        if (warp == 0 && lane == 0)
+        if (warp == 0) {
             produce<FS_STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
-        if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, any = false;
             for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
                 for (int kb = 0; kb < a.num_kb; ++kb) {
-                    if (!mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) ||
-                        !mbar_wait(full0 + 8 * stage, phase, abort_flag)) {
-                        raise_error(abort_flag);
+                    const bool go = mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) &&
+                                    mbar_wait(full0 + 8 * stage, phase, abort_flag);
+                    if (!__all_sync(0xFFFFFFFFu, go)) {
+                        if (lane == 0) raise_error(abort_flag);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = smem_desc_sw128(sA + stage * HALF);
+                        const uint64_t bd = smem_desc_sw128(sB + stage * HALF);
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        mma_f8f6f4_pair(tmem + acc * BN, smem_desc_sw128(sA + stage * HALF + 32 * k),
-                                        smem_desc_sw128(sB + stage * HALF + 32 * k), a.idesc, k != 0);
-                    mma_commit_pair(empty0 + 8 * stage, 0x3);
-                    mma_commit_pair(accf0 + 8 * acc, 0x3);
+                        for (int k = 0; k < BK / 32; ++k)
+                            mma_f8f6f4_pair(tmem + acc * BN, ad + 2 * k, bd + 2 * k, a.idesc, k != 0);
+                        mma_commit_pair(empty0 + 8 * stage, 0x3);
+                        mma_commit_pair(accf0 + 8 * acc, 0x3);
+                    }
+                    __syncwarp();
                     any = true;
                     if (++stage == FS_STAGES) {
                         stage = 0;
@@ -559,7 +571,8 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                 }
             }
             if (!ok && any) {
-                mma_commit_pair(drain, 0x1);
+                if (elect_one()) mma_commit_pair(drain, 0x1);
+                __syncwarp();
                 mbar_wait(drain, 0, nullptr, 100000000ull);
             }
         }
