@@ -65,38 +65,61 @@ struct Team {
 // Sum of a pair over the team, in a fixed order, the same in every thread.  A CTA's
 // calls alternate between two buffers: a buffer is written again only after a
 // barrier that follows its last read.
-__device__ __forceinline__ uint64_t warp_sum2(uint64_t v) {
+// The warps' sums meet in shared memory (unused places hold zeros); every thread adds up
+// all of them, which is a shorter way than five more exchanges between lanes.
+template <bool WARP>
+__device__ __forceinline__ float2 team_sum2(float a, float b, uint64_t (&buf)[16]) {
+    uint64_t v = f32x2_pack(a, b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) v = f32x2_add(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-template <bool WARP>
-__device__ __forceinline__ float2 team_sum2(float a, float b, uint64_t (&buf)[32]) {
-    uint64_t v = warp_sum2(f32x2_pack(a, b));
     if constexpr (!WARP) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = v;
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = warp_sum2(lane < static_cast<int>(blockDim.x >> 5) ? buf[lane] : 0);
+        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(buf);
+        uint64_t s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const ulonglong2 u = p[i];
+            s[i] = f32x2_add(u.x, u.y);
+        }
+        v = f32x2_add(f32x2_add(s[0], s[1]), f32x2_add(s[2], s[3]));
+        if (blockDim.x > 256) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const ulonglong2 u = p[4 + i];
+                s[i] = f32x2_add(u.x, u.y);
+            }
+            v = f32x2_add(v, f32x2_add(f32x2_add(s[0], s[1]), f32x2_add(s[2], s[3])));
+        }
     }
     f32x2_unpack(v, a, b);
     return make_float2(a, b);
 }
 // One value: half the exchanges.
 template <bool WARP>
-__device__ __forceinline__ float team_sum(float a, uint64_t (&buf)[32]) {
+__device__ __forceinline__ float team_sum(float a, uint64_t (&buf)[16]) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) a = __fadd_rn(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
     if constexpr (!WARP) {
-        const int lane = threadIdx.x & 31;
-        float *f = reinterpret_cast<float *>(buf);
-        if (lane == 0) f[threadIdx.x >> 5] = a;
+        if ((threadIdx.x & 31) == 0) reinterpret_cast<float *>(buf)[threadIdx.x >> 5] = a;
         __syncthreads();
-        a = lane < static_cast<int>(blockDim.x >> 5) ? f[lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) a = __fadd_rn(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        const ulonglong2 *p = reinterpret_cast<const ulonglong2 *>(buf);
+        ulonglong2 u = p[0], w = p[1];
+        uint64_t v = f32x2_add(f32x2_add(u.x, u.y), f32x2_add(w.x, w.y));
+        if (blockDim.x > 256) {
+            u = p[2], w = p[3];
+            v = f32x2_add(v, f32x2_add(f32x2_add(u.x, u.y), f32x2_add(w.x, w.y)));
+        }
+        float lo, hi;
+        f32x2_unpack(v, lo, hi);
+        a = __fadd_rn(lo, hi);
     }
     return a;
+}
+// Zeros in both buffers, before their first use.
+__device__ __forceinline__ void clear_sums(uint64_t (&buf)[2][16]) {
+    if (threadIdx.x < 32) buf[threadIdx.x >> 4][threadIdx.x & 15] = 0;
+    __syncthreads();
 }
 
 __device__ __forceinline__ float sum2(uint64_t v) {
@@ -169,8 +192,9 @@ template <typename T, int VPT, bool WARP, int VEC>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const LnFwdArgs a) {
     using L = Lay<T, VEC>;
     constexpr int E = L::E, P = L::P;
-    __shared__ uint64_t buf[2][32];
+    __shared__ __align__(16) uint64_t buf[2][16];
     const Team<WARP> team;
+    clear_sums(buf);
     pdl_wait();
     pdl_trigger();
     const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.cols));
@@ -232,8 +256,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
 
 // Rows too long for a CTA's registers: x is read again for each use.
 template <typename T>
-__global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
-    __shared__ uint64_t buf[2][32];
+__global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const LnFwdArgs a) {
+    __shared__ __align__(16) uint64_t buf[2][16];
+    clear_sums(buf);
     pdl_wait();
     pdl_trigger();
     const float n = static_cast<float>(a.cols);
@@ -246,7 +271,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
         const T *xr = static_cast<const T *>(a.x) + row * a.ldx;
         RawRow8<T> raw;
         uint64_t x[4], s2 = 0;
-        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+        for (int64_t w = warp0; w < a.cols; w += 8 * 512) {
             const int64_t c = w + 8 * (threadIdx.x & 31);
             raw.load(xr, c, a.cols);
             raw.get(xr, c, a.cols, x);
@@ -256,7 +281,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
         const float mu = __fdiv_rn(team_sum<false>(sum2(s2), buf[0]), n);
         const uint64_t nmu2 = splat_f32x2(-mu);
         s2 = 0;
-        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+        for (int64_t w = warp0; w < a.cols; w += 8 * 512) {
             const int64_t c = w + 8 * (threadIdx.x & 31);
             raw.load(xr, c, a.cols);
             raw.get(xr, c, a.cols, x);
@@ -268,7 +293,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_wide_kernel(const LnFwdArgs a) {
             a.mean[row] = mu;
             a.rstd[row] = rs;
         }
-        for (int64_t w = warp0; w < a.cols; w += 8 * 1024) {
+        for (int64_t w = warp0; w < a.cols; w += 8 * 512) {
             const int64_t c = w + 8 * (threadIdx.x & 31);
             uint64_t g[4], b[4];
             load_param(a.gamma, a.wtype, c, a.cols, g);
@@ -365,15 +390,16 @@ __device__ __forceinline__ void ln_bwd_accumulate(uint64_t nmu2, uint64_t rs2, c
 
 // Wide rows: the two row sums, in a pass of their own.
 template <typename T, bool SAVED>
-__global__ void __launch_bounds__(1024) ln_bwd_sums_kernel(const LnBwdArgs a) {
-    __shared__ uint64_t buf[2][32];
+__global__ void __launch_bounds__(512) ln_bwd_sums_kernel(const LnBwdArgs a) {
+    __shared__ __align__(16) uint64_t buf[2][16];
+    clear_sums(buf);
     pdl_wait();
     pdl_trigger();
     int flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         const uint64_t nmu2 = splat_f32x2(-a.mean[row]), rs2 = splat_f32x2(a.rstd[row]);
         uint64_t s1 = 0, s2 = 0;
-        for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * 1024) {
+        for (int64_t c = 8 * threadIdx.x; c < a.cols; c += 8 * 512) {
             const T *dyr = static_cast<const T *>(a.dy) + row * a.lddy;
             RawRow8<T> rdy;
             RawX<T, SAVED, 0> rx;
@@ -430,7 +456,7 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const RingArgs r) {
     constexpr int VPT = 2, kSize = static_cast<int>(sizeof(T));
     const LnBwdArgs &a = r.a;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ uint64_t buf[2][32];
+    __shared__ __align__(16) uint64_t buf[2][16];
     __shared__ uint64_t bars[kRing];
     __shared__ int gave_up;
     const uint32_t bar0 = smem_u32(bars), stage_bytes = r.dy_span + r.x_span;
@@ -439,7 +465,7 @@ __global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const RingArgs r) {
         gave_up = 0;
         fence_mbar_init();
     }
-    __syncthreads();
+    clear_sums(buf);
     pdl_wait();
     pdl_trigger();
     const uint8_t *dy0 = static_cast<const uint8_t *>(a.dy), *x0 = static_cast<const uint8_t *>(a.x);
@@ -541,8 +567,9 @@ template <typename T, bool SAVED, int VPT, bool WARP, bool WIDE, int VEC>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const LnBwdArgs a) {
     using L = Lay<T, VEC>;
     constexpr int E = L::E, P = L::P;
-    __shared__ uint64_t buf[2][32];
+    __shared__ __align__(16) uint64_t buf[2][16];
     const Team<WARP> team;
+    clear_sums(buf);
     pdl_wait();
     pdl_trigger();
     const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
@@ -677,7 +704,7 @@ cudaError_t ln_fwd_typed(const LnFwdArgs &a, bool vec, int sms, cudaStream_t st)
         if (a.cols <= 8192) return ln_fwd_rows<T, 2, false, 0>(a, sms, st);
         if (a.cols <= 16384) return ln_fwd_rows<T, 4, false, 0>(a, sms, st);
     }
-    return launch_pdl(ln_fwd_wide_kernel<T>, dim3(capped(a.rows, 2 * sms)), dim3(1024), 0, st, a);
+    return launch_pdl(ln_fwd_wide_kernel<T>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
 }
 
 constexpr int64_t kBwdNarrow = 512;   // rows up to this belong to one warp
@@ -730,7 +757,7 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
         e = ln_bwd_ring<T, SAVED>(a, g, st);
     } else {
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * a.cols);
-        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 2 * 152)), dim3(1024), 0, st, a);
+        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * 152)), dim3(512), 0, st, a);
         if (e != cudaSuccess) return e;
         const dim3 slabs(g, static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab));
         e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, false, true, VEC>, slabs, dim3(256), 0, st, a);
