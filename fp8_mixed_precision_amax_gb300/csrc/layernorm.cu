@@ -128,6 +128,12 @@ __device__ __forceinline__ float sum2(uint64_t v) {
     return __fadd_rn(lo, hi);
 }
 
+// s / n given 1 / n: the product, corrected by its remainder.
+__device__ __forceinline__ float quotient(float s, float n, float inv_n) {
+    const float q = __fmul_rn(s, inv_n);
+    return __fmaf_rn(__fmaf_rn(-q, n, s), inv_n, q);
+}
+
 struct LnFwdArgs {
     const void *x;
     int64_t rows, cols, ldx;
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
     clear_sums(buf);
     pdl_wait();
     pdl_trigger();
-    const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.cols));
+    const float n = static_cast<float>(a.cols), inv_n = __fdiv_rn(1.0f, n);
     const int left0 = static_cast<int>(a.cols) - E * team.id;
     RowWriter wx, wy;
     wx.start(a.x8, team.row, team.step, E * team.id);
@@ -231,13 +237,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
             for (int i = 0; i < P; ++i) s2 = f32x2_add(s2, x[k][i]);
         }
         if (row + team.step < a.rows) fetch(row + team.step);
-        const float mu = __fmul_rn(team_sum<WARP>(sum2(s2), buf[0]), inv_n);
+        const float mu = quotient(team_sum<WARP>(sum2(s2), buf[0]), n, inv_n);
         const uint64_t nmu2 = splat_f32x2(-mu);
         s2 = 0;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) s2 = deviations(x[k], nmu2, left0 - E * k * team.size, s2);
-        const float var = __fmul_rn(team_sum<WARP>(sum2(s2), buf[1]), inv_n);
-        const float rs = rsqrtf(__fadd_rn(var, a.eps));
+        const float var = quotient(team_sum<WARP>(sum2(s2), buf[1]), n, inv_n);
+        const float rs = __frsqrt_rn(__fadd_rn(var, a.eps));
         if (team.id == 0) {
             a.mean[row] = mu;
             a.rstd[row] = rs;
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const LnFwdArgs a) {
             s2 = deviations(x, nmu2, static_cast<int>(a.cols - c), s2);
         }
         const float var = __fdiv_rn(team_sum<false>(sum2(s2), buf[1]), n);
-        const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+        const float rs = __frsqrt_rn(__fadd_rn(var, a.eps));
         if (threadIdx.x == 0) {
             a.mean[row] = mu;
             a.rstd[row] = rs;
@@ -451,8 +457,8 @@ struct RingArgs {
     uint32_t dy_span, x_span;   // bytes of a row's place: dy, then x or its codes
 };
 
-template <typename T, bool SAVED>
-__global__ void __launch_bounds__(512) ln_bwd_ring_kernel(const RingArgs r) {
+template <typename T, bool SAVED, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingArgs r) {
     constexpr int VPT = 2, kSize = static_cast<int>(sizeof(T));
     const LnBwdArgs &a = r.a;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -711,36 +717,47 @@ constexpr int64_t kBwdNarrow = 512;   // rows up to this belong to one warp
 constexpr int64_t kBwdWide = 8192;    // rows up to this are held in a CTA's registers
 constexpr int64_t kBwdSlab = 4096;    // columns of a wide row's slab, 16 for each of 256 threads
 
-// CTAs that keep column sums of their own, at most: as many as the registers (128 per
-// thread) allow at once on 152 SMs; one per SM and slab of a wide row.
+// CTAs per SM of the ring kernel: of up to 288 threads (4608 columns) two fit beside
+// each other at 112 registers per thread, smaller ones by threads.
+constexpr unsigned kRingHalf = 288;
+int64_t ring_ctas_per_sm(unsigned threads) {
+    return threads > kRingHalf ? 1 : threads > 128 ? 2 : 512 / threads;
+}
+
+// CTAs that keep column sums of their own, at most: as many as are resident on 152 SMs;
+// one per SM and slab of a wide row.
 int64_t bwd_ctas(int64_t rows, int64_t cols) {
     constexpr int64_t sms = 152;
     if (cols <= kBwdNarrow) return capped((rows + kWarps - 1) / kWarps, 2 * sms);
     if (cols > kBwdWide) return capped(rows, sms);
-    const unsigned threads = row_threads(cols, 16);
-    return capped(rows, sms * (threads < 512 ? 512 / threads : 1));
+    return capped(rows, sms * ring_ctas_per_sm(row_threads(cols, 16)));
 }
 
 // As many rows in flight as the CTAs of an SM have shared memory for.
-template <typename T, bool SAVED>
-cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
+template <typename T, bool SAVED, int THREADS, int CTAS>
+cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cudaStream_t st) {
     constexpr int64_t kSize = sizeof(T), kBytes = 200 << 10;
-    const unsigned threads = row_threads(a.cols, 16);
     RingArgs r{a, 0, 0, 0};
     r.dy_span = static_cast<uint32_t>((a.cols * kSize + 15 + 127) / 128 * 128 + 128);
     r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
-    const int64_t per_sm = threads < 512 ? 512 / threads : 1;
-    const int64_t fit = kBytes / per_sm / (r.dy_span + r.x_span);
+    const int64_t fit = kBytes / ring_ctas_per_sm(threads) / (r.dy_span + r.x_span);
     r.stages = static_cast<int>(fit < kRing ? fit : kRing);
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
-        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED>,
+        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes));
     });
     if (err != cudaSuccess) return err;
-    return launch_pdl(ln_bwd_ring_kernel<T, SAVED>, dim3(grid), dim3(threads),
+    return launch_pdl(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS>, dim3(grid), dim3(threads),
                       static_cast<size_t>(r.stages) * (r.dy_span + r.x_span), st, r);
+}
+
+template <typename T, bool SAVED>
+cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
+    const unsigned threads = row_threads(a.cols, 16);
+    return threads > kRingHalf ? ln_bwd_ring_sized<T, SAVED, 512, 1>(a, grid, threads, st)
+                               : ln_bwd_ring_sized<T, SAVED, kRingHalf, 2>(a, grid, threads, st);
 }
 
 template <typename T, bool SAVED, int VEC>
