@@ -245,7 +245,7 @@ struct SwigluSmem {
 };
 
 // The three results of a tile in registers at once: 192 KB of the SM's 256.
-template <typename T, int FMT, int AFMT>
+template <typename T, int FMT, int AFMT, int HFMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_bwd_kernel(const T *__restrict__ da, int64_t M, int64_t F, int64_t ld, bool vec,
                       const BlockView h8, const BlockView dh8, const BlockView dh8t,
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int r = 0; r < kTileRows; ++r) {
             uint64_t d[2], g[2], u[2];
             staged4<T>(sm.da[stage] + part * kSize, r, d);
-            staged_codes4(sm.gate[stage] + part, r, h8.fmt, __shfl_sync(0xFFFFFFFFu, sc, r), g);
-            staged_codes4(sm.value[stage] + part, r, h8.fmt, __shfl_sync(0xFFFFFFFFu, sc, r + 8), u);
+            staged_codes4(sm.gate[stage] + part, r, HFMT, __shfl_sync(0xFFFFFFFFu, sc, r), g);
+            staged_codes4(sm.value[stage] + part, r, HFMT, __shfl_sync(0xFFFFFFFFu, sc, r + 8), u);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float g0, g1;
@@ -461,9 +461,13 @@ template <typename T, int FMT, int AFMT>
 cudaError_t swiglu_bwd_tiles(const MatView &da, const BlockView &h8, const BlockView &dh8,
                              const BlockView &dh8t, const BlockView &a8t, int sm_count,
                              cudaStream_t st) {
-    return launch_tiles<swiglu_bwd_kernel<T, FMT, AFMT>, SwigluSmem<T>>(
-        1, da.rows, da.cols, sm_count, st, static_cast<const T *>(da.data), da.rows, da.cols, da.ld,
-        rows_vec(da, static_cast<int>(16 / sizeof(T))), h8, dh8, dh8t, a8t);
+    const T *p = static_cast<const T *>(da.data);
+    const bool vec = rows_vec(da, static_cast<int>(16 / sizeof(T)));
+    if (h8.fmt == 0)
+        return launch_tiles<swiglu_bwd_kernel<T, FMT, AFMT, 0>, SwigluSmem<T>>(
+            1, da.rows, da.cols, sm_count, st, p, da.rows, da.cols, da.ld, vec, h8, dh8, dh8t, a8t);
+    return launch_tiles<swiglu_bwd_kernel<T, FMT, AFMT, 1>, SwigluSmem<T>>(
+        1, da.rows, da.cols, sm_count, st, p, da.rows, da.cols, da.ld, vec, h8, dh8, dh8t, a8t);
 }
 
 template <typename T>
