@@ -328,6 +328,11 @@ __device__ __forceinline__ float load_any(const void *p, int type, int64_t c) {
     return to_f32(static_cast<const __half *>(p)[c]);
 }
 
+// row * ld, both below 2^31, in one instruction
+__device__ __forceinline__ int64_t row_at(unsigned row, int64_t ld) {
+    return static_cast<int64_t>(static_cast<uint64_t>(row) * static_cast<uint32_t>(ld));
+}
+
 // ------------------------------------------------------------ block scales --
 
 // E8M0 byte of a block: e + 127 for the smallest e >= -127 with amax <= fmax 2^e.
@@ -457,34 +462,27 @@ __device__ __forceinline__ void store_code_word(uint8_t *p, uint32_t w, int64_t 
 struct RowWriter {
     uint8_t *code;     // of this thread's first column
     uint8_t *scale;
-    int64_t code_step, scale_step;   // bytes from one of the team's rows to the next
-    bool e5m2, f32;
 
-    __device__ __forceinline__ void start(const BlockView &q, int64_t row, int64_t rows_step, int64_t c) {
-        e5m2 = q.fmt != 0;
-        f32 = q.scale_f32 != 0;
-        const int64_t size = f32 ? 4 : 1;
+    __device__ __forceinline__ void start(const BlockView &q, int64_t row, int64_t c) {
         code = q.codes + row * q.ld + c;
-        scale = static_cast<uint8_t *>(q.scales) + (row * q.ld_s + (c >> 7)) * size;
-        code_step = rows_step * q.ld;
-        scale_step = rows_step * q.ld_s * size;
+        scale = static_cast<uint8_t *>(q.scales) + (row * q.ld_s + (c >> 7)) * (q.scale_f32 ? 4 : 1);
     }
-    __device__ __forceinline__ void next_row() {
-        code += code_step;
-        scale += scale_step;
+    __device__ __forceinline__ void move(const BlockView &q, unsigned rows) {
+        code += row_at(rows, q.ld);
+        scale += row_at(rows, q.ld_s) * (q.scale_f32 ? 4 : 1);
     }
     // All lanes of the warp take part; `left` columns of the row are from the values'
     // first on (0 or less: none; the values there are 0).  at: columns past the
     // thread's first.
     template <int P>
-    __device__ __forceinline__ void put(const uint64_t (&v)[P], int at, int left) const {
-        if (e5m2)
-            put_as<1>(v, at, left);
+    __device__ __forceinline__ void put(const BlockView &q, const uint64_t (&v)[P], int at, int left) const {
+        if (q.fmt != 0)
+            put_as<1>(q, v, at, left);
         else
-            put_as<0>(v, at, left);
+            put_as<0>(q, v, at, left);
     }
     template <int FMT, int P>
-    __device__ __forceinline__ void put_as(const uint64_t (&v)[P], int at, int left) const {
+    __device__ __forceinline__ void put_as(const BlockView &q, const uint64_t (&v)[P], int at, int left) const {
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < P; ++i) m = absmax3(m, v[i]);
@@ -503,7 +501,7 @@ struct RowWriter {
             w[i] = encode4<FMT>(f32x2_mul(v[2 * i], inv2), f32x2_mul(v[2 * i + 1], inv2));
         if (left <= 0) return;
         if ((threadIdx.x & (64 / P - 1)) == 0) {
-            if (f32)
+            if (q.scale_f32)
                 *reinterpret_cast<float *>(scale + (at >> 7) * 4) = scale_value(byte);
             else
                 scale[at >> 7] = static_cast<uint8_t>(byte);
@@ -565,11 +563,6 @@ struct TileWalk {
         col0 = c * kTile;
     }
 };
-
-// row * ld, both below 2^31, in one instruction
-__device__ __forceinline__ int64_t row_at(unsigned row, int64_t ld) {
-    return static_cast<int64_t>(static_cast<uint64_t>(row) * static_cast<uint32_t>(ld));
-}
 
 __host__ __device__ constexpr int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 

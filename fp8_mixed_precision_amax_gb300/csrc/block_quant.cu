@@ -224,13 +224,13 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
             a2[i] = f32x2_mul(f32x2_mul(g2[i], s), u2[i]);
         }
         RowWriter out;
-        out.start(a8, row, 0, c);
-        out.put(a2, 0, 8);
+        out.start(a8, row, c);
+        out.put(a8, a2, 0, 8);
         if (h8.codes != nullptr) {
-            out.start(h8, row, 0, c);
-            out.put(g2, 0, 8);
-            out.start(h8, row, 0, F + c);
-            out.put(u2, 0, 8);
+            out.start(h8, row, c);
+            out.put(h8, g2, 0, 8);
+            out.start(h8, row, F + c);
+            out.put(h8, u2, 0, 8);
         }
     }
 }

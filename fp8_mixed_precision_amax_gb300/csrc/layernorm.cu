@@ -153,14 +153,14 @@ __device__ __forceinline__ void ln_finish(const LnFwdArgs &a, T *yr, const RowWr
                                           const RowWriter &wx, int64_t c, int at, int left,
                                           uint64_t nmu2, uint64_t rs2, const uint64_t (&g)[P],
                                           const uint64_t (&b)[P], const uint64_t (&x)[P]) {
-    if (a.x8.codes != nullptr) wx.put(x, at, left);
+    if (a.x8.codes != nullptr) wx.put(a.x8, x, at, left);
     if (a.y == nullptr && a.y8.codes == nullptr) return;
     uint64_t y[P];
 #pragma unroll
     for (int i = 0; i < P; ++i)
         y[i] = f32x2_fma(f32x2_mul(f32x2_add(x[i], nmu2), rs2), g[i], b[i]);
     if (a.y != nullptr) Lay<T, P == 8 ? 16 : 0>::store(yr, c, a.cols, y);
-    if (a.y8.codes != nullptr) wy.put(y, at, left);
+    if (a.y8.codes != nullptr) wy.put(a.y8, y, at, left);
 }
 
 template <int P>
@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
     const float n = static_cast<float>(a.cols), inv_n = __fdiv_rn(1.0f, n);
     const int left0 = static_cast<int>(a.cols) - E * team.id;
     RowWriter wx, wy;
-    wx.start(a.x8, team.row, team.step, E * team.id);
-    wy.start(a.y8, team.row, team.step, E * team.id);
+    wx.start(a.x8, team.row, E * team.id);
+    wy.start(a.y8, team.row, E * team.id);
     typename L::Raw raw[VPT];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -255,8 +255,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const 
             ln_finish<T, P>(a, static_cast<T *>(a.y) + row * a.ldy, wy, wx, E * team.id + at, at,
                             left0 - at, nmu2, splat_f32x2(rs), g[k % kKept], b[k % kKept], x[k]);
         }
-        wx.next_row();
-        wy.next_row();
+        wx.move(a.x8, static_cast<unsigned>(team.step));
+        wy.move(a.y8, static_cast<unsigned>(team.step));
     }
 }
 
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const LnFwdArgs a) {
     // whole warps stay together: the exchanges between lanes need all of them
     const int64_t warp0 = 8 * (threadIdx.x & ~31);
     RowWriter wx, wy;
-    wx.start(a.x8, blockIdx.x, gridDim.x, 8 * threadIdx.x);
-    wy.start(a.y8, blockIdx.x, gridDim.x, 8 * threadIdx.x);
+    wx.start(a.x8, blockIdx.x, 8 * threadIdx.x);
+    wy.start(a.y8, blockIdx.x, 8 * threadIdx.x);
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const T *xr = static_cast<const T *>(a.x) + row * a.ldx;
         RawRow8<T> raw;
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const LnFwdArgs a) {
             ln_finish<T, 4>(a, static_cast<T *>(a.y) + row * a.ldy, wy, wx, c, static_cast<int>(w - warp0),
                          static_cast<int>(a.cols - c), nmu2, splat_f32x2(rs), g, b, x);
         }
-        wx.next_row();
-        wy.next_row();
+        wx.move(a.x8, gridDim.x);
+        wy.move(a.y8, gridDim.x);
     }
 }
 
