@@ -265,7 +265,7 @@ struct RawVec {
 // take part, lane l + 1 with the columns after lane l's.
 template <typename T>
 __device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t cols, const uint64_t (&v)[4]) {
-    constexpr int kWords = 2 * static_cast<int>(sizeof(T));
+    constexpr int kWords = 2 * static_cast<int>(sizeof(T)), kBlocks = kWords / 4;
     const int lane = threadIdx.x & 31;
     uint32_t w[kWords + 8];   // the lane before's last block, this lane's words, room to shift
 #pragma unroll
@@ -284,7 +284,7 @@ __device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t cols, cons
     if (off == 0) {
         if (full) {
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i)
+            for (int i = 0; i < kBlocks; ++i)
                 reinterpret_cast<uint4 *>(p)[i] =
                     make_uint4(w[4 + 4 * i], w[5 + 4 * i], w[6 + 4 * i], w[7 + 4 * i]);
             return;
@@ -295,24 +295,36 @@ __device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t cols, cons
             w[i] = __shfl_up_sync(0xFFFFFFFFu, w[kWords + i], 1);
             w[kWords + 4 + i] = 0;
         }
-        uint32_t x[kWords];
-        shift_words<kWords, kWords + 8>(w, 16u - off, x);
+        uint32_t x[kWords + 4];   // whole blocks from the one that holds p on
+        shift_words<kWords + 4, kWords + 8>(w, 16u - off, x);
         if (full) {
-            uint4 *blocks = reinterpret_cast<uint4 *>(p - off);
+            uint32_t *at = reinterpret_cast<uint32_t *>(p - off);
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i)   // block 0 starts in the lane before
+            for (int i = 0; i < kBlocks; ++i)   // block 0 starts in the lane before
                 if (i > 0 || lane > 0)
-                    blocks[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    reinterpret_cast<uint4 *>(at)[i] =
+                        make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            if (lane == 0) {   // nobody before: the part of block 0 from p on
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+                    if (4 * j >= off) at[j] = x[j];
+                    else if (sizeof(T) == 2 && 4 * j + 2 == off)
+                        reinterpret_cast<uint16_t *>(at)[2 * j + 1] = static_cast<uint16_t>(x[j] >> 16);
+            }
+            if (lane == 31 || c + 16 > cols) {   // nobody after: the beginning of the last block
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+                    if (4 * j + 4 <= off) at[kWords + j] = x[kWords + j];
+                    else if (sizeof(T) == 2 && 4 * j + 2 == off)
+                        reinterpret_cast<uint16_t *>(at)[2 * (kWords + j)] = static_cast<uint16_t>(x[kWords + j]);
+            }
+            return;
         }
     }
-    // what no whole block covers: the first lane's beginning, the end that the next lane
-    // does not take, and a group that the row's end cuts
-    const int head = full && lane > 0 ? 0 : full ? static_cast<int>(16 - off) / static_cast<int>(sizeof(T)) : 8;
-    const int tail = full && (lane == 31 || c + 16 > cols) ? static_cast<int>(off) / static_cast<int>(sizeof(T)) : 0;
-    if (head == 0 && tail == 0) return;
+    // a group that the row's end cuts
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if ((i < head || i >= 8 - tail) && c + i < cols) {
+        if (c + i < cols) {
             if constexpr (sizeof(T) == 4)
                 reinterpret_cast<uint32_t *>(p)[i] = w[4 + i];
             else
@@ -367,9 +379,17 @@ __device__ __forceinline__ void store_scale(const BlockView &q, int64_t rb, int6
     else
         static_cast<uint8_t *>(q.scales)[scale_at(q, rb, cb)] = static_cast<uint8_t>(byte);
 }
+// A scale on its way, and its value: apart, so that a scale can be fetched ahead of its
+// use (the first instruction on a loaded value waits for it).
+__device__ __forceinline__ uint32_t fetch_scale(const BlockView &q, int64_t rb, int64_t cb) {
+    if (q.scale_f32) return static_cast<const uint32_t *>(q.scales)[scale_at(q, rb, cb)];
+    return static_cast<const uint8_t *>(q.scales)[scale_at(q, rb, cb)];
+}
+__device__ __forceinline__ float fetched_scale(const BlockView &q, uint32_t raw) {
+    return q.scale_f32 ? __uint_as_float(raw) : scale_value(raw);
+}
 __device__ __forceinline__ float load_scale(const BlockView &q, int64_t rb, int64_t cb) {
-    if (q.scale_f32) return static_cast<const float *>(q.scales)[scale_at(q, rb, cb)];
-    return scale_value(static_cast<const uint8_t *>(q.scales)[scale_at(q, rb, cb)]);
+    return fetched_scale(q, fetch_scale(q, rb, cb));
 }
 
 // Four FP8 codes (a word) to fp32, exactly (by way of FP16, which holds both formats).

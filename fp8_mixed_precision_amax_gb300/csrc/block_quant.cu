@@ -267,22 +267,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fetch_rows<1>(smem_u32(sm.value[stage]) + part, h8.codes + F, h8.ld, M, F, true, r0, c0);
     };
     // lanes 0 .. 7: the rows' scales of gate; lanes 8 .. 15: of value
-    auto fetch_scale = [&](unsigned r0, unsigned c0) {
+    auto scale_of = [&](unsigned r0, unsigned c0) {
         const unsigned row = r0 + warp * kTileRows + (lane & 7);
-        return lane < 16 && row < M ? load_scale(h8, row, (c0 + (lane < 8 ? 0 : F)) / kTile) : 0.0f;
+        return lane < 16 && row < M ? fetch_scale(h8, row, (c0 + (lane < 8 ? 0 : F)) / kTile) : 0u;
     };
     fetch(0, row0, col0);
     cp_async_commit();
-    float sc_next = fetch_scale(row0, col0);
+    uint32_t sc_next = scale_of(row0, col0);
     int stage = 0;
     for (bool more = true; more;) {
-        const float sc = sc_next;
+        const float sc = fetched_scale(h8, sc_next);
         unsigned next_row0 = 0, next_col0 = 0;
         walk.next();
         more = walk.there();
         if (more) {
             walk.origin(next_row0, next_col0);
-            sc_next = fetch_scale(next_row0, next_col0);
+            sc_next = scale_of(next_row0, next_col0);
         }
         if constexpr (kStages == 2) {
             __syncwarp();   // the warp has read its part of the other stage

@@ -358,22 +358,21 @@ template <typename T, int VEC>
 struct RawX<T, true, VEC> {
     static constexpr int P = Lay<T, VEC>::P;
     static_assert(P == 4, "8 codes");
-    uint32_t w[P / 2];
-    float scale;
+    uint32_t w[P / 2], scale;
     __device__ __forceinline__ void load(const LnBwdArgs &a, int64_t row, int64_t c) {
         const uint8_t *p = a.x8.codes + row * a.x8.ld + c;
         if (c < a.cols) {
             const uint2 u = *reinterpret_cast<const uint2 *>(p);
             w[0] = u.x, w[1] = u.y;
-            scale = load_scale(a.x8, row, c >> 7);
+            scale = fetch_scale(a.x8, row, c >> 7);
         } else {
 #pragma unroll
             for (int i = 0; i < P / 2; ++i) w[i] = 0;
-            scale = 0.0f;
+            scale = 0;
         }
     }
     __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t, int64_t c, uint64_t (&v)[P]) const {
-        codes8(make_uint2(w[0], w[1]), a.x8.fmt, scale, VEC ? 8 : static_cast<int>(a.cols - c), v);
+        codes8(make_uint2(w[0], w[1]), a.x8.fmt, fetched_scale(a.x8, scale), VEC ? 8 : static_cast<int>(a.cols - c), v);
     }
 };
 
@@ -497,13 +496,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
 #pragma unroll
     for (int k = 0; k < VPT; ++k) load_param(a.gamma, a.wtype, col(k), a.cols, g[k]);
     // what does not go through the ring is fetched a row ahead
-    float mu_next = 0.0f, rs_next = 0.0f, sc_next[VPT] = {};
+    float mu_next = 0.0f, rs_next = 0.0f;
+    uint32_t sc_next[VPT] = {};
     auto fetch = [&](int64_t row) {
         mu_next = a.mean[row], rs_next = a.rstd[row];
         if constexpr (SAVED) {
 #pragma unroll
             for (int k = 0; k < VPT; ++k)
-                if (col(k) < cols) sc_next[k] = load_scale(a.x8, row, col(k) >> 7);
+                if (col(k) < cols) sc_next[k] = fetch_scale(a.x8, row, col(k) >> 7);
         }
     };
     if (blockIdx.x < a.rows) fetch(blockIdx.x);
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
         const uint64_t nmu2 = splat_f32x2(-mu_next), rs2 = splat_f32x2(rs_next);
         float sc[VPT];
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) sc[k] = sc_next[k];
+        for (int k = 0; k < VPT; ++k) sc[k] = SAVED ? fetched_scale(a.x8, sc_next[k]) : 0.0f;
         if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
         if (!mbar_wait(bar0 + 8 * s, phase, &gave_up)) {
             // goes on with what is there, so that every thread still meets every barrier
