@@ -333,13 +333,6 @@ __device__ __forceinline__ void store_row8(T *row, int64_t c, int64_t cols, cons
     }
 }
 
-// gamma or beta (type known at run time) at column c.
-__device__ __forceinline__ float load_any(const void *p, int type, int64_t c) {
-    if (type == kTypeF32) return static_cast<const float *>(p)[c];
-    if (type == kTypeBF16) return to_f32(static_cast<const __nv_bfloat16 *>(p)[c]);
-    return to_f32(static_cast<const __half *>(p)[c]);
-}
-
 // row * ld, both below 2^31, in one instruction
 __device__ __forceinline__ int64_t row_at(unsigned row, int64_t ld) {
     return static_cast<int64_t>(static_cast<uint64_t>(row) * static_cast<uint32_t>(ld));

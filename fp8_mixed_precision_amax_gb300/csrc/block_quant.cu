@@ -108,6 +108,18 @@ __global__ void __launch_bounds__(256) block_dequantize_kernel(const BlockView q
 
 // ------------------------------------------------ LayerNorm's output again --
 
+// gamma or beta at columns c .. c + 3; 0 past the row.  One branch on the type, so that
+// the loads are on their way together.
+__device__ __forceinline__ void load_param4(const void *p, int type, int64_t c, int64_t cols,
+                                            float (&v)[4]) {
+    if (type == kTypeF32)
+        load_row<float, 4>(static_cast<const float *>(p), c, cols, false, v);
+    else if (type == kTypeBF16)
+        load_row<__nv_bfloat16, 4>(static_cast<const __nv_bfloat16 *>(p), c, cols, false, v);
+    else
+        load_row<__half, 4>(static_cast<const __half *>(p), c, cols, false, v);
+}
+
 struct RecomputeSmem {
     uint8_t in[2][kTile * kTile];
     ColsSmem cols;
@@ -149,11 +161,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         const float mu = there ? mean[row] : 0.0f, rs = there ? rstd[row] : 0.0f;
         const int64_t c = col0 + 4 * lane;
         float g[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            g[j] = c + j < x8.cols ? load_any(gamma, wtype, c + j) : 0.0f;
-            b[j] = c + j < x8.cols ? load_any(beta, wtype, c + j) : 0.0f;
-        }
+        load_param4(gamma, wtype, c, x8.cols, g);
+        load_param4(beta, wtype, c, x8.cols, b);
         cp_async_wait<1>();
         __syncwarp();
         TileValues v;

@@ -163,13 +163,38 @@ __device__ __forceinline__ void ln_finish(const LnFwdArgs &a, T *yr, const RowWr
     if (a.y8.codes != nullptr) wy.put(a.y8, y, at, left);
 }
 
+// gamma or beta at columns c .. c + 2 P - 1 (c a multiple of 8); 0 past the row.  One
+// branch on the type, so that all loads are on their way together (a branch per element
+// made them wait for one another: 10 us of a call).
+template <typename T, int P>
+__device__ __forceinline__ void load_param_as(const T *p, int64_t c, int64_t cols, uint64_t (&v)[P]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && c + 2 * P <= cols) {
+#pragma unroll
+        for (int k = 0; k < P / 4; ++k) {
+            RawVec<T, 8> raw;
+            raw.load(p, c + 8 * k, cols);
+            uint64_t x[4];
+            raw.get(p, 0, 0, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * k + i] = x[i];
+        }
+    } else {
+        float f[2 * P];
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i) f[i] = c + i < cols ? to_f32(p[c + i]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = f32x2_pack(f[2 * i], f[2 * i + 1]);
+    }
+}
 template <int P>
 __device__ __forceinline__ void load_param(const void *p, int type, int64_t c, int64_t cols,
                                            uint64_t (&v)[P]) {
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-        v[i] = f32x2_pack(c + 2 * i < cols ? load_any(p, type, c + 2 * i) : 0.0f,
-                          c + 2 * i + 1 < cols ? load_any(p, type, c + 2 * i + 1) : 0.0f);
+    if (type == kTypeF32)
+        load_param_as(static_cast<const float *>(p), c, cols, v);
+    else if (type == kTypeBF16)
+        load_param_as(static_cast<const __nv_bfloat16 *>(p), c, cols, v);
+    else
+        load_param_as(static_cast<const __half *>(p), c, cols, v);
 }
 
 // sum of (x - mean)^2; columns past the row do not count
@@ -456,7 +481,8 @@ struct RingArgs {
     uint32_t dy_span, x_span;   // bytes of a row's place: dy, then x or its codes
 };
 
-template <typename T, bool SAVED, int THREADS, int CTAS>
+// ALIGNED: every row starts on a 16-byte boundary and is a multiple of 8 columns long.
+template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingArgs r) {
     constexpr int VPT = 2, kSize = static_cast<int>(sizeof(T));
     const LnBwdArgs &a = r.a;
@@ -529,15 +555,26 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
         for (int k = 0; k < VPT; ++k) {
             const int left = cols - col(k);
             if (left > 0) {
-                RawRow8<T> raw;
-                raw.load_shared(stage + col(k) * kSize, doff != 0);
-                raw.get(doff, left, dy[k]);
+                if constexpr (ALIGNED) {
+                    RawVec<T, 8> raw;
+                    raw.load(reinterpret_cast<const T *>(stage), col(k), cols);
+                    raw.get(nullptr, 0, 0, dy[k]);
+                    if constexpr (!SAVED) {
+                        raw.load(reinterpret_cast<const T *>(stage + r.dy_span), col(k), cols);
+                        raw.get(nullptr, 0, 0, x[k]);
+                    }
+                } else {
+                    RawRow8<T> raw;
+                    raw.load_shared(stage + col(k) * kSize, doff != 0);
+                    raw.get(doff, left, dy[k]);
+                    if constexpr (!SAVED) {
+                        raw.load_shared(stage + r.dy_span + col(k) * kSize, xoff != 0);
+                        raw.get(xoff, left, x[k]);
+                    }
+                }
                 if constexpr (SAVED) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(stage + r.dy_span + col(k));
-                    codes8(w, a.x8.fmt, sc[k], left, x[k]);
-                } else {
-                    raw.load_shared(stage + r.dy_span + col(k) * kSize, xoff != 0);
-                    raw.get(xoff, left, x[k]);
+                    codes8(w, a.x8.fmt, sc[k], ALIGNED ? 8 : left, x[k]);
                 }
             } else {
 #pragma unroll
@@ -554,7 +591,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 dy[k][i] = f32x2_mul(f32x2_fma(x[k][i], nm2, f32x2_add(dy[k][i], nm1)), rs2);
-            store_row8<T>(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
+            if constexpr (ALIGNED)
+                RawVec<T, 8>::store(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
+            else
+                store_row8<T>(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
         }
         if (++s == r.stages) s = 0, phase ^= 1u;
     }
@@ -734,7 +774,7 @@ int64_t bwd_ctas(int64_t rows, int64_t cols) {
 }
 
 // As many rows in flight as the CTAs of an SM have shared memory for.
-template <typename T, bool SAVED, int THREADS, int CTAS>
+template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cudaStream_t st) {
     constexpr int64_t kSize = sizeof(T), kBytes = 200 << 10;
     RingArgs r{a, 0, 0, 0};
@@ -745,19 +785,19 @@ cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cu
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
-        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS>,
+        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>,
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes));
     });
     if (err != cudaSuccess) return err;
-    return launch_pdl(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS>, dim3(grid), dim3(threads),
+    return launch_pdl(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, dim3(grid), dim3(threads),
                       static_cast<size_t>(r.stages) * (r.dy_span + r.x_span), st, r);
 }
 
-template <typename T, bool SAVED>
+template <typename T, bool SAVED, bool ALIGNED>
 cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
     const unsigned threads = row_threads(a.cols, 16);
-    return threads > kRingHalf ? ln_bwd_ring_sized<T, SAVED, 512, 1>(a, grid, threads, st)
-                               : ln_bwd_ring_sized<T, SAVED, kRingHalf, 2>(a, grid, threads, st);
+    return threads > kRingHalf ? ln_bwd_ring_sized<T, SAVED, 512, 1, ALIGNED>(a, grid, threads, st)
+                               : ln_bwd_ring_sized<T, SAVED, kRingHalf, 2, ALIGNED>(a, grid, threads, st);
 }
 
 template <typename T, bool SAVED, int VEC>
@@ -771,7 +811,7 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
         e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, true, false, VEC>, grid, dim3(32 * kWarps),
                        static_cast<size_t>(2 * a.cols * 4), st, a);
     } else if (a.cols <= kBwdWide) {
-        e = ln_bwd_ring<T, SAVED>(a, g, st);
+        e = ln_bwd_ring<T, SAVED, VEC != 0>(a, g, st);
     } else {
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * a.cols);
         e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * 152)), dim3(512), 0, st, a);
