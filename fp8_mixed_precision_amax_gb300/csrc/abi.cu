@@ -43,6 +43,12 @@ const char *fp8_last_error(void) { return g_last_error.c_str(); }
 fp8_status fp8_sync_status(void *stream) {
     unsigned flags = 0;
     cudaError_t e = fp8k::read_and_clear_error_flag(&flags, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) {   // the stream is idle now
+        unsigned block_flags = 0, ln_flags = 0;
+        e = fp8k::read_and_clear_block_gemm_error_flag(&block_flags);
+        if (e == cudaSuccess) e = fp8k::read_and_clear_ln_error_flag(&ln_flags);
+        flags |= block_flags | ln_flags;
+    }
     if (e != cudaSuccess) return cuda_fail(e, "fp8_sync_status");
     if (flags & 1u) return fail(FP8_ERR_TIMEOUT, "a kernel gave up a bounded wait");
     return FP8_OK;

@@ -1,4 +1,5 @@
-// raster.cuh -- the order in which the persistent GEMM kernels visit output tiles.
+// raster.cuh -- the order in which the persistent block-scaled GEMM kernels visit output
+// tiles: the per-tensor GEMM's (gemm.cu).
 #pragma once
 
 #include <cstdint>
