@@ -634,24 +634,12 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                 if (ok) {
                     tc_fence_after();
                     const uint32_t t = t0 + acc * BN;
-                    uint32_t r[2][16];
                     uint64_t sb2[4];
-                    tmem_load_16x256b_x4(t, r[0]);
 #pragma unroll
                     for (int h = 0; h < 8; ++h) {
                         // 32 columns (h / 2) of the quarter's lanes 16 (h mod 2) .. + 15
-                        uint32_t(&v)[16] = r[h & 1];
-                        tmem_wait_16cols(v);
-                        if (h < 7) {
-                            tmem_load_16x256b_x4(t + ((h + 1) >> 1) * 32 +
-                                                     (static_cast<uint32_t>((h + 1) & 1) << 20),
-                                                 r[(h + 1) & 1]);
-                        } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive_cluster_relaxed(mapa_shared(acce0 + 8 * acc, 0));
-                        }
+                        uint32_t v[16];
+                        tmem_load_16x256b_x4(t + (h >> 1) * 32 + (static_cast<uint32_t>(h & 1) << 20), v);
                         if (PER_ROW && (h & 1) == 0) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
@@ -659,6 +647,13 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                                     sbk + (h >> 1) * 8 + 4 * j);
                                 sb2[2 * j] = u.x, sb2[2 * j + 1] = u.y;
                             }
+                        }
+                        tmem_wait_16cols(v);
+                        if (h == 7) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive_cluster_relaxed(mapa_shared(acce0 + 8 * acc, 0));
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
