@@ -13,6 +13,7 @@ import ctypes
 import logging
 import os
 import re
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -148,7 +149,24 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+def _load_packed() -> ctypes.CDLL:
+    """The library once more, with prototypes of the block-scaled calls that take packed structs."""
+    lib = ctypes.CDLL(LIB_PATH)
+    s, vp, i64, i32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    for name, args in {
+            "fp8_block_quantize": [s, s, s, vp], "fp8_block_dequantize": [s, s, vp],
+            "fp8_block_gemm_tn": [s, s, s, vp],
+            "fp8_layernorm_fwd": [s, vp, vp, i32, ctypes.c_float, s, s, s, vp, vp, vp],
+            "fp8_layernorm_bwd": [s, s, s, vp, i32, vp, vp, s, vp, vp, vp, i64, vp],
+            "fp8_layernorm_recompute": [s, vp, vp, i32, vp, vp, s, vp],
+            "fp8_swiglu_fwd": [s, s, s, vp], "fp8_swiglu_bwd": [s, s, s, s, s, vp]}.items():
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, ctypes.c_int
+    return lib
+
+
 _lib = _load()
+_packed = _load_packed()
 
 
 def header_functions() -> list[str]:
@@ -716,6 +734,13 @@ def fp8_allreduce(grad: torch.Tensor, fmt: int, margin: int = 0, group=None,
 
 # ---------------------------------------------------------- block scaling --
 
+# The block-scaled calls get their structs as packed bytes, which ctypes hands over as they
+# are: a Structure object per argument took as long as the rest of the call's checks.
+_PACK_MATRIX = struct.Struct("@Pqqqixxxx").pack
+_PACK_BLOCK = struct.Struct("@PqqqPqiiixxxx").pack
+assert struct.calcsize("@Pqqqixxxx") == ctypes.sizeof(fp8_matrix)
+assert struct.calcsize("@PqqqPqiiixxxx") == ctypes.sizeof(fp8_block_tensor)
+
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _SCALE_TYPES = {torch.uint8: SCALE_E8M0, torch.float32: SCALE_F32}
 
@@ -790,9 +815,9 @@ def _block(q: BlockFp8 | None, name: str):
                          f"contiguous along the columns; got {tuple(scales.shape)}")
     if scale_type == SCALE_E8M0 and spitch < -(-nb // 4) * 4:
         raise ValueError(f"{name}: rows of E8M0 scales must hold whole words of 4; got {spitch}")
-    return fp8_block_tensor(codes.data_ptr(), rows, cols, ld if rows > 1 and pitch else pitch,
-                            scales.data_ptr(), lds if srows > 1 and spitch else spitch, q.fmt,
-                            block_rows, scale_type)
+    return _PACK_BLOCK(codes.data_ptr(), rows, cols, ld if rows > 1 and pitch else pitch,
+                       scales.data_ptr(), lds if srows > 1 and spitch else spitch, q.fmt,
+                       block_rows, scale_type)
 
 
 def _matrix(t: torch.Tensor | None, name: str):
@@ -809,7 +834,7 @@ def _matrix(t: torch.Tensor | None, name: str):
     ld, inner = t.stride()
     if inner != 1 and cols > 1 and rows:
         raise ValueError(f"{name} must be contiguous along its columns")
-    return fp8_matrix(t.data_ptr(), rows, cols, ld if rows > 1 and cols else cols, dtype)
+    return _PACK_MATRIX(t.data_ptr(), rows, cols, ld if rows > 1 and cols else cols, dtype)
 
 
 def _vector(t: torch.Tensor, n: int, name: str, dtype=None) -> int:
@@ -846,17 +871,17 @@ def fp8_block_quantize(x: torch.Tensor, q: BlockFp8 | None = None, qt: BlockFp8 
                        stream=None) -> None:
     """x into ``q`` and / or its transpose into ``qt``, with a power-of-two
     scale for each block of 128 (of format and ``block_rows`` as they say)."""
-    _check(_lib.fp8_block_quantize(_matrix(x, "x"), _block(q, "q"), _block(qt, "qt"),
+    _check(_packed.fp8_block_quantize(_matrix(x, "x"), _block(q, "q"), _block(qt, "qt"),
                                    _stream(stream)))
 
 
 def fp8_block_dequantize(q: BlockFp8, out: torch.Tensor, stream=None) -> None:
-    _check(_lib.fp8_block_dequantize(_block(q, "q"), _matrix(out, "out"), _stream(stream)))
+    _check(_packed.fp8_block_dequantize(_block(q, "q"), _matrix(out, "out"), _stream(stream)))
 
 
 def fp8_block_gemm_tn(A: BlockFp8, B: BlockFp8, D: torch.Tensor, stream=None) -> None:
     """D [M, N] (bfloat16) = A [M, K] B [N, K]^T of two block-scaled matrices."""
-    _check(_lib.fp8_block_gemm_tn(_block(A, "A"), _block(B, "B"), _matrix(D, "D"),
+    _check(_packed.fp8_block_gemm_tn(_block(A, "A"), _block(B, "B"), _matrix(D, "D"),
                                   _stream(stream)))
 
 
@@ -867,12 +892,13 @@ def fp8_layernorm_fwd(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor, 
     """LayerNorm of x: mean and rstd (float32), and any of y (of x's type),
     y8 (y block quantized) and x8 (x kept in 8 bits for the backward pass)."""
     xm = _matrix(x, "x")
+    rows, cols = x.shape
     if gamma.dtype != beta.dtype:
         raise ValueError("gamma and beta must have the same dtype")
-    _check(_lib.fp8_layernorm_fwd(
-        xm, _param(gamma, xm.cols, "gamma"), _param(beta, xm.cols, "beta"), _DTYPES[gamma.dtype],
-        eps, _matrix(y, "y"), _block(y8, "y8"), _block(x8, "x8"), _stat(mean, xm.rows, "mean"),
-        _stat(rstd, xm.rows, "rstd"), _stream(stream)))
+    _check(_packed.fp8_layernorm_fwd(
+        xm, _param(gamma, cols, "gamma"), _param(beta, cols, "beta"), _DTYPES[gamma.dtype],
+        eps, _matrix(y, "y"), _block(y8, "y8"), _block(x8, "x8"), _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), _stream(stream)))
 
 
 def fp8_layernorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: torch.Tensor,
@@ -885,12 +911,12 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: tor
     ``fp8_layernorm_bwd_workspace(rows, cols)`` bytes of CUDA memory; taken
     from torch's allocator when None."""
     dym = _matrix(dy, "dy")
-    rows, cols = dym.rows, dym.cols
+    rows, cols = dy.shape
     need = _lib.fp8_layernorm_bwd_workspace(rows, cols)
     if workspace is None:
         workspace = _scratch(need, dy.device, stream)
     saved = isinstance(x, BlockFp8)
-    _check(_lib.fp8_layernorm_bwd(
+    _check(_packed.fp8_layernorm_bwd(
         dym, None if saved else _matrix(x, "x"), _block(x, "x") if saved else None,
         _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], _stat(mean, rows, "mean"),
         _stat(rstd, rows, "rstd"), _matrix(dx, "dx"), _stat(dgamma, cols, "dgamma"),
@@ -911,7 +937,7 @@ def fp8_layernorm_recompute(x8: BlockFp8, gamma: torch.Tensor, beta: torch.Tenso
     if gamma.dtype != beta.dtype:
         raise ValueError("gamma and beta must have the same dtype")
     rows, cols = x8.shape
-    _check(_lib.fp8_layernorm_recompute(
+    _check(_packed.fp8_layernorm_recompute(
         _block(x8, "x8"), _param(gamma, cols, "gamma"), _param(beta, cols, "beta"),
         _DTYPES[gamma.dtype], _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"),
         _block(yt, "yt"), _stream(stream)))
@@ -921,7 +947,7 @@ def fp8_swiglu_fwd(h: torch.Tensor, a8: BlockFp8, h8: BlockFp8 | None = None,
                    stream=None) -> None:
     """SwiGLU of h = [gate | value], block quantized into ``a8``; ``h8``: h
     itself in 8 bits, for fp8_swiglu_bwd."""
-    _check(_lib.fp8_swiglu_fwd(_matrix(h, "h"), _block(a8, "a8"), _block(h8, "h8"),
+    _check(_packed.fp8_swiglu_fwd(_matrix(h, "h"), _block(a8, "a8"), _block(h8, "h8"),
                                _stream(stream)))
 
 
@@ -931,5 +957,5 @@ def fp8_swiglu_bwd(da: torch.Tensor, h8: BlockFp8, dh8: BlockFp8 | None = None,
     """Backward of SwiGLU from its 8-bit input: the gradient of h, block
     quantized as it is (``dh8``) and transposed (``dh8t``), and the forward's
     output again, transposed (``a8t``)."""
-    _check(_lib.fp8_swiglu_bwd(_matrix(da, "da"), _block(h8, "h8"), _block(dh8, "dh8"),
+    _check(_packed.fp8_swiglu_bwd(_matrix(da, "da"), _block(h8, "h8"), _block(dh8, "dh8"),
                                _block(dh8t, "dh8t"), _block(a8t, "a8t"), _stream(stream)))

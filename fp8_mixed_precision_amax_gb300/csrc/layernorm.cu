@@ -339,6 +339,8 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const LnFwdArgs a) {
     }
 }
 
+__host__ __device__ constexpr int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
 struct LnBwdArgs {
     const void *dy, *x;
     int64_t rows, cols, lddy, ldx, lddx;
@@ -347,7 +349,7 @@ struct LnBwdArgs {
     int wtype;
     const float *mean, *rstd;
     void *dx;
-    float *part;       // [gridDim.x][2][cols]: a CTA's sums of dy * xhat and dy
+    float *part;       // [gridDim.x][2][up8(cols)]: a CTA's sums of dy * xhat and dy
     float2 *row_sums;  // wide rows: [rows] sums of u and u * xhat
 };
 
@@ -446,23 +448,21 @@ __global__ void __launch_bounds__(512) ln_bwd_sums_kernel(const LnBwdArgs a) {
     }
 }
 
-// A CTA's sums over its rows, to its part of the workspace.
+// A CTA's sums over its rows, to its part of the workspace: [2][cols up to a multiple of 8].
 template <int VPT, int P, typename Col>
 __device__ __forceinline__ void store_part(const LnBwdArgs &a, Col col, const uint64_t (&dg)[VPT][P],
                                            const uint64_t (&db)[VPT][P]) {
-    float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+    const int64_t padded = up8(a.cols);
+    float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * padded;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const int64_t c = col(k);
+        if (c >= a.cols) continue;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            float lo, hi;
-            f32x2_unpack(dg[k][i], lo, hi);
-            if (c + 2 * i < a.cols) part[c + 2 * i] = lo;
-            if (c + 2 * i + 1 < a.cols) part[c + 2 * i + 1] = hi;
-            f32x2_unpack(db[k][i], lo, hi);
-            if (c + 2 * i < a.cols) part[a.cols + c + 2 * i] = lo;
-            if (c + 2 * i + 1 < a.cols) part[a.cols + c + 2 * i + 1] = hi;
+        for (int i = 0; i < P / 2; ++i) {
+            *reinterpret_cast<ulonglong2 *>(part + c + 4 * i) = make_ulonglong2(dg[k][2 * i], dg[k][2 * i + 1]);
+            *reinterpret_cast<ulonglong2 *>(part + padded + c + 4 * i) =
+                make_ulonglong2(db[k][2 * i], db[k][2 * i + 1]);
         }
     }
 }
@@ -663,35 +663,43 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const 
             L::store(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
         }
     }
-    float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
     if constexpr (WARP) {
-        // the warps add theirs one after the other
-        extern __shared__ float sums[];   // [2][cols]
+        // the warps that had rows (the first one always) add theirs one after the other;
+        // [column of the lane][lane], so that a warp's accesses meet no bank twice
+        __shared__ float sums[2][VPT * E][32];
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         for (int w = 0; w < kWarps; ++w) {
-            if (static_cast<int>(threadIdx.x >> 5) == w) {
+            if (warp == w && team.row < a.rows) {
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
-                        const int64_t c = col(k) + i;
-                        if (c >= a.cols) continue;
                         float lo, hi, lo2, hi2;
                         f32x2_unpack(dg[k][i / 2], lo, hi);
                         f32x2_unpack(db[k][i / 2], lo2, hi2);
-                        const float p = i & 1 ? hi : lo, q = i & 1 ? hi2 : lo2;
-                        sums[c] = w ? __fadd_rn(sums[c], p) : p;
-                        sums[a.cols + c] = w ? __fadd_rn(sums[a.cols + c], q) : q;
+                        float *p = &sums[0][k * E + i][lane], *q = &sums[1][k * E + i][lane];
+                        *p = w ? __fadd_rn(*p, i & 1 ? hi : lo) : i & 1 ? hi : lo;
+                        *q = w ? __fadd_rn(*q, i & 1 ? hi2 : lo2) : i & 1 ? hi2 : lo2;
                     }
             }
+            if (blockIdx.x * kWarps + w + 1 >= a.rows) break;   // no later warp had rows
             __syncthreads();
         }
-        for (int64_t c = threadIdx.x; c < 2 * a.cols; c += blockDim.x) part[c] = sums[c];
+        __syncthreads();
+        const int64_t padded = up8(a.cols);
+        float *part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * padded;
+        for (int64_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
+            const int slot = static_cast<int>(c / (32 * E)) * E + static_cast<int>(c % E);
+            const int of = static_cast<int>(c / E) & 31;
+            part[c] = sums[0][slot][of];
+            part[padded + c] = sums[1][slot][of];
+        }
     } else {
         store_part(a, col, dg, db);
     }
 }
 
-// dgamma and dbeta from the CTAs' sums [parts][2 cols]: 32 columns per CTA, 32
+// dgamma and dbeta from the CTAs' sums [parts][2][padded]: 32 columns per CTA, 32
 // threads down the parts for each, then a fixed tree.
 __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float *__restrict__ part,
                                                              int parts, int64_t cols,
@@ -701,21 +709,29 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float *__rest
     pdl_wait();
     pdl_trigger();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx;
+    const int64_t padded = up8(cols), c = static_cast<int64_t>(blockIdx.x) * 32 + tx;
     float s = 0.0f;
-    if (c < 2 * cols)
-        for (int p = ty; p < parts; p += 32) s = __fadd_rn(s, part[p * 2 * cols + c]);
+    if (c < 2 * padded) {
+        for (int p = ty; p < parts; p += 32 * 5) {   // five reads on their way together
+            float v[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                v[i] = p + 32 * i < parts ? part[(p + 32 * i) * 2 * padded + c] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) s = __fadd_rn(s, v[i]);
+        }
+    }
     red[ty][tx] = s;
     __syncthreads();
     s = red[tx][ty];
 #pragma unroll
     for (int o = 16; o; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
     const int64_t out = static_cast<int64_t>(blockIdx.x) * 32 + ty;
-    if (tx == 0 && out < 2 * cols) {
+    if (tx == 0) {
         if (out < cols)
             dgamma[out] = s;
-        else
-            dbeta[out - cols] = s;
+        else if (out >= padded && out < padded + cols)
+            dbeta[out - padded] = s;
     }
 }
 
@@ -770,7 +786,11 @@ int64_t bwd_ctas(int64_t rows, int64_t cols) {
     constexpr int64_t sms = 152;
     if (cols <= kBwdNarrow) return capped((rows + kWarps - 1) / kWarps, 2 * sms);
     if (cols > kBwdWide) return capped(rows, sms);
-    return capped(rows, sms * ring_ctas_per_sm(row_threads(cols, 16)));
+    // eight rows each once there is a CTA per SM: every CTA's sums are written, read and
+    // added (2048 x 1024: 18.7 us with 1216 CTAs)
+    const int64_t some = rows / 8 > sms ? rows / 8 : sms;
+    const int64_t most = sms * ring_ctas_per_sm(row_threads(cols, 16));
+    return capped(rows, some < most ? some : most);
 }
 
 // As many rows in flight as the CTAs of an SM have shared memory for.
@@ -808,19 +828,18 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
     const dim3 grid(g);
     cudaError_t e;
     if (a.cols <= kBwdNarrow) {
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, true, false, VEC>, grid, dim3(32 * kWarps),
-                       static_cast<size_t>(2 * a.cols * 4), st, a);
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, true, false, VEC>, grid, dim3(32 * kWarps), 0, st, a);
     } else if (a.cols <= kBwdWide) {
         e = ln_bwd_ring<T, SAVED, VEC != 0>(a, g, st);
     } else {
-        a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * a.cols);
+        a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * up8(a.cols));
         e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * 152)), dim3(512), 0, st, a);
         if (e != cudaSuccess) return e;
         const dim3 slabs(g, static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab));
         e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, false, true, VEC>, slabs, dim3(256), 0, st, a);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32)),
+    return launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * up8(a.cols) + 31) / 32)),
                       dim3(1024), 0, st, static_cast<const float *>(a.part), g, a.cols, dgamma,
                       dbeta);
 }
@@ -841,7 +860,7 @@ cudaError_t launch_ln_fwd(const MatView &x, const void *gamma, const void *beta,
 }
 
 int64_t ln_bwd_workspace(int64_t rows, int64_t cols) {
-    return bwd_ctas(rows, cols) * 2 * cols * 4 + (cols > kBwdWide ? rows * 8 : 0);
+    return bwd_ctas(rows, cols) * 2 * up8(cols) * 4 + (cols > kBwdWide ? rows * 8 : 0);
 }
 
 cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
