@@ -477,8 +477,9 @@ struct RowWriter {
     uint8_t *scale;
 
     __device__ __forceinline__ void start(const BlockView &q, int64_t row, int64_t c) {
-        code = q.codes + row * q.ld + c;
-        scale = static_cast<uint8_t *>(q.scales) + (row * q.ld_s + (c >> 7)) * (q.scale_f32 ? 4 : 1);
+        code = q.codes + row_at(static_cast<unsigned>(row), q.ld) + c;
+        scale = static_cast<uint8_t *>(q.scales) +
+                (row_at(static_cast<unsigned>(row), q.ld_s) + (c >> 7)) * (q.scale_f32 ? 4 : 1);
     }
     __device__ __forceinline__ void move(const BlockView &q, unsigned rows) {
         code += row_at(rows, q.ld);
