@@ -90,16 +90,41 @@ struct ScaleStream {
 // loads its own 128 rows of A and 128 of the 256 rows of B, and the even CTA
 // issues MMAs that read both CTAs' shared memory and write both CTAs' TMEM.
 
+// The tiles of the last, partial wave are cut into four pieces by columns where that many
+// pairs would have nothing to do otherwise (4096 x 11008 has 9 waves of 76 pairs and 4
+// tiles: 16 pieces).  Each sum is the same.
+constexpr int kPieces = 4;
+
 struct PairArgs {
     CUtensorMap mapA, mapB, mapD;
+    CUtensorMap mapBPart;   // mapB with the rows of a piece
     BlockView A, B;
     __nv_bfloat16 *D;
     int64_t M, N, ldd;
     bool tma_d;     // D's rows are 16-byte aligned: store by TMA
     bool pairs_d;   // D's rows are 4-byte aligned
-    int tiles_m, tiles_n, num_tiles, num_kb, group_m;
-    uint32_t idesc;
+    int tiles_m, tiles_n, num_items, num_kb, group_m;
+    int whole;   // items from this one on are pieces
+    uint32_t idesc, idesc_part;
 };
+
+struct Item {
+    int64_t row0;   // of the pair's 256 rows of D
+    int64_t col0;
+    int width;      // columns: 256, of a piece 64
+};
+
+__device__ __forceinline__ Item item_at(const PairArgs &a, int item) {
+    const bool part = item >= a.whole;
+    const int tile = part ? a.whole + (item - a.whole) / kPieces : item;
+    int mb, nb;
+    tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+    Item t;
+    t.row0 = static_cast<int64_t>(mb) * 2 * BM;
+    t.width = part ? BN / kPieces : BN;
+    t.col0 = static_cast<int64_t>(nb) * BN + (part ? (item - a.whole) % kPieces * t.width : 0);
+    return t;
+}
 
 // The producer warp: A and B slices of every k-block of the pair's tiles.
 template <int STAGES>
@@ -110,11 +135,12 @@ __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int un
     uint32_t phase = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
-        int mb, nb;
-        tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
-        const int32_t arow = mb * 2 * BM + static_cast<int32_t>(rank) * BM;
-        const int32_t brow = nb * BN + static_cast<int32_t>(rank) * (BN / 2);
+    for (int item = unit; ok && item < a.num_items; item += num_units) {
+        const Item t = item_at(a, item);
+        const int32_t arow = static_cast<int32_t>(t.row0) + static_cast<int32_t>(rank) * BM;
+        const int32_t brow = static_cast<int32_t>(t.col0) + static_cast<int32_t>(rank) * (t.width / 2);
+        const CUtensorMap *mapB = t.width == BN ? &a.mapB : &a.mapBPart;
+        const uint32_t bytes = 2 * HALF + t.width * BK;
         for (int kb = 0; kb < a.num_kb; ++kb) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag))) {
                 if ((threadIdx.x & 31) == 0) raise_error(abort_flag);
@@ -124,9 +150,9 @@ __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int un
             if (elect_one()) {
                 // both CTAs' halves complete on the even CTA's barrier
                 const uint32_t fb = full0 + 8 * stage, fb0 = mapa_shared(fb, 0);
-                if (rank == 0) mbar_arrive_expect_tx(fb, 4 * HALF);
+                if (rank == 0) mbar_arrive_expect_tx(fb, bytes);
                 tma_load_2d_pair(sA + stage * HALF, &a.mapA, fb0, kb * BK, arow);
-                tma_load_2d_pair(sB + stage * HALF, &a.mapB, fb0, kb * BK, brow);
+                tma_load_2d_pair(sB + stage * HALF, mapB, fb0, kb * BK, brow);
             }
             __syncwarp();
             ++issued;
@@ -158,13 +184,13 @@ __device__ __forceinline__ void produce(const PairArgs &a, uint32_t rank, int un
 
 // A warp's 32 rows x 64 columns of BF16 to D at (row0, col0) from its staging buffer,
 // where 16-byte chunk j of row r sits at j ^ (r mod 8): the 128-byte swizzle of D's
-// tensor map.  Rows of D that TMA cannot address go out with each warp instruction
-// along one row.
+// tensor map.  Rows of D that TMA cannot address, and chunks of 32 columns, go out with
+// each warp instruction along one row.
 __device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, int64_t row0,
-                                            int64_t col0) {
+                                            int64_t col0, int cols = EPI_COLS) {
     const int lane = threadIdx.x & 31;
     // a TMA store clips at 16-byte steps: a chunk that ends inside one goes the other way
-    if (a.tma_d && (col0 + EPI_COLS <= a.N || a.N % 8 == 0)) {
+    if (a.tma_d && cols == EPI_COLS && (col0 + EPI_COLS <= a.N || a.N % 8 == 0)) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -175,7 +201,7 @@ __device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, in
         return;
     }
     __syncwarp();
-    const int64_t c = col0 + 2 * lane;
+    const int64_t c = col0 + 2 * lane, end = min(a.N, col0 + cols);
     const int rows = row0 >= a.M ? 0 : a.M - row0 < 32 ? static_cast<int>(a.M - row0) : 32;
     for (int r = 0; r < rows; ++r) {
         uint32_t w;
@@ -184,11 +210,11 @@ __device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, in
                      : "r"(sbuf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2))
                      : "memory");
         uint16_t *d = reinterpret_cast<uint16_t *>(a.D + (row0 + r) * a.ldd + c);
-        if (a.pairs_d && c + 1 < a.N) {
+        if (a.pairs_d && c + 1 < end) {
             *reinterpret_cast<uint32_t *>(d) = w;
         } else {
-            if (c < a.N) d[0] = static_cast<uint16_t>(w);
-            if (c + 1 < a.N) d[1] = static_cast<uint16_t>(w >> 16);
+            if (c < end) d[0] = static_cast<uint16_t>(w);
+            if (c + 1 < end) d[1] = static_cast<uint16_t>(w >> 16);
         }
     }
     __syncwarp();
@@ -213,6 +239,9 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 // CTA's rows of A, 8 for the tile's rows of B, the same in all four lane quarters);
 // the MMAs of k-block 4 g + b name byte b in their descriptor.  A block of 128 is
 // four of the instruction's blocks of 32 with the same scale.
+//
+// Bound by the tensor pipe, and in back-to-back calls by the power limit: 8192 x 11008 x
+// 4096 takes 218 us (3390 TFLOP/s), 8192 x 28672 x 8192 1067 us (3610).
 
 constexpr int MX_STAGES = 6;
 constexpr int MX_THREADS = 384;
@@ -277,7 +306,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             int stage = 0, sf = 0, it = 0;
             uint32_t phase = 0, sf_phase = 0;
             bool ok = true, any = false;
-            for (int tile = unit; ok && tile < a.num_tiles; tile += num_units, ++it) {
+            for (int item = unit; ok && item < a.num_items; item += num_units, ++it) {
+                const uint32_t idesc0 = item < a.whole ? a.idesc : a.idesc_part;
                 // the previous tile's epilogue has read the columns the two share
                 const bool freed =
                     it == 0 || mbar_wait(acce, static_cast<uint32_t>(it - 1) & 1u, abort_flag);
@@ -300,7 +330,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t sfa = tmem + MX_SF + sf * MX_SF_STRIDE, sfb = sfa + 4;
-                        const uint32_t idesc = a.idesc | static_cast<uint32_t>(kb & 3) << 4 |
+                        const uint32_t idesc = idesc0 | static_cast<uint32_t>(kb & 3) << 4 |
                                                static_cast<uint32_t>(kb & 3) << 29;
                         const uint64_t ad = smem_desc_sw128(sA + stage * HALF);
                         const uint64_t bd = smem_desc_sw128(sB + stage * HALF);
@@ -339,19 +369,17 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         int sf = 0;
         uint32_t sf_phase = 0;
         bool ok = true;
-        for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
-            int mb, nb;
-            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
-            const uint8_t *ra[4], *rb[8];
+        for (int item = unit; ok && item < a.num_items; item += num_units) {
+            const Item t = item_at(a, item);
+            const uint8_t *ra[4], *rb[8];   // of a piece the first B words are used
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t r = min(static_cast<int64_t>(mb) * 2 * BM + rank * BM + 32 * j + lane,
-                                      a.M - 1);
+                const int64_t r = min(t.row0 + rank * BM + 32 * j + lane, a.M - 1);
                 ra[j] = pa + (a.A.block_rows == 1 ? r : r >> 7) * a.A.ld_s;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int64_t r = min(static_cast<int64_t>(nb) * BN + 32 * j + lane, a.N - 1);
+                const int64_t r = min(t.col0 + 32 * j + lane, a.N - 1);
                 rb[j] = pb + (a.B.block_rows == 1 ? r : r >> 7) * a.B.ld_s;
             }
             for (int kb = 0; kb < a.num_kb; kb += 4) {
@@ -391,9 +419,8 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         const int q = warp & 3;   // TMEM lane quarter
         uint32_t chunk = 0;       // chunks staged so far (selects the buffer)
         int it = 0;
-        for (int tile = unit; tile < a.num_tiles; tile += num_units, ++it) {
-            int mb, nb;
-            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
+        for (int item = unit; item < a.num_items; item += num_units, ++it) {
+            const Item tile = item_at(a, item);
             const bool got = mbar_wait(accf0 + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got)) {
                 if (lane == 0) raise_error(abort_flag);
@@ -401,10 +428,11 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
             }
             tc_fence_after();
             const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + ((it & 1) ? MX_ACC1 : 0);
-            const int64_t row0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM + q * 32;
+            const int64_t row0 = tile.row0 + rank * BM + q * 32;
+            const int chunks_here = tile.width / EPI_COLS;
 #pragma unroll 1
-            for (int i = 0; i < BN / EPI_COLS; ++i) {
-                const int c = (it & 1) ? i : BN / EPI_COLS - 1 - i;   // the shared columns first
+            for (int i = 0; i < chunks_here; ++i) {
+                const int c = (it & 1) ? i : chunks_here - 1 - i;   // the shared columns first
                 uint32_t r[2][32];
                 tmem_load_32cols(t + c * EPI_COLS, r[0]);
                 tmem_load_32cols(t + c * EPI_COLS + 32, r[1]);
@@ -428,7 +456,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
                 for (int j = 0; j < 8; ++j)
                     st_shared_v4(sbuf + lane * 128 + ((j ^ (lane & 7)) << 4), packed[4 * j],
                                  packed[4 * j + 1], packed[4 * j + 2], packed[4 * j + 3]);
-                store_chunk(a, sbuf, row0, static_cast<int64_t>(nb) * BN + c * EPI_COLS);
+                store_chunk(a, sbuf, row0, tile.col0 + c * EPI_COLS);
                 ++chunk;
             }
         }
@@ -459,7 +487,7 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool pred) {
 
 // ----------------------------------------------------------------- f32 kernel --
 // Warps: 0 TMA, 1 MMA (2 and 3 idle), 4-11 sums: warp w has lane quarter w mod 4 and
-// half (w - 4) / 4 of the tile's columns, 128 sums per thread.  Each k-block's MMAs
+// half (w - 4) / 4 of the item's columns, 128 sums per thread.  Each k-block's MMAs
 // start a fresh accumulator in one of two TMEM buffers; while one is summed the other
 // is computed.  Of the launch's 384 x 168 registers the first four warps hand back
 // 96 each per thread and the eight summing warps take 48 more: 128 x 72 + 256 x 216.
@@ -470,6 +498,11 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool pred) {
 // it needs 128 of B, and their 128 x 32 lanes x 4 bytes from shared memory took twice
 // the MMAs' time.)  PER_ROW: B has one scale per row; otherwise the 128 columns of a
 // warp share one.
+//
+// Bound by TMEM: MMAs that accumulate and the sums' reads share it, and a k-block takes
+// some 1300 cycles where its MMAs alone take 512.  8192 x 11008 x 4096 with tiles of B:
+// 465 us, 1590 TFLOP/s; 4096 x 11008 x 8192 with a scale per row of B, which costs each
+// sum a multiplication more: 512 us, 1440 TFLOP/s.
 
 constexpr int FS_STAGES = 5;
 constexpr int FS_THREADS = 384;
@@ -482,6 +515,58 @@ constexpr int FS_BARS = 2 * FS_STAGES + 4 + 1;
 constexpr int FS_CLASS = 36, FS_SB = 8 * FS_CLASS;
 constexpr size_t FS_SMEM = 1024 + FS_STAGES * 2 * HALF + 8 * EPI_BUF + 8 * (FS_SB + BM) * 4 +
                            FS_BARS * 8 + 16;
+
+// 16 lanes x 32 columns of a k-block's dot products, times their scales onto the sums; h / 2
+// is the group of 32 columns, h mod 2 the half of the lanes.  LAST: the accumulator has
+// been read.
+template <bool PER_ROW>
+__device__ __forceinline__ void add_step(int h, bool last, uint32_t t, const float *sbk,
+                                         const uint64_t (&sa2)[4], uint64_t (&sb2)[4],
+                                         uint32_t freed, uint64_t (&sum)[4][16]) {
+    uint32_t v[16];
+    tmem_load_16x256b_x4(t + (h >> 1) * 32 + (static_cast<uint32_t>(h & 1) << 20), v);
+    if (PER_ROW && (h & 1) == 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(sbk + (h >> 1) * 8 + 4 * j);
+            sb2[2 * j] = u.x, sb2[2 * j + 1] = u.y;
+        }
+    }
+    tmem_wait_16cols(v);
+    if (last) {
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_cluster_relaxed(mapa_shared(freed, 0));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t x = f32x2_pack(__uint_as_float(v[4 * j + 2 * i]),
+                                          __uint_as_float(v[4 * j + 2 * i + 1]));
+            const uint64_t s1 = sa2[2 * (h & 1) + i];
+            uint64_t &to = sum[2 * (h & 1) + i][4 * (h >> 1) + j];
+            to = f32x2_fma(x, PER_ROW ? f32x2_mul(s1, sb2[j]) : s1, to);
+        }
+    }
+}
+
+// A warp's share of a k-block: 128 columns, or 32 of a piece.
+template <bool PER_ROW>
+__device__ __forceinline__ void add_block(uint32_t t, const float *sbk, const uint64_t (&sa2)[4],
+                                          uint32_t freed, bool whole, uint64_t (&sum)[4][16]) {
+    uint64_t sb2[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) add_step<PER_ROW>(h, false, t, sbk, sa2, sb2, freed, sum);
+    if (whole) {
+#pragma unroll
+        for (int h = 2; h < 8; ++h) add_step<PER_ROW>(h, h == 7, t, sbk, sa2, sb2, freed, sum);
+    } else {
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive_cluster_relaxed(mapa_shared(freed, 0));
+    }
+}
 
 template <bool PER_ROW>
 __global__ void __launch_bounds__(FS_THREADS, 1)
@@ -539,7 +624,8 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true, any = false;
-            for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+            for (int item = unit; ok && item < a.num_items; item += num_units) {
+                const uint32_t idesc = item < a.whole ? a.idesc : a.idesc_part;
                 for (int kb = 0; kb < a.num_kb; ++kb) {
                     const bool go = mbar_wait(acce0 + 8 * acc, acc_phase ^ 1u, abort_flag) &&
                                     mbar_wait(full0 + 8 * stage, phase, abort_flag);
@@ -554,7 +640,7 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                         const uint64_t bd = smem_desc_sw128(sB + stage * HALF);
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            mma_f8f6f4_pair(tmem + acc * BN, ad + 2 * k, bd + 2 * k, a.idesc, k != 0);
+                            mma_f8f6f4_pair(tmem + acc * BN, ad + 2 * k, bd + 2 * k, idesc, k != 0);
                         mma_commit_pair(empty0 + 8 * stage, 0x3);
                         mma_commit_pair(accf0 + 8 * acc, 0x3);
                     }
@@ -580,24 +666,24 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FS_REGS_SUMS));
         const int q = warp & 3, half = (warp - 4) >> 2;
         const int et = threadIdx.x - 128;   // 0..255: the column (and row) whose scales it fetches
-        const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
         const uint32_t sbuf = sD + (warp - 4) * EPI_BUF;
-        const int own_col = (et >> 7) * 4 * FS_CLASS + ((et >> 1) & 3) * FS_CLASS +
-                            ((et >> 3) & 15) * 2 + (et & 1);
         const int my_cols = half * 4 * FS_CLASS + (lane & 3) * FS_CLASS;
         const int my_row = q * 32 + (lane >> 2);
-        int acc = 0;
-        uint32_t acc_phase = 0;
+        uint32_t n = 0;   // k-blocks so far: accumulator n mod 2
         bool ok = true;
-        for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
-            int mb, nb;
-            tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
-            const int64_t crow0 = static_cast<int64_t>(mb) * 2 * BM + rank * BM;
-            const int64_t col0 = static_cast<int64_t>(nb) * BN;
+        for (int item = unit; ok && item < a.num_items; item += num_units) {
+            const int hw = item < a.whole ? 128 : 32;   // columns of a half of the item
+            const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * hw;
+            const int own_col = (et >= hw ? 4 * FS_CLASS : 0) + ((et >> 1) & 3) * FS_CLASS +
+                                ((et & (hw - 1)) >> 3) * 2 + (et & 1);
+            const bool has_col = et < 2 * hw;
             // rows and columns past the end repeat the last one
             ScaleStream fa, fb;
-            if (et < BM) fa.start(a.A, min(crow0 + et, a.M - 1), 0, a.num_kb);
-            fb.start(a.B, min(col0 + et, a.N - 1), 0, a.num_kb);
+            {
+                const Item tile = item_at(a, item);
+                if (et < BM) fa.start(a.A, min(tile.row0 + rank * BM + et, a.M - 1), 0, a.num_kb);
+                fb.start(a.B, min(tile.col0 + et, a.N - 1), 0, a.num_kb);
+            }
             uint64_t sum[4][16];   // [row lane / 4 + 8 i][columns 8 j + 2 (lane mod 4), + 1]
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -617,68 +703,35 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                     fb.take();
                     fb.fetch((kb >> 2) + 1);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sbs[((kb & 7) + i) * FS_SB + own_col] = fb.cur[i];
+                    for (int i = 0; i < 4; ++i)
+                        if (has_col) sbs[((kb & 7) + i) * FS_SB + own_col] = fb.cur[i];
                     asm volatile("bar.sync 1, 256;" ::: "memory");
                 }
                 const float *sbk = sbs + (kb & 7) * FS_SB + my_cols;
                 const float *sak = sas + (kb & 7) * BM + my_row;
-                uint64_t sa2[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sa2[i] = splat_f32x2(PER_ROW ? sak[8 * i] : __fmul_rn(sak[8 * i], sbk[0]));
-                const bool got = mbar_wait(accf0 + 8 * acc, acc_phase, abort_flag);
+                const bool got = mbar_wait(accf0 + 8 * (n & 1), (n >> 1) & 1u, abort_flag);
                 if (!__all_sync(0xFFFFFFFFu, got)) {
                     if (lane == 0) raise_error(abort_flag);
                     ok = false;   // goes on to this tile's end, where all agree to stop
                 }
+                uint64_t sa2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sa2[i] = splat_f32x2(PER_ROW ? sak[8 * i] : __fmul_rn(sak[8 * i], sbk[0]));
                 if (ok) {
                     tc_fence_after();
-                    const uint32_t t = t0 + acc * BN;
-                    uint64_t sb2[4];
-#pragma unroll
-                    for (int h = 0; h < 8; ++h) {
-                        // 32 columns (h / 2) of the quarter's lanes 16 (h mod 2) .. + 15
-                        uint32_t v[16];
-                        tmem_load_16x256b_x4(t + (h >> 1) * 32 + (static_cast<uint32_t>(h & 1) << 20), v);
-                        if (PER_ROW && (h & 1) == 0) {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(
-                                    sbk + (h >> 1) * 8 + 4 * j);
-                                sb2[2 * j] = u.x, sb2[2 * j + 1] = u.y;
-                            }
-                        }
-                        tmem_wait_16cols(v);
-                        if (h == 7) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive_cluster_relaxed(mapa_shared(acce0 + 8 * acc, 0));
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint64_t x = f32x2_pack(__uint_as_float(v[4 * j + 2 * i]),
-                                                              __uint_as_float(v[4 * j + 2 * i + 1]));
-                                const uint64_t s1 = sa2[2 * (h & 1) + i];
-                                uint64_t &to = sum[2 * (h & 1) + i][4 * (h >> 1) + j];
-                                to = f32x2_fma(x, PER_ROW ? f32x2_mul(s1, sb2[j]) : s1, to);
-                            }
-                        }
-                    }
+                    add_block<PER_ROW>(t0 + (n & 1) * BN, sbk, sa2, acce0 + 8 * (n & 1), item < a.whole, sum);
                 }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
-                }
+                ++n;
             }
             // all have read the last scales before the next tile's are written, and all
             // go on or none: a warp alone in the next tile's barriers would stay there
             ok = barrier_and(1, 256, ok);
             if (ok) {
+                const Item tile = item_at(a, item);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    if (c * EPI_COLS >= hw) break;
                     if (lane == 0) bulk_wait_group_read<0>();
                     __syncwarp();
 #pragma unroll
@@ -694,7 +747,8 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
                                          : "memory");
                         }
                     }
-                    store_chunk(a, sbuf, crow0 + q * 32, col0 + half * 128 + c * EPI_COLS);
+                    store_chunk(a, sbuf, tile.row0 + rank * BM + q * 32, tile.col0 + half * hw + c * EPI_COLS,
+                                min(hw, EPI_COLS));
                 }
             }
         }
@@ -1190,6 +1244,7 @@ cudaError_t launch_few_any(const BlockView &A, const BlockView &B, const MatView
 
 constexpr int64_t kFewRows = 128;   // the few kernel up to this many rows of A,
 constexpr int64_t kFewTiles = 38;   // or up to this many 256 x 256 tiles
+constexpr int kMxPieceWaves = 6;
 
 }  // namespace
 
@@ -1225,12 +1280,27 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     a.ldd = D.ld;
     a.tiles_m = static_cast<int>((D.rows + 2 * BM - 1) / (2 * BM));
     a.tiles_n = static_cast<int>((D.cols + BN - 1) / BN);
-    a.num_tiles = a.tiles_m * a.tiles_n;
+    // The last wave in pieces.  With float scales it always pays (4096 x 11008 x 8192, 9
+    // waves: 512 us, whole 530; 2304 x 2560 x 4096: 45.3 and 52.5).  The mx kernel runs into the power limit where there are
+    // many waves, and the pairs that idle in the last one cost nothing (2304 x 2560 x 4096,
+    // 1.2 waves: 25.7 us, whole 28.0; 4 waves 58.7 and 60.0; 8 waves 106.3 and 105.3).
+    const int num_tiles = a.tiles_m * a.tiles_n, rest = num_tiles % pk.slots;
+    const bool pieces = kPieces * rest <= pk.slots && (!mx || num_tiles < kMxPieceWaves * pk.slots);
+    a.whole = pieces ? num_tiles - rest : num_tiles;
+    a.num_items = a.whole + (num_tiles - a.whole) * kPieces;
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
     a.group_m = raster_group(D.rows * A.cols, D.cols * A.cols, a.tiles_m);
     const uint32_t fa = static_cast<uint32_t>(A.fmt), fb = static_cast<uint32_t>(B.fmt);
-    a.idesc = mx ? idesc_mxf8(fa, fb, 2 * BM, BN, 0) : idesc_f8(fa, fb, 2 * BM, BN);
-    const int units = a.num_tiles < pk.slots ? a.num_tiles : pk.slots;
+    const auto idesc = [&](int n) {
+        return mx ? idesc_mxf8(fa, fb, 2 * BM, n, 0) : idesc_f8(fa, fb, 2 * BM, n);
+    };
+    a.idesc = idesc(BN);
+    a.idesc_part = idesc(BN / kPieces);
+    if (!encode_tmap_2d(&a.mapBPart, B.codes, false, B.cols, B.rows, BK, BN / 2 / kPieces, true, B.ld)) {
+        *what = "cuTensorMapEncodeTiled failed for an operand";
+        return cudaErrorInvalidValue;
+    }
+    const int units = a.num_items < pk.slots ? a.num_items : pk.slots;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), pk.threads, pk.smem, 2, attr, st);
     return cudaLaunchKernelEx(&cfg, pk.kernel, a);

@@ -222,6 +222,22 @@ def test_gemm_larger(M, N, K, sd):
 
 
 @pytest.mark.parametrize("sd", [torch.uint8, torch.float32])
+@pytest.mark.parametrize("bb", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(2200, 2250, 300), (2304, 2305, 1100), (2500, 2503, 640),
+                                   (2560, 2560, 130), (4900, 4801, 40)])
+def test_gemm_last_wave_in_pieces(M, N, K, sd, bb):
+    """A few more 256 x 256 tiles than CTA pairs: the last ones are cut by columns."""
+    f = _lib()
+    A, B = operand(M, K, 1, 1, sd, M), operand(N, K, 0, bb, sd, N)
+    for pad in (0, 8 - N % 8):
+        D = torch.full((M + 1, N + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        f.fp8_block_gemm_tn(A, B, D[:M, :N])
+        f.fp8_sync_status()
+        check_gemm(A, B, D[:M, :N], (M, N, K, sd, bb, pad))
+        assert (D[M] == 7).all() and (D[:, N:] == 7).all()
+
+
+@pytest.mark.parametrize("sd", [torch.uint8, torch.float32])
 @pytest.mark.parametrize("M,N,K", [(4, 256, 512), (300, 256, 512)])
 def test_gemm_special_values(M, N, K, sd):
     """NaN codes, NaN scales, infinities (E5M2) and a block of zeros under the smallest scale."""
