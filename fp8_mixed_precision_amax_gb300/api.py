@@ -912,16 +912,19 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: tor
     from torch's allocator when None."""
     dym = _matrix(dy, "dy")
     rows, cols = dy.shape
-    need = _lib.fp8_layernorm_bwd_workspace(rows, cols)
     if workspace is None:
-        workspace = _scratch(need, dy.device, stream)
+        room = _lib.fp8_layernorm_bwd_workspace(rows, cols)
+        workspace = _scratch(room, dy.device, stream)
+        place = workspace.data_ptr()
+    else:
+        room = workspace.numel() * workspace.element_size()
+        place = _ptr(workspace, None, "workspace")
     saved = isinstance(x, BlockFp8)
     _check(_packed.fp8_layernorm_bwd(
         dym, None if saved else _matrix(x, "x"), _block(x, "x") if saved else None,
         _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], _stat(mean, rows, "mean"),
         _stat(rstd, rows, "rstd"), _matrix(dx, "dx"), _stat(dgamma, cols, "dgamma"),
-        _stat(dbeta, cols, "dbeta"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        _stat(dbeta, cols, "dbeta"), place, room, _stream(stream)))
 
 
 def fp8_layernorm_bwd_workspace(rows: int, cols: int) -> int:

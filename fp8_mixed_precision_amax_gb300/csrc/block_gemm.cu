@@ -776,9 +776,9 @@ __global__ void __launch_bounds__(FS_THREADS, 1)
 //        accumulators, so that the MMAs run ahead of the sums.
 // Shared memory and TMEM allow two CTAs per SM, so that one's start and end overlap the
 // other's loads.  One SM alone reads some 65 GB/s whatever its ring holds, so K is split
-// until all SMs read: 1 x 4096 x 4096 takes 13.4 us unsplit and 6.8 in 8 parts.  The
-// join costs more with more tokens: 128 x 11008 x 4096 takes 18.9 us unsplit and
-// 19.1 in 3 parts, and a tile of 128 tokens is not split.
+// until all SMs read: 1 x 4096 x 4096 took 13.4 us unsplit and 6.8 in 8 parts (5.5 since
+// the MMA warp issues as one).  The join costs more with more tokens: 128 x 11008 x 4096
+// takes 18.9 us unsplit and 19.1 in 3 parts, and a tile of 128 tokens is not split.
 
 template <int NT, bool MX>
 struct Few {

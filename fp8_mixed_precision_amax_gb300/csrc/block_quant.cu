@@ -3,8 +3,10 @@
 // output again, and SwiGLU forward and backward.  The formulas are in
 // include/fp8amax.h; block.cuh has the scale rule and the tile's layout.
 //
-// All are bound by HBM.  What has to be written transposed goes tile by tile
-// (128 x 128, one block wide both ways), the rest row by row.
+// Each value is read once and each result written once.  What has to be written
+// transposed goes tile by tile (128 x 128, one block wide both ways), the rest row by
+// row.  HBM is the floor; the instructions per element bind before it where much is
+// computed of each.
 #include <cstdint>
 #include <mutex>
 
@@ -23,7 +25,9 @@ struct QuantSmem {
     uint32_t red[2][16];
 };
 
-// Both ways or the transpose alone; also tiles row-major.
+// Both ways or the transpose alone; also tiles row-major.  Two CTAs per SM, so that one's
+// barriers fall into the other's work: 8192 x 4096 BF16 both ways 24 us, 5.6 TB/s of the
+// bytes it must move (0.83 of a copy's rate); 1000 x 2731 fp32 in tiles 9.4 us, a latency.
 template <typename T, int FMT, bool TILE>
 __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 4 ? 1 : 2)
     block_quantize_kernel(const T *__restrict__ x, int64_t rows, int64_t cols, int64_t ld, bool vec,
@@ -206,7 +210,8 @@ __device__ __forceinline__ float sigmoid(float x) {
     return s;
 }
 
-// 16 lanes per block of 128 columns of a row, two blocks per warp.
+// 16 lanes per block of 128 columns of a row, two blocks per warp.  777 x 2688 BF16: 4.6
+// us, where reading and writing alone is 2.2.
 template <typename T>
 __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h, int64_t M, int64_t F,
                                                          int64_t ld, bool vec, const BlockView a8,
@@ -253,7 +258,9 @@ struct SwigluSmem {
     ColsSmem cols[3];   // d gate, d value, the output
 };
 
-// The three results of a tile in registers at once: 192 KB of the SM's 256.
+// The three results of a tile in registers at once: 192 KB of the SM's 256, so one CTA
+// per SM.  Bound by issue slots (57 %; 46 instructions per element of da) and the three
+// barriers of a tile: 8192 x 11008 BF16 176 us, 4.6 TB/s (0.68 of a copy's rate).
 template <typename T, int FMT, int AFMT, int HFMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_bwd_kernel(const T *__restrict__ da, int64_t M, int64_t F, int64_t ld, bool vec,

@@ -221,7 +221,8 @@ __device__ __forceinline__ uint64_t deviations(const uint64_t (&x)[P], uint64_t 
 
 // A team works on R rows side by side, one step apart: their sums share the exchanges and
 // the barriers, and one row's arithmetic fills the other's waits (8192 x 4096, y alone:
-// 27.7 us with two, 31.0 with one).  Rows that have to be shifted into place leave no
+// 27.7 us with two, 31.0 with one; y and x in 8 bits: 37.4 us, of which the blocks' maxima
+// and codes are about half).  Rows that have to be shifted into place leave no
 // registers for a second.
 template <typename T, int VPT, bool WARP, int VEC>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_fwd_kernel(const LnFwdArgs a) {
@@ -501,7 +502,9 @@ __device__ __forceinline__ void store_part(const LnBwdArgs &a, Col col, const ui
 // dy and x are on their way into a ring in shared memory by bulk copies of the 16-byte
 // blocks that hold them, whatever their alignment; the barrier of a row's sums
 // also tells that its place in the ring may be filled again.  (With the next row in
-// registers instead, one row's loads were in flight per CTA: 91 us at 8192 x 8192.)
+// registers instead, one row's loads were in flight per CTA: 91 us at 8192 x 8192, and 73
+// so, 0.82 of a copy's rate.  Issue slots (44 %) and the row's barrier bind now; rows that
+// start anywhere cost 640 instructions per warp for 350: 5003 x 4111 from 8 bits 56 us.)
 constexpr int kRing = 8;   // most rows in flight
 
 struct RingArgs {
