@@ -383,8 +383,10 @@ struct LnBwdArgs {
     float2 *row_sums;  // wide rows: [rows] sums of u and u * xhat
 };
 
-// 8 codes times their scale; `left` of them belong to the row, the others may be anything.
-__device__ __forceinline__ void codes8(uint2 w, int fmt, float scale, int left, uint64_t (&v)[4]) {
+// 8 codes times their scale plus a number; `left` of them belong to the row, the others
+// may be anything.  (A code times a power of two is exact: one rounding either way.)
+__device__ __forceinline__ void codes8(uint2 w, int fmt, float scale, uint64_t plus, int left,
+                                       uint64_t (&v)[4]) {
     const uint64_t s2 = splat_f32x2(scale);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -394,21 +396,29 @@ __device__ __forceinline__ void codes8(uint2 w, int fmt, float scale, int left, 
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = 4 * i + k < left ? f[k] : 0.0f;
         }
-        v[2 * i] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
-        v[2 * i + 1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
+        v[2 * i] = f32x2_fma(f32x2_pack(f[0], f[1]), s2, plus);
+        v[2 * i + 1] = f32x2_fma(f32x2_pack(f[2], f[3]), s2, plus);
     }
 }
 
-// Columns of x on their way: as they are, or codes with their block's scale.
+// v + plus
+template <int P>
+__device__ __forceinline__ void add_all(uint64_t plus, uint64_t (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = f32x2_add(v[i], plus);
+}
+
+// Columns of x on their way, as they are or codes with their block's scale; get: x - mean.
 template <typename T, bool SAVED, int VEC>
 struct RawX {
     typename Lay<T, VEC>::Raw raw;
     __device__ __forceinline__ void load(const LnBwdArgs &a, int64_t row, int64_t c) {
         raw.load(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols);
     }
-    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t row, int64_t c,
+    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t row, int64_t c, uint64_t nmu2,
                                         uint64_t (&v)[Lay<T, VEC>::P]) const {
         raw.get(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, v);
+        add_all(nmu2, v);
     }
 };
 template <typename T, int VEC>
@@ -428,20 +438,23 @@ struct RawX<T, true, VEC> {
             scale = 0;
         }
     }
-    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t, int64_t c, uint64_t (&v)[P]) const {
-        codes8(make_uint2(w[0], w[1]), a.x8.fmt, fetched_scale(a.x8, scale), VEC ? 8 : static_cast<int>(a.cols - c), v);
+    __device__ __forceinline__ void get(const LnBwdArgs &a, int64_t, int64_t c, uint64_t nmu2,
+                                        uint64_t (&v)[P]) const {
+        codes8(make_uint2(w[0], w[1]), a.x8.fmt, fetched_scale(a.x8, scale), nmu2,
+               VEC ? 8 : static_cast<int>(a.cols - c), v);
     }
 };
 
-// xhat in place of x, and u in place of dy; their sums for the row, and the column sums
+// xhat in place of x - mean, and u in place of dy; their sums for the row, and the column
+// sums
 template <int P>
-__device__ __forceinline__ void ln_bwd_accumulate(uint64_t nmu2, uint64_t rs2, const uint64_t (&g)[P],
+__device__ __forceinline__ void ln_bwd_accumulate(uint64_t rs2, const uint64_t (&g)[P],
                                                   uint64_t (&dy)[P], uint64_t (&x)[P],
                                                   uint64_t (&dg)[P], uint64_t (&db)[P], uint64_t &s1,
                                                   uint64_t &s2) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        x[i] = f32x2_mul(f32x2_add(x[i], nmu2), rs2);
+        x[i] = f32x2_mul(x[i], rs2);
         dg[i] = f32x2_fma(dy[i], x[i], dg[i]);
         db[i] = f32x2_add(db[i], dy[i]);
         dy[i] = f32x2_mul(dy[i], g[i]);
@@ -470,8 +483,8 @@ __global__ void __launch_bounds__(512) ln_bwd_sums_kernel(const LnBwdArgs a) {
             uint64_t dy[4], x[4], g[4], dg[4] = {}, db[4] = {};
             load_param(a.gamma, a.wtype, c, a.cols, g);
             rdy.get(dyr, c, a.cols, dy);
-            rx.get(a, row, c, x);
-            ln_bwd_accumulate(nmu2, rs2, g, dy, x, dg, db, s1, s2);
+            rx.get(a, row, c, nmu2, x);
+            ln_bwd_accumulate(rs2, g, dy, x, dg, db, s1, s2);
         }
         const float2 s = team_sum2<false>(sum2(s1), sum2(s2), buf[flip]);
         if (threadIdx.x == 0) a.row_sums[row] = s;
@@ -594,6 +607,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
                     if constexpr (!SAVED) {
                         raw.load(reinterpret_cast<const T *>(stage + r.dy_span), col(k), cols);
                         raw.get(nullptr, 0, 0, x[k]);
+                        add_all(nmu2, x[k]);
                     }
                 } else {
                     RawRow8<T> raw;
@@ -602,17 +616,18 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
                     if constexpr (!SAVED) {
                         raw.load_shared(stage + r.dy_span + col(k) * kSize, xoff != 0);
                         raw.get(xoff, left, x[k]);
+                        add_all(nmu2, x[k]);
                     }
                 }
                 if constexpr (SAVED) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(stage + r.dy_span + col(k));
-                    codes8(w, a.x8.fmt, sc[k], ALIGNED ? 8 : left, x[k]);
+                    codes8(w, a.x8.fmt, sc[k], nmu2, ALIGNED ? 8 : left, x[k]);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dy[k][i] = x[k][i] = 0;
             }
-            ln_bwd_accumulate(nmu2, rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
+            ln_bwd_accumulate(rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
         }
         const float2 sum = team_sum2<false>(sum2(s1), sum2(s2), buf[flip]);
         if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
@@ -675,12 +690,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const 
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             rdy[k].get(static_cast<const T *>(a.dy) + row * a.lddy, col(k), a.cols, dy[k]);
-            rx[k].get(a, row, col(k), x[k]);
+            rx[k].get(a, row, col(k), nmu2, x[k]);
         }
         if (row + team.step < a.rows) fetch(row + team.step);
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            ln_bwd_accumulate(nmu2, rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
+            ln_bwd_accumulate(rs2, g[k], dy[k], x[k], dg[k], db[k], s1, s2);
         float2 s;
         if constexpr (WIDE)
             s = a.row_sums[row];
@@ -806,7 +821,9 @@ constexpr int64_t kBwdWide = 8192;    // rows up to this are held in a CTA's reg
 constexpr int64_t kBwdSlab = 4096;    // columns of a wide row's slab, 16 for each of 256 threads
 
 // CTAs per SM of the ring kernel: of up to 288 threads (4608 columns) two fit beside
-// each other at 112 registers per thread, smaller ones by threads.
+// each other, smaller ones by threads.  Two of 256 threads have 128 registers each, two of
+// 288 only 96, since their 18 warps put five on one of the SM's four schedulers (8192 x
+// 4096: 41.0 us, and 50.8 with the 96 of the larger one).
 constexpr unsigned kRingHalf = 288;
 int64_t ring_ctas_per_sm(unsigned threads) {
     return threads > kRingHalf ? 1 : threads > 128 ? 2 : 512 / threads;
@@ -848,8 +865,9 @@ cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cu
 template <typename T, bool SAVED, bool ALIGNED>
 cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
     const unsigned threads = row_threads(a.cols, 16);
-    return threads > kRingHalf ? ln_bwd_ring_sized<T, SAVED, 512, 1, ALIGNED>(a, grid, threads, st)
-                               : ln_bwd_ring_sized<T, SAVED, kRingHalf, 2, ALIGNED>(a, grid, threads, st);
+    if (threads > kRingHalf) return ln_bwd_ring_sized<T, SAVED, 512, 1, ALIGNED>(a, grid, threads, st);
+    if (threads > 256) return ln_bwd_ring_sized<T, SAVED, kRingHalf, 2, ALIGNED>(a, grid, threads, st);
+    return ln_bwd_ring_sized<T, SAVED, 256, 2, ALIGNED>(a, grid, threads, st);
 }
 
 template <typename T, bool SAVED, int VEC>
