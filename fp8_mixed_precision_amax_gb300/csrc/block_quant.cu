@@ -227,8 +227,10 @@ __device__ __forceinline__ float sigmoid(float x) {
     return s;
 }
 
-// 16 lanes per block of 128 columns of a row, two blocks per warp.  777 x 2688 BF16: 4.6
-// us, where reading and writing alone is 2.2; 8192 x 11008 with h kept: 146 and 93.
+// 8 lanes per block of 128 columns of a row, four blocks per warp.  8192 x 11008 BF16
+// with h kept: 124 us, where reading and writing alone is 93; 777 x 2688 4.1 and 2.2.  (16
+// lanes per block, with twice the exchanges and scales per value: 146 and 4.4, but 2.2 for
+// one token of 11008, here 2.7.)
 template <typename T>
 __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h, int64_t M, int64_t F,
                                                          int64_t ld, bool vec, const BlockView a8,
@@ -236,19 +238,24 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
     pdl_wait();
     pdl_trigger();
     const unsigned per_row = static_cast<unsigned>(F / 128);
-    const int64_t total = M * per_row, step = static_cast<int64_t>(gridDim.x) * 16;
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; w < total;
+    const int64_t total = M * per_row, step = static_cast<int64_t>(gridDim.x) * 32;
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 5) * 4; w < total;
          w += step) {
-        // the warp's second half may be past the end: it repeats the first half's block
-        int64_t blk = w + ((threadIdx.x >> 4) & 1);
+        // the warp's later quarters may be past the end: they repeat the first one's block
+        int64_t blk = w + ((threadIdx.x >> 3) & 3);
         if (blk >= total) blk = w;
-        const int64_t row = blk / per_row, c = (blk - row * per_row) * 128 + 8 * (threadIdx.x & 15);
-        float g[8], u[8];
-        load_row<T, 8>(h + row * ld, c, 2 * F, vec, g);
-        load_row<T, 8>(h + row * ld, F + c, 2 * F, vec, u);
-        uint64_t g2[4], u2[4], a2[4];
+        // a division of 32 bits where that is enough
+        const int64_t row = total >> 32 ? blk / per_row : static_cast<uint32_t>(blk) / per_row;
+        const int64_t c = (blk - row * per_row) * 128 + 16 * (threadIdx.x & 7);
+        float g[16], u[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int k = 0; k < 2; ++k) {
+            load_row<T, 8>(h + row * ld, c + 8 * k, 2 * F, vec, *reinterpret_cast<float(*)[8]>(g + 8 * k));
+            load_row<T, 8>(h + row * ld, F + c + 8 * k, 2 * F, vec, *reinterpret_cast<float(*)[8]>(u + 8 * k));
+        }
+        uint64_t g2[8], u2[8], a2[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
             g2[i] = f32x2_pack(g[2 * i], g[2 * i + 1]);
             u2[i] = f32x2_pack(u[2 * i], u[2 * i + 1]);
             const uint64_t s = f32x2_pack(sigmoid(g[2 * i]), sigmoid(g[2 * i + 1]));
@@ -256,12 +263,12 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
         }
         RowWriter out;
         out.start(a8, row, c);
-        out.put(a8, a2, 0, 8);
+        out.put(a8, a2, 0, 16);
         if (h8.codes != nullptr) {
             out.start(h8, row, c);
-            out.put(h8, g2, 0, 8);
+            out.put(h8, g2, 0, 16);
             out.start(h8, row, F + c);
-            out.put(h8, u2, 0, 8);
+            out.put(h8, u2, 0, 16);
         }
     }
 }
@@ -477,7 +484,7 @@ cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const Block
                               int sm_count, cudaStream_t st) {
     if (h.rows == 0 || h.cols == 0) return cudaSuccess;
     const int64_t F = h.cols / 2;
-    const dim3 grid(capped((h.rows * (F / 128) + 15) / 16, static_cast<int64_t>(sm_count) * 64));
+    const dim3 grid(capped((h.rows * (F / 128) + 31) / 32, static_cast<int64_t>(sm_count) * 64));
     const bool vec = rows_vec(h, 8);
     if (h.type == kTypeF32)
         return launch_pdl(swiglu_fwd_kernel<float>, grid, dim3(256), 0, st,
