@@ -128,10 +128,12 @@ __device__ __forceinline__ float sum2(uint64_t v) {
     return __fadd_rn(lo, hi);
 }
 
-// s / n given 1 / n: the product, corrected by its remainder.
+// s / n given 1 / n: the product, corrected by its remainder.  An infinite sum has none
+// (inf - inf): its quotient is infinite, as a division gives it.
 __device__ __forceinline__ float quotient(float s, float n, float inv_n) {
     const float q = __fmul_rn(s, inv_n);
-    return __fmaf_rn(__fmaf_rn(-q, n, s), inv_n, q);
+    const float r = __fmaf_rn(__fmaf_rn(-q, n, s), inv_n, q);
+    return is_inf(fabsf(q)) ? q : r;
 }
 
 struct LnFwdArgs {
