@@ -216,15 +216,21 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 
 // ----------------------------------------------------------------- SwiGLU --
 
-// 1 / (1 + exp(-x)) to a few units in the last place and |x| 2^-24: 0 for -inf, 1 for
-// +inf.  The instructions that flush subnormal numbers serve here: exp(-x) below 2^-126
-// is nothing beside 1, and a result below 2^-126 is far below any 8-bit step.  (The
-// general ones come with 7 more instructions per value.)
-__device__ __forceinline__ float sigmoid(float x) {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(x, -1.44269504f)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
-    return s;
+// 1 / (1 + exp(-x)) of a pair to a few units in the last place and |x| 2^-24: 0 for -inf, 1
+// for +inf.  The instructions that flush subnormal numbers serve here: exp(-x) below 2^-126
+// is nothing beside 1, and the reciprocal is taken of a quarter of 1 + exp(-x), so that it
+// stays a normal number as long as exp(-x) is finite (x > -88.7) and the last product gives
+// the result below 2^-126 that a block of such gates is made of: its scale may be as small
+// as 2^-127.  (The reciprocal that keeps subnormal numbers comes with 7 more instructions.)
+__device__ __forceinline__ uint64_t sigmoid2(float x, float y) {
+    float s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(i ? y : x, -1.44269504f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(__fmaf_rn(e, 0.25f, 0.25f)));
+    }
+    return f32x2_mul(f32x2_pack(s[0], s[1]), splat_f32x2(0.25f));
 }
 
 // 8 lanes per block of 128 columns of a row, four blocks per warp.  8192 x 11008 BF16
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(256) swiglu_fwd_kernel(const T *__restrict__ h
         for (int i = 0; i < 8; ++i) {
             g2[i] = f32x2_pack(g[2 * i], g[2 * i + 1]);
             u2[i] = f32x2_pack(u[2 * i], u[2 * i + 1]);
-            const uint64_t s = f32x2_pack(sigmoid(g[2 * i]), sigmoid(g[2 * i + 1]));
+            const uint64_t s = sigmoid2(g[2 * i], g[2 * i + 1]);
             a2[i] = f32x2_mul(f32x2_mul(g2[i], s), u2[i]);
         }
         RowWriter out;
@@ -284,7 +290,7 @@ struct SwigluSmem {
 
 // The three results of a tile in registers at once: 192 KB of the SM's 256, so one CTA
 // per SM.  Bound by issue slots (57 %; 46 instructions per element of da) and the three
-// barriers of a tile: 8192 x 11008 BF16 176 us, 4.6 TB/s (0.68 of a copy's rate).
+// barriers of a tile: 8192 x 11008 BF16 178.5 us, 4.5 TB/s (0.67 of a copy's rate).
 template <typename T, int FMT, int AFMT, int HFMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
     swiglu_bwd_kernel(const T *__restrict__ da, int64_t M, int64_t F, int64_t ld, bool vec,
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int p = 0; p < 2; ++p) {
                 float g0, g1;
                 f32x2_unpack(g[p], g0, g1);
-                const uint64_t s = f32x2_pack(sigmoid(g0), sigmoid(g1));
+                const uint64_t s = sigmoid2(g0, g1);
                 const uint64_t gs = f32x2_mul(g[p], s);
                 a[r][p] = f32x2_mul(gs, u[p]);
                 du[r][p] = f32x2_mul(d[p], gs);

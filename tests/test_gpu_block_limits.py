@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import block_ref as ref
-from test_gpu_saved import EPS, near
+from test_gpu_saved import EPS, near, near_block
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,42 @@ def test_layernorm_statistics_beyond_fp32(cols, dtype):
                         beta.double().abs())
     for r in (0, 5):
         near(y[r], y0[r], tol[r] + torch.finfo(dtype).eps / 2 * (y0[r].abs() + tol[r]), ("y", r))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low,high", [(-88.5, -87.5), (-88.5, -80.0), (-20.0, 3.0)])
+def test_swiglu_of_gates_that_leave_next_to_nothing(dtype, low, high):
+    """Gates down to where exp(-gate) is the largest fp32 number: sigmoid is a subnormal number
+    there, its products with the gate and the value are not, and a block's scale reaches down to
+    them.  Tolerance: |gate| 2^-22 for the rounding of the X sigmoid's own rounding is 2^-22; no absolute part."""
+    f = _lib()
+    M, F = 40, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rnd = lambda r, c: torch.rand(r, c, generator=g, device="cuda")
+    gate = low + (high - low) * rnd(M, F)
+    value = (1 + rnd(M, F)) * torch.where(rnd(M, F) < 0.5, -1000.0, 1000.0)
+    h = torch.cat([gate, value], 1).to(dtype)
+    a8 = f.BlockFp8.empty(M, F)
+    f.fp8_swiglu_fwd(h, a8)
+    torch.cuda.synchronize()
+    want = ref.swiglu(h)
+    rel = 2.0 ** -19 + h[:, :F].double().abs() * 2.0 ** -22
+    near_block(a8, want, want.abs() * rel, "a8")
+    h8 = f.BlockFp8.empty(M, 2 * F)
+    f.fp8_block_quantize(torch.cat([gate, value], 1), h8)
+    seen = ref.values(h8)[0]
+    assert seen[:, :F].min() > -88.7    # in 8 bits too
+    da = ((1 + rnd(M, F)) * 1000).to(dtype)
+    dh, a = ref.swiglu_bwd(da, seen), ref.swiglu(seen)
+    gs, u = seen.chunk(2, 1)
+    s = torch.sigmoid(gs)
+    rel = 2.0 ** -19 + gs.abs() * 2.0 ** -22
+    size = da.double().abs() * u.abs() * s * (1 + 2 * gs.abs())
+    tol = torch.cat([size * rel, da.double().abs() * (gs * s).abs() * rel], 1)
+    dh8, dh8t, a8t = f.BlockFp8.empty(M, 2 * F, 1), f.BlockFp8.empty(2 * F, M, 1), f.BlockFp8.empty(F, M)
+    f.fp8_swiglu_bwd(da, h8, dh8, dh8t, a8t)
+    torch.cuda.synchronize()
+    near_block(dh8, dh, tol, "dh8")
+    near_block(dh8t, dh.t(), tol.t(), "dh8t")
+    near_block(a8t, a.t(), (a.abs() * rel).t(), "a8t")
