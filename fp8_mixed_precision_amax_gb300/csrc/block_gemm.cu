@@ -1244,7 +1244,16 @@ cudaError_t launch_few_any(const BlockView &A, const BlockView &B, const MatView
 
 constexpr int64_t kFewRows = 128;   // the few kernel up to this many rows of A,
 constexpr int64_t kFewTiles = 38;   // or up to this many 256 x 256 tiles
+constexpr int64_t kFewCols = int64_t(65535) * 128;   // of D in one launch: tiles count in gridDim.y
 constexpr int kMxPieceWaves = 6;
+
+// The columns of D from c on, at most n of them, and the rows of B that give them.
+void take_columns(BlockView &B, MatView &D, int64_t c, int64_t n) {
+    B.codes += c * B.ld;
+    B.scales = static_cast<uint8_t *>(B.scales) + c / B.block_rows * B.ld_s * (B.scale_f32 ? 4 : 1);
+    D.data = static_cast<__nv_bfloat16 *>(D.data) + c;
+    B.rows = D.cols = D.cols - c < n ? D.cols - c : n;
+}
 
 }  // namespace
 
@@ -1252,6 +1261,16 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
                               int sm_count, cudaStream_t st, const char **what) {
     if (D.rows == 0 || D.cols == 0) return cudaSuccess;
     if (A.cols == 0) return cudaMemset2DAsync(D.data, D.ld * 2, 0, D.cols * 2, D.rows, st);
+    if (D.rows <= kFewRows && D.cols > kFewCols) {
+        for (int64_t c = 0; c < D.cols; c += kFewCols) {
+            BlockView part = B;
+            MatView to = D;
+            take_columns(part, to, c, kFewCols);
+            const cudaError_t e = launch_block_gemm(A, part, to, sm_count, st, what);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    }
     const bool mx = A.scale_f32 == 0;
     PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
     const int64_t pair_tiles = ((D.rows + 255) / 256) * ((D.cols + 255) / 256);

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import block_ref as ref
+from test_gpu_block import check_gemm, operand
 from test_gpu_saved import EPS, near, near_block
 
 pytestmark = pytest.mark.gpu
@@ -92,3 +93,20 @@ def test_swiglu_of_gates_that_leave_next_to_nothing(dtype, low, high):
     near_block(dh8, dh, tol, "dh8")
     near_block(dh8t, dh.t(), tol.t(), "dh8t")
     near_block(a8t, a.t(), (a.abs() * rel).t(), "a8t")
+
+
+@pytest.mark.parametrize("sd", [torch.uint8, torch.float32])
+@pytest.mark.parametrize("M,bb", [(1, 1), (17, 128)])
+def test_gemm_of_few_rows_with_more_tiles_than_a_grid_dimension(M, bb, sd):
+    """65,537 tiles of 128 rows of B: more than the second and third grid dimensions count."""
+    f = _lib()
+    edge, K = 65535 * 128, 16
+    N = edge + 128 + 5
+    A, B = operand(M, K, 0, 1, sd, 1), operand(N, K, 0, bb, sd, 2)
+    D = torch.full((M, N + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    f.fp8_block_gemm_tn(A, B, D[:, :N])
+    f.fp8_sync_status()
+    assert not D[:, :N].isnan().any() and D[:, N:].isnan().all()
+    for lo, hi in ((0, 1000), (edge - 256, edge), (edge, N)):
+        part = f.BlockFp8(B.codes[lo:hi], B.scales[lo // bb:-(-hi // bb)], K, 0, bb)
+        check_gemm(A, part, D[:, lo:hi], (M, lo, sd))
