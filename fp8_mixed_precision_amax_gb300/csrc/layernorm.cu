@@ -656,8 +656,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) ln_bwd_ring_kernel(const RingAr
 }
 
 // Narrow rows (WARP) and wide ones.  Rows in turn; a thread keeps its columns (as in the forward) and their sums over
-// the CTA's rows.  WIDE: blockIdx.y is a slab of 8 VPT blockDim.x columns and the rows'
-// sums are already there.
+// the CTA's rows.  WIDE: blockIdx.y, and blockIdx.z where there are more than 65535, is a
+// slab of 8 VPT blockDim.x columns, and the rows' sums are already there.
 template <typename T, bool SAVED, int VPT, bool WARP, bool WIDE, int VEC>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const LnBwdArgs a) {
     using L = Lay<T, VEC>;
@@ -668,7 +668,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) ln_bwd_kernel(const 
     pdl_wait();
     pdl_trigger();
     const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
-    const int64_t base = WIDE ? static_cast<int64_t>(blockIdx.y) * E * VPT * blockDim.x : 0;
+    const int64_t slab = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+    const int64_t base = WIDE ? slab * E * VPT * blockDim.x : 0;   // past the last column: nothing to do
     auto col = [&](int k) { return base + E * (team.id + k * team.size); };
     typename L::Raw rdy[VPT];
     RawX<T, SAVED, VEC> rx[VPT];
@@ -887,8 +888,10 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * up8(a.cols));
         e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * 152)), dim3(512), 0, st, a);
         if (e != cudaSuccess) return e;
-        const dim3 slabs(g, static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab));
-        e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, false, true, VEC>, slabs, dim3(256), 0, st, a);
+        const unsigned slabs = static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab);
+        const unsigned z = (slabs + 65534) / 65535;
+        e = launch_pdl(ln_bwd_kernel<T, SAVED, VPT, false, true, VEC>, dim3(g, (slabs + z - 1) / z, z),
+                       dim3(256), 0, st, a);
     }
     if (e != cudaSuccess) return e;
     return launch_pdl(ln_bwd_reduce_kernel, dim3(static_cast<unsigned>((2 * up8(a.cols) + 31) / 32)),

@@ -110,3 +110,37 @@ def test_gemm_of_few_rows_with_more_tiles_than_a_grid_dimension(M, bb, sd):
     for lo, hi in ((0, 1000), (edge - 256, edge), (edge, N)):
         part = f.BlockFp8(B.codes[lo:hi], B.scales[lo // bb:-(-hi // bb)], K, 0, bb)
         check_gemm(A, part, D[:, lo:hi], (M, lo, sd))
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_layernorm_bwd_with_more_slabs_than_a_grid_dimension(saved):
+    """65,537 slabs of 4096 columns: more than the second and third grid dimensions count.
+    One row with mean 0 and rstd 1, gamma 1 and few nonzero gradients, so that its sums are exact:
+    xhat = x, s1 = sum dy, s2 = sum dy x; dgamma = dy x and dbeta = dy without rounding."""
+    f = _lib()
+    cols = 65536 * 4096 + 24
+    x = torch.zeros(1, cols, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros_like(x)
+    at = torch.tensor([0, 4095, 4096, 32768 * 4096 - 1, 32768 * 4096, 32769 * 4096 + 7, 65535 * 4096 - 1,
+                       65535 * 4096, 65536 * 4096 + 3, cols - 1], device="cuda")
+    dy[0, at] = torch.tensor([1, 2, -3, 4, 5, -6, 7, 8, -16, 12], device="cuda").bfloat16()
+    x[0, at] = torch.tensor([2, -1, 4, 1, 8, -2, 1, 4, 2, -8], device="cuda").bfloat16()
+    x[0, 100:200] = 3
+    src = x
+    if saved:
+        src = f.BlockFp8.empty(1, cols)
+        f.fp8_block_quantize(x, src)
+    one = torch.ones(1, device="cuda")
+    gamma = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full_like(x, float("nan"))
+    dgamma, dbeta = torch.full((2, cols), float("nan"), device="cuda")
+    f.fp8_layernorm_bwd(dy, src, gamma, 0 * one, one, dx, dgamma, dbeta)
+    f.fp8_sync_status()
+    assert torch.equal(dbeta, dy[0].float())
+    assert torch.equal(dgamma, dy[0].float() * x[0].float())
+    xd, dyd = x[0].float(), dy[0].float()
+    s1, s2 = float(dyd.double().sum()), float((dyd * xd).double().sum())
+    want = dyd - s1 / cols - xd * (s2 / cols)
+    # one rounding to BF16 and fp32 ones of each of the terms
+    tol = 2.0 ** -8 * want.abs() + 2.0 ** -22 * (dyd.abs() + abs(s1) / cols + xd.abs() * abs(s2) / cols)
+    assert ((dx[0].float() - want).abs() <= tol).all()
