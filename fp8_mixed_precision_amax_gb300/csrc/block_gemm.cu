@@ -14,10 +14,11 @@
 //         over a cluster whose CTAs join their sums in shared memory.
 //
 // Every wait is bounded.
+#include <atomic>
 #include <cstdint>
-#include <mutex>
 
 #include "block.cuh"
+#include "once_per_device.h"
 #include "raster.cuh"
 
 namespace fp8k {
@@ -1165,26 +1166,31 @@ cudaLaunchConfig_t cluster_config(dim3 grid, int threads, size_t smem, int clust
 }
 
 // The pair kernel's shared-memory limit is set and the number of CTA pairs that
-// can be resident at once is found on the first call.
+// can be resident at once is found on a device's first call.
 struct PairKernel {
     void (*kernel)(PairArgs);
     int threads;
     size_t smem;
-    std::once_flag once;
-    cudaError_t err = cudaSuccess;
-    int slots = 0;
+    SmemLimit limit;
+    OncePerDevice once;
+    std::atomic<int> slots[kDeviceSlots] = {};
 
-    void init(int sm_count) {
-        std::call_once(once, [this, sm_count] {
-            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-            if (err != cudaSuccess) return;
+    cudaError_t init(int sm_count, int *slots_here) {
+        int device = 0;
+        const cudaError_t err = once.run([this, sm_count](int dev) {
+            cudaError_t e = limit.allow(kernel, smem);
+            if (e != cudaSuccess) return e;
             cudaLaunchAttribute attr[2];
             cudaLaunchConfig_t cfg =
                 cluster_config(dim3(sm_count & ~1), threads, smem, 2, attr, nullptr);
             cfg.numAttrs = 1;
-            err = cudaOccupancyMaxActiveClusters(&slots, kernel, &cfg);
-        });
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            slots[dev] = n;
+            return e;
+        }, &device);
+        *slots_here = slots[device];
+        return err;
     }
 };
 PairKernel g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
@@ -1210,13 +1216,8 @@ cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D,
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
     const uint32_t fw = static_cast<uint32_t>(B.fmt), fx = static_cast<uint32_t>(A.fmt);
     a.idesc = MX ? idesc_mxf8(fw, fx, 128, NT, 0) : idesc_f8(fw, fx, 128, NT);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(block_gemm_few_kernel<NT, MX>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(C::SMEM));
-    });
+    static SmemLimit limit;
+    const cudaError_t attr_err = limit.allow(block_gemm_few_kernel<NT, MX>, C::SMEM);
     if (attr_err != cudaSuccess) return attr_err;
     const int64_t tw = (D.cols + 127) / 128, tx = (D.rows + NT - 1) / NT;
     // as many CTAs as run at once, two per SM, with at least two k-blocks each
@@ -1274,9 +1275,12 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     const bool mx = A.scale_f32 == 0;
     PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
     const int64_t pair_tiles = ((D.rows + 255) / 256) * ((D.cols + 255) / 256);
-    if (D.rows > kFewRows && pair_tiles > kFewTiles) pk.init(sm_count);
-    if (pk.err != cudaSuccess) return pk.err;
-    if (D.rows <= kFewRows || pair_tiles <= kFewTiles || pk.slots < 1)
+    int slots = 0;
+    if (D.rows > kFewRows && pair_tiles > kFewTiles) {
+        const cudaError_t e = pk.init(sm_count, &slots);
+        if (e != cudaSuccess) return e;
+    }
+    if (slots < 1)
         return mx ? launch_few_any<true>(A, B, D, sm_count, st, what)
                   : launch_few_any<false>(A, B, D, sm_count, st, what);
     PairArgs a;
@@ -1303,8 +1307,8 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     // waves: 512 us, whole 530; 2304 x 2560 x 4096: 45.3 and 52.5).  The mx kernel runs into the power limit where there are
     // many waves, and the pairs that idle in the last one cost nothing (2304 x 2560 x 4096,
     // 1.2 waves: 25.7 us, whole 28.0; 4 waves 58.7 and 60.0; 8 waves 106.3 and 105.3).
-    const int num_tiles = a.tiles_m * a.tiles_n, rest = num_tiles % pk.slots;
-    const bool pieces = kPieces * rest <= pk.slots && (!mx || num_tiles < kMxPieceWaves * pk.slots);
+    const int num_tiles = a.tiles_m * a.tiles_n, rest = num_tiles % slots;
+    const bool pieces = kPieces * rest <= slots && (!mx || num_tiles < kMxPieceWaves * slots);
     a.whole = pieces ? num_tiles - rest : num_tiles;
     a.num_items = a.whole + (num_tiles - a.whole) * kPieces;
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
@@ -1319,7 +1323,7 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
         *what = "cuTensorMapEncodeTiled failed for an operand";
         return cudaErrorInvalidValue;
     }
-    const int units = a.num_items < pk.slots ? a.num_items : pk.slots;
+    const int units = a.num_items < slots ? a.num_items : slots;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), pk.threads, pk.smem, 2, attr, st);
     return cudaLaunchKernelEx(&cfg, pk.kernel, a);

@@ -8,9 +8,9 @@
 // row.  HBM is the floor; the instructions per element bind before it where much is
 // computed of each.
 #include <cstdint>
-#include <mutex>
 
 #include "block.cuh"
+#include "once_per_device.h"
 
 namespace fp8k {
 
@@ -412,17 +412,13 @@ unsigned capped(int64_t n, int64_t cap) { return static_cast<unsigned>(n < cap ?
 
 unsigned tiles_of(int64_t n) { return static_cast<unsigned>((n + kTile - 1) / kTile); }
 
-// A persistent tile kernel with `per_sm` CTAs per SM, its shared-memory limit set on the
-// first launch.
+// A persistent tile kernel with `per_sm` CTAs per SM, its shared-memory limit set on a
+// device's first launch.
 template <auto KERNEL, typename Smem, typename... Args>
 cudaError_t launch_tiles(int per_sm, int64_t rows, int64_t cols, int sm_count, cudaStream_t st,
                          Args... args) {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(sizeof(Smem)));
-    });
+    static SmemLimit limit;
+    const cudaError_t err = limit.allow(KERNEL, sizeof(Smem));
     if (err != cudaSuccess) return err;
     const unsigned r = tiles_of(rows), c = tiles_of(cols);
     const dim3 grid(capped(static_cast<int64_t>(r) * c, static_cast<int64_t>(sm_count) * per_sm));

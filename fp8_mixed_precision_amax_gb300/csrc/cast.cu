@@ -17,10 +17,10 @@
 //  * the scaled cast of fp32 tensors (no transposed copy).
 #include <cfloat>
 #include <cstdint>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once_per_device.h"
 
 namespace fp8k {
 
@@ -981,12 +981,8 @@ static cudaError_t lnf_launch(int64_t rows, int cols, int sm_count, cudaStream_t
                               const void *x, const void *g, const void *b, float eps,
                               const float *scale, float *mean, float *rstd, uint8_t *out,
                               float *amax) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(ln_cast_rows_kernel<FMT, MODE>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    });
+    static SmemLimit limit;
+    const cudaError_t attr = limit.allow(ln_cast_rows_kernel<FMT, MODE>, 160 * 1024);
     if (attr != cudaSuccess) return attr;
     int64_t grid = (rows + kLnfWarps - 1) / kLnfWarps;
     if (grid > sm_count) grid = sm_count;
@@ -1029,13 +1025,8 @@ cudaError_t launch_ln_stats(const void *x, const void *gamma, const void *beta, 
         const int warps = ln_bulk_warps(cols);
         const size_t smem = ln_bulk_smem(warps, cols);
         // at most 200 KB of row buffers plus the barriers (ln_bulk_warps)
-        static std::once_flag once;
-        static cudaError_t attr_err = cudaSuccess;
-        std::call_once(once, [] {
-            attr_err = cudaFuncSetAttribute(ln_stats_bulk_kernel,
-                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                            210 * 1024);
-        });
+        static SmemLimit limit;
+        const cudaError_t attr_err = limit.allow(ln_stats_bulk_kernel, 210 * 1024);
         if (attr_err != cudaSuccess) return attr_err;
         int64_t bgrid = (rows + warps - 1) / warps;
         if (bgrid > sm_count) bgrid = sm_count;
@@ -1163,13 +1154,8 @@ cudaError_t launch_quantize_f32(const float *x, int64_t n, const float *scale, i
 
 template <int FMT, bool CURRENT>
 static cudaError_t qt_launch(const CastArgs &args, int sm_count, cudaStream_t st) {
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(quantize_transpose_kernel<FMT, CURRENT>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(kQtSmem));
-    });
+    static SmemLimit limit;
+    const cudaError_t attr_err = limit.allow(quantize_transpose_kernel<FMT, CURRENT>, kQtSmem);
     if (attr_err != cudaSuccess) return attr_err;
     if (args.num_tiles == 0) return cudaSuccess;
     int64_t blocks = static_cast<int64_t>(sm_count) * 2;
@@ -1269,13 +1255,9 @@ cudaError_t launch_scale_update(float *history, float *amax, float *scale, float
                                 bool clear_amax, cudaStream_t st) {
     const size_t smem = static_cast<size_t>(L) * sizeof(float);
     if (smem > 48 * 1024) {
-        static bool raised = false;
-        if (!raised) {
-            cudaError_t e = cudaFuncSetAttribute(
-                scale_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-            if (e != cudaSuccess) return e;
-            raised = true;
-        }
+        static SmemLimit limit;
+        const cudaError_t e = limit.allow(scale_update_kernel, 64 * 1024);
+        if (e != cudaSuccess) return e;
     }
     return launch_pdl(scale_update_kernel, dim3(num_tensors), dim3(kUpdThreads), smem, st, history,
                       amax, scale, scale_inv, L, format_mask, margin, clear_amax ? 1 : 0);

@@ -37,10 +37,10 @@
 
 #include <atomic>
 #include <cstdint>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once_per_device.h"
 
 namespace fp8k {
 
@@ -444,13 +444,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_tn_kernel(const __grid_co
 
 template <bool PAIR>
 cudaError_t set_smem_attr() {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(gemm_tn_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   static_cast<int>(Cfg<PAIR>::SMEM));
-    });
-    return err;
+    static SmemLimit limit;
+    return limit.allow(gemm_tn_kernel<PAIR>, Cfg<PAIR>::SMEM);
 }
 
 // attr must have room for two attributes: the cluster shape and, with pdl,
@@ -473,20 +468,23 @@ cudaLaunchConfig_t pair_config(int grid, cudaLaunchAttribute *attr, cudaStream_t
 }
 
 // Number of CTA pairs that can be resident at once (clusters of two need two
-// SMs of the same GPC), cached per process.
+// SMs of the same GPC), cached per device.
 int pair_slots(int sm_count) {
-    static std::once_flag once;
-    static int slots = 0;
-    std::call_once(once, [sm_count] {
-        if (set_smem_attr<true>() != cudaSuccess) return;
+    static OncePerDevice once;
+    static std::atomic<int> slots[kDeviceSlots];
+    int device = 0;
+    const cudaError_t err = once.run([sm_count](int dev) {
+        const cudaError_t e = set_smem_attr<true>();
+        if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = pair_config(sm_count & ~1, attr, nullptr, false);
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, gemm_tn_kernel<true>, &cfg) != cudaSuccess || n < 1)
             n = 0;
-        slots = n;
-    });
-    return slots;
+        slots[dev] = n;
+        return cudaSuccess;
+    }, &device);
+    return err == cudaSuccess ? slots[device].load() : 0;
 }
 
 }  // namespace

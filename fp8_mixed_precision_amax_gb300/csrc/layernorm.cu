@@ -10,9 +10,9 @@
 // Both are bound by HBM: each value is read and written once, and a row stays
 // in its CTA's registers between the sums and the use of the sums.
 #include <cstdint>
-#include <mutex>
 
 #include "block.cuh"
+#include "once_per_device.h"
 
 namespace fp8k {
 
@@ -854,12 +854,8 @@ cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cu
     r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
     const int64_t fit = kBytes / ring_ctas_per_sm(threads) / (r.dy_span + r.x_span);
     r.stages = static_cast<int>(fit < kRing ? fit : kRing);
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes));
-    });
+    static SmemLimit limit;
+    const cudaError_t err = limit.allow(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, kBytes);
     if (err != cudaSuccess) return err;
     return launch_pdl(ln_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, dim3(grid), dim3(threads),
                       static_cast<size_t>(r.stages) * (r.dy_span + r.x_span), st, r);

@@ -22,10 +22,10 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "once_per_device.h"
 
 namespace fp8k {
 
@@ -986,13 +986,8 @@ __global__ void __launch_bounds__(256) adam_init_kernel(const uint16_t *__restri
 template <int FMT, int MODE>
 cudaError_t launch_dq(int64_t grid, const uint8_t *parts, int nranks, int64_t n,
                       const float *scale, uint16_t *o, cudaStream_t st) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(dequant_sum_kernel<FMT, MODE>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kDqSmem));
-    });
+    static SmemLimit limit;
+    const cudaError_t attr = limit.allow(dequant_sum_kernel<FMT, MODE>, kDqSmem);
     if (attr != cudaSuccess) return attr;
     return launch_pdl(dequant_sum_kernel<FMT, MODE>, dim3(static_cast<unsigned>(grid)),
                       dim3(kDqConsumers + 32), kDqSmem, st, parts, nranks, n, scale, o);
