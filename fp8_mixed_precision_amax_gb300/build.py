@@ -20,7 +20,7 @@ OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libfp8amax.so")
 SOURCES = ["abi.cu", "block_abi.cu", "block_gemm.cu", "block_quant.cu", "cast.cu", "gemm.cu",
            "layernorm.cu", "noalloc.cu", "optim.cu", "tmap.cu"]
-HEADERS = ["abi_checks.h", "block.cuh", "common.cuh", "kernels.h", "once_per_device.h",
+HEADERS = ["abi_checks.h", "block.cuh", "common.cuh", "kernels.h", "ln_plan.h", "once_per_device.h",
            "raster.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -247,7 +247,7 @@ fp8_status fp8_layernorm_bwd(const fp8_matrix *dy, const fp8_matrix *x,
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_ln_bwd(vdy, vx, vx8, gamma, wtype, mean, rstd, vdx, dgamma, dbeta,
-                                 workspace, static_cast<cudaStream_t>(stream)),
+                                 workspace, sms, static_cast<cudaStream_t>(stream)),
              fn);
     return FP8_OK;
 }

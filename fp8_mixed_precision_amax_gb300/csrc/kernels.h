@@ -204,7 +204,7 @@ cudaError_t launch_ln_fwd(const MatView &x, const void *gamma, const void *beta,
 int64_t ln_bwd_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
                           const void *gamma, int wtype, const float *mean, const float *rstd,
-                          const MatView &dx, float *dgamma, float *dbeta, void *ws,
+                          const MatView &dx, float *dgamma, float *dbeta, void *ws, int sm_count,
                           cudaStream_t st);
 // yt = quantized transpose of LayerNorm(x8) (block_quant.cu).
 cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,

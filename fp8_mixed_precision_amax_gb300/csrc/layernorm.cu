@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "block.cuh"
+#include "ln_plan.h"
 #include "once_per_device.h"
 
 namespace fp8k {
@@ -27,7 +28,6 @@ __device__ unsigned g_ln_error_flags = 0;
 // share a block's maximum.  The backward takes 8 like the general case, so that its
 // sums are the same bits at any alignment.  The row after the one in work is already
 // being loaded, into registers.
-constexpr int kWarps = 8;
 
 template <typename T, int VEC>
 struct Lay {
@@ -785,13 +785,6 @@ __global__ void __launch_bounds__(1024) ln_bwd_reduce_kernel(const float *__rest
     }
 }
 
-// Threads of a CTA that shares a row: whole warps, `each` columns per thread.
-unsigned row_threads(int64_t cols, int each) {
-    return static_cast<unsigned>((cols + 32 * each - 1) / (32 * each) * 32);
-}
-
-unsigned capped(int64_t n, int64_t cap) { return static_cast<unsigned>(n < cap ? n : cap); }
-
 bool aligned_rows(const void *p, int64_t ld, int type) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * (type == kTypeF32 ? 4 : 2) % 16 == 0;
 }
@@ -819,32 +812,6 @@ cudaError_t ln_fwd_typed(const LnFwdArgs &a, bool vec, int sms, cudaStream_t st)
     return launch_pdl(ln_fwd_wide_kernel<T>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
 }
 
-constexpr int64_t kBwdNarrow = 512;   // rows up to this belong to one warp
-constexpr int64_t kBwdWide = 8192;    // rows up to this are held in a CTA's registers
-constexpr int64_t kBwdSlab = 4096;    // columns of a wide row's slab, 16 for each of 256 threads
-
-// CTAs per SM of the ring kernel: of up to 288 threads (4608 columns) two fit beside
-// each other, smaller ones by threads.  Two of 256 threads have 128 registers each, two of
-// 288 only 96, since their 18 warps put five on one of the SM's four schedulers (8192 x
-// 4096: 41.0 us, and 50.8 with the 96 of the larger one).
-constexpr unsigned kRingHalf = 288;
-int64_t ring_ctas_per_sm(unsigned threads) {
-    return threads > kRingHalf ? 1 : threads > 128 ? 2 : 512 / threads;
-}
-
-// CTAs that keep column sums of their own, at most: as many as are resident on 152 SMs;
-// one per SM and slab of a wide row.
-int64_t bwd_ctas(int64_t rows, int64_t cols) {
-    constexpr int64_t sms = 152;
-    if (cols <= kBwdNarrow) return capped((rows + kWarps - 1) / kWarps, 2 * sms);
-    if (cols > kBwdWide) return capped(rows, sms);
-    // eight rows each once there is a CTA per SM: every CTA's sums are written, read and
-    // added (2048 x 1024: 18.7 us with 1216 CTAs)
-    const int64_t some = rows / 8 > sms ? rows / 8 : sms;
-    const int64_t most = sms * ring_ctas_per_sm(row_threads(cols, 16));
-    return capped(rows, some < most ? some : most);
-}
-
 // As many rows in flight as the CTAs of an SM have shared memory for.
 template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 cudaError_t ln_bwd_ring_sized(const LnBwdArgs &a, int grid, unsigned threads, cudaStream_t st) {
@@ -870,9 +837,9 @@ cudaError_t ln_bwd_ring(const LnBwdArgs &a, int grid, cudaStream_t st) {
 }
 
 template <typename T, bool SAVED, int VEC>
-cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cudaStream_t st) {
+cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, int sms, cudaStream_t st) {
     constexpr int VPT = 2;   // 16 columns per thread
-    const int g = static_cast<int>(bwd_ctas(a.rows, a.cols));
+    const int g = static_cast<int>(bwd_ctas(a.rows, a.cols, sms));
     a.part = static_cast<float *>(ws);
     const dim3 grid(g);
     cudaError_t e;
@@ -882,7 +849,7 @@ cudaError_t ln_bwd_typed(LnBwdArgs a, float *dgamma, float *dbeta, void *ws, cud
         e = ln_bwd_ring<T, SAVED, VEC != 0>(a, g, st);
     } else {
         a.row_sums = reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(g) * 2 * up8(a.cols));
-        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * 152)), dim3(512), 0, st, a);
+        e = launch_pdl(ln_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
         if (e != cudaSuccess) return e;
         const unsigned slabs = static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab);
         const unsigned z = (slabs + 65534) / 65535;
@@ -911,12 +878,12 @@ cudaError_t launch_ln_fwd(const MatView &x, const void *gamma, const void *beta,
 }
 
 int64_t ln_bwd_workspace(int64_t rows, int64_t cols) {
-    return bwd_ctas(rows, cols) * 2 * up8(cols) * 4 + (cols > kBwdWide ? rows * 8 : 0);
+    return bwd_ctas_most(rows, cols) * 2 * up8(cols) * 4 + (cols > kBwdWide ? rows * 8 : 0);
 }
 
 cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
                           const void *gamma, int wtype, const float *mean, const float *rstd,
-                          const MatView &dx, float *dgamma, float *dbeta, void *ws,
+                          const MatView &dx, float *dgamma, float *dbeta, void *ws, int sm_count,
                           cudaStream_t st) {
     if (dy.rows == 0) {
         cudaError_t e = cudaMemsetAsync(dgamma, 0, dy.cols * 4, st);
@@ -929,10 +896,10 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
     const bool vec = dy.cols % 8 == 0 && aligned_rows(dy.data, dy.ld, dy.type) &&
                      aligned_rows(x.data, x.ld, dy.type) && aligned_rows(dx.data, dx.ld, dy.type);
 #define FP8K_LN_BWD(T)                                                            \
-    (saved ? vec ? ln_bwd_typed<T, true, 8>(a, dgamma, dbeta, ws, st)          \
-                 : ln_bwd_typed<T, true, 0>(a, dgamma, dbeta, ws, st)         \
-     : vec ? ln_bwd_typed<T, false, 8>(a, dgamma, dbeta, ws, st)               \
-           : ln_bwd_typed<T, false, 0>(a, dgamma, dbeta, ws, st))
+    (saved ? vec ? ln_bwd_typed<T, true, 8>(a, dgamma, dbeta, ws, sm_count, st)          \
+                 : ln_bwd_typed<T, true, 0>(a, dgamma, dbeta, ws, sm_count, st)         \
+     : vec ? ln_bwd_typed<T, false, 8>(a, dgamma, dbeta, ws, sm_count, st)               \
+           : ln_bwd_typed<T, false, 0>(a, dgamma, dbeta, ws, sm_count, st))
     if (dy.type == kTypeF32) return FP8K_LN_BWD(float);
     if (dy.type == kTypeBF16) return FP8K_LN_BWD(__nv_bfloat16);
     return FP8K_LN_BWD(__half);

@@ -27,6 +27,10 @@ def test_setup_runs_once_on_each_device(tmp_path):
     run_check("once_per_device_check", tmp_path)
 
 
+def test_layernorm_backward_starts_what_is_resident(tmp_path):
+    run_check("ln_plan_check", tmp_path)
+
+
 def test_kernel_attributes_are_set_by_that_alone():
     """cudaFuncSetAttribute acts on the current device: behind a flag of the process it would
     leave the kernels of every other device without it."""
