@@ -82,6 +82,7 @@ class Fp8BlockMlp:
         self.W2q, self.W2t = e(K, F, 128), e(F, K, 128)
         # kept from forward to backward
         self.x8, self.h8, self.mean, self.rstd = e(M, K), e(M, 2 * F), v(M), v(M)
+        self._kept = False    # nothing yet
         # results
         self.y, self.dx = b(M, K), b(M, K)
         self.dW1, self.dW2, self.dgamma, self.dbeta = b(2 * F, K), b(K, F), v(K), v(K)
@@ -112,12 +113,15 @@ class Fp8BlockMlp:
         fp8_block_gemm_tn(s.n8, self.W1q, s.h, stream)
         fp8_swiglu_fwd(s.h, s.a8, self.h8, stream)
         fp8_block_gemm_tn(s.a8, self.W2q, self.y, stream)
+        self._kept = True
         return self.y
 
     def backward(self, dy: torch.Tensor, stream=None):
         """(dx, dW1, dW2, dgamma, dbeta) of the last forward; dy [M, K]."""
         if tuple(dy.shape) != (self.M, self.K):
             raise ValueError(f"dy must be [{self.M}, {self.K}], got {tuple(dy.shape)}")
+        if not self._kept:
+            raise RuntimeError("backward needs a forward before it")
         s = self.scratch
         fp8_block_quantize(dy, s.dy8, s.dy8t, stream)
         fp8_block_gemm_tn(s.dy8, self.W2t, s.da, stream)

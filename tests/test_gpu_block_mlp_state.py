@@ -65,3 +65,14 @@ def test_scratch_of_other_sizes_is_refused():
         f.Fp8BlockMlp(*args, 16, grad_fmt=f.E4M3, scratch=scratch)
     with pytest.raises(ValueError, match="scratch"):
         f.Fp8BlockMlp(z(64), z(64), z(512, 64), z(64, 256), 16, scratch=scratch)
+
+
+def test_backward_before_any_forward_is_refused():
+    """There is nothing kept to go back from, only what the memory held before."""
+    f, mlp, (_, _, _, _, x, dy) = build(16, 64, 128)
+    with pytest.raises(RuntimeError, match="forward"):
+        mlp.backward(dy)
+    mlp.forward(x)
+    first = [t.clone() for t in mlp.backward(dy)]
+    for a, b in zip(first, mlp.backward(dy)):    # what is kept stays for a second one
+        assert torch.equal(a, b)
