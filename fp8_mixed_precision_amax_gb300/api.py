@@ -9,6 +9,7 @@ fallback: if ``libfp8amax.so`` is missing, importing this module fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import logging
 import os
@@ -784,8 +785,9 @@ class BlockFp8:
         return self.codes.numel() + self.scales.numel() * self.scales.element_size()
 
     def dequantize(self, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-        """The matrix in 16 or 32 bits."""
-        out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
+        """The matrix in 16 or 32 bits, on the given (else the current) stream."""
+        with _on_stream(stream, self.codes.device):
+            out = torch.empty(self.shape, dtype=dtype, device=self.codes.device)
         fp8_block_dequantize(self, out, stream)
         return out
 
@@ -856,15 +858,15 @@ def _stat(t: torch.Tensor, n: int, name: str) -> int:
     return _vector(t, n, name, torch.float32)
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Device memory that is free again once the work on ``stream`` is done."""
-    if stream is None or (isinstance(stream, torch.cuda.Stream)
-                          and stream == torch.cuda.current_stream()):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _on_stream(stream, device):
+    """A context in which torch allocates memory for work on ``stream``: memory that is free
+    again once that stream's work is done.  (Memory of the current stream's may still be in use
+    by that one's pending work, which another stream does not wait for.)"""
+    if stream is None:
+        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return torch.cuda.stream(stream)
 
 
 def fp8_block_quantize(x: torch.Tensor, q: BlockFp8 | None = None, qt: BlockFp8 | None = None,
@@ -914,7 +916,8 @@ def fp8_layernorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: tor
     rows, cols = dy.shape
     if workspace is None:
         room = _lib.fp8_layernorm_bwd_workspace(rows, cols)
-        workspace = _scratch(room, dy.device, stream)
+        with _on_stream(stream, dy.device):
+            workspace = torch.empty(room, dtype=torch.uint8, device=dy.device)
         place = workspace.data_ptr()
     else:
         room = workspace.numel() * workspace.element_size()

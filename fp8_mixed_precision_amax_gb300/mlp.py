@@ -18,7 +18,7 @@ import torch
 
 from .api import (E4M3, E5M2, BlockFp8, fp8_block_gemm_tn, fp8_block_quantize, fp8_layernorm_bwd,
                   fp8_layernorm_bwd_workspace, fp8_layernorm_fwd, fp8_layernorm_recompute,
-                  fp8_swiglu_bwd, fp8_swiglu_fwd)
+                  fp8_swiglu_bwd, fp8_swiglu_fwd, _on_stream)
 
 _log = logging.getLogger(__name__)
 
@@ -66,7 +66,8 @@ class Fp8BlockMlp:
             raise ValueError(f"W2's columns must be a multiple of 128, got {F}")
         dev = W1.device
         if scratch is None:
-            scratch = BlockMlpScratch(M, K, F, grad_fmt, dev)
+            with _on_stream(stream, dev):
+                scratch = BlockMlpScratch(M, K, F, grad_fmt, dev)
         elif scratch.key != (M, K, F, grad_fmt):
             raise ValueError(f"scratch is of (M, K, F, grad_fmt) {scratch.key}, "
                              f"not {(M, K, F, grad_fmt)}")
@@ -77,15 +78,16 @@ class Fp8BlockMlp:
         e = lambda r, c, block=1: BlockFp8.empty(r, c, E4M3, block, device=dev)
         b = lambda r, c: torch.empty((r, c), dtype=torch.bfloat16, device=dev)
         v = lambda n: torch.empty(n, dtype=torch.float32, device=dev)
-        # weights, in tiles of 128 x 128, and their transposes for the input gradients
-        self.W1q, self.W1t = e(2 * F, K, 128), e(K, 2 * F, 128)
-        self.W2q, self.W2t = e(K, F, 128), e(F, K, 128)
-        # kept from forward to backward
-        self.x8, self.h8, self.mean, self.rstd = e(M, K), e(M, 2 * F), v(M), v(M)
+        with _on_stream(stream, dev):
+            # weights, in tiles of 128 x 128, and their transposes for the input gradients
+            self.W1q, self.W1t = e(2 * F, K, 128), e(K, 2 * F, 128)
+            self.W2q, self.W2t = e(K, F, 128), e(F, K, 128)
+            # kept from forward to backward
+            self.x8, self.h8, self.mean, self.rstd = e(M, K), e(M, 2 * F), v(M), v(M)
+            # results
+            self.y, self.dx = b(M, K), b(M, K)
+            self.dW1, self.dW2, self.dgamma, self.dbeta = b(2 * F, K), b(K, F), v(K), v(K)
         self._kept = False    # nothing yet
-        # results
-        self.y, self.dx = b(M, K), b(M, K)
-        self.dW1, self.dW2, self.dgamma, self.dbeta = b(2 * F, K), b(K, F), v(K), v(K)
         self.load_weights(W1, W2, stream)
         _log.info("FP8 block-scaled MLP [%d -> %d -> %d], %d tokens: E4M3 forward, %s backward, "
                   "%.1f MB kept per pass, %.1f MB of scratch", K, F, K, M,
