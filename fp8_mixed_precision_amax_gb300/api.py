@@ -150,24 +150,22 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
-def _load_packed() -> ctypes.CDLL:
-    """The library once more, with prototypes of the block-scaled calls that take packed structs."""
+def _load_packed(prototypes: ctypes.CDLL) -> ctypes.CDLL:
+    """The library once more: the block-scaled calls with the same prototypes, but structs as
+    packed bytes."""
     lib = ctypes.CDLL(LIB_PATH)
-    s, vp, i64, i32 = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
-    for name, args in {
-            "fp8_block_quantize": [s, s, s, vp], "fp8_block_dequantize": [s, s, vp],
-            "fp8_block_gemm_tn": [s, s, s, vp],
-            "fp8_layernorm_fwd": [s, vp, vp, i32, ctypes.c_float, s, s, s, vp, vp, vp],
-            "fp8_layernorm_bwd": [s, s, s, vp, i32, vp, vp, s, vp, vp, vp, i64, vp],
-            "fp8_layernorm_recompute": [s, vp, vp, i32, vp, vp, s, vp],
-            "fp8_swiglu_fwd": [s, s, s, vp], "fp8_swiglu_bwd": [s, s, s, s, s, vp]}.items():
-        f = getattr(lib, name)
-        f.argtypes, f.restype = args, ctypes.c_int
+    structs = (ctypes.POINTER(fp8_matrix), ctypes.POINTER(fp8_block_tensor))
+    for name in ("fp8_block_quantize", "fp8_block_dequantize", "fp8_block_gemm_tn",
+                 "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_recompute",
+                 "fp8_swiglu_fwd", "fp8_swiglu_bwd"):
+        f, of = getattr(lib, name), getattr(prototypes, name)
+        f.argtypes = [ctypes.c_char_p if a in structs else a for a in of.argtypes]
+        f.restype = of.restype
     return lib
 
 
 _lib = _load()
-_packed = _load_packed()
+_packed = _load_packed(_lib)
 
 
 def header_functions() -> list[str]:
