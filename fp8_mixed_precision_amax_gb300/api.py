@@ -566,7 +566,10 @@ class Fp8LayerNormLinear(Fp8Linear):
     """LayerNorm in front of an FP8 linear (te.LayerNormLinear): the forward
     normalises X with gamma / beta and casts the result straight to E4M3
     (fp8_layernorm_linear_fwd); the backward is the linear's, on that FP8
-    LayerNorm output.  mean / rstd are kept for a LayerNorm backward."""
+    LayerNorm output: its dX is the gradient of that output.  LayerNorm's own
+    backward takes it on from there, with the mean and rstd kept here:
+    ``fp8_layernorm_bwd(dX, X, gamma, layer.mean, layer.rstd, dx, dgamma,
+    dbeta)``, where dx may be dX."""
 
     def __init__(self, W: torch.Tensor, M: int, gamma: torch.Tensor, beta: torch.Tensor,
                  eps: float = 1e-5, recipe: Recipe | None = None):
