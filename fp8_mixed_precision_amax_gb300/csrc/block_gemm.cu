@@ -1243,8 +1243,14 @@ cudaError_t launch_few_any(const BlockView &A, const BlockView &B, const MatView
     return launch_few<128, MX>(A, B, D, sm_count, st, what);
 }
 
-constexpr int64_t kFewRows = 128;   // the few kernel up to this many rows of A,
-constexpr int64_t kFewTiles = 38;   // or up to this many 256 x 256 tiles
+// The few kernel takes up to kFewRows rows of A, and more as long as its 128 x 128 tiles, four
+// to a 256 x 256 tile, run at once: one for each SM.  On 152 SMs that is up to 38 tiles.  Float
+// scales, K = 4096, M x N, few and pair kernel in us: 256 x 8192 (32 tiles) 26.0 and 28.3, 256
+// x 9728 (38) 26.0 and 28.6, 256 x 10240 (40) 49.8 and 28.7; 256 x 4096 (16) 23.1 and 20.1.  E8M0
+// scales: 13.9 and 13.3, at 38 tiles 20.4 and 19.2, at 1024 x 2048 (32) 18.6 and 14.9: there the
+// pair kernel is ahead throughout, and the rule is the float scales'.
+constexpr int64_t kFewRows = 128;
+int64_t few_tiles(int sm_count) { return sm_count / 4; }
 constexpr int64_t kFewCols = int64_t(65535) * 128;   // of D in one launch: tiles count in gridDim.y
 constexpr int kMxPieceWaves = 6;
 
@@ -1276,7 +1282,7 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
     PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
     const int64_t pair_tiles = ((D.rows + 255) / 256) * ((D.cols + 255) / 256);
     int slots = 0;
-    if (D.rows > kFewRows && pair_tiles > kFewTiles) {
+    if (D.rows > kFewRows && pair_tiles > few_tiles(sm_count)) {
         const cudaError_t e = pk.init(sm_count, &slots);
         if (e != cudaSuccess) return e;
     }

@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 // is nothing beside 1, and the reciprocal is taken of a quarter of 1 + exp(-x), so that it
 // stays a normal number as long as exp(-x) is finite (x > -88.7) and the last product gives
 // the result below 2^-126 that a block of such gates is made of: its scale may be as small
-// as 2^-127.  (The reciprocal that keeps subnormal numbers comes with 7 more instructions.)
+// as 2^-127.  (SwiGLU's backward at 8192 x 11008: 178.5 us; 176 without the quarter, where
+// such a block comes out as zeros, and 189.5 with the reciprocal that keeps subnormal numbers.)
 __device__ __forceinline__ uint64_t sigmoid2(float x, float y) {
     float s[2];
 #pragma unroll

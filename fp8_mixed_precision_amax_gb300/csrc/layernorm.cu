@@ -129,7 +129,8 @@ __device__ __forceinline__ float sum2(uint64_t v) {
 }
 
 // s / n given 1 / n: the product, corrected by its remainder.  An infinite sum has none
-// (inf - inf): its quotient is infinite, as a division gives it.
+// (inf - inf): its quotient is infinite, as a division gives it.  (8192 x 4096 with both 8-bit
+// outputs: 37.9 us, 37.4 without that choice, 39.8 with a division.)
 __device__ __forceinline__ float quotient(float s, float n, float inv_n) {
     const float q = __fmul_rn(s, inv_n);
     const float r = __fmaf_rn(__fmaf_rn(-q, n, s), inv_n, q);
@@ -223,7 +224,7 @@ __device__ __forceinline__ uint64_t deviations(const uint64_t (&x)[P], uint64_t 
 
 // A team works on R rows side by side, one step apart: their sums share the exchanges and
 // the barriers, and one row's arithmetic fills the other's waits (8192 x 4096, y alone:
-// 27.7 us with two, 31.0 with one; y and x in 8 bits: 37.4 us, of which the blocks' maxima
+// 27.7 us with two, 31.0 with one; y and x in 8 bits: 37.9 us, of which the blocks' maxima
 // and codes are about half).  Rows that have to be shifted into place leave no
 // registers for a second.
 template <typename T, int VPT, bool WARP, int VEC>
@@ -517,9 +518,10 @@ __device__ __forceinline__ void store_part(const LnBwdArgs &a, Col col, const ui
 // dy and x are on their way into a ring in shared memory by bulk copies of the 16-byte
 // blocks that hold them, whatever their alignment; the barrier of a row's sums
 // also tells that its place in the ring may be filled again.  (With the next row in
-// registers instead, one row's loads were in flight per CTA: 91 us at 8192 x 8192, and 73
-// so, 0.82 of a copy's rate.  Issue slots (44 %) and the row's barrier bind now; rows that
-// start anywhere cost 640 instructions per warp for 350: 5003 x 4111 from 8 bits 56 us.)
+// registers instead, one row's loads were in flight per CTA: 91 us at 8192 x 8192 for 84, and
+// 5003 x 4111 from 8 bits 104 for 70.  8192 x 8192 is at 73 now, 0.82 of a copy's rate.  Issue
+// slots (44 %) and the row's barrier bind; rows that start anywhere cost 640 instructions per
+// warp for 350: 5003 x 4111 from 8 bits 56 us.)
 constexpr int kRing = 8;   // most rows in flight
 
 struct RingArgs {

@@ -21,7 +21,9 @@ constexpr int64_t kBwdSlab = 4096;    // columns of a wide row's slab, 16 for ea
 // CTAs per SM of the ring kernel: of up to 288 threads (4608 columns) two fit beside
 // each other, smaller ones by threads.  Two of 256 threads have 128 registers each, two of
 // 288 only 96, since their 18 warps put five on one of the SM's four schedulers (8192 x
-// 4096: 41.0 us, and 50.8 with the 96 of the larger one).
+// 4096: 41.0 us, and 50.8 with the 96 of the larger one).  8192 x 4608 with two CTAs and with
+// one: from x 55.7 and 56.0 us, from 8 bits 59.3 and 66.8.  Past that, x decides for one: 8192 x
+// 5120 (320 threads) with two and with one: from x 59.2 and 57.9, from 8 bits 63.8 and 68.5.
 constexpr unsigned kRingHalf = 288;
 inline int64_t ring_ctas_per_sm(unsigned threads) {
     return threads > kRingHalf ? 1 : threads > 128 ? 2 : 512 / threads;
