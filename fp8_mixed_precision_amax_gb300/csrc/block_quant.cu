@@ -235,7 +235,7 @@ __device__ __forceinline__ uint64_t sigmoid2(float x, float y) {
 }
 
 // 8 lanes per block of 128 columns of a row, four blocks per warp.  8192 x 11008 BF16
-// with h kept: 124 us, where reading and writing alone is 93; 777 x 2688 4.1 and 2.2.  (16
+// with h kept: 127 us, where reading and writing alone is 93; 777 x 2688 4.1 and 2.2.  (16
 // lanes per block, with twice the exchanges and scales per value: 146 and 4.4, but 2.2 for
 // one token of 11008, here 2.7.)
 template <typename T>
@@ -290,7 +290,7 @@ struct SwigluSmem {
 };
 
 // The three results of a tile in registers at once: 192 KB of the SM's 256, so one CTA
-// per SM.  Bound by issue slots (57 %; 46 instructions per element of da) and the three
+// per SM.  Bound by issue slots (59 %; some 46 instructions per element of da) and the three
 // barriers of a tile: 8192 x 11008 BF16 178.5 us, 4.5 TB/s (0.67 of a copy's rate).
 template <typename T, int FMT, int AFMT, int HFMT>
 __global__ void __launch_bounds__(kTileThreads, 1)
