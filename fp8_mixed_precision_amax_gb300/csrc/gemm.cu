@@ -41,6 +41,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "once_per_device.h"
+#include "raster.cuh"
 
 namespace fp8k {
 
@@ -57,9 +58,6 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 128;
 constexpr int NUM_THREADS = 192;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int GROUP_M = 16;                 // row-blocks per raster group when neither operand
-constexpr int GROUP_M_SMALL = 8;            // fits: GROUP_M when A is the smaller, else GROUP_M_SMALL
-constexpr int64_t RESIDENT_BYTES = 48 << 20;   // an operand this small is kept in L2
 constexpr int MAX_PROBLEMS = 2;
 constexpr int EPI_COLS = 64;                      // output columns per TMA store (128 B of BF16)
 constexpr int EPI_BUF = 32 * EPI_COLS * 2;        // one warp's staging buffer: 32 rows x 128 B
@@ -86,7 +84,7 @@ struct GemmProblem {
     const float *b_scale_inv;
     int64_t M, N;
     int tiles_m, tiles_n, num_kb;
-    int group_m;      // row-blocks per raster group (see make_args)
+    int group_m;      // row-blocks per raster group (raster_group)
     int tile_begin;   // first index of this problem's tiles in the launch's tile list
     uint32_t idesc;
 };
@@ -99,16 +97,6 @@ struct GemmArgs {
     int num_tiles;
     unsigned long long *clock_probe;      // diagnostic: {SM cycles, ns} of CTA 0, or null
 };
-
-__device__ __forceinline__ void tile_coords(int tile, int tiles_m, int tiles_n, int group_m,
-                                            int &mb, int &nb) {
-    const int group = tile / (group_m * tiles_n);
-    const int first_m = group * group_m;
-    const int gm = min(tiles_m - first_m, group_m);
-    const int in = tile - group * group_m * tiles_n;
-    mb = first_m + in % gm;
-    nb = in / gm;
-}
 
 // Problem and (row-block, column-block) of a tile of the launch's list.
 __device__ __forceinline__ int locate(const GemmArgs &a, int tile, int &mb, int &nb) {
@@ -529,23 +517,7 @@ cudaError_t launch_gemm_group(const GemmSpec *specs, int n, int sm_count, cudaSt
         p.tiles_m = static_cast<int>((g.M + tile_m - 1) / tile_m);
         p.tiles_n = static_cast<int>((g.N + BN - 1) / BN);
         p.num_kb = static_cast<int>((g.K + BK - 1) / BK);
-        // Raster: tiles are walked down groups of group_m row-blocks.  When
-        // one operand is small enough to stay in L2, walk so that it does
-        // and the other streams through once: all row-blocks at a time when
-        // A is the smaller (A resident), two row-blocks when B is (B
-        // resident).  When neither fits: groups of GROUP_M row-blocks when
-        // A is the smaller, so that the larger B is walked fewer times, and
-        // of GROUP_M_SMALL otherwise, which keeps more of B in L2 from one
-        // group's waves to the next.  (70B-shaped layer, DRAM bytes per
-        // launch: fprop 1.10 GB with 16 against 1.47 GB with 8; the grouped
-        // backward 3.85 GB with 8 and 8 against 4.51 GB with 16 and 16.)
-        const int64_t a_bytes = g.M * g.K, b_bytes = g.N * g.K;
-        if (a_bytes <= b_bytes && a_bytes <= RESIDENT_BYTES)
-            p.group_m = p.tiles_m;
-        else if (b_bytes < a_bytes && b_bytes <= RESIDENT_BYTES)
-            p.group_m = 2;
-        else
-            p.group_m = a_bytes < b_bytes ? GROUP_M : GROUP_M_SMALL;
+        p.group_m = raster_group(g.M * g.K, g.N * g.K, p.tiles_m);
         p.tile_begin = tiles;
         p.idesc = idesc_f8(static_cast<uint32_t>(g.fa), static_cast<uint32_t>(g.fb),
                            static_cast<uint32_t>(tile_m), BN);

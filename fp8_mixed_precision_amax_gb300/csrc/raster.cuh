@@ -1,5 +1,5 @@
-// raster.cuh -- the order in which the persistent block-scaled GEMM kernels visit output
-// tiles: the per-tensor GEMM's (gemm.cu).
+// raster.cuh -- the order in which the persistent GEMM kernels (gemm.cu, block_gemm.cu)
+// visit output tiles.
 #pragma once
 
 #include <cstdint>
@@ -23,11 +23,12 @@ __device__ __forceinline__ void tile_coords(int tile, int tiles_m, int tiles_n, 
 // resident), two row-blocks when B is (B resident).  When neither fits: groups
 // of kGroupM row-blocks when A is the smaller, so that the larger B is walked
 // fewer times, and of kGroupMSmall otherwise, which keeps more of B in L2 from
-// one group's waves to the next.  The constants are the per-tensor GEMM's, which
-// reads the same operands: its DRAM bytes at 8192 x 28672 x 8192 are 1.10 GB with 16
-// and 1.47 GB with 8.  The block-scaled kernels' times do not tell the two apart (E8M0
-// scales: 1120 us with 16, 1130 to 1144 with 8; 28672 x 8192 x 8192 1265 to 1299 either way):
-// the tensor pipe and the power limit bind first.
+// one group's waves to the next.  (Per-tensor GEMM, 70B-shaped layer, DRAM bytes per
+// launch: fprop 1.10 GB with 16 against 1.47 GB with 8; the grouped backward 3.85 GB
+// with 8 and 8 against 4.51 GB with 16 and 16.  The block-scaled kernels' times do not
+// tell them apart, the tensor pipe and the power limit bind first: E8M0 scales, 8192 x
+// 28672 x 8192 1120 us with 16, 1130 to 1144 with 8; 28672 x 8192 x 8192 1265 to 1299
+// with either.)
 constexpr int kGroupM = 16, kGroupMSmall = 8;
 constexpr int64_t kResidentBytes = 48 << 20;   // an operand this small is kept in L2
 
