@@ -183,10 +183,14 @@ def _check(status: int) -> None:
         raise Fp8Error(status, _lib.fp8_last_error().decode())
 
 
+# The current stream without a Stream object (a tenth of a short call's time): torch's own, not
+# part of its interface, so done without where there is none.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> "ctypes.c_void_p | int":
-    if stream is None and torch.cuda.is_initialized():
-        # the current device's current stream, without a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None and _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
     if stream is None:
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):

@@ -50,3 +50,16 @@ def test_mlp_made_on_another_stream():
     for name in ("W1q", "W1t", "W2q", "W2t"):
         assert torch.equal(getattr(mlp, name).codes, getattr(want, name).codes), name
         assert torch.equal(getattr(mlp, name).scales[:, :8], getattr(want, name).scales[:, :8]), name
+
+
+@pytest.mark.parametrize("private", [True, False])
+def test_calls_go_to_the_current_stream(monkeypatch, private):
+    from fp8_mixed_precision_amax_gb300 import api
+    if not private:
+        monkeypatch.setattr(api, "_raw_stream", None)
+    handle = lambda s: getattr(s, "value", s) or 0
+    assert handle(api._stream(None)) == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert handle(api._stream(None)) == side.cuda_stream
+    assert handle(api._stream(side)) == handle(api._stream(side.cuda_stream)) == side.cuda_stream
