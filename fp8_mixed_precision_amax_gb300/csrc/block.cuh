@@ -539,7 +539,8 @@ struct RowWriter {
 // pairs, so v[r][p] is row 8 w + r, columns 4 l + 2 p, + 1.  Elements outside the
 // matrix are 0: they leave every maximum as it is.  While a tile is worked on, each
 // warp's rows of the CTA's next tile are already on their way into shared memory
-// (cp.async, waited for by that warp alone).
+// (cp.async, waited for by that warp alone).  Rows that are not 16-byte aligned are not:
+// the warp copies them element by element before it goes on, 32 loads one after the other.
 //
 // A row's maximum is one warp reduction.  A column's is taken over a thread's 8
 // rows, then over the 16 warps by one thread per column.  The transposed codes go
