@@ -83,6 +83,10 @@ class fp8_block_tensor(ctypes.Structure):
                 ("block_rows", ctypes.c_int32), ("scale_type", ctypes.c_int32)]
 
 
+class fp8_vector(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 SCALE_E8M0, SCALE_F32 = 0, 1
 
 
@@ -130,6 +134,7 @@ def _load() -> ctypes.CDLL:
                                    ctypes.c_int),
     }
     pm, pb = ctypes.POINTER(fp8_matrix), ctypes.POINTER(fp8_block_tensor)
+    pv = ctypes.POINTER(fp8_vector)
     st = ctypes.c_int
     sig.update({
         "fp8_block_quantize": ([pm, pb, pb, vp], st),
@@ -139,6 +144,13 @@ def _load() -> ctypes.CDLL:
         "fp8_layernorm_bwd": ([pm, pm, pb, vp, i32, vp, vp, pm, vp, vp, vp, i64, vp], st),
         "fp8_layernorm_bwd_workspace": ([i64, i64], i64),
         "fp8_layernorm_recompute": ([pb, vp, vp, i32, vp, vp, pb, vp], st),
+        "fp8_rmsnorm_fwd": ([pm, pm, vp, i32, ctypes.c_float, pm, pm, pb, pb, vp, vp], st),
+        "fp8_rmsnorm_bwd": ([pm, pm, pb, vp, i32, vp, pm, pm, vp, vp, i64, vp], st),
+        "fp8_rmsnorm_bwd_workspace": ([i64, i64], i64),
+        "fp8_rmsnorm_recompute": ([pb, vp, i32, vp, pb, vp], st),
+        "fp8_grad_norm": ([pv, i32, vp, vp, i64, vp], st),
+        "fp8_grad_norm_workspace": ([i32], i64),
+        "fp8_grad_clip": ([pv, pv, i32, vp, ctypes.c_float, vp], st),
         "fp8_swiglu_fwd": ([pm, pb, pb, vp], st),
         "fp8_swiglu_bwd": ([pm, pb, pb, pb, pb, vp], st),
     })
@@ -151,13 +163,15 @@ def _load() -> ctypes.CDLL:
 
 
 def _load_packed(prototypes: ctypes.CDLL) -> ctypes.CDLL:
-    """The library once more: the block-scaled calls with the same prototypes, but structs as
-    packed bytes."""
+    """The library once more: the block-scaled calls and those on lists of gradients with the
+    same prototypes, but structs as packed bytes."""
     lib = ctypes.CDLL(LIB_PATH)
-    structs = (ctypes.POINTER(fp8_matrix), ctypes.POINTER(fp8_block_tensor))
+    structs = (ctypes.POINTER(fp8_matrix), ctypes.POINTER(fp8_block_tensor),
+               ctypes.POINTER(fp8_vector))
     for name in ("fp8_block_quantize", "fp8_block_dequantize", "fp8_block_gemm_tn",
                  "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_recompute",
-                 "fp8_swiglu_fwd", "fp8_swiglu_bwd"):
+                 "fp8_swiglu_fwd", "fp8_swiglu_bwd", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd",
+                 "fp8_rmsnorm_recompute", "fp8_grad_norm", "fp8_grad_clip"):
         f, of = getattr(lib, name), getattr(prototypes, name)
         f.argtypes = [ctypes.c_char_p if a in structs else a for a in of.argtypes]
         f.restype = of.restype
@@ -954,6 +968,79 @@ def fp8_layernorm_recompute(x8: BlockFp8, gamma: torch.Tensor, beta: torch.Tenso
         _block(yt, "yt"), _stream(stream)))
 
 
+def _here(*tensors) -> None:
+    """The calls work on the current device: refuses tensors (None: not given) of another one."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if isinstance(t, BlockFp8):
+            t = t.codes
+        if t.get_device() != device and t.is_cuda:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{device}")
+
+
+def fp8_rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, rstd: torch.Tensor,
+                    residual: torch.Tensor | None = None, sum: torch.Tensor | None = None,
+                    y: torch.Tensor | None = None, y8: BlockFp8 | None = None,
+                    x8: BlockFp8 | None = None, stream=None) -> None:
+    """Root-mean-square norm of s = x + residual (x alone without one): rstd (float32), and any
+    of sum (s itself, rounded to x's type, which the norm is taken of; may be x or residual),
+    y (of x's type), y8 (y block quantized) and x8 (s kept in 8 bits for the backward pass)."""
+    xm = _matrix(x, "x")
+    rows, cols = x.shape
+    _here(x, gamma, rstd, residual, sum, y, y8, x8)
+    _check(_packed.fp8_rmsnorm_fwd(
+        xm, _matrix(residual, "residual"), _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], eps,
+        _matrix(sum, "sum"), _matrix(y, "y"), _block(y8, "y8"), _block(x8, "x8"),
+        _stat(rstd, rows, "rstd"), _stream(stream)))
+
+
+def fp8_rmsnorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: torch.Tensor,
+                    rstd: torch.Tensor, dx: torch.Tensor, dgamma: torch.Tensor,
+                    dsum: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Backward of the RMS norm from s, the forward's ``sum`` (``x`` without a residual), or its
+    8-bit copy (the forward's ``x8``): dx (of dy's type; may be dy or dsum), the gradient of x
+    and of the residual alike, and dgamma (float32).  ``dsum``: the gradient that reaches s by
+    the residual's way.  ``workspace``: at least ``fp8_rmsnorm_bwd_workspace(rows, cols)``
+    bytes of CUDA memory; taken from torch's allocator when None."""
+    dym = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    _here(dy, x, gamma, rstd, dx, dgamma, dsum, workspace)
+    if workspace is None:
+        room = _lib.fp8_rmsnorm_bwd_workspace(rows, cols)
+        with _on_stream(stream, dy.device):
+            workspace = torch.empty(room, dtype=torch.uint8, device=dy.device)
+        place = workspace.data_ptr()
+    else:
+        room = workspace.numel() * workspace.element_size()
+        place = _ptr(workspace, None, "workspace")
+    saved = isinstance(x, BlockFp8)
+    _check(_packed.fp8_rmsnorm_bwd(
+        dym, None if saved else _matrix(x, "x"), _block(x, "x") if saved else None,
+        _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], _stat(rstd, rows, "rstd"),
+        _matrix(dsum, "dsum"), _matrix(dx, "dx"), _stat(dgamma, cols, "dgamma"), place, room,
+        _stream(stream)))
+
+
+def fp8_rmsnorm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that fp8_rmsnorm_bwd needs."""
+    return _lib.fp8_rmsnorm_bwd_workspace(rows, cols)
+
+
+def fp8_rmsnorm_recompute(x8: BlockFp8, gamma: torch.Tensor, rstd: torch.Tensor, yt: BlockFp8,
+                          stream=None) -> None:
+    """The RMS norm's output again from the 8-bit copy of its input, transposed and block
+    quantized along the tokens: the weight gradient's operand."""
+    rows, cols = x8.shape
+    xb = _block(x8, "x8")
+    _here(x8, gamma, rstd, yt)
+    _check(_packed.fp8_rmsnorm_recompute(
+        xb, _param(gamma, cols, "gamma"), _DTYPES[gamma.dtype], _stat(rstd, rows, "rstd"),
+        _block(yt, "yt"), _stream(stream)))
+
+
 def fp8_swiglu_fwd(h: torch.Tensor, a8: BlockFp8, h8: BlockFp8 | None = None,
                    stream=None) -> None:
     """SwiGLU of h = [gate | value], block quantized into ``a8``; ``h8``: h
@@ -970,3 +1057,68 @@ def fp8_swiglu_bwd(da: torch.Tensor, h8: BlockFp8, dh8: BlockFp8 | None = None,
     output again, transposed (``a8t``)."""
     _check(_packed.fp8_swiglu_bwd(_matrix(da, "da"), _block(h8, "h8"), _block(dh8, "dh8"),
                                _block(dh8t, "dh8t"), _block(a8t, "a8t"), _stream(stream)))
+
+
+# ------------------------------------------------------- lists of gradients --
+
+assert struct.calcsize("@Pqixxxx") == ctypes.sizeof(fp8_vector)
+
+
+def _vectors(tensors, name: str) -> bytes:
+    words = []
+    for i, t in enumerate(tensors):
+        if not t.is_cuda:
+            raise ValueError(f"{name}[{i}] must be a CUDA tensor")
+        dtype = _DTYPES.get(t.dtype)
+        if dtype is None:
+            raise ValueError(f"{name}[{i}] must be float32, bfloat16 or float16, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        words += (t.data_ptr(), t.numel(), dtype)
+    return struct.pack("@" + "Pqixxxx" * len(tensors), *words)
+
+
+def fp8_grad_norm(grads, norm: torch.Tensor, workspace: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """norm (float32, one element) = the 2-norm of all the tensors together (contiguous, any
+    shapes, float32, bfloat16 or float16; NaN or infinity where they hold one).
+    ``workspace``: at least ``fp8_grad_norm_workspace(len(grads))`` bytes of CUDA memory;
+    taken from torch's allocator when None."""
+    grads = list(grads)
+    v = _vectors(grads, "grads")
+    _here(*grads, norm, workspace)
+    if workspace is None:
+        room = _lib.fp8_grad_norm_workspace(len(grads))
+        with _on_stream(stream, norm.device):
+            workspace = torch.empty(room, dtype=torch.uint8, device=norm.device)
+        place = workspace.data_ptr()
+    else:
+        room = workspace.numel() * workspace.element_size()
+        place = _ptr(workspace, None, "workspace")
+    _check(_packed.fp8_grad_norm(v, len(grads), _stat(norm, 1, "norm"), place, room,
+                                 _stream(stream)))
+
+
+def fp8_grad_norm_workspace(count: int) -> int:
+    """Bytes of workspace that fp8_grad_norm needs for a list of ``count`` tensors."""
+    return _lib.fp8_grad_norm_workspace(count)
+
+
+def fp8_grad_clip(grads, norm: torch.Tensor, max_norm: float, outs=None, stream=None) -> None:
+    """outs[i] = grads[i] * max_norm / norm where max_norm < norm < infinity, else grads[i], in
+    float32 and rounded to the type of outs[i] (None: in place).  ``norm``: fp8_grad_norm's,
+    read on the device, so that nothing waits for it; after an all-reduce of its square over
+    the ranks it is the norm of all their gradients.  A norm that is not finite changes
+    nothing: the caller sees it there, and skips the step."""
+    grads = list(grads)
+    outs = grads if outs is None else list(outs)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(grads)} grads, but {len(outs)} outs")
+    v = _vectors(grads, "grads")
+    o = v if outs is grads else _vectors(outs, "outs")
+    places = [t.data_ptr() for t in outs if t.numel()]
+    if len(set(places)) != len(places):
+        raise ValueError("a tensor is twice among those to be written")
+    _here(*grads, norm, *(outs if outs is not grads else ()))
+    _check(_packed.fp8_grad_clip(v, o, len(grads), _stat(norm, 1, "norm"), max_norm,
+                                 _stream(stream)))

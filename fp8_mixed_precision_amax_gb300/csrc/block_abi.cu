@@ -93,6 +93,15 @@ fp8_status check_rows_out(const char *fn, const fp8_block_tensor *q, const fp8k:
     return FP8_OK;
 }
 
+// an optional matrix of another one's shape and type
+fp8_status check_like(const char *fn, const fp8_matrix *m, const fp8k::MatView &v, const char *name,
+                      const fp8k::MatView &of, const char *of_name) {
+    if (m == nullptr) return FP8_OK;
+    FP8_TRY(check_shape(fn, v, name, of.rows, of.cols));
+    if (v.type != of.type) return fail(FP8_ERR_ARG, "%s: %s must have %s's type", fn, name, of_name);
+    return FP8_OK;
+}
+
 fp8_status check_tiles(const char *fn, int64_t rows, int64_t cols) {
     if (((rows + 127) / 128) * ((cols + 127) / 128) >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: more than 2^31 tiles", fn);
@@ -103,6 +112,25 @@ fp8_status check_param(const char *fn, const void *p, int32_t type, const char *
     if (p == nullptr) return fail(FP8_ERR_ARG, "%s: %s is NULL", fn, name);
     if (reinterpret_cast<uintptr_t>(p) % (type == FP8_DTYPE_F32 ? 4 : 2))
         return fail(FP8_ERR_ALIGN, "%s: %s is not aligned to its elements", fn, name);
+    return FP8_OK;
+}
+
+constexpr int64_t kMaxVector = int64_t(1) << 40;   // elements
+
+fp8_status check_vectors(const char *fn, const fp8_vector *v, int32_t count, const char *name) {
+    if (count < 0) return fail(FP8_ERR_ARG, "%s: count %d", fn, count);
+    if (v == nullptr && count > 0) return fail(FP8_ERR_ARG, "%s: %s is NULL", fn, name);
+    for (int32_t i = 0; i < count; ++i) {
+        if (v[i].dtype != FP8_DTYPE_F32 && v[i].dtype != FP8_DTYPE_BF16 && v[i].dtype != FP8_DTYPE_F16)
+            return fail(FP8_ERR_ARG, "%s: %s[%d]: bad type %d", fn, name, i, v[i].dtype);
+        if (v[i].n < 0 || v[i].n > kMaxVector)
+            return fail(FP8_ERR_ARG, "%s: %s[%d]: bad length %lld", fn, name, i,
+                        static_cast<long long>(v[i].n));
+        if (v[i].data == nullptr && v[i].n > 0)
+            return fail(FP8_ERR_ARG, "%s: %s[%d] has no data", fn, name, i);
+        if (reinterpret_cast<uintptr_t>(v[i].data) % (v[i].dtype == FP8_DTYPE_F32 ? 4 : 2))
+            return fail(FP8_ERR_ALIGN, "%s: %s[%d] is not aligned to its elements", fn, name, i);
+    }
     return FP8_OK;
 }
 
@@ -278,6 +306,103 @@ fp8_status fp8_layernorm_recompute(const fp8_block_tensor *x8, const void *gamma
     return FP8_OK;
 }
 
+fp8_status fp8_rmsnorm_fwd(const fp8_matrix *x, const fp8_matrix *residual, const void *gamma,
+                           int32_t wtype, float eps, const fp8_matrix *sum, const fp8_matrix *y,
+                           const fp8_block_tensor *y8, const fp8_block_tensor *x8, float *rstd,
+                           void *stream) {
+    const char *fn = "fp8_rmsnorm_fwd";
+    const fp8k::CallRange range(fn);
+    fp8k::MatView vx, vr, vs, vy;
+    fp8k::BlockView vy8, vx8;
+    FP8_TRY(view(fn, x, "x", false, &vx));
+    FP8_TRY(view(fn, residual, "residual", true, &vr));
+    FP8_TRY(view(fn, sum, "sum", true, &vs));
+    FP8_TRY(view(fn, y, "y", true, &vy));
+    FP8_TRY(view(fn, y8, "y8", true, &vy8));
+    FP8_TRY(view(fn, x8, "x8", true, &vx8));
+    if (vx.cols < 1) return fail(FP8_ERR_ARG, "%s: x has no columns", fn);
+    if (!(eps >= 0.0f)) return fail(FP8_ERR_ARG, "%s: eps must be >= 0", fn);
+    FP8_TRY(check_type(fn, wtype, "gamma"));
+    FP8_TRY(check_param(fn, gamma, wtype, "gamma"));
+    if (sum != nullptr && residual == nullptr)
+        return fail(FP8_ERR_ARG, "%s: sum is given without a residual", fn);
+    FP8_TRY(check_like(fn, residual, vr, "residual", vx, "x"));
+    FP8_TRY(check_like(fn, sum, vs, "sum", vx, "x"));
+    FP8_TRY(check_like(fn, y, vy, "y", vx, "x"));
+    FP8_TRY(check_rows_out(fn, y8, vy8, "y8", vx.rows, vx.cols));
+    FP8_TRY(check_rows_out(fn, x8, vx8, "x8", vx.rows, vx.cols));
+    FP8_TRY(check_scalar(fn, rstd, "rstd", vx.rows == 0));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    FP8_CUDA(fp8k::launch_rms_fwd(vx, vr, gamma, wtype, eps, vs, vy, vy8, vx8, rstd, sms,
+                                  static_cast<cudaStream_t>(stream)),
+             fn);
+    return FP8_OK;
+}
+
+int64_t fp8_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+    return rows <= 0 || cols <= 0 ? 0 : fp8k::rms_bwd_workspace(rows, cols);
+}
+
+fp8_status fp8_rmsnorm_bwd(const fp8_matrix *dy, const fp8_matrix *x, const fp8_block_tensor *x8,
+                           const void *gamma, int32_t wtype, const float *rstd,
+                           const fp8_matrix *dsum, const fp8_matrix *dx, float *dgamma,
+                           void *workspace, int64_t workspace_bytes, void *stream) {
+    const char *fn = "fp8_rmsnorm_bwd";
+    const fp8k::CallRange range(fn);
+    fp8k::MatView vdy, vx, vds, vdx;
+    fp8k::BlockView vx8;
+    FP8_TRY(view(fn, dy, "dy", false, &vdy));
+    FP8_TRY(view(fn, x, "x", true, &vx));
+    FP8_TRY(view(fn, x8, "x8", true, &vx8));
+    FP8_TRY(view(fn, dsum, "dsum", true, &vds));
+    FP8_TRY(view(fn, dx, "dx", false, &vdx));
+    if ((x != nullptr) == (x8 != nullptr))
+        return fail(FP8_ERR_ARG, "%s: exactly one of x and x8 is given", fn);
+    if (vdy.cols < 1) return fail(FP8_ERR_ARG, "%s: dy has no columns", fn);
+    FP8_TRY(check_like(fn, x, vx, "x", vdy, "dy"));
+    FP8_TRY(check_rows_out(fn, x8, vx8, "x8", vdy.rows, vdy.cols));
+    FP8_TRY(check_like(fn, dsum, vds, "dsum", vdy, "dy"));
+    FP8_TRY(check_like(fn, dx, vdx, "dx", vdy, "dy"));
+    FP8_TRY(check_type(fn, wtype, "gamma"));
+    FP8_TRY(check_param(fn, gamma, wtype, "gamma"));
+    const bool empty = vdy.rows == 0;
+    FP8_TRY(check_scalar(fn, rstd, "rstd", empty));
+    FP8_TRY(check_scalar(fn, dgamma, "dgamma", false));
+    FP8_TRY(check_ptr(fn, workspace, "workspace", empty));
+    const int64_t need = fp8_rmsnorm_bwd_workspace(vdy.rows, vdy.cols);
+    if (workspace_bytes < need)
+        return fail(FP8_ERR_ARG, "%s: workspace of %lld bytes, %lld are needed", fn,
+                    static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    FP8_CUDA(fp8k::launch_rms_bwd(vdy, vx, vx8, gamma, wtype, rstd, vds, vdx, dgamma, workspace, sms,
+                                  static_cast<cudaStream_t>(stream)),
+             fn);
+    return FP8_OK;
+}
+
+fp8_status fp8_rmsnorm_recompute(const fp8_block_tensor *x8, const void *gamma, int32_t wtype,
+                                 const float *rstd, const fp8_block_tensor *yt, void *stream) {
+    const char *fn = "fp8_rmsnorm_recompute";
+    const fp8k::CallRange range(fn);
+    fp8k::BlockView vx8, vyt;
+    FP8_TRY(view(fn, x8, "x8", false, &vx8));
+    FP8_TRY(view(fn, yt, "yt", false, &vyt));
+    FP8_TRY(check_rows_out(fn, x8, vx8, "x8", vx8.rows, vx8.cols));
+    FP8_TRY(check_rows_out(fn, yt, vyt, "yt", vx8.cols, vx8.rows));
+    FP8_TRY(check_type(fn, wtype, "gamma"));
+    FP8_TRY(check_param(fn, gamma, wtype, "gamma"));
+    FP8_TRY(check_scalar(fn, rstd, "rstd", vx8.rows == 0 || vx8.cols == 0));
+    FP8_TRY(check_tiles(fn, vx8.rows, vx8.cols));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    FP8_CUDA(fp8k::launch_rms_recompute(vx8, gamma, wtype, rstd, vyt, sms,
+                                        static_cast<cudaStream_t>(stream)),
+             fn);
+    return FP8_OK;
+}
+
 fp8_status fp8_swiglu_fwd(const fp8_matrix *h, const fp8_block_tensor *a8,
                           const fp8_block_tensor *h8, void *stream) {
     const char *fn = "fp8_swiglu_fwd";
@@ -327,6 +452,49 @@ fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_swiglu_bwd(vda, vh8, vdh8, vdh8t, va8t, sms,
                                      static_cast<cudaStream_t>(stream)),
+             fn);
+    return FP8_OK;
+}
+
+int64_t fp8_grad_norm_workspace(int32_t count) { return fp8k::grad_norm_workspace(count); }
+
+fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, void *workspace,
+                         int64_t workspace_bytes, void *stream) {
+    const char *fn = "fp8_grad_norm";
+    const fp8k::CallRange range(fn);
+    FP8_TRY(check_vectors(fn, grads, count, "grads"));
+    FP8_TRY(check_scalar(fn, norm, "norm", false));
+    if (workspace == nullptr) return fail(FP8_ERR_ARG, "%s: workspace is NULL", fn);
+    if (reinterpret_cast<uintptr_t>(workspace) % 8)
+        return fail(FP8_ERR_ALIGN, "%s: workspace is not 8-byte aligned", fn);
+    const int64_t need = fp8_grad_norm_workspace(count);
+    if (workspace_bytes < need)
+        return fail(FP8_ERR_ARG, "%s: workspace of %lld bytes, %lld are needed", fn,
+                    static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    FP8_CUDA(fp8k::launch_grad_norm(reinterpret_cast<const fp8k::VectorView *>(grads), count, norm, workspace, sms, static_cast<cudaStream_t>(stream)), fn);
+    return FP8_OK;
+}
+
+fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_t count,
+                         const float *norm, float max_norm, void *stream) {
+    const char *fn = "fp8_grad_clip";
+    const fp8k::CallRange range(fn);
+    FP8_TRY(check_vectors(fn, grads, count, "grads"));
+    if (outs == nullptr) outs = grads;
+    FP8_TRY(check_vectors(fn, outs, count, "outs"));
+    for (int32_t i = 0; i < count; ++i)
+        if (outs[i].n != grads[i].n)
+            return fail(FP8_ERR_ARG, "%s: outs[%d] has %lld elements, grads[%d] %lld", fn, i,
+                        static_cast<long long>(outs[i].n), i, static_cast<long long>(grads[i].n));
+    FP8_TRY(check_scalar(fn, norm, "norm", false));
+    if (!(max_norm >= 0.0f)) return fail(FP8_ERR_ARG, "%s: max_norm must be >= 0", fn);
+    int sms;
+    FP8_TRY(current_device(&sms));
+    FP8_CUDA(fp8k::launch_grad_clip(reinterpret_cast<const fp8k::VectorView *>(grads),
+                                    reinterpret_cast<const fp8k::VectorView *>(outs), count, norm, max_norm,
+                                    sms, static_cast<cudaStream_t>(stream)),
              fn);
     return FP8_OK;
 }

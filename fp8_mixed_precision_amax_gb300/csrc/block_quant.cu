@@ -137,9 +137,10 @@ struct RecomputeSmem {
 // The forward's formula on the codes, so the same roundings.  8192 x 4096: 21.5 us, bound
 // by instructions; reading and writing alone is 10.  (With scalar arithmetic, a bound on
 // every element and the rows' statistics fetched when needed: 32.)
-template <int FMT>
+// RMS: the RMS norm's output, without mean and beta.
+template <int FMT, bool RMS>
 __global__ void __launch_bounds__(kTileThreads, 2)
-    ln_recompute_kernel(const BlockView x8, const void *__restrict__ gamma,
+    norm_recompute_kernel(const BlockView x8, const void *__restrict__ gamma,
                         const void *__restrict__ beta, int wtype, const float *__restrict__ mean,
                         const float *__restrict__ rstd, const BlockView yt, unsigned tiles_r,
                         unsigned tiles_c) {
@@ -161,7 +162,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         const unsigned row = r0 + warp * kTileRows + (lane & 7);
         if (row < x8.rows) {
             sc_next = fetch_scale(x8, row, c0 / kTile);
-            mu_next = mean[row], rs_next = rstd[row];
+            if constexpr (!RMS) mu_next = mean[row];
+            rs_next = rstd[row];
         }
     };
     fetch_stats(row0, col0);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         if (more) fetch_stats(next_row0, next_col0);
         uint64_t g[2], b[2];
         load_param4(gamma, wtype, col0 + 4 * lane, x8.cols, g);
-        load_param4(beta, wtype, col0 + 4 * lane, x8.cols, b);
+        if constexpr (!RMS) load_param4(beta, wtype, col0 + 4 * lane, x8.cols, b);
         cp_async_wait<1>();
         __syncwarp();
         // columns past the end may hold anything: they are rows of yt that are not stored
@@ -189,14 +191,19 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 #pragma unroll
         for (int r = 0; r < kTileRows; ++r) {
             const uint64_t s2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, sc, r));
-            const uint64_t nm2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, nmu, r));
+            uint64_t nm2 = 0;
+            if constexpr (!RMS) nm2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, nmu, r));
             const uint64_t rs2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, rs, r));
             float f[4];
             decode4(*reinterpret_cast<const uint32_t *>(sm.in[stage] + part + r * kTile + lane * 4), x8.fmt, f);
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                v[r][p] = f32x2_fma(f32x2_mul(f32x2_fma(f32x2_pack(f[2 * p], f[2 * p + 1]), s2, nm2), rs2),
-                                    g[p], b[p]);
+            for (int p = 0; p < 2; ++p) {
+                const uint64_t code = f32x2_pack(f[2 * p], f[2 * p + 1]);
+                if constexpr (RMS)
+                    v[r][p] = f32x2_mul(f32x2_mul(f32x2_mul(code, s2), rs2), g[p]);
+                else
+                    v[r][p] = f32x2_fma(f32x2_mul(f32x2_fma(code, s2, nm2), rs2), g[p], b[p]);
+            }
         }
         if (row0 + kTile > x8.rows) {
 #pragma unroll
@@ -477,10 +484,22 @@ cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const vo
                                 int sm_count, cudaStream_t st) {
     if (x8.rows == 0 || x8.cols == 0) return cudaSuccess;
     if (yt.fmt == 0)
-        return launch_tiles<ln_recompute_kernel<0>, RecomputeSmem>(2, x8.rows, x8.cols, sm_count, st,
-                                                                   x8, gamma, beta, wtype, mean, rstd, yt);
-    return launch_tiles<ln_recompute_kernel<1>, RecomputeSmem>(2, x8.rows, x8.cols, sm_count, st, x8,
-                                                               gamma, beta, wtype, mean, rstd, yt);
+        return launch_tiles<norm_recompute_kernel<0, false>, RecomputeSmem>(
+            2, x8.rows, x8.cols, sm_count, st, x8, gamma, beta, wtype, mean, rstd, yt);
+    return launch_tiles<norm_recompute_kernel<1, false>, RecomputeSmem>(
+        2, x8.rows, x8.cols, sm_count, st, x8, gamma, beta, wtype, mean, rstd, yt);
+}
+
+cudaError_t launch_rms_recompute(const BlockView &x8, const void *gamma, int wtype, const float *rstd,
+                                 const BlockView &yt, int sm_count, cudaStream_t st) {
+    if (x8.rows == 0 || x8.cols == 0) return cudaSuccess;
+    const void *no_beta = nullptr;
+    const float *no_mean = nullptr;
+    if (yt.fmt == 0)
+        return launch_tiles<norm_recompute_kernel<0, true>, RecomputeSmem>(
+            2, x8.rows, x8.cols, sm_count, st, x8, gamma, no_beta, wtype, no_mean, rstd, yt);
+    return launch_tiles<norm_recompute_kernel<1, true>, RecomputeSmem>(
+        2, x8.rows, x8.cols, sm_count, st, x8, gamma, no_beta, wtype, no_mean, rstd, yt);
 }
 
 cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const BlockView &h8,

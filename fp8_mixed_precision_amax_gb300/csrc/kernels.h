@@ -210,6 +210,20 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
 cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,
                                 const float *mean, const float *rstd, const BlockView &yt,
                                 int sm_count, cudaStream_t st);
+// RMS norm with the residual's addition, forward and backward (rmsnorm.cu); residual, sum,
+// y, y8, x8 and dsum may be empty, and one of x and x8 is in the backward.
+cudaError_t launch_rms_fwd(const MatView &x, const MatView &residual, const void *gamma, int wtype,
+                           float eps, const MatView &sum, const MatView &y, const BlockView &y8,
+                           const BlockView &x8, float *rstd, int sm_count, cudaStream_t st);
+int64_t rms_bwd_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_rms_bwd(const MatView &dy, const MatView &x, const BlockView &x8,
+                           const void *gamma, int wtype, const float *rstd, const MatView &dsum,
+                           const MatView &dx, float *dgamma, void *ws, int sm_count,
+                           cudaStream_t st);
+// yt = quantized transpose of the RMS norm's output (block_quant.cu).
+cudaError_t launch_rms_recompute(const BlockView &x8, const void *gamma, int wtype,
+                                 const float *rstd, const BlockView &yt, int sm_count,
+                                 cudaStream_t st);
 // SwiGLU (block_quant.cu).
 cudaError_t launch_swiglu_fwd(const MatView &h, const BlockView &a8, const BlockView &h8,
                               int sm_count, cudaStream_t st);
@@ -217,10 +231,24 @@ cudaError_t launch_swiglu_bwd(const MatView &da, const BlockView &h8, const Bloc
                               const BlockView &dh8t, const BlockView &a8t, int sm_count,
                               cudaStream_t st);
 
-// Read and clear the device error flags of the block GEMM (block_gemm.cu) and of
-// LayerNorm's backward (layernorm.cu).
+// A vector of n elements in 32 or 16 bits.
+struct VectorView {
+    void *data;
+    int64_t n;
+    int type;
+};
+// The norm of all vectors together, and clipping by it (clip.cu).
+int64_t grad_norm_workspace(int64_t count);
+cudaError_t launch_grad_norm(const VectorView *v, int count, float *norm, void *ws, int sm_count,
+                             cudaStream_t st);
+cudaError_t launch_grad_clip(const VectorView *v, const VectorView *out, int count,
+                             const float *norm, float max_norm, int sm_count, cudaStream_t st);
+
+// Read and clear the device error flags of the block GEMM (block_gemm.cu), of
+// LayerNorm's backward (layernorm.cu) and of the RMS norm's (rmsnorm.cu).
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags);
 cudaError_t read_and_clear_ln_error_flag(unsigned *flags);
+cudaError_t read_and_clear_rms_error_flag(unsigned *flags);
 
 // Diagnostic: while acc is not null, the first CTA of every GEMM launch adds
 // its SM clock cycles to acc[0] and its nanoseconds to acc[1] (gemm.cu).

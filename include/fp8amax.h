@@ -562,6 +562,44 @@ fp8_status fp8_layernorm_recompute(const fp8_block_tensor *x8, const void *gamma
                                    const void *beta, int32_t wtype, const float *mean,
                                    const float *rstd, const fp8_block_tensor *yt, void *stream);
 
+/* Root-mean-square norm with the residual's addition, x [rows][cols], in fp32:
+ *   s = x + residual, rounded to x's type (residual NULL: s = x),
+ *   rstd = 1 / sqrt(sum s^2 / cols + eps),  y = (s * rstd) * gamma.
+ * The norm is taken of s as it is stored.  Writes rstd (fp32 [rows]) and any of:
+ * sum, s itself (with a residual only); y (both of x's type); y8, y block
+ * quantized straight from fp32 (block_rows 1), the operand of a following product;
+ * x8, s in 8 bits (block_rows 1), which fp8_rmsnorm_bwd and
+ * fp8_rmsnorm_recompute take in s's place.  residual is of x's type; sum may be
+ * x's or the residual's own memory (same address and stride), the other outputs
+ * overlap nothing.  gamma [cols] is of type wtype (fp8_dtype).  cols >= 1. */
+fp8_status fp8_rmsnorm_fwd(const fp8_matrix *x, const fp8_matrix *residual, const void *gamma,
+                           int32_t wtype, float eps, const fp8_matrix *sum, const fp8_matrix *y,
+                           const fp8_block_tensor *y8, const fp8_block_tensor *x8, float *rstd,
+                           void *stream);
+
+/* Backward of fp8_rmsnorm_fwd from dy [rows][cols] and s, either x (the forward's
+ * sum) or its 8-bit copy x8 (the other NULL), with the forward's rstd:
+ *   xhat = s * rstd,  u = dy * gamma,
+ *   dx = dsum + rstd * (u - xhat * sum(u * xhat) / cols)   (per row),
+ *   dgamma = sum over rows of dy * xhat.
+ * dsum: the gradient that reaches s by the residual's way (NULL: none).  dx is the
+ * gradient of x and of the residual alike.  dy, x, dsum and dx are of one type;
+ * dgamma is fp32 [cols], overwritten; dx may be dy or dsum (same address and
+ * stride).  workspace: DEVICE, 16-byte aligned, of at least
+ * fp8_rmsnorm_bwd_workspace(rows, cols) bytes, in use until the call's kernels
+ * are done.  The sums' order is fixed: equal calls give equal bits. */
+fp8_status fp8_rmsnorm_bwd(const fp8_matrix *dy, const fp8_matrix *x, const fp8_block_tensor *x8,
+                           const void *gamma, int32_t wtype, const float *rstd,
+                           const fp8_matrix *dsum, const fp8_matrix *dx, float *dgamma,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+int64_t fp8_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* The RMS norm's output again from the 8-bit copy of s, transposed: yt
+ * [cols][rows] (block_rows 1: blocks along the tokens), the operand of the weight
+ * gradient of the product that follows the norm. */
+fp8_status fp8_rmsnorm_recompute(const fp8_block_tensor *x8, const void *gamma, int32_t wtype,
+                                 const float *rstd, const fp8_block_tensor *yt, void *stream);
+
 /* SwiGLU of h [M][2F] = [gate | value]: a = gate / (1 + exp(-gate)) * value in
  * fp32, block quantized into a8 [M][F] (block_rows 1).  h8 (or NULL): h itself
  * in 8 bits [M][2F], for fp8_swiglu_bwd.  F a multiple of 128, so that no
@@ -580,6 +618,41 @@ fp8_status fp8_swiglu_fwd(const fp8_matrix *h, const fp8_block_tensor *a8,
 fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
                           const fp8_block_tensor *dh8, const fp8_block_tensor *dh8t,
                           const fp8_block_tensor *a8t, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The norm of many gradients together, and clipping by it */
+
+/* n consecutive elements of type dtype (fp8_dtype), DEVICE, aligned to the element
+ * (16-byte aligned ones are faster); n >= 0. */
+typedef struct {
+    void *data;
+    int64_t n;
+    int32_t dtype;
+} fp8_vector;
+
+/* norm[0] (DEVICE, fp32) = sqrt(sum over the vectors of the sum of their squares),
+ * of any size: squares are summed in 32 bits with the additions' rounding errors
+ * kept, or in 64 bits where they could leave 32 bits' range, and the sums are joined
+ * in 64 bits.  A NaN or an infinity among the elements gives NaN or infinity, no
+ * elements 0.  grads: HOST array of count vectors (count >= 0), read before the call
+ * returns.  workspace: DEVICE, 8-byte aligned, of at least
+ * fp8_grad_norm_workspace(count) bytes, in use until the call's kernels are done.
+ * The sums' order is fixed: equal calls give equal bits.  One kernel for each 1000
+ * vectors, and one that joins their sums. */
+fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+int64_t fp8_grad_norm_workspace(int32_t count);
+
+/* outs[i] = grads[i] * c in fp32, rounded to the type of outs[i], with the norm
+ * read on the device:
+ *   c = max_norm / norm  where max_norm < norm < infinity, else 1,
+ * so that gradients whose norm is not finite pass through as they are (the caller
+ * sees it by the norm, and skips the step).  outs (NULL: grads, in place): HOST
+ * array of count vectors of the grads' lengths; outs[i] may be grads[i] (same
+ * address and type), and overlaps nothing else.  max_norm >= 0.  One kernel for
+ * each 1000 vectors. */
+fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_t count,
+                         const float *norm, float max_norm, void *stream);
 
 #ifdef __cplusplus
 }
