@@ -7,7 +7,8 @@ it loads the library and fails if it has not been built (``build.build()``).
 from .api import (AdamHyper, E4M3, E5M2, NUM_SLOTS, SLOT_DX, SLOT_DY, SLOT_W, SLOT_X, SLOT_Y,
                   BlockFp8, Fp8AdamState, Fp8Error, Fp8LayerNormLinear, Fp8Linear, Meta, Recipe,
                   allreduce_amax, fp8_allreduce, fp8_amax, fp8_amax_scale_update,
-                  fp8_block_dequantize, fp8_block_gemm_tn, fp8_block_quantize,
+                  fp8_block_dequantize, fp8_block_gemm_swiglu_bwd, fp8_block_gemm_swiglu_fwd,
+                  fp8_block_gemm_tn, fp8_block_quantize,
                   fp8_dequant_sum, fp8_exchange_sum, fp8_gemm_tn, fp8_gemm_tn_grouped,
                   fp8_grad_clip, fp8_grad_norm, fp8_grad_norm_workspace,
                   fp8_layernorm_bwd, fp8_layernorm_bwd_workspace, fp8_layernorm_fwd,

@@ -144,6 +144,8 @@ def _load() -> ctypes.CDLL:
         "fp8_layernorm_bwd": ([pm, pm, pb, vp, i32, vp, vp, pm, vp, vp, vp, i64, vp], st),
         "fp8_layernorm_bwd_workspace": ([i64, i64], i64),
         "fp8_layernorm_recompute": ([pb, vp, vp, i32, vp, vp, pb, vp], st),
+        "fp8_block_gemm_swiglu_fwd": ([pb, pb, pb, pb, vp], st),
+        "fp8_block_gemm_swiglu_bwd": ([pb, pb, pb, pb, pb, pb, vp], st),
         "fp8_rmsnorm_fwd": ([pm, pm, vp, i32, ctypes.c_float, pm, pm, pb, pb, vp, vp], st),
         "fp8_rmsnorm_bwd": ([pm, pm, pb, vp, i32, vp, pm, pm, vp, vp, i64, vp], st),
         "fp8_rmsnorm_bwd_workspace": ([i64, i64], i64),
@@ -171,7 +173,8 @@ def _load_packed(prototypes: ctypes.CDLL) -> ctypes.CDLL:
     for name in ("fp8_block_quantize", "fp8_block_dequantize", "fp8_block_gemm_tn",
                  "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_recompute",
                  "fp8_swiglu_fwd", "fp8_swiglu_bwd", "fp8_rmsnorm_fwd", "fp8_rmsnorm_bwd",
-                 "fp8_rmsnorm_recompute", "fp8_grad_norm", "fp8_grad_clip"):
+                 "fp8_rmsnorm_recompute", "fp8_grad_norm", "fp8_grad_clip",
+                 "fp8_block_gemm_swiglu_fwd", "fp8_block_gemm_swiglu_bwd"):
         f, of = getattr(lib, name), getattr(prototypes, name)
         f.argtypes = [ctypes.c_char_p if a in structs else a for a in of.argtypes]
         f.restype = of.restype
@@ -1057,6 +1060,30 @@ def fp8_swiglu_bwd(da: torch.Tensor, h8: BlockFp8, dh8: BlockFp8 | None = None,
     output again, transposed (``a8t``)."""
     _check(_packed.fp8_swiglu_bwd(_matrix(da, "da"), _block(h8, "h8"), _block(dh8, "dh8"),
                                _block(dh8t, "dh8t"), _block(a8t, "a8t"), _stream(stream)))
+
+
+def fp8_block_gemm_swiglu_fwd(A: BlockFp8, B: BlockFp8, a8: BlockFp8, h8: BlockFp8 | None = None,
+                              stream=None) -> None:
+    """SwiGLU of the product h = A B^T = [gate | value] in one kernel: A [M, K], B [2F, K], both
+    with E8M0 scales; block quantized into ``a8`` [M, F].  ``h8``: h itself in 8 bits, for
+    fp8_block_gemm_swiglu_bwd."""
+    Ab = _block(A, "A")
+    _here(A, B, a8, h8)
+    _check(_packed.fp8_block_gemm_swiglu_fwd(Ab, _block(B, "B"), _block(a8, "a8"), _block(h8, "h8"),
+                                             _stream(stream)))
+
+
+def fp8_block_gemm_swiglu_bwd(A: BlockFp8, B: BlockFp8, h8: BlockFp8, dh8: BlockFp8 | None = None,
+                              dh8t: BlockFp8 | None = None, a8t: BlockFp8 | None = None,
+                              stream=None) -> None:
+    """Backward of SwiGLU from the product da = A B^T, A [M, K] = dy and B [F, K], and the 8-bit
+    ``h8`` in one kernel: the gradient of h, block quantized as it is (``dh8``) and transposed
+    (``dh8t``), and SwiGLU's output again, transposed (``a8t``)."""
+    Ab = _block(A, "A")
+    _here(A, B, h8, dh8, dh8t, a8t)
+    _check(_packed.fp8_block_gemm_swiglu_bwd(Ab, _block(B, "B"), _block(h8, "h8"), _block(dh8, "dh8"),
+                                             _block(dh8t, "dh8t"), _block(a8t, "a8t"),
+                                             _stream(stream)))
 
 
 # ------------------------------------------------------- lists of gradients --

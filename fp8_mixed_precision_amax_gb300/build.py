@@ -18,10 +18,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build", "obj")
 LIB = os.path.join(PKG, "libfp8amax.so")
-SOURCES = ["abi.cu", "block_abi.cu", "block_gemm.cu", "block_quant.cu", "cast.cu", "clip.cu",
+SOURCES = ["abi.cu", "block_abi.cu", "block_gated.cu", "block_gemm.cu", "block_quant.cu", "cast.cu", "clip.cu",
            "gemm.cu", "layernorm.cu", "noalloc.cu", "optim.cu", "rmsnorm.cu", "tmap.cu"]
-HEADERS = ["abi_checks.h", "block.cuh", "common.cuh", "kernels.h", "ln_plan.h", "norm_rows.cuh",
-           "once_per_device.h", "raster.cuh"]
+HEADERS = ["abi_checks.h", "block.cuh", "block_mma.cuh", "common.cuh", "kernels.h", "ln_plan.h",
+           "norm_rows.cuh", "once_per_device.h", "raster.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",

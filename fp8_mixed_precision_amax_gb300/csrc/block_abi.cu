@@ -456,6 +456,79 @@ fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
     return FP8_OK;
 }
 
+// operands of the gated product: E8M0 scales, at least one column
+static fp8_status check_gated_operands(const char *fn, const fp8k::BlockView &a, const fp8k::BlockView &b) {
+    if (a.cols != b.cols)
+        return fail(FP8_ERR_ARG, "%s: A has %lld columns, B %lld", fn, static_cast<long long>(a.cols),
+                    static_cast<long long>(b.cols));
+    if (a.cols < 1) return fail(FP8_ERR_ARG, "%s: A has no columns", fn);
+    if (a.scale_f32 || b.scale_f32) return fail(FP8_ERR_ARG, "%s: A and B must have E8M0 scales", fn);
+    return FP8_OK;
+}
+
+fp8_status fp8_block_gemm_swiglu_fwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
+                                     const fp8_block_tensor *a8, const fp8_block_tensor *h8,
+                                     void *stream) {
+    const char *fn = "fp8_block_gemm_swiglu_fwd";
+    const fp8k::CallRange range(fn);
+    fp8k::BlockView a, b, va8, vh8;
+    FP8_TRY(view(fn, A, "A", false, &a));
+    FP8_TRY(view(fn, B, "B", false, &b));
+    FP8_TRY(view(fn, a8, "a8", false, &va8));
+    FP8_TRY(view(fn, h8, "h8", true, &vh8));
+    FP8_TRY(check_gated_operands(fn, a, b));
+    if (b.rows % 256)
+        return fail(FP8_ERR_ALIGN, "%s: B has %lld rows: half of them must be a multiple of 128", fn,
+                    static_cast<long long>(b.rows));
+    FP8_TRY(check_rows_out(fn, a8, va8, "a8", a.rows, b.rows / 2));
+    FP8_TRY(check_rows_out(fn, h8, vh8, "h8", a.rows, b.rows));
+    FP8_TRY(check_tiles(fn, a.rows, b.rows));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    const char *what = nullptr;
+    const cudaError_t e =
+        fp8k::launch_gated_fwd(a, b, va8, vh8, sms, static_cast<cudaStream_t>(stream), &what);
+    if (e != cudaSuccess) return what ? fail(FP8_ERR_CUDA, "%s: %s", fn, what) : cuda_fail(e, fn);
+    return FP8_OK;
+}
+
+fp8_status fp8_block_gemm_swiglu_bwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
+                                     const fp8_block_tensor *h8, const fp8_block_tensor *dh8,
+                                     const fp8_block_tensor *dh8t, const fp8_block_tensor *a8t,
+                                     void *stream) {
+    const char *fn = "fp8_block_gemm_swiglu_bwd";
+    const fp8k::CallRange range(fn);
+    fp8k::BlockView a, b, vh8, vdh8, vdh8t, va8t;
+    FP8_TRY(view(fn, A, "A", false, &a));
+    FP8_TRY(view(fn, B, "B", false, &b));
+    FP8_TRY(view(fn, h8, "h8", false, &vh8));
+    FP8_TRY(view(fn, dh8, "dh8", true, &vdh8));
+    FP8_TRY(view(fn, dh8t, "dh8t", true, &vdh8t));
+    FP8_TRY(view(fn, a8t, "a8t", true, &va8t));
+    FP8_TRY(check_gated_operands(fn, a, b));
+    const int64_t M = a.rows, F = b.rows;
+    if (F % 128)
+        return fail(FP8_ERR_ALIGN, "%s: B has %lld rows: they must be a multiple of 128", fn,
+                    static_cast<long long>(F));
+    if (dh8 == nullptr && dh8t == nullptr && a8t == nullptr)
+        return fail(FP8_ERR_ARG, "%s: dh8, dh8t and a8t are all NULL", fn);
+    if (F >= kMaxDim / 2) return fail(FP8_ERR_ARG, "%s: B: bad size %lld", fn, static_cast<long long>(F));
+    FP8_TRY(check_rows_out(fn, h8, vh8, "h8", M, 2 * F));
+    FP8_TRY(check_rows_out(fn, dh8, vdh8, "dh8", M, 2 * F));
+    FP8_TRY(check_rows_out(fn, dh8t, vdh8t, "dh8t", 2 * F, M));
+    FP8_TRY(check_rows_out(fn, a8t, va8t, "a8t", F, M));
+    if (dh8 != nullptr && dh8t != nullptr && vdh8.fmt != vdh8t.fmt)
+        return fail(FP8_ERR_ARG, "%s: dh8 and dh8t differ in format", fn);
+    FP8_TRY(check_tiles(fn, M, F));
+    int sms;
+    FP8_TRY(current_device(&sms));
+    const char *what = nullptr;
+    const cudaError_t e = fp8k::launch_gated_bwd(a, b, vh8, vdh8, vdh8t, va8t, sms,
+                                                 static_cast<cudaStream_t>(stream), &what);
+    if (e != cudaSuccess) return what ? fail(FP8_ERR_CUDA, "%s: %s", fn, what) : cuda_fail(e, fn);
+    return FP8_OK;
+}
+
 int64_t fp8_grad_norm_workspace(int32_t count) { return fp8k::grad_norm_workspace(count); }
 
 fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, void *workspace,

@@ -14,11 +14,9 @@
 //         over a cluster whose CTAs join their sums in shared memory.
 //
 // Every wait is bounded.
-#include <atomic>
 #include <cstdint>
 
-#include "block.cuh"
-#include "once_per_device.h"
+#include "block_mma.cuh"
 #include "raster.cuh"
 
 namespace fp8k {
@@ -27,8 +25,6 @@ namespace {
 
 __device__ unsigned g_block_gemm_error_flags = 0;
 
-constexpr int BM = 128, BN = 256, BK = 128;   // a CTA's rows, the pair's columns, a k-block
-constexpr int HALF = BM * BK;                 // bytes of a CTA's A (or B) slice of one k-block
 constexpr int EPI_COLS = 64;                  // output columns staged at a time (128 B of BF16)
 constexpr int EPI_BUF = 32 * EPI_COLS * 2;    // a warp's staging buffer: 32 rows x 128 B
 
@@ -222,11 +218,6 @@ __device__ __forceinline__ void store_chunk(const PairArgs &a, uint32_t sbuf, in
     if (lane == 0) bulk_commit_group();   // an empty one: each chunk is one group
 }
 
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
-                                       ~static_cast<uintptr_t>(1023));
-}
-
 // ------------------------------------------------------------------ mx kernel --
 // Warps: 0 TMA, 1 MMA, 4-7 scales, 8-11 epilogue (2 and 3 idle: tcgen05.st and .ld
 // reach the lane quarter of the warp's number mod 4).
@@ -246,9 +237,6 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 
 constexpr int MX_STAGES = 6;
 constexpr int MX_THREADS = 384;
-constexpr int MX_ACC1 = 224;       // first column of the second accumulator
-constexpr int MX_SF = 480;         // first column of the scales
-constexpr int MX_SF_STRIDE = 16;   // columns per stage of scales: 4 for A, 8 for B
 constexpr int MX_BARS = 2 * MX_STAGES + 2 + 1 + 4 + 1;
 constexpr size_t MX_SMEM = 1024 + MX_STAGES * 2 * HALF + 4 * 2 * EPI_BUF + MX_BARS * 8 + 16;
 
@@ -472,18 +460,6 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
-}
-
-// Named barrier of n threads that tells all of them whether pred held for each.
-__device__ __forceinline__ bool barrier_and(int id, int n, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-        "barrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"(id), "r"(n), "r"(static_cast<uint32_t>(pred))
-        : "memory");
-    return r != 0;
 }
 
 // ----------------------------------------------------------------- f32 kernel --
@@ -808,12 +784,6 @@ struct FewArgs {
     int num_kb;
     uint32_t idesc;
 };
-
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
 
 template <int NT, bool MX>
 __global__ void __launch_bounds__(Few<NT, MX>::THREADS, NT <= 64 ? 2 : 1)
@@ -1146,56 +1116,9 @@ __global__ void __launch_bounds__(Few<NT, MX>::THREADS, NT <= 64 ? 2 : 1)
 
 // --------------------------------------------------------------------- host --
 
-// attr must have room for two attributes: the cluster shape and PDL.
-cudaLaunchConfig_t cluster_config(dim3 grid, int threads, size_t smem, int cluster,
-                                  cudaLaunchAttribute *attr, cudaStream_t st) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cfg;
-}
-
-// The pair kernel's shared-memory limit is set and the number of CTA pairs that
-// can be resident at once is found on a device's first call.
-struct PairKernel {
-    void (*kernel)(PairArgs);
-    int threads;
-    size_t smem;
-    SmemLimit limit;
-    OncePerDevice once;
-    std::atomic<int> slots[kDeviceSlots] = {};
-
-    cudaError_t init(int sm_count, int *slots_here) {
-        int device = 0;
-        const cudaError_t err = once.run([this, sm_count](int dev) {
-            cudaError_t e = limit.allow(kernel, smem);
-            if (e != cudaSuccess) return e;
-            cudaLaunchAttribute attr[2];
-            cudaLaunchConfig_t cfg =
-                cluster_config(dim3(sm_count & ~1), threads, smem, 2, attr, nullptr);
-            cfg.numAttrs = 1;
-            int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            slots[dev] = n;
-            return e;
-        }, &device);
-        *slots_here = slots[device];
-        return err;
-    }
-};
-PairKernel g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
-PairKernel g_f32_tiles{block_gemm_f32_kernel<false>, FS_THREADS, FS_SMEM};
-PairKernel g_f32_rows{block_gemm_f32_kernel<true>, FS_THREADS, FS_SMEM};
+PairKernel<PairArgs> g_mx{block_gemm_mx_kernel, MX_THREADS, MX_SMEM};
+PairKernel<PairArgs> g_f32_tiles{block_gemm_f32_kernel<false>, FS_THREADS, FS_SMEM};
+PairKernel<PairArgs> g_f32_rows{block_gemm_f32_kernel<true>, FS_THREADS, FS_SMEM};
 
 template <int NT, bool MX>
 cudaError_t launch_few(const BlockView &A, const BlockView &B, const MatView &D, int sm_count,
@@ -1279,7 +1202,7 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
         return cudaSuccess;
     }
     const bool mx = A.scale_f32 == 0;
-    PairKernel &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
+    PairKernel<PairArgs> &pk = mx ? g_mx : B.block_rows == 1 ? g_f32_rows : g_f32_tiles;
     const int64_t pair_tiles = ((D.rows + 255) / 256) * ((D.cols + 255) / 256);
     int slots = 0;
     if (D.rows > kFewRows && pair_tiles > few_tiles(sm_count)) {

@@ -223,24 +223,6 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 
 // ----------------------------------------------------------------- SwiGLU --
 
-// 1 / (1 + exp(-x)) of a pair to a few units in the last place and |x| 2^-24: 0 for -inf, 1
-// for +inf.  The instructions that flush subnormal numbers serve here: exp(-x) below 2^-126
-// is nothing beside 1, and the reciprocal is taken of a quarter of 1 + exp(-x), so that it
-// stays a normal number as long as exp(-x) is finite (x > -88.7) and the last product gives
-// the result below 2^-126 that a block of such gates is made of: its scale may be as small
-// as 2^-127.  (SwiGLU's backward at 8192 x 11008: 178.5 us; 176 without the quarter, where
-// such a block comes out as zeros, and 189.5 with the reciprocal that keeps subnormal numbers.)
-__device__ __forceinline__ uint64_t sigmoid2(float x, float y) {
-    float s[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(i ? y : x, -1.44269504f)));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(__fmaf_rn(e, 0.25f, 0.25f)));
-    }
-    return f32x2_mul(f32x2_pack(s[0], s[1]), splat_f32x2(0.25f));
-}
-
 // 8 lanes per block of 128 columns of a row, four blocks per warp.  8192 x 11008 BF16
 // with h kept: 127 us, where reading and writing alone is 93; 777 x 2688 4.1 and 2.2.  (16
 // lanes per block, with twice the exchanges and scales per value: 146 and 4.4, but 2.2 for

@@ -210,6 +210,13 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
 cudaError_t launch_ln_recompute(const BlockView &x8, const void *gamma, const void *beta, int wtype,
                                 const float *mean, const float *rstd, const BlockView &yt,
                                 int sm_count, cudaStream_t st);
+// The gated feed-forward product, forward and backward (block_gated.cu); h8 of the forward
+// and dh8, dh8t and a8t may be empty.
+cudaError_t launch_gated_fwd(const BlockView &A, const BlockView &B, const BlockView &a8,
+                             const BlockView &h8, int sm_count, cudaStream_t st, const char **what);
+cudaError_t launch_gated_bwd(const BlockView &A, const BlockView &B, const BlockView &h8,
+                             const BlockView &dh8, const BlockView &dh8t, const BlockView &a8t,
+                             int sm_count, cudaStream_t st, const char **what);
 // RMS norm with the residual's addition, forward and backward (rmsnorm.cu); residual, sum,
 // y, y8, x8 and dsum may be empty, and one of x and x8 is in the backward.
 cudaError_t launch_rms_fwd(const MatView &x, const MatView &residual, const void *gamma, int wtype,
@@ -244,9 +251,11 @@ cudaError_t launch_grad_norm(const VectorView *v, int count, float *norm, void *
 cudaError_t launch_grad_clip(const VectorView *v, const VectorView *out, int count,
                              const float *norm, float max_norm, int sm_count, cudaStream_t st);
 
-// Read and clear the device error flags of the block GEMM (block_gemm.cu), of
-// LayerNorm's backward (layernorm.cu) and of the RMS norm's (rmsnorm.cu).
+// Read and clear the device error flags of the block GEMM (block_gemm.cu), of the gated
+// product (block_gated.cu), of LayerNorm's backward (layernorm.cu) and of the RMS norm's
+// (rmsnorm.cu).
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags);
+cudaError_t read_and_clear_gated_error_flag(unsigned *flags);
 cudaError_t read_and_clear_ln_error_flag(unsigned *flags);
 cudaError_t read_and_clear_rms_error_flag(unsigned *flags);
 

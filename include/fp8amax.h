@@ -619,6 +619,32 @@ fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
                           const fp8_block_tensor *dh8, const fp8_block_tensor *dh8t,
                           const fp8_block_tensor *a8t, void *stream);
 
+/* The gated feed-forward product: both projections, SiLU and the product in one
+ * kernel, and nothing of it in 16 bits on the way.  A [M][K] and B [2F][K] = [gate
+ * rows | value rows], both with E8M0 scales, E4M3 or E5M2, block_rows 1 or 128:
+ *   [g | u] = A . B^T as fp8_block_gemm_tn sums it, in fp32,
+ *   a = g / (1 + exp(-g)) * u,
+ * a block quantized into a8 [M][F], and [g | u] into h8 [M][2F] (or NULL) for
+ * fp8_block_gemm_swiglu_bwd, both straight from fp32 (block_rows 1).  F a multiple
+ * of 128, K >= 1, M >= 0.  fp8_block_gemm_tn and fp8_swiglu_fwd do the same in two steps
+ * with h in between, which serves float scales and one wanting h. */
+fp8_status fp8_block_gemm_swiglu_fwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
+                                     const fp8_block_tensor *a8, const fp8_block_tensor *h8,
+                                     void *stream);
+
+/* Its backward: A = dy [M][K] and B [F][K] (the transpose of the matrix that takes
+ * a back to the output), scales as above, and h8 [M][2F] = [g | u]:
+ *   da = A . B^T in fp32,  s = 1 / (1 + exp(-g)),
+ *   d g = da * u * s * (1 + g * (1 - s)),  d u = da * (g * s)
+ * block quantized into dh8 [M][2F] and dh8t [2F][M], and a again, g * s * u, into
+ * a8t [F][M]: what fp8_swiglu_bwd writes, from the product itself, in one kernel.
+ * All block_rows 1; any of the three may be NULL, not all; dh8 and dh8t have the
+ * same format. */
+fp8_status fp8_block_gemm_swiglu_bwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
+                                     const fp8_block_tensor *h8, const fp8_block_tensor *dh8,
+                                     const fp8_block_tensor *dh8t, const fp8_block_tensor *a8t,
+                                     void *stream);
+
 /* ------------------------------------------------------------------------
  * The norm of many gradients together, and clipping by it */
 
