@@ -19,10 +19,9 @@
 // that columns j and 128 + j of a tile make one a, and a tile is one block of a wide.
 // Backward: 256 columns of da, two blocks.
 //
-// Warps: 0 TMA, 1 MMA (2 and 3 idle), 4-7 scales, 8-15 the elementwise part (warp w has the
-// TMEM lanes 32 (w mod 4) .. + 31, a row of the tile each, and half of the columns of a
-// block), of one tile while the next one's MMAs run.  Of the launch's 512 x 128 registers
-// the first eight warps hand back 64 each per thread and the other eight take them.
+// Warps: the first ones (8 forward, 16 backward) do the elementwise part of one tile while
+// the next one's MMAs run; then TMA, MMA, two idle ones, and four that bring scales to TMEM.
+// The latter eight hand back registers, and the elementwise warps take them.
 //
 // TMEM: as in the matrix product of block_gemm.cu the two accumulators overlap by 32 columns
 // (0-255 and 224-479), and columns 480-511 hold two stages of scales.  The elementwise
@@ -45,12 +44,9 @@ __device__ __forceinline__ void raise_error(volatile int *abort_flag) {
     *abort_flag = 1;
 }
 
-constexpr int GP_THREADS = 512;
-constexpr int GP_REGS_CONTROL = 64, GP_REGS_ELEMENTS = 192;
-static_assert(256 * GP_REGS_CONTROL + 256 * GP_REGS_ELEMENTS <= GP_THREADS * 128, "register split");
-
 struct GatedArgs {
     CUtensorMap mapA, mapB;
+    CUtensorMap map_a8, map_h8;   // forward: 32 rows of a block
     BlockView A, B;
     int64_t M, F;
     int64_t b_second;   // from the even CTA's first row of B to the odd one's
@@ -75,19 +71,27 @@ template <bool BWD>
 struct GatedShared;
 template <>
 struct GatedShared<false> {
-    float3 row_max[2][2][BM];   // [tile mod 2][half of the columns][row]: of a, gate, value
+    uint8_t codes[4][3][32 * kTile];   // [lane quarter][a, gate, value]: 32 rows, in TMA's 128-byte swizzle
+    float3 row_max[2][2][BM];          // [tile mod 2][half of the columns][row]
 };
 template <>
 struct GatedShared<true> {
-    uint8_t codes[3][kTile * kTile];   // [d gate, d value, a][column][row]
-    uint32_t col_max[3][4][kTile];     // [..][lane quarter][column]
+    float da[kTile * kTile];
+    uint8_t codes[3][kTile * kTile];   // d gate, d value, a: by columns
+    uint32_t max[3][kTile];            // column maxima; 0 between their uses
     float inv[3][kTile];
-    float2 row_max[2][BM];             // [half of the columns][row]: of d gate, d value
 };
 
+// Registers: of the launch's, which are equal for all warps, the control warps keep
+// REGS_CONTROL per thread and the elementwise warps have REGS_ELEMENTS.
 template <bool BWD>
 struct Gated {
-    static constexpr int STAGES = BWD ? 5 : 6;
+    static constexpr int STAGES = BWD ? 3 : 5;
+    static constexpr int WARPS = BWD ? 16 : 8;   // elementwise ones
+    static constexpr int THREADS = 32 * (WARPS + 8);
+    static constexpr int REGS_CONTROL = BWD ? 48 : 64, REGS_ELEMENTS = BWD ? 96 : 192;
+    static constexpr int REGS_LAUNCH = 65536 / THREADS / 8 * 8;
+    static_assert(256 * REGS_CONTROL + 32 * WARPS * REGS_ELEMENTS <= THREADS * REGS_LAUNCH, "register split");
     static constexpr int NUM_BARS = 2 * STAGES + 2 + 1 + 4 + 1;
     static constexpr size_t SMEM =
         1024 + STAGES * 2 * HALF + sizeof(GatedShared<BWD>) + NUM_BARS * 8 + 16;
@@ -224,23 +228,20 @@ __device__ __forceinline__ void gated_scales(const GatedArgs &a, uint32_t rank, 
     bool ok = true;
     for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
         const Tile t = tile_at(a, tile);
-        const uint8_t *ra[4], *rb[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = min(t.row0 + rank * BM + 32 * j + lane, a.M - 1);
-            ra[j] = static_cast<const uint8_t *>(a.A.scales) + (a.A.block_rows == 1 ? r : r >> 7) * a.A.ld_s;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t r = min(t.col0 + (j >> 2) * a.b_second + 32 * (j & 3) + lane, a.B.rows - 1);
-            rb[j] = static_cast<const uint8_t *>(a.B.scales) + (a.B.block_rows == 1 ? r : r >> 7) * a.B.ld_s;
-        }
+        const uint8_t *pa = static_cast<const uint8_t *>(a.A.scales), *pb = static_cast<const uint8_t *>(a.B.scales);
+        const int sa = a.A.block_rows == 1 ? 0 : 7, sb = a.B.block_rows == 1 ? 0 : 7;
+        const unsigned ra = static_cast<unsigned>(t.row0 + rank * BM + lane), most_a = static_cast<unsigned>(a.M - 1);
+        const unsigned rb = static_cast<unsigned>(t.col0 + lane), most_b = static_cast<unsigned>(a.B.rows - 1);
+        const unsigned second = static_cast<unsigned>(a.b_second);
         for (int kb = 0; kb < a.num_kb; kb += 4) {
             uint32_t wa[4], wb[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) wa[j] = *reinterpret_cast<const uint32_t *>(ra[j] + kb);
+            for (int j = 0; j < 4; ++j)
+                wa[j] = *reinterpret_cast<const uint32_t *>(pa + row_at(min(ra + 32 * j, most_a) >> sa, a.A.ld_s) + kb);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) wb[j] = *reinterpret_cast<const uint32_t *>(rb[j] + kb);
+            for (int j = 0; j < 8; ++j)
+                wb[j] = *reinterpret_cast<const uint32_t *>(
+                    pb + row_at(min(rb + (j >> 2) * second + 32 * (j & 3), most_b) >> sb, a.B.ld_s) + kb);
             const bool got = mbar_wait(sfe0 + 8 * sf, sf_phase ^ 1u, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got)) {
                 if (lane == 0) raise_error(abort_flag);
@@ -316,21 +317,23 @@ __device__ __forceinline__ void gate_value16(uint32_t t, int c, const uint32_t (
     }
 }
 
-// 16 values of a row to 16 bytes of codes
+// 16 values of this lane's row as codes, its 16-byte chunk `at` of 32 staged rows
 template <int FMT>
-__device__ __forceinline__ void store_codes16(uint8_t *p, const uint64_t *v, float inv) {
+__device__ __forceinline__ void stage_codes16(uint32_t rows, int at, const uint64_t *v, float inv) {
+    const int lane = threadIdx.x & 31;
     const uint64_t inv2 = splat_f32x2(inv);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = encode4<FMT>(f32x2_mul(v[2 * i], inv2), f32x2_mul(v[2 * i + 1], inv2));
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    st_shared_v4(rows + lane * kTile + ((at ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
 }
+__device__ __forceinline__ void quarter_sync(int q) { asm volatile("bar.sync %0, 64;" ::"r"(2 + q) : "memory"); }
 
 // AFMT, HFMT: formats of a8 and h8.
 template <int AFMT, int HFMT>
-__device__ __forceinline__ bool gated_fwd_tile(const GatedArgs &a, GatedShared<false> &sm, const Tile &tile,
+__device__ __forceinline__ void gated_fwd_tile(const GatedArgs &a, GatedShared<false> &sm, const Tile &tile,
                                                uint32_t rank, int it, uint32_t tmem, uint32_t acce0) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 8) >> 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = warp >> 2;
     const bool odd = it & 1;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const uint32_t t = lanes + (odd ? MX_ACC1 : 0) + 64 * half;
@@ -357,230 +360,346 @@ __device__ __forceinline__ bool gated_fwd_tile(const GatedArgs &a, GatedShared<f
     // the other half of the row's block is the partner warp's
     const int r = 32 * q + lane;
     sm.row_max[it & 1][half][r] = make_float3(ma, mg, mu);
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + q) : "memory");
+    if (half == 0 && lane == 0) bulk_wait_group_read<0>();   // the staged rows before these have left
+    __syncwarp();
+    quarter_sync(q);
     const float3 other = sm.row_max[it & 1][half ^ 1][r];
     const uint32_t ba = scale_byte<AFMT>(__float_as_uint(fmaxf(ma, other.x)));
     const uint32_t bg = scale_byte<HFMT>(__float_as_uint(fmaxf(mg, other.y)));
     const uint32_t bu = scale_byte<HFMT>(__float_as_uint(fmaxf(mu, other.z)));
-    const int64_t row = tile.row0 + rank * BM + r;
-    const bool in = row < a.M, keep_h = a.h8.codes != nullptr;
-    if (in && half == 0) {
+    const int64_t row0 = tile.row0 + rank * BM + 32 * q, row = row0 + lane;
+    const bool keep_h = a.h8.codes != nullptr;
+    if (row < a.M && half == 0) {
         store_scale(a.a8, row, tile.col0 / kTile, ba);
         if (keep_h) {
             store_scale(a.h8, row, tile.col0 / kTile, bg);
             store_scale(a.h8, row, (a.F + tile.col0) / kTile, bu);
         }
     }
-    if (in) {
-        uint8_t *p = a.a8.codes + row * a.a8.ld + tile.col0 + 64 * half;
+    const uint32_t to = smem_u32(sm.codes[q]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) store_codes16<AFMT>(p + 16 * c, av + 8 * c, scale_inverse(ba));
-    }
+    for (int c = 0; c < 4; ++c) stage_codes16<AFMT>(to, 4 * half + c, av + 8 * c, scale_inverse(ba));
     if (keep_h) {
-        uint8_t *p = a.h8.codes + row * a.h8.ld + tile.col0 + 64 * half;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint64_t g[8], u[8];
             gate_value16(t, c, keep, keep_g, keep_u, g, u);
-            if (in) {
-                store_codes16<HFMT>(p + 16 * c, g, scale_inverse(bg));
-                store_codes16<HFMT>(p + a.F + 16 * c, u, scale_inverse(bu));
-            }
+            stage_codes16<HFMT>(to + 32 * kTile, 4 * half + c, g, scale_inverse(bg));
+            stage_codes16<HFMT>(to + 2 * 32 * kTile, 4 * half + c, u, scale_inverse(bu));
         }
     }
     tc_fence_before();
-    return true;
+    fence_proxy_async_smem();
+    quarter_sync(q);
+    if (half == 0 && lane == 0 && row0 < a.M) {
+        const int32_t x = static_cast<int32_t>(tile.col0), y = static_cast<int32_t>(row0);
+        tma_store_2d(&a.map_a8, to, x, y);
+        if (keep_h) {
+            tma_store_2d(&a.map_h8, to + 32 * kTile, x, y);
+            tma_store_2d(&a.map_h8, to + 2 * 32 * kTile, x + static_cast<int32_t>(a.F), y);
+        }
+        bulk_commit_group();
+    }
 }
 
-// gate and value of 4 columns from their codes
-__device__ __forceinline__ void decode_pairs(uint32_t w, int fmt, uint64_t scale2, uint64_t (&v)[2]) {
+// gate or value of 4 columns from their codes
+__device__ __forceinline__ void decode_pairs(uint32_t w, int fmt, float scale, uint64_t (&v)[2]) {
     float f[4];
     decode4(w, fmt, f);
-    v[0] = f32x2_mul(f32x2_pack(f[0], f[1]), scale2);
-    v[1] = f32x2_mul(f32x2_pack(f[2], f[3]), scale2);
-}
-__device__ __forceinline__ uint32_t word_of(const uint4 (&u)[4], int i) {
-    const uint4 &v = u[i >> 2];
-    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    const uint64_t s2 = splat_f32x2(scale);
+    v[0] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
+    v[1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
 }
 
-// The largest magnitudes of 4 columns over the warp's rows; column k's goes to lane k0 + k.
-__device__ __forceinline__ void column_max4(const uint64_t (&v)[2], bool inf, int k0, uint32_t &mine) {
-    const int lane = threadIdx.x & 31;
-    float x[4];
-    f32x2_unpack(inf ? without_inf(v[0]) : v[0], x[0], x[1]);
-    f32x2_unpack(inf ? without_inf(v[1]) : v[1], x[2], x[3]);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(absmax3(0.0f, x[k], x[k])));
-        if (lane == k0 + k) mine = m;
+// Backward, a block of 128 columns of da.  It goes through shared memory from TMEM's layout
+// (a lane is a row) to one in which warp w of 16 has the 8 rows from 8 w on and lane l
+// columns 4 l .. 4 l + 3: a row's maximum is then one warp reduction, a column's is taken over a
+// thread's 8 rows first, and rows of h8 and dh8 are read and written 128 bytes at a time.
+// Everything is computed twice from da and the codes, for the maxima and again for the
+// results: kept, the three results of a tile are most of an SM's registers, and code for
+// fewer warps with more of them is too long for the instruction cache.  (8192 x 4096 -> 11008:
+// with a row per lane throughout 676 us; with 8 warps that keep two of the three 467.)
+struct BlockCodes {   // of h8, for this lane's 4 columns of its warp's 8 rows, two rows at a time
+    const uint8_t *at_g, *at_u;   // gate's and value's codes of the next two rows
+    int rows;                     // of the 8, that there are
+    uint32_t scale;               // lanes 0 .. 7: the rows' scales of gate; lanes 8 .. 15: of value
+    uint32_t g[2], u[2];
+
+    __device__ __forceinline__ void start(const GatedArgs &a, int64_t row0, int64_t col0) {
+        const int lane = threadIdx.x & 31;
+        const int64_t r0 = row0 + (threadIdx.x >> 5) * kTileRows;
+        at_g = a.h8.codes + r0 * a.h8.ld + col0 + 4 * lane;
+        at_u = at_g + a.F;
+        rows = a.M - r0 >= kTileRows ? kTileRows : static_cast<int>(a.M - r0);
+        scale = lane < 16 && (lane & 7) < rows
+                    ? fetch_scale(a.h8, r0 + (lane & 7), (lane < 8 ? col0 : a.F + col0) / kTile)
+                    : 0u;
+        fetch(a, 0);
     }
+    // rows i and i + 1, each call the next two
+    __device__ __forceinline__ void fetch(const GatedArgs &a, int i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool in = i + k < rows;
+            g[k] = in ? *reinterpret_cast<const uint32_t *>(at_g) : 0u;
+            u[k] = in ? *reinterpret_cast<const uint32_t *>(at_u) : 0u;
+            at_g += a.h8.ld, at_u += a.h8.ld;
+        }
+    }
+    __device__ __forceinline__ void rewind(const GatedArgs &a) {
+        at_g -= kTileRows * a.h8.ld, at_u -= kTileRows * a.h8.ld;
+        fetch(a, 0);
+    }
+};
+
+// 4 codes as fp32, exactly
+__device__ __forceinline__ void decode_pairs(uint32_t w, int fmt, uint64_t (&v)[2]) {
+    float f[4];
+    decode4(w, fmt, f);
+    v[0] = f32x2_pack(f[0], f[1]);
+    v[1] = f32x2_pack(f[2], f[3]);
 }
 
-// 4 columns' codes of this lane's row into a tile kept by columns
-template <int FMT>
-__device__ __forceinline__ void put_columns4(uint8_t *codes, const uint64_t (&v)[2], const float4 &inv) {
-    const uint32_t w = encode4<FMT>(f32x2_mul(v[0], f32x2_pack(inv.x, inv.y)), f32x2_mul(v[1], f32x2_pack(inv.z, inv.w)));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) codes[k * kTile] = static_cast<uint8_t>(w >> (8 * k));
-}
+// d gate, d value and a of a row of the warp's, from its codes
+template <int HFMT>
+struct RowValues {
+    uint64_t dg[2], du[2], a[2];
 
-// One block of 128 columns of da; `first`: the one that holds the columns shared by the two
-// accumulators.  FMT, AFMT: formats of dh8 / dh8t and of a8t.
-template <int FMT, int AFMT>
-__device__ __forceinline__ void gated_bwd_block(const GatedArgs &a, GatedShared<true> &sm, int64_t row0, int64_t col0,
-                                                bool first, uint32_t t, uint32_t acce0) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 8) >> 2;
-    const int et = threadIdx.x - 256, r = 32 * q + lane;
-    const int64_t row = row0 + r;
-    const bool in = row < a.M;
-    const bool want_t = a.dh8t.codes != nullptr, want_a = a.a8t.codes != nullptr, want_r = a.dh8.codes != nullptr;
-    uint4 gc[4], uc[4];
-    float sg = 0.0f, su = 0.0f;
-    auto fetch = [&] {
+    __device__ __forceinline__ RowValues(const float *da, int i, uint32_t gc, uint32_t uc, float scale) {
+        const int lane = threadIdx.x & 31, r = kTileRows * (threadIdx.x >> 5) + i;
+        const ulonglong2 d = *reinterpret_cast<const ulonglong2 *>(&da[r * kTile + ((lane ^ (r & 31)) << 2)]);
+        const float sg = __shfl_sync(0xFFFFFFFFu, scale, i), su = __shfl_sync(0xFFFFFFFFu, scale, 8 + i);
+        const uint64_t sg2 = splat_f32x2(sg), sl2 = splat_f32x2(__fmul_rn(sg, -1.44269504f)), su2 = splat_f32x2(su);
+        const uint64_t one2 = splat_f32x2(1.0f), quarter2 = splat_f32x2(0.25f);
+        uint64_t cg[2], cu[2];
+        decode_pairs(gc, HFMT, cg);
+        decode_pairs(uc, HFMT, cu);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) gc[i] = uc[i] = make_uint4(0, 0, 0, 0);
-        if (in) {
-            const uint8_t *p = a.h8.codes + row * a.h8.ld + col0 + 64 * half;
+        for (int p = 0; p < 2; ++p) {
+            // sigmoid2, with the logarithm's factor in the scale
+            float e0, e1, q0, q1;
+            f32x2_unpack(f32x2_mul(cg[p], sl2), e0, e1);
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e0));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e1));
+            f32x2_unpack(f32x2_fma(f32x2_pack(e0, e1), quarter2, quarter2), q0, q1);
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(q0));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(q1));
+            const uint64_t s = f32x2_mul(f32x2_pack(q0, q1), quarter2);
+            const uint64_t gs = f32x2_mul(f32x2_mul(cg[p], sg2), s), u = f32x2_mul(cu[p], su2), dp = p ? d.y : d.x;
+            a[p] = f32x2_mul(gs, u);
+            du[p] = f32x2_mul(dp, gs);
+            // s (1 + g (1 - s))
+            dg[p] = f32x2_mul(f32x2_mul(dp, u), f32x2_fma(gs, f32x2_sub(one2, s), s));
+        }
+    }
+};
+
+// The largest magnitudes: of this lane's columns over the warp's rows, and lane i's of row i.
+struct Maxima {
+    float col[3][4];
+    uint32_t row_g, row_u;
+
+    // FINITE: infinities do not count
+    template <int HFMT, bool FINITE>
+    __device__ __forceinline__ void take(const GatedArgs &a, const float *da, BlockCodes &h, float scale) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                gc[i] = reinterpret_cast<const uint4 *>(p)[i];
-                uc[i] = reinterpret_cast<const uint4 *>(p + a.F)[i];
+        for (int k = 0; k < 3; ++k) col[k][0] = col[k][1] = col[k][2] = col[k][3] = 0.0f;
+        row_g = row_u = 0;
+#pragma unroll 1
+        for (int i = 0; i < kTileRows; i += 2) {
+            const uint32_t g[2] = {h.g[0], h.g[1]}, u[2] = {h.u[0], h.u[1]};
+            if (i + 2 < kTileRows)
+                h.fetch(a, i + 2);
+            else
+                h.rewind(a);   // for the next pass
+            RowValues<HFMT> r[2] = {{da, i, g[0], u[0], scale}, {da, i + 1, g[1], u[1], scale}};
+            if constexpr (FINITE) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        r[k].dg[p] = without_inf(r[k].dg[p]);
+                        r[k].du[p] = without_inf(r[k].du[p]);
+                        r[k].a[p] = without_inf(r[k].a[p]);
+                    }
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                columns(0, p, r[0].dg[p], r[1].dg[p]);
+                columns(1, p, r[0].du[p], r[1].du[p]);
+                columns(2, p, r[0].a[p], r[1].a[p]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t mg = row(r[k].dg), mu = row(r[k].du);
+                if (lane == i + k) row_g = mg, row_u = mu;
             }
         }
-    };
-    if (in) {
-        sg = load_scale(a.h8, row, col0 / kTile);
-        su = load_scale(a.h8, row, (a.F + col0) / kTile);
     }
-    fetch();
-    const uint64_t sg2 = splat_f32x2(sg), su2 = splat_f32x2(su), one2 = splat_f32x2(1.0f);
-    uint64_t dg[32], du[32];
+    __device__ __forceinline__ void columns(int k, int p, uint64_t a, uint64_t b) {
+        float x, y, z, w;
+        f32x2_unpack(a, x, y);
+        f32x2_unpack(b, z, w);
+        col[k][2 * p] = absmax3(col[k][2 * p], x, z);
+        col[k][2 * p + 1] = absmax3(col[k][2 * p + 1], y, w);
+    }
+    static __device__ __forceinline__ uint32_t row(const uint64_t (&v)[2]) {
+        return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(absmax3(absmax3(0.0f, v[0]), v[1])));
+    }
+    __device__ __forceinline__ bool infinite() const {
+        float m = 0.0f;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t v[16];
-        tmem_load_16cols(t + 64 * half + 16 * c, v);
-        tmem_wait_16cols(v);
+        for (int k = 0; k < 3; ++k) m = fmaxf(m, fmaxf(fmaxf(col[k][0], col[k][1]), fmaxf(col[k][2], col[k][3])));
+        return is_inf(m);
+    }
+};
+
+// Two rows' codes of this lane's 4 columns: word p has columns 2 p and 2 p + 1, 16 bits each.
+template <int FMT>
+__device__ __forceinline__ void encode_columns2(const uint64_t (&a)[2], const uint64_t (&b)[2], const float *inv,
+                                                uint32_t (&w)[2]) {
+    const ulonglong2 inv2 = *reinterpret_cast<const ulonglong2 *>(inv + 4 * (threadIdx.x & 31));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) du[8 * c + i] = pair_of(v[2 * i], v[2 * i + 1]);   // da for now
+    for (int p = 0; p < 2; ++p) {
+        float a0, a1, b0, b1;
+        f32x2_unpack(f32x2_mul(a[p], p ? inv2.y : inv2.x), a0, a1);
+        f32x2_unpack(f32x2_mul(b[p], p ? inv2.y : inv2.x), b0, b1);
+        w[p] = encode4<FMT>(f32x2_pack(a0, b0), f32x2_pack(a1, b1));
+    }
+}
+// Four rows' into a tile whose row is a column of 128 bytes; word n of column c (rows 4 n ..
+// 4 n + 3) is kept at place n ^ (c >> 2), so that a warp's lanes write to 32 banks.
+__device__ __forceinline__ void put_columns4(uint8_t *codes, int n, const uint32_t (&a)[2], const uint32_t (&b)[2]) {
+    const int lane = threadIdx.x & 31;
+    uint32_t *to = reinterpret_cast<uint32_t *>(codes) + 4 * lane * (kTile / 4) + (n ^ lane);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        to[2 * p * (kTile / 4)] = __byte_perm(a[p], b[p], 0x5410);
+        to[(2 * p + 1) * (kTile / 4)] = __byte_perm(a[p], b[p], 0x7632);
+    }
+}
+
+// The tile's columns as rows of o from first_row on, 8 threads each.
+__device__ __forceinline__ void put_tile(const BlockView &o, int64_t first_row, int64_t row0, int64_t M,
+                                         const uint8_t *codes) {
+    const int k = threadIdx.x & 7, c0 = threadIdx.x >> 3;
+    const int64_t left = M - (row0 + 16 * k);
+    uint8_t *p = o.codes + (first_row + c0) * o.ld + row0 + 16 * k;
+#pragma unroll
+    for (int i = 0; i < 2; ++i, p += 64 * o.ld) {
+        const int c = c0 + 64 * i, x = c >> 2;   // words 4 k .. 4 k + 3 are a block of four, in another order
+        uint4 u = *reinterpret_cast<const uint4 *>(codes + c * kTile + ((k ^ (x >> 2)) << 4));
+        if (x & 1) u = make_uint4(u.y, u.x, u.w, u.z);
+        if (x & 2) u = make_uint4(u.z, u.w, u.x, u.y);
+        if (left >= 16) {
+            *reinterpret_cast<uint4 *>(p) = u;
+        } else if (left > 0) {
+            store_code_word(p, u.x, left);
+            store_code_word(p + 4, u.y, left - 4);
+            store_code_word(p + 8, u.z, left - 8);
+            store_code_word(p + 12, u.w, left - 12);
+        }
+    }
+}
+
+__device__ __forceinline__ void elements_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+
+// h: the block's codes; `first`: the block that holds the columns shared by the two accumulators.
+// FMT, AFMT, HFMT: formats of dh8 / dh8t, of a8t and of h8.  next: called once h is done with.
+template <int FMT, int AFMT, int HFMT, typename Next>
+__device__ __forceinline__ void gated_bwd_block(const GatedArgs &a, GatedShared<true> &sm, BlockCodes &h,
+                                                int64_t row0, int64_t col0, bool first, uint32_t t, uint32_t acce0,
+                                                Next next) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2;
+    const bool want_t = a.dh8t.codes != nullptr, want_a = a.a8t.codes != nullptr, want_r = a.dh8.codes != nullptr;
+    elements_sync();   // the block before has left shared memory
+    // 16-byte chunk k of a row of da is kept at place k ^ (row mod 32): no bank twice, either way
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t d[16];
+        tmem_load_16cols(t + 32 * part + 16 * k, d);
+        tmem_wait_16cols(d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(&sm.da[(32 * q + lane) * kTile + (((8 * part + 4 * k + j) ^ lane) << 2)]) =
+                make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]);
     }
     if (first) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(acce0);
     }
-    float mg = 0.0f, mu = 0.0f;
-    uint32_t mine[3] = {0, 0, 0};
+    elements_sync();
+    const float scale = fetched_scale(a.h8, h.scale);
+    Maxima m;
+    m.take<HFMT, false>(a, sm.da, h, scale);
+    if (__any_sync(0xFFFFFFFFu, m.infinite())) m.take<HFMT, true>(a, sm.da, h, scale);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {   // 4 columns at a time
-        uint64_t g[2], u[2], av[2];
-        decode_pairs(word_of(gc, i), a.h8.fmt, sg2, g);
-        decode_pairs(word_of(uc, i), a.h8.fmt, su2, u);
-        float m = 0.0f;
+    for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float g0, g1;
-            f32x2_unpack(g[p], g0, g1);
-            const uint64_t s = sigmoid2(g0, g1), gs = f32x2_mul(g[p], s), d = du[2 * i + p];
-            av[p] = f32x2_mul(gs, u[p]);
-            dg[2 * i + p] = f32x2_mul(f32x2_mul(f32x2_mul(d, u[p]), s), f32x2_fma(g[p], f32x2_sub(one2, s), one2));
-            du[2 * i + p] = f32x2_mul(d, gs);
-            m = absmax3(absmax3(absmax3(m, av[p]), dg[2 * i + p]), du[2 * i + p]);
-        }
-        const bool inf = is_inf(m);
-        const uint64_t dgp[2] = {dg[2 * i], dg[2 * i + 1]}, dup[2] = {du[2 * i], du[2 * i + 1]};
-        mg = block_max(dgp, mg);
-        mu = block_max(dup, mu);
-        if (want_t) {
-            column_max4(dgp, inf, (4 * i) & 31, mine[0]);
-            column_max4(dup, inf, (4 * i) & 31, mine[1]);
-        }
-        if (want_a) column_max4(av, inf, (4 * i) & 31, mine[2]);
-        if ((i & 7) == 7) {
-#pragma unroll
-            for (int k = 0; k < 3; ++k) sm.col_max[k][q][64 * half + 4 * (i & 8) + lane] = mine[k];
-        }
-    }
-    sm.row_max[half][r] = make_float2(mg, mu);
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    for (int i = et; i < 3 * kTile; i += 256) {
-        const int k = i / kTile, c = i % kTile;
-        uint32_t m = 0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) m = max(m, sm.col_max[k][w][c]);
-        const uint32_t byte = k == 2 ? scale_byte<AFMT>(m) : scale_byte<FMT>(m);
+        for (int j = 0; j < 4; ++j) atomicMax(&sm.max[k][4 * lane + j], __float_as_uint(m.col[k][j]));
+    elements_sync();
+    if (threadIdx.x < 3 * kTile) {
+        const int k = threadIdx.x / kTile, c = threadIdx.x % kTile;
+        const uint32_t byte = k == 2 ? scale_byte<AFMT>(sm.max[k][c]) : scale_byte<FMT>(sm.max[k][c]);
+        sm.max[k][c] = 0;
         sm.inv[k][c] = scale_inverse(byte);
         if (row0 < a.M) {
             if (k < 2 && want_t) store_scale(a.dh8t, (k ? a.F : 0) + col0 + c, row0 / kTile, byte);
             if (k == 2 && want_a) store_scale(a.a8t, col0 + c, row0 / kTile, byte);
         }
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (want_r && in) {
-        const float2 other = sm.row_max[half ^ 1][r];
-        const uint32_t bg = scale_byte<FMT>(__float_as_uint(fmaxf(mg, other.x)));
-        const uint32_t bu = scale_byte<FMT>(__float_as_uint(fmaxf(mu, other.y)));
-        if (half == 0) {
-            store_scale(a.dh8, row, col0 / kTile, bg);
-            store_scale(a.dh8, row, (a.F + col0) / kTile, bu);
-        }
-        uint8_t *p = a.dh8.codes + row * a.dh8.ld + col0 + 64 * half;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            store_codes16<FMT>(p + 16 * c, dg + 8 * c, scale_inverse(bg));
-            store_codes16<FMT>(p + a.F + 16 * c, du + 8 * c, scale_inverse(bu));
-        }
+    elements_sync();
+    const int64_t r0 = row0 + kTileRows * warp;
+    const uint32_t bg = scale_byte<FMT>(m.row_g), bu = scale_byte<FMT>(m.row_u);
+    if (want_r && lane < kTileRows && lane < h.rows) {
+        store_scale(a.dh8, r0 + lane, col0 / kTile, bg);
+        store_scale(a.dh8, r0 + lane, (a.F + col0) / kTile, bu);
     }
-    if (want_t) {
+    const float ig = scale_inverse(bg), iu = scale_inverse(bu);
+    uint8_t *pg = a.dh8.codes + r0 * a.dh8.ld + col0 + 4 * lane, *pu = pg + a.F;
+#pragma unroll 1
+    for (int i = 0; i < kTileRows; i += 4) {
+        uint32_t w[3][2][2];   // [d gate, d value, a][two rows]
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = 64 * half + 4 * i;
-            const uint64_t dgp[2] = {dg[2 * i], dg[2 * i + 1]}, dup[2] = {du[2 * i], du[2 * i + 1]};
-            put_columns4<FMT>(&sm.codes[0][c * kTile + r], dgp, *reinterpret_cast<const float4 *>(&sm.inv[0][c]));
-            put_columns4<FMT>(&sm.codes[1][c * kTile + r], dup, *reinterpret_cast<const float4 *>(&sm.inv[1][c]));
-        }
-    }
-    if (want_a) {
-        fetch();   // again: kept, they would not fit beside dg and du
+        for (int n = 0; n < 2; ++n) {
+            const int at = i + 2 * n;
+            const uint32_t g[2] = {h.g[0], h.g[1]}, u[2] = {h.u[0], h.u[1]};
+            if (at + 2 < kTileRows) h.fetch(a, at + 2);
+            const RowValues<HFMT> r[2] = {{sm.da, at, g[0], u[0], scale}, {sm.da, at + 1, g[1], u[1], scale}};
+            if (want_r) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = 64 * half + 4 * i;
-            uint64_t g[2], u[2];
-            decode_pairs(word_of(gc, i), a.h8.fmt, sg2, g);
-            decode_pairs(word_of(uc, i), a.h8.fmt, su2, u);
-            const uint64_t av[2] = {silu_times(g[0], u[0]), silu_times(g[1], u[1])};
-            put_columns4<AFMT>(&sm.codes[2][c * kTile + r], av, *reinterpret_cast<const float4 *>(&sm.inv[2][c]));
-        }
-    }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    // the columns leave as rows of 128 bytes, 8 threads each
-    const int k = et & 7, c0 = et >> 3;
-    const int64_t left = a.M - (row0 + 16 * k);
-    auto store = [&](const BlockView &o, int64_t first_row, const uint8_t *codes) {
-        uint8_t *p = o.codes + (first_row + c0) * o.ld + row0 + 16 * k;
-#pragma unroll
-        for (int i = 0; i < kTile / 32; ++i, p += 32 * o.ld) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(codes + (c0 + 32 * i) * kTile + 16 * k);
-            if (left >= 16) {
-                *reinterpret_cast<uint4 *>(p) = u;
-            } else if (left > 0) {
-                store_code_word(p, u.x, left);
-                store_code_word(p + 4, u.y, left - 4);
-                store_code_word(p + 8, u.z, left - 8);
-                store_code_word(p + 12, u.w, left - 12);
+                for (int k = 0; k < 2; ++k, pg += a.dh8.ld, pu += a.dh8.ld) {
+                    const uint64_t g2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, ig, at + k));
+                    const uint64_t u2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, iu, at + k));
+                    const uint32_t wg = encode4<FMT>(f32x2_mul(r[k].dg[0], g2), f32x2_mul(r[k].dg[1], g2));
+                    const uint32_t wu = encode4<FMT>(f32x2_mul(r[k].du[0], u2), f32x2_mul(r[k].du[1], u2));
+                    if (at + k < h.rows) {
+                        *reinterpret_cast<uint32_t *>(pg) = wg;
+                        *reinterpret_cast<uint32_t *>(pu) = wu;
+                    }
+                }
             }
+            encode_columns2<FMT>(r[0].dg, r[1].dg, sm.inv[0], w[0][n]);
+            encode_columns2<FMT>(r[0].du, r[1].du, sm.inv[1], w[1][n]);
+            encode_columns2<AFMT>(r[0].a, r[1].a, sm.inv[2], w[2][n]);
         }
-    };
-    if (want_t) {
-        store(a.dh8t, col0, sm.codes[0]);
-        store(a.dh8t, a.F + col0, sm.codes[1]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) put_columns4(sm.codes[k], 2 * warp + i / 4, w[k][0], w[k][1]);
     }
-    if (want_a) store(a.a8t, col0, sm.codes[2]);
+    next();
+    elements_sync();
+    if (want_t) {
+        put_tile(a.dh8t, col0, row0, a.M, sm.codes[0]);
+        put_tile(a.dh8t, a.F + col0, row0, a.M, sm.codes[1]);
+    }
+    if (want_a) put_tile(a.a8t, col0, row0, a.M, sm.codes[2]);
 }
 
-// F0, F1: formats of a8 and h8, or of dh8 / dh8t and a8t.
-template <bool BWD, int F0, int F1>
-__global__ void __launch_bounds__(GP_THREADS, 1) gated_pair_kernel(const __grid_constant__ GatedArgs a) {
+// F0, F1, F2: formats of a8 and h8, or of dh8 / dh8t, a8t and h8.
+template <bool BWD, int F0, int F1, int F2>
+__global__ void __launch_bounds__(Gated<BWD>::THREADS, 1) gated_pair_kernel(const __grid_constant__ GatedArgs a) {
     using C = Gated<BWD>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align1024(smem_raw);
@@ -607,14 +726,17 @@ __global__ void __launch_bounds__(GP_THREADS, 1) gated_pair_kernel(const __grid_
             mbar_init(sff0 + 8 * b, 8);   // four scale warps of each CTA
             mbar_init(sfe0 + 8 * b, 1);
         }
-        mbar_init(acce, 16);              // eight elementwise warps of each CTA
+        mbar_init(acce, 2 * C::WARPS);    // the elementwise warps of both CTAs
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&a.mapA);
         prefetch_tmap(&a.mapB);
     }
-    if (warp == 1) {
+    if constexpr (BWD) {
+        if (threadIdx.x < 3 * kTile) sm.max[threadIdx.x / kTile][threadIdx.x % kTile] = 0;
+    }
+    if (warp == C::WARPS + 1) {
         tmem_alloc_pair(smem_u32(tmem_slot), 512);
         tmem_relinquish_pair();
         tc_fence_before();
@@ -627,49 +749,72 @@ __global__ void __launch_bounds__(GP_THREADS, 1) gated_pair_kernel(const __grid_
     pdl_wait();
     pdl_trigger();
 
-    if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GP_REGS_CONTROL));
-        if (warp == 0)
+    if (warp >= C::WARPS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
+        const int role = warp - C::WARPS;
+        if (role == 0)
             gated_produce<C::STAGES>(a, rank, unit, num_units, sA, sB, full0, empty0, abort_flag);
-        else if (warp == 1 && rank == 0)
+        else if (role == 1 && rank == 0)
             gated_mma<C::STAGES>(a, unit, num_units, tmem, sA, sB, full0, empty0, accf0, acce, sff0, sfe0, drain,
                                  abort_flag);
-        else if (warp >= 4)
+        else if (role >= 4)
             gated_scales(a, rank, unit, num_units, tmem, sff0, sfe0, abort_flag);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GP_REGS_ELEMENTS));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_ELEMENTS));
         const uint32_t acce0 = mapa_shared(acce, 0);
         int it = 0;
+        BlockCodes h;   // backward: of the next block, while this one is in work
+        auto fetch = [&](int tile_index, int n, int j) {   // block j of the CTA's n-th tile
+            if (tile_index >= a.num_tiles) return;
+            const Tile tile = tile_at(a, tile_index);
+            const int64_t c = tile.col0 + ((n & 1) == j ? kTile : 0);
+            if (c < a.F) h.start(a, tile.row0 + rank * BM, c);
+        };
+        if constexpr (BWD) fetch(unit, 0, 0);
         for (int i = unit; i < a.num_tiles; i += num_units, ++it) {
             const Tile tile = tile_at(a, i);
+            // of two blocks the one with the columns that two accumulators share comes first
+            const auto col_of = [&](int j) { return tile.col0 + ((it & 1) == j ? kTile : 0); };
             const bool got = mbar_wait(accf0 + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got) && lane == 0) raise_error(abort_flag);
             // all go on or none: a warp alone in a tile's barriers would stay there
-            if (!barrier_and(1, 256, got)) break;
+            if (!barrier_and(1, 32 * C::WARPS, got)) break;
             tc_fence_after();
             if constexpr (BWD) {
                 const uint32_t t = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ((it & 1) ? MX_ACC1 : 0);
-                const int64_t row0 = tile.row0 + rank * BM;
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    const int b = (it & 1) ? j : 1 - j;   // the shared columns' block first
-                    if (tile.col0 + b * kTile < a.F) {
-                        gated_bwd_block<F0, F1>(a, sm, row0, tile.col0 + b * kTile, j == 0, t + b * kTile, acce0);
-                    } else if (j == 0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(acce0);
+                    const int64_t col0 = col_of(j);
+                    if (col0 >= a.F) {
+                        if (j == 0) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster_relaxed(acce0);
+                            fetch(i, it, 1);
+                        } else {
+                            fetch(i + num_units, it + 1, 0);
+                        }
+                        continue;
                     }
+                    gated_bwd_block<F0, F1, F2>(a, sm, h, tile.row0 + rank * BM, col0, j == 0,
+                                            t + static_cast<uint32_t>(col0 - tile.col0), acce0, [&] {
+                                                if (j == 0)
+                                                    fetch(i, it, 1);
+                                                else
+                                                    fetch(i + num_units, it + 1, 0);
+                                            });
                 }
                 tc_fence_before();
             } else {
                 gated_fwd_tile<F0, F1>(a, sm, tile, rank, it, tmem, acce0);
             }
         }
+        if (!BWD && lane == 0) bulk_wait_group<0>();
+        __syncwarp();
     }
     __syncthreads();
     __syncwarp();
     cluster_sync();   // the other SM is done with this CTA's memory
-    if (warp == 1) {
+    if (warp == C::WARPS + 1) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
@@ -678,9 +823,9 @@ __global__ void __launch_bounds__(GP_THREADS, 1) gated_pair_kernel(const __grid_
 
 // --------------------------------------------------------------------- host --
 
-template <bool BWD, int F0, int F1>
+template <bool BWD, int F0, int F1, int F2 = 0>
 cudaError_t launch_pair(GatedArgs &a, int sm_count, cudaStream_t st, const char **what) {
-    static PairKernel<GatedArgs> pk{gated_pair_kernel<BWD, F0, F1>, GP_THREADS, Gated<BWD>::SMEM};
+    static PairKernel<GatedArgs> pk{gated_pair_kernel<BWD, F0, F1, F2>, Gated<BWD>::THREADS, Gated<BWD>::SMEM};
     int slots = 0;
     const cudaError_t e = pk.init(sm_count, &slots);
     if (e != cudaSuccess) return e;
@@ -694,6 +839,12 @@ cudaError_t launch_pair(GatedArgs &a, int sm_count, cudaStream_t st, const char 
         *what = "cuTensorMapEncodeTiled failed for an operand";
         return cudaErrorInvalidValue;
     }
+    if (!BWD && (!encode_tmap_2d(&a.map_a8, a.a8.codes, false, a.F, a.M, kTile, 32, true, a.a8.ld) ||
+                 (a.h8.codes != nullptr &&
+                  !encode_tmap_2d(&a.map_h8, a.h8.codes, false, 2 * a.F, a.M, kTile, 32, true, a.h8.ld)))) {
+        *what = "cuTensorMapEncodeTiled failed for an output";
+        return cudaErrorInvalidValue;
+    }
     a.b_second = BWD ? BM : a.F;
     a.tile_cols = BWD ? BN : BM;
     a.tiles_m = static_cast<int>((a.M + 2 * BM - 1) / (2 * BM));
@@ -704,15 +855,14 @@ cudaError_t launch_pair(GatedArgs &a, int sm_count, cudaStream_t st, const char 
     a.idesc = idesc_mxf8(static_cast<uint32_t>(A.fmt), static_cast<uint32_t>(B.fmt), 2 * BM, BN, 0);
     const int units = a.num_tiles < slots ? a.num_tiles : slots;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), GP_THREADS, Gated<BWD>::SMEM, 2, attr, st);
-    return cudaLaunchKernelEx(&cfg, gated_pair_kernel<BWD, F0, F1>, a);
+    cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), Gated<BWD>::THREADS, Gated<BWD>::SMEM, 2, attr, st);
+    return cudaLaunchKernelEx(&cfg, gated_pair_kernel<BWD, F0, F1, F2>, a);
 }
 
-template <bool BWD>
-cudaError_t launch_pair_formats(GatedArgs &a, int f0, int f1, int sm_count, cudaStream_t st, const char **what) {
-    if (f0 == 0)
-        return f1 == 0 ? launch_pair<BWD, 0, 0>(a, sm_count, st, what) : launch_pair<BWD, 0, 1>(a, sm_count, st, what);
-    return f1 == 0 ? launch_pair<BWD, 1, 0>(a, sm_count, st, what) : launch_pair<BWD, 1, 1>(a, sm_count, st, what);
+template <int FMT, int AFMT>
+cudaError_t launch_bwd_formats(GatedArgs &a, int sm_count, cudaStream_t st, const char **what) {
+    return a.h8.fmt == 0 ? launch_pair<true, FMT, AFMT, 0>(a, sm_count, st, what)
+                         : launch_pair<true, FMT, AFMT, 1>(a, sm_count, st, what);
 }
 
 }  // namespace
@@ -723,7 +873,12 @@ cudaError_t launch_gated_fwd(const BlockView &A, const BlockView &B, const Block
     GatedArgs a{};
     a.A = A, a.B = B, a.a8 = a8, a.h8 = h8;
     a.M = A.rows, a.F = B.rows / 2;
-    return launch_pair_formats<false>(a, a8.fmt, h8.codes != nullptr ? h8.fmt : 0, sm_count, st, what);
+    const int hfmt = h8.codes != nullptr ? h8.fmt : 0;
+    if (a8.fmt == 0)
+        return hfmt == 0 ? launch_pair<false, 0, 0>(a, sm_count, st, what)
+                         : launch_pair<false, 0, 1>(a, sm_count, st, what);
+    return hfmt == 0 ? launch_pair<false, 1, 0>(a, sm_count, st, what)
+                     : launch_pair<false, 1, 1>(a, sm_count, st, what);
 }
 
 cudaError_t launch_gated_bwd(const BlockView &A, const BlockView &B, const BlockView &h8, const BlockView &dh8,
@@ -734,7 +889,12 @@ cudaError_t launch_gated_bwd(const BlockView &A, const BlockView &B, const Block
     a.A = A, a.B = B, a.h8 = h8, a.dh8 = dh8, a.dh8t = dh8t, a.a8t = a8t;
     a.M = A.rows, a.F = B.rows;
     const int fmt = dh8.codes != nullptr ? dh8.fmt : dh8t.codes != nullptr ? dh8t.fmt : 0;
-    return launch_pair_formats<true>(a, fmt, a8t.codes != nullptr ? a8t.fmt : 0, sm_count, st, what);
+    const int afmt = a8t.codes != nullptr ? a8t.fmt : 0;
+    if (fmt == 0)
+        return afmt == 0 ? launch_bwd_formats<0, 0>(a, sm_count, st, what)
+                         : launch_bwd_formats<0, 1>(a, sm_count, st, what);
+    return afmt == 0 ? launch_bwd_formats<1, 0>(a, sm_count, st, what)
+                     : launch_bwd_formats<1, 1>(a, sm_count, st, what);
 }
 
 cudaError_t read_and_clear_gated_error_flag(unsigned *flags) {
