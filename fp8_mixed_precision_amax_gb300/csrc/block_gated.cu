@@ -821,6 +821,294 @@ __global__ void __launch_bounds__(Gated<BWD>::THREADS, 1) gated_pair_kernel(cons
     }
 }
 
+// ----------------------------------------------------------------- few kernel --
+// Forward of few tokens (being decoded, or one wave of tiles): a CTA computes one block of 128
+// columns of a for NT tokens over its share of the k-blocks; the block's 128 gate rows of B and
+// its 128 value rows take the instruction's 128-row side, one after the other, and the tokens its
+// columns.  gridDim.x CTAs, a cluster, share a block's k-blocks: one SM alone reads too slowly for
+// the weights of a token.  Their sums [token][gate, value][column] meet in shared memory, and
+// the warps of CTA k of the cluster join, activate and quantize tokens k, k + splits, ..., a token
+// each at a time.
+// Warps: 0 TMA, 1 MMA, 2-9 the sums (thread = weight row; warps w and w + 4 have the same TMEM
+// lanes, one gate, the other value), of which 2-5 bring the scales to TMEM before.
+
+template <int NT>
+struct GatedFew {
+    static constexpr int X_STAGE = NT * BK, STAGE = 2 * HALF + X_STAGE;
+    static constexpr int STAGES = NT <= 32 ? 3 : NT <= 64 ? 5 : 4;
+    static constexpr int CTAS = NT <= 32 ? 2 : 1;       // per SM
+    static constexpr int MOST_SPLITS = 8;
+    static constexpr int THREADS = 320;
+    static constexpr int SF = 2 * NT, SF_STRIDE = 16;   // TMEM: scales, per stage gate 4, value 4, tokens 4
+    static constexpr int TMEM = NT <= 16 ? 64 : 4 * NT;
+    static constexpr int NUM_BARS = 2 * STAGES + 1 + 4 + 1;
+    static constexpr size_t SMEM = 1024 + STAGES * STAGE + NUM_BARS * 8 + 16;
+    static_assert(STAGES * STAGE >= NT * 256 * 4, "the sums fit where the tiles were");
+    static_assert(SF + 2 * SF_STRIDE <= TMEM, "the scales fit");
+};
+
+struct GatedFewArgs {
+    CUtensorMap mapW, mapX;   // B's rows (128 x 128 boxes) and A's (128 x NT)
+    BlockView W, X, a8, h8;
+    int64_t M, F;
+    int num_kb;
+    uint32_t idesc;
+};
+
+// A block of a row by a warp, 4 columns per lane.
+template <int FMT>
+__device__ __forceinline__ void quantize_block4(const uint64_t (&v)[2], const BlockView &o, int64_t row, int64_t col0) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(block_max(v, 0.0f)));
+    const uint32_t byte = scale_byte<FMT>(m);
+    const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
+    *reinterpret_cast<uint32_t *>(o.codes + row * o.ld + col0 + 4 * lane) =
+        encode4<FMT>(f32x2_mul(v[0], inv2), f32x2_mul(v[1], inv2));
+    if (lane == 0) store_scale(o, row, col0 / kTile, byte);
+}
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <int NT, int AFMT, int HFMT>
+__global__ void __launch_bounds__(GatedFew<NT>::THREADS, GatedFew<NT>::CTAS)
+    gated_few_kernel(const __grid_constant__ GatedFewArgs a) {
+    using C = GatedFew<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    const uint32_t sW = smem_u32(smem), sX = sW + C::STAGES * 2 * HALF;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::STAGES * C::STAGE);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::NUM_BARS);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
+    const uint32_t accf = empty0 + 8 * C::STAGES, sff0 = accf + 8, sfe0 = sff0 + 16, drain = sfe0 + 16;
+    const int splits = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(a.num_kb) * split / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(a.num_kb) * (split + 1) / splits);
+    const int64_t col0 = static_cast<int64_t>(blockIdx.y) * kTile, token0 = static_cast<int64_t>(blockIdx.z) * NT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(accf, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sff0 + 8 * b, 4);
+            mbar_init(sfe0 + 8 * b, 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&a.mapW);
+        prefetch_tmap(&a.mapX);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    const int q = warp & 3, r = 32 * q + lane;   // lane quarter and weight row of a sums warp
+    bool ok = true;
+    if (warp == 0) {
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag))) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                const uint32_t fb = full0 + 8 * stage, to = sW + stage * 2 * HALF;
+                mbar_arrive_expect_tx(fb, C::STAGE);
+                tma_load_2d(to, &a.mapW, fb, kb * BK, static_cast<int32_t>(col0));
+                tma_load_2d(to + HALF, &a.mapW, fb, kb * BK, static_cast<int32_t>(a.F + col0));
+                tma_load_2d(sX + stage * C::X_STAGE, &a.mapX, fb, kb * BK, static_cast<int32_t>(token0));
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (!ok) {
+            // let the copies already issued land before the CTA exits
+            for (int i = 0; i < C::STAGES && issued > 0; ++i, --issued) {
+                stage = stage == 0 ? C::STAGES - 1 : stage - 1;
+                if (stage == C::STAGES - 1) phase ^= 1u;
+                mbar_wait(full0 + 8 * stage, phase, nullptr, 100000000ull);
+            }
+        }
+    } else if (warp == 1) {
+        int stage = 0, sf = 0;
+        uint32_t phase = 0, sf_phase = 0;
+        bool any = false;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            // a stage of scales holds those of four k-blocks, from a multiple of 4 on
+            const bool first = kb == kb0 || (kb & 3) == 0;
+            const bool go = (!first || mbar_wait(sff0 + 8 * sf, sf_phase, abort_flag)) &&
+                            mbar_wait(full0 + 8 * stage, phase, abort_flag);
+            if (!__all_sync(0xFFFFFFFFu, go)) {
+                if (lane == 0) raise_error(abort_flag);
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t gd = smem_desc_sw128(sW + stage * 2 * HALF), ud = smem_desc_sw128(sW + stage * 2 * HALF + HALF);
+                const uint64_t xd = smem_desc_sw128(sX + stage * C::X_STAGE);
+                const uint32_t id = static_cast<uint32_t>(kb & 3), idesc = a.idesc | id << 4 | id << 29;
+                const uint32_t sfg = tmem + C::SF + sf * C::SF_STRIDE, sfx = sfg + 8;
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k) {   // 32 bytes on: 2 in the descriptors' unit
+                    mma_mxf8(tmem, gd + 2 * k, xd + 2 * k, idesc, sfg, sfx, kb != kb0 || k != 0);
+                    mma_mxf8(tmem + NT, ud + 2 * k, xd + 2 * k, idesc, sfg + 4, sfx, kb != kb0 || k != 0);
+                }
+                mma_commit(empty0 + 8 * stage);
+                if ((kb & 3) == 3) mma_commit(sfe0 + 8 * sf);
+                if (kb == kb1 - 1) mma_commit(accf);
+            }
+            __syncwarp();
+            any = true;
+            if (++stage == C::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if ((kb & 3) == 3 && ++sf == 2) {
+                sf = 0;
+                sf_phase ^= 1u;
+            }
+        }
+        if (!ok && any) {
+            if (elect_one()) mma_commit(drain);
+            __syncwarp();
+            mbar_wait(drain, 0, nullptr, 100000000ull);
+        }
+    } else {
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        if (warp < 6) {
+            // scales; rows past the end repeat the last one
+            const uint8_t *pw = static_cast<const uint8_t *>(a.W.scales), *px = static_cast<const uint8_t *>(a.X.scales);
+            const int sw = a.W.block_rows == 1 ? 0 : 7, sx = a.X.block_rows == 1 ? 0 : 7;
+            uint32_t wg[4], wu[4], wx[4] = {0, 0, 0, 0};
+            auto fetch = [&](int kb) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned g = static_cast<unsigned>(col0) + 32 * j + lane, u = static_cast<unsigned>(a.F) + g;
+                    wg[j] = *reinterpret_cast<const uint32_t *>(pw + row_at(g >> sw, a.W.ld_s) + kb);
+                    wu[j] = *reinterpret_cast<const uint32_t *>(pw + row_at(u >> sw, a.W.ld_s) + kb);
+                    const unsigned x = min(static_cast<unsigned>(token0) + 32 * j + lane, static_cast<unsigned>(a.M - 1));
+                    if (32 * j < NT) wx[j] = *reinterpret_cast<const uint32_t *>(px + row_at(x >> sx, a.X.ld_s) + kb);
+                }
+            };
+            int sf = 0;
+            uint32_t sf_phase = 0;
+            if (kb0 < kb1) fetch(kb0 & ~3);
+            for (int kb = kb0 & ~3; kb < kb1; kb += 4) {
+                uint32_t g[4], u[4], x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[j] = wg[j], u[j] = wu[j], x[j] = wx[j];
+                if (kb + 4 < kb1) fetch(kb + 4);
+                const bool got = mbar_wait(sfe0 + 8 * sf, sf_phase ^ 1u, abort_flag);
+                if (!__all_sync(0xFFFFFFFFu, got)) {
+                    if (lane == 0) raise_error(abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = lanes + C::SF + sf * C::SF_STRIDE;
+                tmem_store_4cols(at, g[0], g[1], g[2], g[3]);
+                tmem_store_4cols(at + 4, u[0], u[1], u[2], u[3]);
+                tmem_store_4cols(at + 8, x[0], x[1], x[2], x[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sff0 + 8 * sf);
+                if (++sf == 2) {
+                    sf = 0;
+                    sf_phase ^= 1u;
+                }
+            }
+        }
+        const bool got = kb0 < kb1 && ok && mbar_wait(accf, 0, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+            if (lane == 0 && kb0 < kb1) raise_error(abort_flag);
+            ok = false;
+        }
+        if (ok) {
+            // all MMAs that read the tiles are done: the sums take their place
+            tc_fence_after();
+            const int part = warp < 6 ? 0 : 1;   // gate, value
+            float *red = reinterpret_cast<float *>(smem) + part * kTile + r;
+#pragma unroll
+            for (int h = 0; h < NT / 16; ++h) {
+                uint32_t v[16];
+                tmem_load_16cols(lanes + part * NT + h * 16, v);
+                tmem_wait_16cols(v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) red[(16 * h + c) * 256] = __uint_as_float(v[c]);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2) {
+        // a warp has a token at a time, a lane four columns of its block
+        const int tokens = a.M - token0 < NT ? static_cast<int>(a.M - token0) : NT;
+        const uint32_t red = smem_u32(smem) + 16 * lane;
+        for (int n = split + splits * (warp - 2); n < tokens; n += 8 * splits) {
+            float4 pg[C::MOST_SPLITS], pu[C::MOST_SPLITS];
+#pragma unroll
+            for (int k = 0; k < C::MOST_SPLITS; ++k) {
+                if (k >= splits) break;
+                const uint32_t at = mapa_shared(red + n * 1024, static_cast<uint32_t>(k));
+                pg[k] = ld_shared_cluster4(at);
+                pu[k] = ld_shared_cluster4(at + 512);
+            }
+            uint64_t g[2] = {}, u[2] = {}, v[2];
+#pragma unroll
+            for (int k = 0; k < C::MOST_SPLITS; ++k) {   // in the order of the splits
+                if (k >= splits) break;
+                g[0] = f32x2_add(g[0], f32x2_pack(pg[k].x, pg[k].y));
+                g[1] = f32x2_add(g[1], f32x2_pack(pg[k].z, pg[k].w));
+                u[0] = f32x2_add(u[0], f32x2_pack(pu[k].x, pu[k].y));
+                u[1] = f32x2_add(u[1], f32x2_pack(pu[k].z, pu[k].w));
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) v[p] = silu_times(g[p], u[p]);
+            const int64_t row = token0 + n;
+            quantize_block4<AFMT>(v, a.a8, row, col0);
+            if (a.h8.codes != nullptr) {
+                quantize_block4<HFMT>(g, a.h8, row, col0);
+                quantize_block4<HFMT>(u, a.h8, row, a.F + col0);
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // the others have read this CTA's sums
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
 // --------------------------------------------------------------------- host --
 
 template <bool BWD, int F0, int F1, int F2 = 0>
@@ -865,6 +1153,47 @@ cudaError_t launch_bwd_formats(GatedArgs &a, int sm_count, cudaStream_t st, cons
                          : launch_pair<true, FMT, AFMT, 1>(a, sm_count, st, what);
 }
 
+template <int NT, int AFMT, int HFMT>
+cudaError_t launch_gated_few(const GatedArgs &g, int sm_count, cudaStream_t st, const char **what) {
+    using C = GatedFew<NT>;
+    GatedFewArgs a{};
+    if (!encode_tmap_2d(&a.mapW, g.B.codes, false, g.B.cols, g.B.rows, BK, BM, true, g.B.ld) ||
+        !encode_tmap_2d(&a.mapX, g.A.codes, false, g.A.cols, g.A.rows, BK, NT, true, g.A.ld)) {
+        *what = "cuTensorMapEncodeTiled failed for an operand";
+        return cudaErrorInvalidValue;
+    }
+    a.W = g.B, a.X = g.A, a.a8 = g.a8, a.h8 = g.h8;
+    a.M = g.M, a.F = g.F;
+    a.num_kb = static_cast<int>((g.A.cols + BK - 1) / BK);
+    a.idesc = idesc_mxf8(static_cast<uint32_t>(g.B.fmt), static_cast<uint32_t>(g.A.fmt), BM, NT, 0);
+    static SmemLimit limit;
+    const cudaError_t err = limit.allow(gated_few_kernel<NT, AFMT, HFMT>, C::SMEM);
+    if (err != cudaSuccess) return err;
+    const int64_t tf = g.F / kTile, tx = (g.M + NT - 1) / NT;
+    // as many CTAs as run at once, with at least two k-blocks each
+    int64_t splits = static_cast<int64_t>(C::CTAS) * sm_count / (tf * tx);
+    if (splits > a.num_kb / 2) splits = a.num_kb / 2;
+    if (splits > C::MOST_SPLITS) splits = C::MOST_SPLITS;
+    if (splits < 1) splits = 1;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg =
+        cluster_config(dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tf), static_cast<unsigned>(tx)),
+                       C::THREADS, C::SMEM, static_cast<int>(splits), attr, st);
+    return cudaLaunchKernelEx(&cfg, gated_few_kernel<NT, AFMT, HFMT>, a);
+}
+
+template <int AFMT, int HFMT>
+cudaError_t launch_fwd_formats(GatedArgs &a, int sm_count, cudaStream_t st, const char **what) {
+    const int64_t tf = a.F / kTile;
+    if (tf <= 65535) {   // tiles count in gridDim.y
+        if (a.M <= 16) return launch_gated_few<16, AFMT, HFMT>(a, sm_count, st, what);
+        if (a.M <= 32) return launch_gated_few<32, AFMT, HFMT>(a, sm_count, st, what);
+        if (a.M <= 64) return launch_gated_few<64, AFMT, HFMT>(a, sm_count, st, what);
+        if (tf * ((a.M + 127) / 128) <= sm_count) return launch_gated_few<128, AFMT, HFMT>(a, sm_count, st, what);
+    }
+    return launch_pair<false, AFMT, HFMT>(a, sm_count, st, what);
+}
+
 }  // namespace
 
 cudaError_t launch_gated_fwd(const BlockView &A, const BlockView &B, const BlockView &a8, const BlockView &h8,
@@ -875,10 +1204,10 @@ cudaError_t launch_gated_fwd(const BlockView &A, const BlockView &B, const Block
     a.M = A.rows, a.F = B.rows / 2;
     const int hfmt = h8.codes != nullptr ? h8.fmt : 0;
     if (a8.fmt == 0)
-        return hfmt == 0 ? launch_pair<false, 0, 0>(a, sm_count, st, what)
-                         : launch_pair<false, 0, 1>(a, sm_count, st, what);
-    return hfmt == 0 ? launch_pair<false, 1, 0>(a, sm_count, st, what)
-                     : launch_pair<false, 1, 1>(a, sm_count, st, what);
+        return hfmt == 0 ? launch_fwd_formats<0, 0>(a, sm_count, st, what)
+                         : launch_fwd_formats<0, 1>(a, sm_count, st, what);
+    return hfmt == 0 ? launch_fwd_formats<1, 0>(a, sm_count, st, what)
+                     : launch_fwd_formats<1, 1>(a, sm_count, st, what);
 }
 
 cudaError_t launch_gated_bwd(const BlockView &A, const BlockView &B, const BlockView &h8, const BlockView &dh8,
