@@ -875,6 +875,52 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr) {
     return v;
 }
 
+// The sums of up to S splits to results: a warp has T tokens at a time, a lane four columns of
+// their block.
+template <int S, int T, int AFMT, int HFMT>
+__device__ __forceinline__ void gated_join(const GatedFewArgs &a, uint32_t sums, int split, int splits, int64_t token0,
+                                           int tokens, int64_t col0) {
+    const uint32_t red = sums + 16 * (threadIdx.x & 31);
+    const int first = T * static_cast<int>((threadIdx.x >> 5) - 2);
+    for (int i0 = first; split + i0 * splits < tokens; i0 += 8 * T) {
+        float4 pg[T][S], pu[T][S];
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const int n = split + (i0 + i) * splits;
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                pg[i][k] = pu[i][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (k < splits && n < tokens) {
+                    const uint32_t at = mapa_shared(red + n * 1024, static_cast<uint32_t>(k));
+                    pg[i][k] = ld_shared_cluster4(at);
+                    pu[i][k] = ld_shared_cluster4(at + 512);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const int n = split + (i0 + i) * splits;
+            if (n >= tokens) break;
+            uint64_t g[2] = {}, u[2] = {}, v[2];
+#pragma unroll
+            for (int k = 0; k < S; ++k) {   // in the order of the splits
+                g[0] = f32x2_add(g[0], f32x2_pack(pg[i][k].x, pg[i][k].y));
+                g[1] = f32x2_add(g[1], f32x2_pack(pg[i][k].z, pg[i][k].w));
+                u[0] = f32x2_add(u[0], f32x2_pack(pu[i][k].x, pu[i][k].y));
+                u[1] = f32x2_add(u[1], f32x2_pack(pu[i][k].z, pu[i][k].w));
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) v[p] = silu_times(g[p], u[p]);
+            const int64_t row = token0 + n;
+            quantize_block4<AFMT>(v, a.a8, row, col0);
+            if (a.h8.codes != nullptr) {
+                quantize_block4<HFMT>(g, a.h8, row, col0);
+                quantize_block4<HFMT>(u, a.h8, row, a.F + col0);
+            }
+        }
+    }
+}
+
 template <int NT, int AFMT, int HFMT>
 __global__ void __launch_bounds__(GatedFew<NT>::THREADS, GatedFew<NT>::CTAS)
     gated_few_kernel(const __grid_constant__ GatedFewArgs a) {
@@ -1069,36 +1115,13 @@ __global__ void __launch_bounds__(GatedFew<NT>::THREADS, GatedFew<NT>::CTAS)
     __syncwarp();
     cluster_sync();
     if (warp >= 2) {
-        // a warp has a token at a time, a lane four columns of its block
         const int tokens = a.M - token0 < NT ? static_cast<int>(a.M - token0) : NT;
-        const uint32_t red = smem_u32(smem) + 16 * lane;
-        for (int n = split + splits * (warp - 2); n < tokens; n += 8 * splits) {
-            float4 pg[C::MOST_SPLITS], pu[C::MOST_SPLITS];
-#pragma unroll
-            for (int k = 0; k < C::MOST_SPLITS; ++k) {
-                if (k >= splits) break;
-                const uint32_t at = mapa_shared(red + n * 1024, static_cast<uint32_t>(k));
-                pg[k] = ld_shared_cluster4(at);
-                pu[k] = ld_shared_cluster4(at + 512);
-            }
-            uint64_t g[2] = {}, u[2] = {}, v[2];
-#pragma unroll
-            for (int k = 0; k < C::MOST_SPLITS; ++k) {   // in the order of the splits
-                if (k >= splits) break;
-                g[0] = f32x2_add(g[0], f32x2_pack(pg[k].x, pg[k].y));
-                g[1] = f32x2_add(g[1], f32x2_pack(pg[k].z, pg[k].w));
-                u[0] = f32x2_add(u[0], f32x2_pack(pu[k].x, pu[k].y));
-                u[1] = f32x2_add(u[1], f32x2_pack(pu[k].z, pu[k].w));
-            }
-#pragma unroll
-            for (int p = 0; p < 2; ++p) v[p] = silu_times(g[p], u[p]);
-            const int64_t row = token0 + n;
-            quantize_block4<AFMT>(v, a.a8, row, col0);
-            if (a.h8.codes != nullptr) {
-                quantize_block4<HFMT>(g, a.h8, row, col0);
-                quantize_block4<HFMT>(u, a.h8, row, a.F + col0);
-            }
-        }
+        if (splits == 1)
+            gated_join<1, 4, AFMT, HFMT>(a, smem_u32(smem), split, splits, token0, tokens, col0);
+        else if (splits <= 4)
+            gated_join<4, 2, AFMT, HFMT>(a, smem_u32(smem), split, splits, token0, tokens, col0);
+        else
+            gated_join<8, 1, AFMT, HFMT>(a, smem_u32(smem), split, splits, token0, tokens, col0);
     }
     __syncwarp();
     cluster_sync();   // the others have read this CTA's sums
@@ -1182,6 +1205,14 @@ cudaError_t launch_gated_few(const GatedArgs &g, int sm_count, cudaStream_t st, 
     return cudaLaunchKernelEx(&cfg, gated_few_kernel<NT, AFMT, HFMT>, a);
 }
 
+// The few kernel takes up to 128 tokens, and more as long as they are so few pair tiles that
+// most SMs would idle, an eighth of the SMs' number.  M x K -> F with h kept, few and pair kernel in us:
+// 128 x 4096 -> 11008 27.8 and 34.2, 128 x 1000 -> 2688 9.2 and 9.4; 512 x 4096 -> 1024 (16
+// pair tiles) 11.7 and 15.6, 129 x 4096 -> 1024 (8) 11.7 and 15.5, 200 x 4096 -> 1024 (8) 16.7 and
+// 15.5; 256 x 1000 -> 2688 (21) 10.1 and 9.4, 600 x 1024 -> 1024 (24) 9.4 and 9.2, 777 x 1000 -> 2688
+// (84) 15.9 and 13.1.
+constexpr int64_t kFewTokens = 128;
+
 template <int AFMT, int HFMT>
 cudaError_t launch_fwd_formats(GatedArgs &a, int sm_count, cudaStream_t st, const char **what) {
     const int64_t tf = a.F / kTile;
@@ -1189,7 +1220,8 @@ cudaError_t launch_fwd_formats(GatedArgs &a, int sm_count, cudaStream_t st, cons
         if (a.M <= 16) return launch_gated_few<16, AFMT, HFMT>(a, sm_count, st, what);
         if (a.M <= 32) return launch_gated_few<32, AFMT, HFMT>(a, sm_count, st, what);
         if (a.M <= 64) return launch_gated_few<64, AFMT, HFMT>(a, sm_count, st, what);
-        if (tf * ((a.M + 127) / 128) <= sm_count) return launch_gated_few<128, AFMT, HFMT>(a, sm_count, st, what);
+        if (a.M <= kFewTokens || tf * ((a.M + 255) / 256) <= sm_count / 8)
+            return launch_gated_few<128, AFMT, HFMT>(a, sm_count, st, what);
     }
     return launch_pair<false, AFMT, HFMT>(a, sm_count, st, what);
 }
