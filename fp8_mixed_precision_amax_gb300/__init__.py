@@ -20,6 +20,6 @@ from .api import (AdamHyper, E4M3, E5M2, NUM_SLOTS, SLOT_DX, SLOT_DY, SLOT_W, SL
                   fp8_rmsnorm_fwd, fp8_rmsnorm_recompute, fp8_scale_update, fp8_selftest_wait_timeout,
                   fp8_set_clock_probe, fp8_shard_len, fp8_swiglu_bwd, fp8_swiglu_fwd,
                   fp8_sync_status, header_functions, library)
-from .mlp import BlockMlpScratch, Fp8BlockMlp
+from .mlp import BlockMlpScratch, Fp8BlockMlp, Fp8GatedMlp, GatedMlpScratch
 
 __all__ = [n for n in dir() if not n.startswith("_")]
