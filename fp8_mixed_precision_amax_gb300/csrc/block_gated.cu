@@ -46,24 +46,30 @@ __device__ __forceinline__ void raise_error(volatile int *abort_flag) {
 
 struct GatedArgs {
     CUtensorMap mapA, mapB;
+    CUtensorMap mapBHalf;         // mapB with half the rows
     CUtensorMap map_a8, map_h8;   // forward: 32 rows of a block
     BlockView A, B;
     int64_t M, F;
     int64_t b_second;   // from the even CTA's first row of B to the odd one's
     int tile_cols;      // columns of a or da in a tile
-    int tiles_m, tiles_n, num_tiles, num_kb, group_m;
-    uint32_t idesc;
+    int tiles_m, tiles_n, num_items, num_kb, group_m;
+    int whole;          // items from this one on are halves of tiles (backward: a block of da)
+    uint32_t idesc, idesc_half;
     BlockView a8, h8;              // forward: outputs (h8's codes may be null); backward: h8 is read
     BlockView dh8, dh8t, a8t;      // backward: outputs, codes null: not wanted
 };
 
 struct Tile {
     int64_t row0, col0;   // of the pair's 256 rows; of the columns of a or da
+    bool half;
 };
-__device__ __forceinline__ Tile tile_at(const GatedArgs &a, int tile) {
+__device__ __forceinline__ Tile tile_at(const GatedArgs &a, int item) {
+    const bool half = item >= a.whole, own = a.tile_cols == kTile;   // own: of a tile's width
+    const int tile = half && !own ? a.whole + (item - a.whole) / 2 : item;
     int mb, nb;
     tile_coords(tile, a.tiles_m, a.tiles_n, a.group_m, mb, nb);
-    return Tile{static_cast<int64_t>(mb) * 2 * BM, static_cast<int64_t>(nb) * a.tile_cols};
+    return Tile{static_cast<int64_t>(mb) * 2 * BM,
+                static_cast<int64_t>(nb) * a.tile_cols + (half && !own ? (item - a.whole) % 2 * kTile : 0), half};
 }
 
 // What the elementwise warps of a CTA share.
@@ -108,10 +114,12 @@ __device__ __forceinline__ void gated_produce(const GatedArgs &a, uint32_t rank,
     uint32_t phase = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+    for (int tile = unit; ok && tile < a.num_items; tile += num_units) {
         const Tile t = tile_at(a, tile);
         const int32_t arow = static_cast<int32_t>(t.row0 + rank * BM);
-        const int32_t brow = static_cast<int32_t>(t.col0 + rank * a.b_second);
+        const int32_t brow = static_cast<int32_t>(t.col0 + rank * (t.half ? BM / 2 : a.b_second));
+        const CUtensorMap *mapB = t.half ? &a.mapBHalf : &a.mapB;
+        const uint32_t bytes = t.half ? 3 * HALF : 4 * HALF;
         for (int kb = 0; kb < a.num_kb; ++kb) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1u, abort_flag))) {
                 if ((threadIdx.x & 31) == 0) raise_error(abort_flag);
@@ -121,9 +129,9 @@ __device__ __forceinline__ void gated_produce(const GatedArgs &a, uint32_t rank,
             if (elect_one()) {
                 // both CTAs' halves complete on the even CTA's barrier
                 const uint32_t fb = full0 + 8 * stage, fb0 = mapa_shared(fb, 0);
-                if (rank == 0) mbar_arrive_expect_tx(fb, 4 * HALF);
+                if (rank == 0) mbar_arrive_expect_tx(fb, bytes);
                 tma_load_2d_pair(sA + stage * HALF, &a.mapA, fb0, kb * BK, arow);
-                tma_load_2d_pair(sB + stage * HALF, &a.mapB, fb0, kb * BK, brow);
+                tma_load_2d_pair(sB + stage * HALF, mapB, fb0, kb * BK, brow);
             }
             __syncwarp();
             ++issued;
@@ -163,7 +171,7 @@ __device__ __forceinline__ void gated_mma(const GatedArgs &a, int unit, int num_
     int stage = 0, sf = 0, it = 0;
     uint32_t phase = 0, sf_phase = 0;
     bool ok = true, any = false;
-    for (int tile = unit; ok && tile < a.num_tiles; tile += num_units, ++it) {
+    for (int tile = unit; ok && tile < a.num_items; tile += num_units, ++it) {
         // the previous tile's shared columns have been read
         const bool freed = it == 0 || mbar_wait(acce, static_cast<uint32_t>(it - 1) & 1u, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, freed)) {
@@ -172,7 +180,7 @@ __device__ __forceinline__ void gated_mma(const GatedArgs &a, int unit, int num_
             break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + ((it & 1) ? MX_ACC1 : 0);
+        const uint32_t d = tmem + ((it & 1) ? MX_ACC1 : 0), idesc0 = tile < a.whole ? a.idesc : a.idesc_half;
         for (int kb = 0; kb < a.num_kb; ++kb) {
             const bool last = kb == a.num_kb - 1;
             const bool go = ((kb & 3) != 0 || mbar_wait(sff0 + 8 * sf, sf_phase, abort_flag)) &&
@@ -185,7 +193,7 @@ __device__ __forceinline__ void gated_mma(const GatedArgs &a, int unit, int num_
             tc_fence_after();
             if (elect_one()) {
                 const uint32_t sfa = tmem + MX_SF + sf * MX_SF_STRIDE, sfb = sfa + 4;
-                const uint32_t idesc = a.idesc | static_cast<uint32_t>(kb & 3) << 4 |
+                const uint32_t idesc = idesc0 | static_cast<uint32_t>(kb & 3) << 4 |
                                        static_cast<uint32_t>(kb & 3) << 29;
                 const uint64_t ad = smem_desc_sw128(sA + stage * HALF);
                 const uint64_t bd = smem_desc_sw128(sB + stage * HALF);
@@ -226,7 +234,7 @@ __device__ __forceinline__ void gated_scales(const GatedArgs &a, uint32_t rank, 
     int sf = 0;
     uint32_t sf_phase = 0;
     bool ok = true;
-    for (int tile = unit; ok && tile < a.num_tiles; tile += num_units) {
+    for (int tile = unit; ok && tile < a.num_items; tile += num_units) {
         const Tile t = tile_at(a, tile);
         const uint8_t *pa = static_cast<const uint8_t *>(a.A.scales), *pb = static_cast<const uint8_t *>(a.B.scales);
         const int sa = a.A.block_rows == 1 ? 0 : 7, sb = a.B.block_rows == 1 ? 0 : 7;
@@ -764,17 +772,21 @@ __global__ void __launch_bounds__(Gated<BWD>::THREADS, 1) gated_pair_kernel(cons
         const uint32_t acce0 = mapa_shared(acce, 0);
         int it = 0;
         BlockCodes h;   // backward: of the next block, while this one is in work
-        auto fetch = [&](int tile_index, int n, int j) {   // block j of the CTA's n-th tile
-            if (tile_index >= a.num_tiles) return;
-            const Tile tile = tile_at(a, tile_index);
-            const int64_t c = tile.col0 + ((n & 1) == j ? kTile : 0);
+        // the columns of block j of the CTA's n-th tile (F: it has none): of two blocks the one with
+        // the columns that two accumulators share comes first
+        const auto col_of = [&](const Tile &tile, int n, int j) {
+            if (tile.half) return j == 0 ? tile.col0 : a.F;
+            return tile.col0 + ((n & 1) == j ? kTile : 0);
+        };
+        auto fetch = [&](int item, int n, int j) {
+            if (item >= a.num_items) return;
+            const Tile tile = tile_at(a, item);
+            const int64_t c = col_of(tile, n, j);
             if (c < a.F) h.start(a, tile.row0 + rank * BM, c);
         };
         if constexpr (BWD) fetch(unit, 0, 0);
-        for (int i = unit; i < a.num_tiles; i += num_units, ++it) {
+        for (int i = unit; i < a.num_items; i += num_units, ++it) {
             const Tile tile = tile_at(a, i);
-            // of two blocks the one with the columns that two accumulators share comes first
-            const auto col_of = [&](int j) { return tile.col0 + ((it & 1) == j ? kTile : 0); };
             const bool got = mbar_wait(accf0 + 8 * (it & 1), static_cast<uint32_t>(it >> 1) & 1u, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got) && lane == 0) raise_error(abort_flag);
             // all go on or none: a warp alone in a tile's barriers would stay there
@@ -784,7 +796,7 @@ __global__ void __launch_bounds__(Gated<BWD>::THREADS, 1) gated_pair_kernel(cons
                 const uint32_t t = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ((it & 1) ? MX_ACC1 : 0);
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
-                    const int64_t col0 = col_of(j);
+                    const int64_t col0 = col_of(tile, it, j);
                     if (col0 >= a.F) {
                         if (j == 0) {
                             __syncwarp();
@@ -1160,11 +1172,33 @@ cudaError_t launch_pair(GatedArgs &a, int sm_count, cudaStream_t st, const char 
     a.tile_cols = BWD ? BN : BM;
     a.tiles_m = static_cast<int>((a.M + 2 * BM - 1) / (2 * BM));
     a.tiles_n = static_cast<int>((a.F + a.tile_cols - 1) / a.tile_cols);
-    a.num_tiles = a.tiles_m * a.tiles_n;
+    a.whole = a.num_items = a.tiles_m * a.tiles_n;
+    if (BWD) {
+        // The last wave in halves (a block of da each) where there are pairs for them, or only
+        // blocks where a pair has fewer of them in a row then: the elementwise part of one takes
+        // some 9 us.  (1537 x 1031 -> 2688, 77 tiles or 147 blocks: 25.3 us in blocks, 33.2 with the last
+        // wave in halves, 35.3 in whole tiles.)
+        const int rest = a.whole % slots, waves = a.whole / slots;
+        const int64_t blocks = a.tiles_m * (a.F / kTile);
+        if ((blocks + slots - 1) / slots < 2 * waves + (rest == 0 ? 0 : 2 * rest <= slots ? 1 : 2)) {
+            a.tile_cols = kTile;
+            a.tiles_n = static_cast<int>(a.F / kTile);
+            a.whole = 0;
+            a.num_items = static_cast<int>(blocks);
+        } else if (2 * rest <= slots) {
+            a.whole -= rest;
+            a.num_items += rest;
+        }
+        if (!encode_tmap_2d(&a.mapBHalf, B.codes, false, B.cols, B.rows, BK, BM / 2, true, B.ld)) {
+            *what = "cuTensorMapEncodeTiled failed for an operand";
+            return cudaErrorInvalidValue;
+        }
+    }
     a.num_kb = static_cast<int>((A.cols + BK - 1) / BK);
     a.group_m = raster_group(A.rows * A.cols, B.rows * B.cols, a.tiles_m);
     a.idesc = idesc_mxf8(static_cast<uint32_t>(A.fmt), static_cast<uint32_t>(B.fmt), 2 * BM, BN, 0);
-    const int units = a.num_tiles < slots ? a.num_tiles : slots;
+    a.idesc_half = idesc_mxf8(static_cast<uint32_t>(A.fmt), static_cast<uint32_t>(B.fmt), 2 * BM, BN / 2, 0);
+    const int units = a.num_items < slots ? a.num_items : slots;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(dim3(2 * units), Gated<BWD>::THREADS, Gated<BWD>::SMEM, 2, attr, st);
     return cudaLaunchKernelEx(&cfg, gated_pair_kernel<BWD, F0, F1, F2>, a);
