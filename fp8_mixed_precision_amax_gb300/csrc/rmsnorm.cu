@@ -14,6 +14,7 @@
 // Both are bound by HBM: each value is read and written once, and a row stays in its
 // CTA's registers between the sum and the use of the sum.
 #include <cstdint>
+#include <type_traits>
 
 #include "norm_rows.cuh"
 #include "once_per_device.h"
@@ -23,6 +24,101 @@ namespace fp8k {
 namespace {
 
 __device__ unsigned g_rms_error_flags = 0;
+
+// Rows that start anywhere (their length is odd, or they are views): element by element, each
+// warp instruction along 32 of them, instead of 16-byte blocks shifted into place.  A thread
+// has kSpread columns 32 apart, a warp 512 in a row, four whole blocks of 128.
+constexpr int kSpread = 16;
+
+template <typename T>
+__device__ __forceinline__ uint32_t raw_of(const T *p) {
+    if constexpr (sizeof(T) == 4)
+        return *reinterpret_cast<const uint32_t *>(p);
+    else
+        return *reinterpret_cast<const uint16_t *>(p);
+}
+template <typename T>
+__device__ __forceinline__ float value_of(uint32_t raw) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(raw);
+    else return to_f32(*reinterpret_cast<const T *>(&raw));
+}
+// kSpread elements from p on, 32 apart; of the first `left` elements from p on (a full warp's: all)
+template <typename T>
+__device__ __forceinline__ void load_spread(const T *p, int left, bool full, uint32_t (&raw)[kSpread]) {
+    if (full) {
+#pragma unroll
+        for (int j = 0; j < kSpread; ++j) raw[j] = raw_of(p + 32 * j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kSpread; ++j) raw[j] = 32 * j < left ? raw_of(p + 32 * j) : 0u;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_spread(T *p, int left, bool full, const uint64_t (&v)[kSpread / 2]) {
+    uint32_t raw[kSpread];
+#pragma unroll
+    for (int i = 0; i < kSpread / 2; ++i) {
+        float lo, hi;
+        f32x2_unpack(v[i], lo, hi);
+        if constexpr (sizeof(T) == 4) {
+            raw[2 * i] = __float_as_uint(lo), raw[2 * i + 1] = __float_as_uint(hi);
+        } else {
+            raw[2 * i] = pack2<T>(lo, hi);
+            raw[2 * i + 1] = raw[2 * i] >> 16;
+        }
+    }
+    using U = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+    U *to = reinterpret_cast<U *>(p);
+    if (full) {
+#pragma unroll
+        for (int j = 0; j < kSpread; ++j) to[32 * j] = static_cast<U>(raw[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kSpread; ++j)
+            if (32 * j < left) to[32 * j] = static_cast<U>(raw[j]);
+    }
+}
+// The warp's four blocks of a row, quantized.  Columns outside the row are 0 and not stored.
+template <int FMT>
+__device__ __forceinline__ void quantize_spread(const BlockView &q, int64_t row, int64_t c, int left, bool full,
+                                                const uint64_t (&v)[kSpread / 2]) {
+    const int lane = threadIdx.x & 31;
+    uint8_t *p = q.codes + row_at(static_cast<unsigned>(row), q.ld) + c;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        float m = absmax3(absmax3(0.0f, v[2 * b]), v[2 * b + 1]);
+        if (is_inf(m)) m = absmax3(absmax3(0.0f, without_inf(v[2 * b])), without_inf(v[2 * b + 1]));
+        const uint32_t byte = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m)));
+        const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
+        const uint32_t w = encode4<FMT>(f32x2_mul(v[2 * b], inv2), f32x2_mul(v[2 * b + 1], inv2));
+        if (lane == 0 && 128 * b < left) store_scale(q, row, (c >> 7) + b, byte);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (full || 128 * b + 32 * k < left) p[128 * b + 32 * k] = static_cast<uint8_t>(w >> (8 * k));
+    }
+}
+__device__ __forceinline__ void quantize_spread(const BlockView &q, int64_t row, int64_t c, int left, bool full,
+                                                const uint64_t (&v)[kSpread / 2]) {
+    if (q.fmt != 0)
+        quantize_spread<1>(q, row, c, left, full, v);
+    else
+        quantize_spread<0>(q, row, c, left, full, v);
+}
+// gamma at the thread's columns; 0 past the row
+__device__ __forceinline__ void load_param_spread(const void *p, int type, int64_t c, int left,
+                                                  uint64_t (&v)[kSpread / 2]) {
+    float f[kSpread];
+#pragma unroll
+    for (int j = 0; j < kSpread; ++j) {
+        f[j] = 0.0f;
+        if (32 * j < left)
+            f[j] = type == kTypeF32    ? static_cast<const float *>(p)[c + 32 * j]
+                   : type == kTypeBF16 ? to_f32(static_cast<const __nv_bfloat16 *>(p)[c + 32 * j])
+                                       : to_f32(static_cast<const __half *>(p)[c + 32 * j]);
+    }
+#pragma unroll
+    for (int i = 0; i < kSpread / 2; ++i) v[i] = f32x2_pack(f[2 * i], f[2 * i + 1]);
+}
 
 struct RmsFwdArgs {
     const void *x, *res;   // res null: no residual
@@ -168,6 +264,51 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_kernel(const
                                  left0 - at, splat_f32x2(rs[j]), g[kKeep ? k : 0], x[j][k]);
             }
         }
+    }
+}
+
+// Rows that start anywhere, up to 8192 columns.
+template <typename T, bool WARP, bool RES>
+__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_spread_kernel(const RmsFwdArgs a) {
+    __shared__ __align__(16) uint64_t buf[2][16];
+    const Team<WARP> team;
+    clear_sums(buf);
+    pdl_wait();
+    pdl_trigger();
+    const float n = static_cast<float>(a.cols), inv_n = __fdiv_rn(1.0f, n);
+    const int64_t c = kSpread * (team.id & ~31) + (team.id & 31);
+    const int left = static_cast<int>(a.cols - c);
+    const bool full = left - 32 * (kSpread - 1) > 31 - (team.id & 31);   // of the whole warp
+    uint32_t raw[kSpread], rawr[RES ? kSpread : 1];
+    auto fetch = [&](int64_t row) {
+        load_spread(static_cast<const T *>(a.x) + row * a.ldx + c, left, full, raw);
+        if constexpr (RES) load_spread(static_cast<const T *>(a.res) + row * a.ldr + c, left, full, rawr);
+    };
+    if (team.row < a.rows) fetch(team.row);
+    uint64_t g[kSpread / 2];
+    load_param_spread(a.gamma, a.wtype, c, left, g);
+    int flip = 0;
+    for (int64_t row = team.row; row < a.rows; row += team.step, flip ^= 1) {
+        uint64_t x[kSpread / 2], s2 = 0;
+#pragma unroll
+        for (int i = 0; i < kSpread / 2; ++i) {
+            x[i] = f32x2_pack(value_of<T>(raw[2 * i]), value_of<T>(raw[2 * i + 1]));
+            if constexpr (RES)
+                x[i] = sum_as<T>(x[i], f32x2_pack(value_of<T>(rawr[2 * i]), value_of<T>(rawr[2 * i + 1])));
+            s2 = f32x2_fma(x[i], x[i], s2);
+        }
+        if (row + team.step < a.rows) fetch(row + team.step);
+        if (RES && a.sum != nullptr) store_spread(static_cast<T *>(a.sum) + row * a.lds + c, left, full, x);
+        const float s = team_sum<WARP>(sum2(s2), buf[flip]);
+        const float rs = __frsqrt_rn(__fadd_rn(quotient(s, n, inv_n), a.eps));
+        if (team.id == 0) a.rstd[row] = rs;
+        if (a.x8.codes != nullptr) quantize_spread(a.x8, row, c, left, full, x);
+        if (a.y == nullptr && a.y8.codes == nullptr) continue;
+        const uint64_t rs2 = splat_f32x2(rs);
+#pragma unroll
+        for (int i = 0; i < kSpread / 2; ++i) x[i] = f32x2_mul(f32x2_mul(x[i], rs2), g[i]);
+        if (a.y != nullptr) store_spread(static_cast<T *>(a.y) + row * a.ldy + c, left, full, x);
+        if (a.y8.codes != nullptr) quantize_spread(a.y8, row, c, left, full, x);
     }
 }
 
@@ -335,27 +476,160 @@ __device__ __forceinline__ void rms_store_part(const RmsBwdArgs &a, Col col, con
     }
 }
 
-// Rows of 513 .. 8192 columns, one at a time per CTA: thread t has columns 8 (t + k
-// threads) .. + 7, k < 2, and their sums over the CTA's rows.  The next rows of dy, x and dsum
-// are on their way into a ring in shared memory by bulk copies of the 16-byte blocks that
-// hold them, whatever their alignment; the barrier of a row's sum also tells that its
-// place in the ring may be filled again (what a thread needs of dsum is in its registers by
-// then).
+// Rows of 513 .. 8192 columns, one at a time per CTA; a thread has 16 columns, and their sums
+// over the CTA's rows.  The next rows of dy, x and dsum are on their way into a ring in
+// shared memory by bulk copies of the 16-byte blocks that hold them, whatever their alignment;
+// the barrier of a row's sum also tells that its place in the ring may be filled again (what a
+// thread needs of dsum is in its registers by then).
 constexpr int kRmsRing = 8;   // most rows in flight
 
 struct RmsRingArgs {
     RmsBwdArgs a;
     int stages;
     uint32_t dy_span, x_span, ds_span;   // bytes of a row's place: dy, x or its codes, dsum
+    uint32_t gamma_span;                 // bytes in front of the ring that hold gamma (or 0)
 };
 
-// ALIGNED: every row starts on a 16-byte boundary and is a multiple of 8 columns long.
+// A thread's columns of a row's copy.  ALIGNED: every row starts on a 16-byte boundary and is a
+// multiple of 8 columns long; thread t has columns 8 (t + k threads) .. + 7, k < 2.  Otherwise
+// columns 32 apart, as in the forward; the copy of a row starts `off` bytes after the boundary.
+template <typename T, bool ALIGNED>
+struct RingColumns;
+template <typename T>
+struct RingColumns<T, true> {
+    int col[2], cols;
+    RawVec<T, 8> raw[2];
+
+    __device__ __forceinline__ explicit RingColumns(int cols_) : cols(cols_) {
+        col[0] = 8 * threadIdx.x, col[1] = 8 * (threadIdx.x + blockDim.x);
+    }
+    __device__ __forceinline__ void load(const uint8_t *place, uint32_t) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) raw[k].load(reinterpret_cast<const T *>(place), col[k], cols);
+    }
+    __device__ __forceinline__ void get(uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint64_t x[4];
+            raw[k].get(nullptr, 0, 0, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * k + i] = x[i];
+        }
+    }
+    __device__ __forceinline__ void param(const void *p, int type, uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint64_t x[4];
+            load_param(p, type, col[k], cols, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * k + i] = x[i];
+        }
+    }
+    uint32_t scale[2];
+    __device__ __forceinline__ void fetch_scales(const BlockView &q, int64_t row) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) scale[k] = col[k] < cols ? fetch_scale(q, row, col[k] >> 7) : 0u;
+    }
+    float sc[2];
+    __device__ __forceinline__ void take_scales(const BlockView &q) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sc[k] = fetched_scale(q, scale[k]);
+    }
+    __device__ __forceinline__ void codes(const uint8_t *place, int fmt, uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint2 w = make_uint2(0, 0);
+            if (col[k] < cols) w = *reinterpret_cast<const uint2 *>(place + col[k]);
+            uint64_t x[4];
+            codes8_times(w, fmt, sc[k], 8, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * k + i] = x[i];
+        }
+    }
+    __device__ __forceinline__ void store(T *row, const uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t x[4] = {v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+            RawVec<T, 8>::store(row, col[k], cols, x);
+        }
+    }
+    __device__ __forceinline__ void store_sums(float *part, const uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (col[k] >= cols) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<ulonglong2 *>(part + col[k] + 4 * i) =
+                    make_ulonglong2(v[4 * k + 2 * i], v[4 * k + 2 * i + 1]);
+        }
+    }
+};
+template <typename T>
+struct RingColumns<T, false> {
+    int c, left;
+    bool full;
+    uint32_t raw[kSpread];
+
+    __device__ __forceinline__ explicit RingColumns(int cols) {
+        const int lane = threadIdx.x & 31;
+        c = kSpread * (threadIdx.x & ~31) + lane;
+        left = cols - c;
+        full = left - 32 * (kSpread - 1) > 31 - lane;   // of the whole warp
+    }
+    __device__ __forceinline__ void load(const uint8_t *place, uint32_t off) {
+        load_spread(reinterpret_cast<const T *>(place + off) + c, left, full, raw);
+    }
+    __device__ __forceinline__ void get(uint64_t (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f32x2_pack(value_of<T>(raw[2 * i]), value_of<T>(raw[2 * i + 1]));
+    }
+    __device__ __forceinline__ void param(const void *p, int type, uint64_t (&v)[8]) const {
+        load_param_spread(p, type, c, left, v);
+    }
+    uint32_t scale;   // lane b: of the warp's block b
+    __device__ __forceinline__ void fetch_scales(const BlockView &q, int64_t row) {
+        const int lane = threadIdx.x & 31, block = ((c - lane) >> 7) + (lane & 3);
+        scale = 128 * block < c - lane + left + lane ? fetch_scale(q, row, block) : 0u;
+    }
+    float sc;
+    __device__ __forceinline__ void take_scales(const BlockView &q) { sc = fetched_scale(q, scale); }
+    __device__ __forceinline__ void codes(const uint8_t *place, int fmt, uint64_t (&v)[8]) const {
+        uint32_t w[kSpread];
+        if (full) {
+#pragma unroll
+            for (int j = 0; j < kSpread; ++j) w[j] = place[c + 32 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSpread; ++j) w[j] = 32 * j < left ? place[c + 32 * j] : 0u;
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float f[4];
+            decode4(__byte_perm(__byte_perm(w[4 * b], w[4 * b + 1], 0x0040),
+                                __byte_perm(w[4 * b + 2], w[4 * b + 3], 0x0040), 0x5410),
+                    fmt, f);
+            const uint64_t s2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, sc, b));
+            v[2 * b] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
+            v[2 * b + 1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
+        }
+    }
+    __device__ __forceinline__ void store(T *row, const uint64_t (&v)[8]) const { store_spread(row + c, left, full, v); }
+    __device__ __forceinline__ void store_sums(float *part, const uint64_t (&v)[8]) const {
+        store_spread(part + c, left, full, v);
+    }
+};
+
+// Two CTAs of 288 threads leave 96 registers each: gamma waits in shared memory, where the
+// columns are single ones (5003 x 4111 from 8 bits 43.3 us, 46.0 with gamma in registers).
+template <int THREADS, bool ALIGNED>
+constexpr bool kGammaShared = THREADS == kRingHalf && !ALIGNED;
+
 template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRingArgs r) {
-    constexpr int VPT = 2, kSize = static_cast<int>(sizeof(T));
-    using Raw = typename Lay<T, ALIGNED ? 8 : 0>::Raw;
+    constexpr int kSize = static_cast<int>(sizeof(T));
     const RmsBwdArgs &a = r.a;
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ __align__(128) uint8_t ring_raw[];
+    uint8_t *const ring = ring_raw + r.gamma_span;
     __shared__ __align__(16) uint64_t buf[2][16];
     __shared__ uint64_t bars[kRmsRing];
     __shared__ int gave_up;
@@ -395,42 +669,24 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
             if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < a.rows)
                 issue(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
     const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
-    auto col = [&](int k) { return static_cast<int>(8 * (threadIdx.x + k * blockDim.x)); };
-    uint64_t dg[VPT][4] = {}, g[VPT][4];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) load_param(a.gamma, a.wtype, col(k), a.cols, g[k]);
+    using Columns = RingColumns<T, ALIGNED>;
+    Columns own(cols);
+    uint64_t dg[8] = {}, g[8];
+    own.param(a.gamma, a.wtype, g);
+    float *gamma = reinterpret_cast<float *>(ring_raw);
+    if constexpr (kGammaShared<THREADS, ALIGNED>) store_spread(gamma + own.c, own.left, own.full, g);   // read again by its writer alone
     // what does not go through the ring is fetched a row ahead
     float rs_next = 0.0f;
-    uint32_t sc_next[VPT] = {};
     auto fetch = [&](int64_t row) {
         rs_next = a.rstd[row];
-        if constexpr (SAVED) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k)
-                if (col(k) < cols) sc_next[k] = fetch_scale(a.x8, row, col(k) >> 7);
-        }
+        if constexpr (SAVED) own.fetch_scales(a.x8, row);
     };
     if (blockIdx.x < a.rows) fetch(blockIdx.x);
-    // 8 elements of a row's copy, which starts `off` bytes after a 16-byte boundary
-    auto take = [&](Raw &raw, const uint8_t *place, int k, uint32_t off) {
-        if constexpr (ALIGNED)
-            raw.load(reinterpret_cast<const T *>(place), col(k), cols);
-        else
-            raw.load_shared(place + col(k) * kSize, off != 0);
-    };
-    auto get = [&](const Raw &raw, int left, uint32_t off, uint64_t (&v)[4]) {
-        if constexpr (ALIGNED)
-            raw.get(nullptr, 0, 0, v);
-        else
-            raw.get(off, left, v);
-    };
     int s = 0, flip = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         const uint64_t rs2 = splat_f32x2(rs_next);
-        float sc[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) sc[k] = SAVED ? fetched_scale(a.x8, sc_next[k]) : 0.0f;
+        if constexpr (SAVED) own.take_scales(a.x8);
         if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
         if (!mbar_wait(bar0 + 8 * s, phase, &gave_up)) {
             // goes on with what is there, so that every thread still meets every barrier
@@ -438,50 +694,34 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
             *static_cast<volatile int *>(&gave_up) = 1;
         }
         const uint8_t *stage = ring + s * stage_bytes;
-        const uint32_t doff = static_cast<uint32_t>(start_of(dy0, row, a.lddy) & 15);
-        const uint32_t xoff = SAVED ? 0u : static_cast<uint32_t>(start_of(x0, row, a.ldx) & 15);
-        const uint32_t eoff = static_cast<uint32_t>(start_of(ds0, row, a.ldds) & 15);
-        uint64_t dy[VPT][4], x[VPT][4], sum = 0;
-        Raw rds[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int left = cols - col(k);
-            if (left > 0) {
-                Raw raw;
-                take(raw, stage, k, doff);
-                get(raw, left, doff, dy[k]);
-                if constexpr (SAVED) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(stage + r.dy_span + col(k));
-                    codes8_times(w, a.x8.fmt, sc[k], ALIGNED ? 8 : left, x[k]);
-                } else {
-                    take(raw, stage + r.dy_span, k, xoff);
-                    get(raw, left, xoff, x[k]);
-                }
-                if (ds0 != nullptr) take(rds[k], stage + r.dy_span + r.x_span, k, eoff);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dy[k][i] = x[k][i] = 0;
-            }
-            rms_bwd_accumulate(rs2, g[k], dy[k], x[k], dg[k], sum);
+        uint64_t dy[8], x[8], sum = 0;
+        own.load(stage, static_cast<uint32_t>(start_of(dy0, row, a.lddy) & 15));
+        own.get(dy);
+        if constexpr (SAVED) {
+            own.codes(stage + r.dy_span, a.x8.fmt, x);
+        } else {
+            own.load(stage + r.dy_span, static_cast<uint32_t>(start_of(x0, row, a.ldx) & 15));
+            own.get(x);
         }
+        if (ds0 != nullptr)
+            own.load(stage + r.dy_span + r.x_span, static_cast<uint32_t>(start_of(ds0, row, a.ldds) & 15));
+        if constexpr (kGammaShared<THREADS, ALIGNED>) {
+            uint32_t raw[kSpread];
+            load_spread(gamma + own.c, own.left, own.full, raw);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = f32x2_pack(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
+        }
+        rms_bwd_accumulate(rs2, g, dy, x, dg, sum);
         const float total = team_sum<false>(sum2(sum), buf[flip]);
         if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
             issue(row + static_cast<int64_t>(r.stages) * gridDim.x, s);
-        const uint64_t nm2 = splat_f32x2(__fmul_rn(total, ninv_n));
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int left = cols - col(k);
-            uint64_t ds[4] = {};
-            if (ds0 != nullptr && left > 0) get(rds[k], left, eoff, ds);
-            rms_bwd_finish(rs2, nm2, x[k], ds, dy[k]);
-            if constexpr (ALIGNED)
-                RawVec<T, 8>::store(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
-            else
-                store_row8<T>(static_cast<T *>(a.dx) + row * a.lddx, col(k), a.cols, dy[k]);
-        }
+        uint64_t ds[8] = {};
+        if (ds0 != nullptr) own.get(ds);
+        rms_bwd_finish(rs2, splat_f32x2(__fmul_rn(total, ninv_n)), x, ds, dy);
+        own.store(static_cast<T *>(a.dx) + row * a.lddx, dy);
         if (++s == r.stages) s = 0, phase ^= 1u;
     }
-    rms_store_part(a, col, dg);
+    own.store_sums(a.part + static_cast<int64_t>(blockIdx.x) * up8(a.cols), dg);
     if (gave_up && threadIdx.x == 0)   // copies still in flight land (bounded) before the CTA exits
         for (int i = 0; i < r.stages; ++i) {
             mbar_wait(bar0 + 8 * s, phase, nullptr, 100000000ull);
@@ -620,6 +860,15 @@ cudaError_t rms_fwd_rows(const RmsFwdArgs &a, int sms, cudaStream_t st) {
     return launch_pdl(rms_fwd_kernel<T, VPT, WARP, VEC, RES>, dim3(grid), dim3(threads), 0, st, a);
 }
 
+template <typename T, bool WARP, bool RES>
+cudaError_t rms_fwd_spread(const RmsFwdArgs &a, int sms, cudaStream_t st) {
+    const unsigned threads = WARP ? 32 * kWarps : row_threads(a.cols, kSpread);
+    // CTAs that the registers allow at once
+    const int64_t resident = static_cast<int64_t>(sms) * (threads < 640 ? 640 / threads : 1);
+    const unsigned grid = capped(WARP ? (a.rows + kWarps - 1) / kWarps : a.rows, resident);
+    return launch_pdl(rms_fwd_spread_kernel<T, WARP, RES>, dim3(grid), dim3(threads), 0, st, a);
+}
+
 template <typename T, bool RES>
 cudaError_t rms_fwd_typed(const RmsFwdArgs &a, bool vec, int sms, cudaStream_t st) {
     if (vec) {
@@ -627,8 +876,8 @@ cudaError_t rms_fwd_typed(const RmsFwdArgs &a, bool vec, int sms, cudaStream_t s
         if (a.cols <= 8192) return rms_fwd_rows<T, 1, false, 16, RES>(a, sms, st);
         if (a.cols <= 16384) return rms_fwd_rows<T, 2, false, 16, RES>(a, sms, st);
     } else {
-        if (a.cols <= 512) return rms_fwd_rows<T, 2, true, 0, RES>(a, sms, st);
-        if (a.cols <= 8192) return rms_fwd_rows<T, 2, false, 0, RES>(a, sms, st);
+        if (a.cols <= 512) return rms_fwd_spread<T, true, RES>(a, sms, st);
+        if (a.cols <= 8192) return rms_fwd_spread<T, false, RES>(a, sms, st);
         if (a.cols <= 16384) return rms_fwd_rows<T, 4, false, 0, RES>(a, sms, st);
     }
     return launch_pdl(rms_fwd_wide_kernel<T, RES>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
@@ -638,18 +887,19 @@ cudaError_t rms_fwd_typed(const RmsFwdArgs &a, bool vec, int sms, cudaStream_t s
 template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 cudaError_t rms_bwd_ring_sized(const RmsBwdArgs &a, int grid, unsigned threads, cudaStream_t st) {
     constexpr int64_t kSize = sizeof(T), kBytes = 200 << 10;
-    RmsRingArgs r{a, 0, 0, 0, 0};
+    RmsRingArgs r{a, 0, 0, 0, 0, 0};
     r.dy_span = static_cast<uint32_t>((a.cols * kSize + 15 + 127) / 128 * 128 + 128);
     r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
     r.ds_span = a.dsum != nullptr ? r.dy_span : 0;
     const int64_t place = r.dy_span + r.x_span + r.ds_span;
-    const int64_t fit = kBytes / ring_ctas_per_sm(threads) / place;
+    if (kGammaShared<THREADS, ALIGNED>) r.gamma_span = static_cast<uint32_t>((a.cols * 4 + 127) / 128 * 128);
+    const int64_t fit = (kBytes / ring_ctas_per_sm(threads) - r.gamma_span) / place;
     r.stages = static_cast<int>(fit < kRmsRing ? fit : kRmsRing);
     static SmemLimit limit;
     const cudaError_t err = limit.allow(rms_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, kBytes);
     if (err != cudaSuccess) return err;
     return launch_pdl(rms_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, dim3(grid), dim3(threads),
-                      static_cast<size_t>(r.stages * place), st, r);
+                      static_cast<size_t>(r.gamma_span + r.stages * place), st, r);
 }
 
 template <typename T, bool SAVED, bool ALIGNED>
