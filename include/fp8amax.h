@@ -664,7 +664,7 @@ typedef struct {
  * returns.  workspace: DEVICE, 8-byte aligned, of at least
  * fp8_grad_norm_workspace(count) bytes, in use until the call's kernels are done.
  * The sums' order is fixed: equal calls give equal bits.  One kernel for each 1000
- * vectors, and one that joins their sums. */
+ * vectors, and one that joins their sums; for few elements one alone. */
 fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, void *workspace,
                          int64_t workspace_bytes, void *stream);
 int64_t fp8_grad_norm_workspace(int32_t count);
