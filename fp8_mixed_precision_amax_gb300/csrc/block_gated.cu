@@ -621,7 +621,8 @@ __device__ __forceinline__ void gated_bwd_block(const GatedArgs &a, GatedShared<
                                                 Next next) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, part = warp >> 2;
     const bool want_t = a.dh8t.codes != nullptr, want_a = a.a8t.codes != nullptr, want_r = a.dh8.codes != nullptr;
-    elements_sync();   // the block before has left shared memory
+    // (the block before has been read from da; its codes may still be on their way out, and the
+    // next ones come three barriers later)
     // 16-byte chunk k of a row of da is kept at place k ^ (row mod 32): no bank twice, either way
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -646,7 +647,10 @@ __device__ __forceinline__ void gated_bwd_block(const GatedArgs &a, GatedShared<
 #pragma unroll
     for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) atomicMax(&sm.max[k][4 * lane + j], __float_as_uint(m.col[k][j]));
+        for (int j = 0; j < 4; ++j)
+            asm volatile("red.shared::cta.max.u32 [%0], %1;" ::"r"(smem_u32(&sm.max[k][4 * lane + j])),
+                         "r"(__float_as_uint(m.col[k][j]))
+                         : "memory");
     elements_sync();
     if (threadIdx.x < 3 * kTile) {
         const int k = threadIdx.x / kTile, c = threadIdx.x % kTile;

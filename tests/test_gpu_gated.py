@@ -323,3 +323,84 @@ def test_empty_calls_do_nothing():
     f.fp8_block_gemm_swiglu_fwd(e(4, 64), e(0, 64), e(4, 0))
     f.fp8_block_gemm_swiglu_bwd(e(0, 64), e(128, 64), e(0, 256), e(0, 256), e(256, 0), e(128, 0))
     f.fp8_sync_status()
+
+
+def test_more_than_2_31_elements():
+    """Offsets past 32 bits: 98400 tokens of [gate | value] 2 x 11008 wide (2.2 G codes); the last
+    block of 128 tokens, partly filled, against the formulas, and the first rows the same bits."""
+    f = _lib()
+    M, F, K = 98400, 11008, 128
+    e = f.BlockFp8.empty
+    rows = slice(98304, M)
+    first = held(96, K, 1.0, 0, 1, 1)
+
+    def repeated(q, into):
+        """The same 96 rows at the beginning, in the last block and, over and over, between."""
+        at = torch.arange(M, device="cuda") % 96
+        at[rows] = torch.arange(96, device="cuda")
+        into.codes.copy_(q.codes[at]), into.scales.copy_(q.scales[at])
+        return into
+
+    A, B = repeated(first, e(M, K)), held(2 * F, K, 1.5 * K ** -0.5, 0, 128, 2)
+    a8, h8 = e(M, F), e(M, 2 * F)
+    f.fp8_block_gemm_swiglu_fwd(A, B, a8, h8)
+    f.fp8_sync_status()
+    part = lambda q, r: f.BlockFp8(q.codes[r], q.scales[r], q.cols, q.fmt)
+    h, a, eh, ta = fwd_plain(first, B)
+    near_q(part(h8, rows), h, eh, "h8")
+    near_q(part(a8, rows), a, ta, "a8")
+
+    def ends_equal(q):
+        nb = q.cols // 128
+        return torch.equal(q.codes[:96], q.codes[rows]) and torch.equal(q.scales[:96, :nb], q.scales[rows, :nb])
+
+    assert ends_equal(a8) and ends_equal(h8)
+    del a8
+    W = held(F, K, K ** -0.5, 0, 128, 4)
+    dh8, dh8t, a8t = e(M, 2 * F, 1), e(2 * F, M, 1), e(F, M)
+    f.fp8_block_gemm_swiglu_bwd(A, W, h8, dh8, dh8t, a8t)
+    f.fp8_sync_status()
+    dh, a, tol, tol_a = bwd_plain(first, W, part(h8, rows))
+    near_q(part(dh8, rows), dh, tol, "dh8")
+    assert ends_equal(dh8)
+    tail = lambda q: f.BlockFp8(q.codes[:, rows.start:], q.scales[:, rows.start // 128:], 96, q.fmt)
+    near_q(tail(dh8t), dh.t(), tol.t(), "dh8t")
+    near_q(tail(a8t), a.t(), tol_a.t(), "a8t")
+
+
+def test_two_calls_at_once():
+    """On two streams, each with data of its own: the same bits as one after the other."""
+    f = _lib()
+    cases = [(300, 640, 512), (16, 1152, 700), (1100, 1024, 256)]
+    data, alone = [], []
+    for k, (M, F, K) in enumerate(cases):
+        A, B, W = held(M, K, 1.0, 0, 1, k), held(2 * F, K, 0.07, 0, 128, k + 9), held(F, K, 0.05, 0, 128, k + 7)
+        data.append((A, B, W))
+
+    def run(k, stream=None):
+        (M, F, K), (A, B, W), e = cases[k], data[k], f.BlockFp8.empty
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            o = (e(M, F), e(M, 2 * F), e(M, 2 * F, 1), e(2 * F, M, 1), e(F, M))
+        for q in o:
+            q.codes.zero_(), q.scales.zero_()
+        torch.cuda.synchronize()
+        return o, lambda: (f.fp8_block_gemm_swiglu_fwd(A, B, o[0], o[1], stream),
+                           f.fp8_block_gemm_swiglu_bwd(A, W, o[1], o[2], o[3], o[4], stream))
+
+    for k in range(3):
+        o, go = run(k)
+        go()
+        alone.append(o)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [run(k, s) for k, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _, go in outs:
+            go()
+    f.fp8_sync_status()
+    torch.cuda.synchronize()
+    for (o, _), want in zip(outs, alone):
+        for p, q in zip(o, want):
+            nb = -(-p.cols // 128)
+            assert torch.equal(p.codes[:, :p.cols], q.codes[:, :p.cols])
+            assert torch.equal(p.scales[:, :nb], q.scales[:, :nb])
