@@ -54,17 +54,15 @@ __device__ __forceinline__ void load_spread(const T *p, int left, bool full, uin
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_spread(T *p, int left, bool full, const uint64_t (&v)[kSpread / 2]) {
+__device__ __forceinline__ void store_spread(T *p, int left, bool full, const float (&v)[kSpread]) {
     uint32_t raw[kSpread];
 #pragma unroll
-    for (int i = 0; i < kSpread / 2; ++i) {
-        float lo, hi;
-        f32x2_unpack(v[i], lo, hi);
+    for (int j = 0; j < kSpread; j += 2) {
         if constexpr (sizeof(T) == 4) {
-            raw[2 * i] = __float_as_uint(lo), raw[2 * i + 1] = __float_as_uint(hi);
+            raw[j] = __float_as_uint(v[j]), raw[j + 1] = __float_as_uint(v[j + 1]);
         } else {
-            raw[2 * i] = pack2<T>(lo, hi);
-            raw[2 * i + 1] = raw[2 * i] >> 16;
+            raw[j] = pack2<T>(v[j], v[j + 1]);
+            raw[j + 1] = raw[j] >> 16;
         }
     }
     using U = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
@@ -81,16 +79,22 @@ __device__ __forceinline__ void store_spread(T *p, int left, bool full, const ui
 // The warp's four blocks of a row, quantized.  Columns outside the row are 0 and not stored.
 template <int FMT>
 __device__ __forceinline__ void quantize_spread(const BlockView &q, int64_t row, int64_t c, int left, bool full,
-                                                const uint64_t (&v)[kSpread / 2]) {
+                                                const float (&v)[kSpread]) {
     const int lane = threadIdx.x & 31;
     uint8_t *p = q.codes + row_at(static_cast<unsigned>(row), q.ld) + c;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        float m = absmax3(absmax3(0.0f, v[2 * b]), v[2 * b + 1]);
-        if (is_inf(m)) m = absmax3(absmax3(0.0f, without_inf(v[2 * b])), without_inf(v[2 * b + 1]));
+        float m = absmax3(absmax3(0.0f, v[4 * b], v[4 * b + 1]), v[4 * b + 2], v[4 * b + 3]);
+        if (is_inf(m)) {
+            m = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (!is_inf(fabsf(v[4 * b + k]))) m = absmax3(m, v[4 * b + k], v[4 * b + k]);
+        }
         const uint32_t byte = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m)));
-        const uint64_t inv2 = splat_f32x2(scale_inverse(byte));
-        const uint32_t w = encode4<FMT>(f32x2_mul(v[2 * b], inv2), f32x2_mul(v[2 * b + 1], inv2));
+        const float inv = scale_inverse(byte);
+        const uint32_t w = cvt2_fp8<FMT>(__fmul_rn(v[4 * b], inv), __fmul_rn(v[4 * b + 1], inv)) |
+                           cvt2_fp8<FMT>(__fmul_rn(v[4 * b + 2], inv), __fmul_rn(v[4 * b + 3], inv)) << 16;
         if (lane == 0 && 128 * b < left) store_scale(q, row, (c >> 7) + b, byte);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -98,26 +102,22 @@ __device__ __forceinline__ void quantize_spread(const BlockView &q, int64_t row,
     }
 }
 __device__ __forceinline__ void quantize_spread(const BlockView &q, int64_t row, int64_t c, int left, bool full,
-                                                const uint64_t (&v)[kSpread / 2]) {
+                                                const float (&v)[kSpread]) {
     if (q.fmt != 0)
         quantize_spread<1>(q, row, c, left, full, v);
     else
         quantize_spread<0>(q, row, c, left, full, v);
 }
 // gamma at the thread's columns; 0 past the row
-__device__ __forceinline__ void load_param_spread(const void *p, int type, int64_t c, int left,
-                                                  uint64_t (&v)[kSpread / 2]) {
-    float f[kSpread];
+__device__ __forceinline__ void load_param_spread(const void *p, int type, int64_t c, int left, float (&v)[kSpread]) {
 #pragma unroll
     for (int j = 0; j < kSpread; ++j) {
-        f[j] = 0.0f;
+        v[j] = 0.0f;
         if (32 * j < left)
-            f[j] = type == kTypeF32    ? static_cast<const float *>(p)[c + 32 * j]
+            v[j] = type == kTypeF32    ? static_cast<const float *>(p)[c + 32 * j]
                    : type == kTypeBF16 ? to_f32(static_cast<const __nv_bfloat16 *>(p)[c + 32 * j])
                                        : to_f32(static_cast<const __half *>(p)[c + 32 * j]);
     }
-#pragma unroll
-    for (int i = 0; i < kSpread / 2; ++i) v[i] = f32x2_pack(f[2 * i], f[2 * i + 1]);
 }
 
 struct RmsFwdArgs {
@@ -285,28 +285,26 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_spread_kerne
         if constexpr (RES) load_spread(static_cast<const T *>(a.res) + row * a.ldr + c, left, full, rawr);
     };
     if (team.row < a.rows) fetch(team.row);
-    uint64_t g[kSpread / 2];
+    float g[kSpread];
     load_param_spread(a.gamma, a.wtype, c, left, g);
     int flip = 0;
     for (int64_t row = team.row; row < a.rows; row += team.step, flip ^= 1) {
-        uint64_t x[kSpread / 2], s2 = 0;
+        float x[kSpread], q = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kSpread / 2; ++i) {
-            x[i] = f32x2_pack(value_of<T>(raw[2 * i]), value_of<T>(raw[2 * i + 1]));
-            if constexpr (RES)
-                x[i] = sum_as<T>(x[i], f32x2_pack(value_of<T>(rawr[2 * i]), value_of<T>(rawr[2 * i + 1])));
-            s2 = f32x2_fma(x[i], x[i], s2);
+        for (int j = 0; j < kSpread; ++j) {
+            x[j] = value_of<T>(raw[j]);
+            if constexpr (RES) x[j] = to_f32(from_f32<T>(__fadd_rn(x[j], value_of<T>(rawr[j]))));
+            q = __fmaf_rn(x[j], x[j], q);
         }
         if (row + team.step < a.rows) fetch(row + team.step);
         if (RES && a.sum != nullptr) store_spread(static_cast<T *>(a.sum) + row * a.lds + c, left, full, x);
-        const float s = team_sum<WARP>(sum2(s2), buf[flip]);
+        const float s = team_sum<WARP>(q, buf[flip]);
         const float rs = __frsqrt_rn(__fadd_rn(quotient(s, n, inv_n), a.eps));
         if (team.id == 0) a.rstd[row] = rs;
         if (a.x8.codes != nullptr) quantize_spread(a.x8, row, c, left, full, x);
         if (a.y == nullptr && a.y8.codes == nullptr) continue;
-        const uint64_t rs2 = splat_f32x2(rs);
 #pragma unroll
-        for (int i = 0; i < kSpread / 2; ++i) x[i] = f32x2_mul(f32x2_mul(x[i], rs2), g[i]);
+        for (int j = 0; j < kSpread; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], rs), g[j]);
         if (a.y != nullptr) store_spread(static_cast<T *>(a.y) + row * a.ldy + c, left, full, x);
         if (a.y8.codes != nullptr) quantize_spread(a.y8, row, c, left, full, x);
     }
@@ -579,13 +577,6 @@ struct RingColumns<T, false> {
     __device__ __forceinline__ void load(const uint8_t *place, uint32_t off) {
         load_spread(reinterpret_cast<const T *>(place + off) + c, left, full, raw);
     }
-    __device__ __forceinline__ void get(uint64_t (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = f32x2_pack(value_of<T>(raw[2 * i]), value_of<T>(raw[2 * i + 1]));
-    }
-    __device__ __forceinline__ void param(const void *p, int type, uint64_t (&v)[8]) const {
-        load_param_spread(p, type, c, left, v);
-    }
     uint32_t scale;   // lane b: of the warp's block b
     __device__ __forceinline__ void fetch_scales(const BlockView &q, int64_t row) {
         const int lane = threadIdx.x & 31, block = ((c - lane) >> 7) + (lane & 3);
@@ -593,7 +584,7 @@ struct RingColumns<T, false> {
     }
     float sc;
     __device__ __forceinline__ void take_scales(const BlockView &q) { sc = fetched_scale(q, scale); }
-    __device__ __forceinline__ void codes(const uint8_t *place, int fmt, uint64_t (&v)[8]) const {
+    __device__ __forceinline__ void codes(const uint8_t *place, int fmt, float (&v)[kSpread]) const {
         uint32_t w[kSpread];
         if (full) {
 #pragma unroll
@@ -608,19 +599,16 @@ struct RingColumns<T, false> {
             decode4(__byte_perm(__byte_perm(w[4 * b], w[4 * b + 1], 0x0040),
                                 __byte_perm(w[4 * b + 2], w[4 * b + 3], 0x0040), 0x5410),
                     fmt, f);
-            const uint64_t s2 = splat_f32x2(__shfl_sync(0xFFFFFFFFu, sc, b));
-            v[2 * b] = f32x2_mul(f32x2_pack(f[0], f[1]), s2);
-            v[2 * b + 1] = f32x2_mul(f32x2_pack(f[2], f[3]), s2);
+            const float s = __shfl_sync(0xFFFFFFFFu, sc, b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * b + k] = __fmul_rn(f[k], s);
         }
-    }
-    __device__ __forceinline__ void store(T *row, const uint64_t (&v)[8]) const { store_spread(row + c, left, full, v); }
-    __device__ __forceinline__ void store_sums(float *part, const uint64_t (&v)[8]) const {
-        store_spread(part + c, left, full, v);
     }
 };
 
 // Two CTAs of 288 threads leave 96 registers each: gamma waits in shared memory, where the
-// columns are single ones (5003 x 4111 from 8 bits 43.3 us, 46.0 with gamma in registers).
+// columns are single ones (5003 x 4111 from 8 bits 38.8 us; with gamma in registers and packed
+// arithmetic 46.0, with packed arithmetic 43.3).
 template <int THREADS, bool ALIGNED>
 constexpr bool kGammaShared = THREADS == kRingHalf && !ALIGNED;
 
@@ -671,10 +659,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
     const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
     using Columns = RingColumns<T, ALIGNED>;
     Columns own(cols);
-    uint64_t dg[8] = {}, g[8];
-    own.param(a.gamma, a.wtype, g);
+    uint64_t dg[8] = {}, g[8];                       // packed, or
+    float own_dg[kSpread] = {}, own_g[kSpread];      // one by one
     float *gamma = reinterpret_cast<float *>(ring_raw);
-    if constexpr (kGammaShared<THREADS, ALIGNED>) store_spread(gamma + own.c, own.left, own.full, g);   // read again by its writer alone
+    if constexpr (ALIGNED) {
+        own.param(a.gamma, a.wtype, g);
+    } else {
+        load_param_spread(a.gamma, a.wtype, own.c, own.left, own_g);
+        if constexpr (kGammaShared<THREADS, ALIGNED>)
+            store_spread(gamma + own.c, own.left, own.full, own_g);   // read again by its writer alone
+    }
     // what does not go through the ring is fetched a row ahead
     float rs_next = 0.0f;
     auto fetch = [&](int64_t row) {
@@ -685,7 +679,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
     int s = 0, flip = 0;
     uint32_t phase = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        const uint64_t rs2 = splat_f32x2(rs_next);
+        const float rs = rs_next;
+        const uint64_t rs2 = splat_f32x2(rs);
         if constexpr (SAVED) own.take_scales(a.x8);
         if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
         if (!mbar_wait(bar0 + 8 * s, phase, &gave_up)) {
@@ -694,6 +689,43 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
             *static_cast<volatile int *>(&gave_up) = 1;
         }
         const uint8_t *stage = ring + s * stage_bytes;
+        if constexpr (!ALIGNED) {
+            // one by one: single columns come as single values, which packed arithmetic would have
+            // to pair first
+            float dy[kSpread], x[kSpread], sum = 0.0f;
+            own.load(stage, static_cast<uint32_t>(start_of(dy0, row, a.lddy) & 15));
+#pragma unroll
+            for (int j = 0; j < kSpread; ++j) dy[j] = value_of<T>(own.raw[j]);
+            if constexpr (SAVED) {
+                own.codes(stage + r.dy_span, a.x8.fmt, x);
+            } else {
+                own.load(stage + r.dy_span, static_cast<uint32_t>(start_of(x0, row, a.ldx) & 15));
+#pragma unroll
+                for (int j = 0; j < kSpread; ++j) x[j] = value_of<T>(own.raw[j]);
+            }
+            uint32_t g_raw[kSpread];
+            if constexpr (kGammaShared<THREADS, ALIGNED>) load_spread(gamma + own.c, own.left, own.full, g_raw);
+#pragma unroll
+            for (int j = 0; j < kSpread; ++j) {
+                float gj;
+                if constexpr (kGammaShared<THREADS, ALIGNED>) gj = __uint_as_float(g_raw[j]);
+                else gj = own_g[j];
+                x[j] = __fmul_rn(x[j], rs);
+                own_dg[j] = __fmaf_rn(dy[j], x[j], own_dg[j]);
+                dy[j] = __fmul_rn(dy[j], gj);
+                sum = __fmaf_rn(dy[j], x[j], sum);
+            }
+            if (ds0 != nullptr)
+                own.load(stage + r.dy_span + r.x_span, static_cast<uint32_t>(start_of(ds0, row, a.ldds) & 15));
+            const float total = team_sum<false>(sum, buf[flip]);
+            if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
+                issue(row + static_cast<int64_t>(r.stages) * gridDim.x, s);
+            const float nm = __fmul_rn(total, ninv_n);
+#pragma unroll
+            for (int j = 0; j < kSpread; ++j)
+                dy[j] = __fmaf_rn(__fmaf_rn(x[j], nm, dy[j]), rs, ds0 != nullptr ? value_of<T>(own.raw[j]) : 0.0f);
+            store_spread(static_cast<T *>(a.dx) + row * a.lddx + own.c, own.left, own.full, dy);
+        } else {
         uint64_t dy[8], x[8], sum = 0;
         own.load(stage, static_cast<uint32_t>(start_of(dy0, row, a.lddy) & 15));
         own.get(dy);
@@ -705,12 +737,6 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
         }
         if (ds0 != nullptr)
             own.load(stage + r.dy_span + r.x_span, static_cast<uint32_t>(start_of(ds0, row, a.ldds) & 15));
-        if constexpr (kGammaShared<THREADS, ALIGNED>) {
-            uint32_t raw[kSpread];
-            load_spread(gamma + own.c, own.left, own.full, raw);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = f32x2_pack(__uint_as_float(raw[2 * i]), __uint_as_float(raw[2 * i + 1]));
-        }
         rms_bwd_accumulate(rs2, g, dy, x, dg, sum);
         const float total = team_sum<false>(sum2(sum), buf[flip]);
         if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
@@ -719,9 +745,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
         if (ds0 != nullptr) own.get(ds);
         rms_bwd_finish(rs2, splat_f32x2(__fmul_rn(total, ninv_n)), x, ds, dy);
         own.store(static_cast<T *>(a.dx) + row * a.lddx, dy);
+        }
         if (++s == r.stages) s = 0, phase ^= 1u;
     }
-    own.store_sums(a.part + static_cast<int64_t>(blockIdx.x) * up8(a.cols), dg);
+    float *part = a.part + static_cast<int64_t>(blockIdx.x) * up8(a.cols);
+    if constexpr (ALIGNED)
+        own.store_sums(part, dg);
+    else
+        store_spread(part + own.c, own.left, own.full, own_dg);
     if (gave_up && threadIdx.x == 0)   // copies still in flight land (bounded) before the CTA exits
         for (int i = 0; i < r.stages; ++i) {
             mbar_wait(bar0 + 8 * s, phase, nullptr, 100000000ull);
