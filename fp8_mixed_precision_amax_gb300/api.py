@@ -891,6 +891,13 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _workspace(room: int, stream, device) -> torch.Tensor:
+    if stream is None:   # without entering a context: 1 us of a short call
+        return torch.empty(room, dtype=_U8, device=device)
+    with _on_stream(stream, device):
+        return torch.empty(room, dtype=_U8, device=device)
+
+
 def fp8_block_quantize(x: torch.Tensor, q: BlockFp8 | None = None, qt: BlockFp8 | None = None,
                        stream=None) -> None:
     """x into ``q`` and / or its transpose into ``qt``, with a power-of-two
@@ -1013,8 +1020,7 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: torch
     _here(dy, x, gamma, rstd, dx, dgamma, dsum, workspace)
     if workspace is None:
         room = _lib.fp8_rmsnorm_bwd_workspace(rows, cols)
-        with _on_stream(stream, dy.device):
-            workspace = torch.empty(room, dtype=torch.uint8, device=dy.device)
+        workspace = _workspace(room, stream, dy.device)
         place = workspace.data_ptr()
     else:
         room = workspace.numel() * workspace.element_size()
@@ -1116,8 +1122,7 @@ def fp8_grad_norm(grads, norm: torch.Tensor, workspace: torch.Tensor | None = No
     _here(*grads, norm, workspace)
     if workspace is None:
         room = _lib.fp8_grad_norm_workspace(len(grads))
-        with _on_stream(stream, norm.device):
-            workspace = torch.empty(room, dtype=torch.uint8, device=norm.device)
+        workspace = _workspace(room, stream, norm.device)
         place = workspace.data_ptr()
     else:
         room = workspace.numel() * workspace.element_size()

@@ -1,9 +1,13 @@
 // block_abi.cu -- the exported C entry points of the block-scaled operators
 // (the second half of include/fp8amax.h): argument checks on the host, then
 // one to three launches in stream order (a product of few rows one for every
-// 8,388,480 columns).  No device memory is allocated and
+// 8,388,480 columns, a list of gradients one for every 1000).  No device memory is allocated and
 // the stream is never synchronized.
 #include "abi_checks.h"
+
+#include <algorithm>
+#include <memory>
+#include <new>
 
 namespace {
 
@@ -115,11 +119,13 @@ fp8_status check_param(const char *fn, const void *p, int32_t type, const char *
     return FP8_OK;
 }
 
-constexpr int64_t kMaxVector = int64_t(1) << 40;   // elements
+constexpr int64_t kMaxVector = int64_t(1) << 40;    // elements
+constexpr int64_t kMaxVectors = int64_t(1) << 44;   // of all together: chunks are counted in 32 bits
 
 fp8_status check_vectors(const char *fn, const fp8_vector *v, int32_t count, const char *name) {
     if (count < 0) return fail(FP8_ERR_ARG, "%s: count %d", fn, count);
     if (v == nullptr && count > 0) return fail(FP8_ERR_ARG, "%s: %s is NULL", fn, name);
+    int64_t all = 0;
     for (int32_t i = 0; i < count; ++i) {
         if (v[i].dtype != FP8_DTYPE_F32 && v[i].dtype != FP8_DTYPE_BF16 && v[i].dtype != FP8_DTYPE_F16)
             return fail(FP8_ERR_ARG, "%s: %s[%d]: bad type %d", fn, name, i, v[i].dtype);
@@ -130,6 +136,42 @@ fp8_status check_vectors(const char *fn, const fp8_vector *v, int32_t count, con
             return fail(FP8_ERR_ARG, "%s: %s[%d] has no data", fn, name, i);
         if (reinterpret_cast<uintptr_t>(v[i].data) % (v[i].dtype == FP8_DTYPE_F32 ? 4 : 2))
             return fail(FP8_ERR_ALIGN, "%s: %s[%d] is not aligned to its elements", fn, name, i);
+        all += v[i].n;
+        if (all > kMaxVectors) return fail(FP8_ERR_ARG, "%s: %s: too many elements together", fn, name);
+    }
+    return FP8_OK;
+}
+
+struct Span {
+    uintptr_t from, to;
+    int32_t i;
+};
+Span span_of(const fp8_vector &v, int32_t i) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(v.data);
+    return {from, from + static_cast<uintptr_t>(v.n) * (v.dtype == FP8_DTYPE_F32 ? 4 : 2), i};
+}
+
+// Each of outs apart from the others, and from all grads but its own, whose place it may take.
+fp8_status check_apart(const char *fn, const fp8_vector *grads, const fp8_vector *outs, int32_t count) {
+    Span few[64];
+    std::unique_ptr<Span[]> many(count > 64 ? new (std::nothrow) Span[count] : nullptr);
+    Span *s = count > 64 ? many.get() : few;
+    if (s == nullptr) return fail(FP8_ERR_ARG, "%s: no host memory for %d vectors", fn, count);
+    int32_t n = 0;
+    for (int32_t i = 0; i < count; ++i)
+        if (outs[i].n > 0) s[n++] = span_of(outs[i], i);
+    std::sort(s, s + n, [](const Span &a, const Span &b) { return a.from < b.from; });
+    for (int32_t k = 1; k < n; ++k)
+        if (s[k].from < s[k - 1].to)
+            return fail(FP8_ERR_ARG, "%s: outs[%d] and outs[%d] overlap", fn, s[k - 1].i, s[k].i);
+    if (outs == grads) return FP8_OK;
+    for (int32_t j = 0; j < count; ++j) {
+        if (grads[j].n == 0) continue;
+        const Span g = span_of(grads[j], j);
+        const Span *at = std::upper_bound(s, s + n, g.from, [](uintptr_t v, const Span &x) { return v < x.to; });
+        for (; at < s + n && at->from < g.to; ++at)
+            if (at->i != j || at->from != g.from || outs[j].dtype != grads[j].dtype)
+                return fail(FP8_ERR_ARG, "%s: outs[%d] and grads[%d] overlap", fn, at->i, j);
     }
     return FP8_OK;
 }
@@ -546,7 +588,9 @@ fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, vo
                     static_cast<long long>(workspace_bytes), static_cast<long long>(need));
     int sms;
     FP8_TRY(current_device(&sms));
-    FP8_CUDA(fp8k::launch_grad_norm(reinterpret_cast<const fp8k::VectorView *>(grads), count, norm, workspace, sms, static_cast<cudaStream_t>(stream)), fn);
+    FP8_CUDA(fp8k::launch_grad_norm(reinterpret_cast<const fp8k::VectorView *>(grads), count, norm,
+                                    workspace, sms, static_cast<cudaStream_t>(stream)),
+             fn);
     return FP8_OK;
 }
 
@@ -563,6 +607,7 @@ fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_
                         static_cast<long long>(outs[i].n), i, static_cast<long long>(grads[i].n));
     FP8_TRY(check_scalar(fn, norm, "norm", false));
     if (!(max_norm >= 0.0f)) return fail(FP8_ERR_ARG, "%s: max_norm must be >= 0", fn);
+    FP8_TRY(check_apart(fn, grads, outs, count));
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_grad_clip(reinterpret_cast<const fp8k::VectorView *>(grads),

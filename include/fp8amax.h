@@ -649,7 +649,7 @@ fp8_status fp8_block_gemm_swiglu_bwd(const fp8_block_tensor *A, const fp8_block_
  * The norm of many gradients together, and clipping by it */
 
 /* n consecutive elements of type dtype (fp8_dtype), DEVICE, aligned to the element
- * (16-byte aligned ones are faster); n >= 0. */
+ * (16-byte aligned ones are faster); 0 <= n <= 2^40, and 2^44 in a list. */
 typedef struct {
     void *data;
     int64_t n;
@@ -675,8 +675,9 @@ int64_t fp8_grad_norm_workspace(int32_t count);
  * so that gradients whose norm is not finite pass through as they are (the caller
  * sees it by the norm, and skips the step).  outs (NULL: grads, in place): HOST
  * array of count vectors of the grads' lengths; outs[i] may be grads[i] (same
- * address and type), and overlaps nothing else.  max_norm >= 0.  One kernel for
- * each 1000 vectors. */
+ * address and type), and overlaps no other vector (FP8_ERR_ARG where it does: a
+ * gradient is twice in the list).  max_norm >= 0.  One kernel for each 1000
+ * vectors. */
 fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_t count,
                          const float *norm, float max_norm, void *stream);
 

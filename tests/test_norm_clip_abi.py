@@ -122,3 +122,32 @@ def test_vector_struct_matches_the_header():
     src = open(api.HEADER_PATH).read()
     body = re.search(r"typedef struct \{([^}]*)\} fp8_vector;", src).group(1)
     assert re.findall(r"(\w+);", body) == [n for n, _ in api.fp8_vector._fields_]
+
+
+def test_what_is_written_overlaps_nothing():
+    def clip(grads, outs=None):
+        a = lambda x: None if x is None else (api.fp8_vector * len(x))(*x)
+        return a(grads), a(outs), len(grads), P, 1.0
+
+    at = lambda place, n=8, dtype=0: vec(n, P + place, dtype)
+    refused(ERR_ARG, "outs[0] and outs[1] overlap", "fp8_grad_clip", *clip([at(0), at(0)]))
+    refused(ERR_ARG, "outs[1] and outs[0] overlap", "fp8_grad_clip", *clip([at(64), at(36)]))
+    refused(ERR_ARG, "outs[0] and outs[2] overlap", "fp8_grad_clip",
+            *clip([at(0), at(64), at(128)], [at(256), at(512), at(284)]))
+    # of another type, of another start, and another one's
+    refused(ERR_ARG, "outs[0] and grads[0] overlap", "fp8_grad_clip", *clip([at(0)], [at(0, dtype=1)]))
+    refused(ERR_ARG, "outs[0] and grads[0] overlap", "fp8_grad_clip", *clip([at(0)], [at(28)]))
+    refused(ERR_ARG, "outs[1] and grads[0] overlap", "fp8_grad_clip",
+            *clip([at(0), at(64)], [at(128), at(0)]))
+    # a long list, where one of 300 covers many
+    apart = [at(64 * i) for i in range(300)]
+    refused(ERR_ARG, "outs[7] and outs[8] overlap", "fp8_grad_clip",
+            *clip(apart[:7] + [at(64 * 7, 2000)] + apart[8:]))
+    outs = [at(64 * i + 32) for i in range(300)]
+    refused(ERR_ARG, "outs[7] and grads[8] overlap", "fp8_grad_clip",
+            *clip(apart, outs[:7] + [at(64 * 7 + 40)] + outs[8:]))
+
+
+def test_long_lists_have_a_limit():
+    many = (api.fp8_vector * 17)(*[vec(1 << 40)] * 17)
+    refused(ERR_ARG, "too many elements", "fp8_grad_norm", many, 17, P, P, 1 << 20)
