@@ -33,9 +33,10 @@ inline int64_t ring_ctas_per_sm(unsigned threads) {
 // per SM and slab of a wide row.  It only grows with sms, up to those of kBwdSms SMs, for
 // which the workspace is sized without asking a device.
 constexpr int64_t kBwdSms = 152;
-inline int64_t bwd_ctas(int64_t rows, int64_t cols, int64_t sms) {
+inline int64_t bwd_ctas(int64_t rows, int64_t cols, int64_t sms, int64_t narrow = kBwdNarrow,
+                        int narrow_ctas = 2) {
     if (sms > kBwdSms) sms = kBwdSms;
-    if (cols <= kBwdNarrow) return capped((rows + kWarps - 1) / kWarps, 2 * sms);
+    if (cols <= narrow) return capped((rows + kWarps - 1) / kWarps, narrow_ctas * sms);
     if (cols > kBwdWide) return capped(rows, sms);
     // eight rows each once there is a CTA per SM: every CTA's sums are written, read and
     // added (2048 x 1024: 18.7 us with 1216 CTAs)

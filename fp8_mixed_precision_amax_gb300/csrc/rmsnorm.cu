@@ -166,6 +166,9 @@ __device__ __forceinline__ void rms_finish(const RmsFwdArgs &a, T *yr, const Row
 
 // A team works on R rows side by side, one step apart: their sums share the exchanges and
 // the barrier.  The rows after those in work are already being loaded, into registers.
+// 8192 x 4096 bf16 with the sum and both in 8 bits 45.2 us = 5.95 TB/s, 0.88 of a copy's rate;
+// half of the issue slots are busy, and 16 warps an SM (118 registers) do not hide the way from a
+// row's sum to its codes any better.  One row of 4096 2.3 us.
 template <typename T, int VPT, bool WARP, int VEC, bool RES>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_kernel(const RmsFwdArgs a) {
     using L = Lay<T, VEC>;
@@ -267,7 +270,8 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_kernel(const
     }
 }
 
-// Rows that start anywhere, up to 8192 columns.
+// Rows that start anywhere, up to 8192 columns: 3001 x 2731 fp32 with the sum 23.0 us = 5.7 TB/s
+// (in 16-byte blocks shifted into place 39.2).
 template <typename T, bool WARP, bool RES>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_spread_kernel(const RmsFwdArgs a) {
     __shared__ __align__(16) uint64_t buf[2][16];
@@ -433,7 +437,7 @@ __device__ __forceinline__ void rms_bwd_finish(uint64_t rs2, uint64_t nm2, const
     for (int i = 0; i < P; ++i) dy[i] = f32x2_fma(f32x2_fma(x[i], nm2, dy[i]), rs2, ds[i]);
 }
 
-// Wide rows: the row sum, in a pass of its own.
+// Longer rows, and unaligned ones past 8192 columns: the row sum, in a pass of its own.
 template <typename T, bool SAVED>
 __global__ void __launch_bounds__(512) rms_bwd_sums_kernel(const RmsBwdArgs a) {
     __shared__ __align__(16) uint64_t buf[2][16];
@@ -474,11 +478,13 @@ __device__ __forceinline__ void rms_store_part(const RmsBwdArgs &a, Col col, con
     }
 }
 
-// Rows of 513 .. 8192 columns, one at a time per CTA; a thread has 16 columns, and their sums
+// Rows of 257 .. 8192 columns, one at a time per CTA; a thread has 16 columns, and their sums
 // over the CTA's rows.  The next rows of dy, x and dsum are on their way into a ring in
 // shared memory by bulk copies of the 16-byte blocks that hold them, whatever their alignment;
 // the barrier of a row's sum also tells that its place in the ring may be filled again (what a
-// thread needs of dsum is in its registers by then).
+// thread needs of dsum is in its registers by then).  8192 x 8192 bf16 with dsum 80.7 us = 6.66
+// TB/s, 0.98 of a copy's rate; 5003 x 4111 from 8 bits with dsum 38.7 us, bound by its 36
+// instructions an element (57 % of the issue slots).
 constexpr int kRmsRing = 8;   // most rows in flight
 
 struct RmsRingArgs {
@@ -760,11 +766,148 @@ __global__ void __launch_bounds__(THREADS, CTAS) rms_bwd_ring_kernel(const RmsRi
         }
 }
 
+// Aligned rows of 8193 .. 16384 columns: as above, but a thread has 32 columns, whose sums and
+// gamma fill its registers, so that it takes dy and x from the ring twice, for the row's sum and
+// for dx, and the row's place is free at its end alone.  (4096 x 12288
+// bf16 with dsum 56.8 us, in two passes over HBM 117.2; fp32, with a place for one row alone, 137
+// and 190.)
+template <typename T, bool SAVED>
+__global__ void __launch_bounds__(512, 1) rms_bwd_long_kernel(const RmsRingArgs r) {
+    constexpr int N = 4;   // times 8 columns
+    const RmsBwdArgs &a = r.a;
+    extern __shared__ __align__(128) uint8_t ring_raw[];
+    __shared__ __align__(16) uint64_t buf[2][16];
+    __shared__ uint64_t bars[kRmsRing];
+    __shared__ int gave_up;
+    const uint32_t bar0 = smem_u32(bars);
+    auto issue = [&](int64_t row, int s) {
+        const uint32_t bar = bar0 + 8 * s, to = smem_u32(ring_raw) + s * (r.dy_span + r.x_span + r.ds_span);
+        const uint32_t n = static_cast<uint32_t>(a.cols * sizeof(T));
+        const uint32_t xn = SAVED ? static_cast<uint32_t>(a.cols + 15) & ~15u : n;
+        mbar_arrive_expect_tx(bar, n + xn + (a.dsum != nullptr ? n : 0));
+        bulk_load_1d(to, static_cast<const T *>(a.dy) + row * a.lddy, n, bar);
+        if constexpr (SAVED)
+            bulk_load_1d(to + r.dy_span, a.x8.codes + row * a.x8.ld, xn, bar);
+        else
+            bulk_load_1d(to + r.dy_span, static_cast<const T *>(a.x) + row * a.ldx, xn, bar);
+        if (a.dsum != nullptr)
+            bulk_load_1d(to + r.dy_span + r.x_span, static_cast<const T *>(a.dsum) + row * a.ldds, n, bar);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < r.stages; ++s) mbar_init(bar0 + 8 * s, 1);
+        gave_up = 0;
+        fence_mbar_init();
+    }
+    clear_sums(buf);
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0)
+        for (int s = 0; s < r.stages; ++s)
+            if (blockIdx.x + static_cast<int64_t>(s) * gridDim.x < a.rows)
+                issue(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+    const float ninv_n = -__fdiv_rn(1.0f, static_cast<float>(a.cols));
+    const int cols = static_cast<int>(a.cols);
+    auto col = [&](int k) { return 8 * static_cast<int>(threadIdx.x + k * blockDim.x); };
+    uint64_t dg[N][4] = {}, g[N][4];
+#pragma unroll
+    for (int k = 0; k < N; ++k) load_param(a.gamma, a.wtype, col(k), cols, g[k]);
+    // what does not go through the ring is fetched a row ahead
+    float rs_next = 0.0f;
+    uint32_t scale[SAVED ? N : 1];
+    auto fetch = [&](int64_t row) {
+        rs_next = a.rstd[row];
+        if constexpr (SAVED) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) scale[k] = col(k) < cols ? fetch_scale(a.x8, row, col(k) >> 7) : 0u;
+        }
+    };
+    if (blockIdx.x < a.rows) fetch(blockIdx.x);
+    int s = 0, flip = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
+        const uint64_t rs2 = splat_f32x2(rs_next);
+        float sc[SAVED ? N : 1];
+        if constexpr (SAVED) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) sc[k] = fetched_scale(a.x8, scale[k]);
+        }
+        if (row + gridDim.x < a.rows) fetch(row + gridDim.x);
+        if (!mbar_wait(bar0 + 8 * s, phase, &gave_up)) {
+            // goes on with what is there, so that every thread still meets every barrier
+            atomicOr(&g_rms_error_flags, kErrWaitTimeout);
+            *static_cast<volatile int *>(&gave_up) = 1;
+        }
+        const uint8_t *stage = ring_raw + s * (r.dy_span + r.x_span + r.ds_span);
+        auto take = [&](const uint8_t *place, int k, uint64_t (&v)[4]) {
+            RawVec<T, 8> raw;
+            raw.load(reinterpret_cast<const T *>(place), col(k), cols);
+            raw.get(nullptr, 0, 0, v);
+        };
+        auto take_x = [&](int k, uint64_t (&v)[4]) {
+            if constexpr (SAVED) {
+                uint2 w = make_uint2(0, 0);
+                if (col(k) < cols) w = *reinterpret_cast<const uint2 *>(stage + r.dy_span + col(k));
+                codes8_times(w, a.x8.fmt, sc[k], 8, v);
+            } else {
+                take(stage + r.dy_span, k, v);
+            }
+        };
+        uint64_t sum = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            uint64_t dy[4], x[4];
+            take(stage, k, dy);
+            take_x(k, x);
+            rms_bwd_accumulate(rs2, g[k], dy, x, dg[k], sum);
+        }
+        const float total = team_sum<false>(sum2(sum), buf[flip]);
+        const uint64_t nm2 = splat_f32x2(__fmul_rn(total, ninv_n));
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            uint64_t dy[4], x[4], ds[4] = {};
+            take(stage, k, dy);
+            take_x(k, x);
+            if (a.dsum != nullptr) take(stage + r.dy_span + r.x_span, k, ds);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f32x2_mul(x[i], rs2), dy[i] = f32x2_mul(dy[i], g[k][i]);
+            rms_bwd_finish(rs2, nm2, x, ds, dy);
+            RawVec<T, 8>::store(static_cast<T *>(a.dx) + row * a.lddx, col(k), cols, dy);
+        }
+        __syncthreads();   // the place has been read
+        if (threadIdx.x == 0 && row + static_cast<int64_t>(r.stages) * gridDim.x < a.rows && !gave_up)
+            issue(row + static_cast<int64_t>(r.stages) * gridDim.x, s);
+        if (++s == r.stages) s = 0, phase ^= 1u;
+    }
+    float *part = a.part + static_cast<int64_t>(blockIdx.x) * up8(a.cols);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (col(k) < cols) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<ulonglong2 *>(part + col(k) + 4 * i) = make_ulonglong2(dg[k][2 * i], dg[k][2 * i + 1]);
+        }
+    if (gave_up && threadIdx.x == 0)   // copies still in flight land (bounded) before the CTA exits
+        for (int i = 0; i < r.stages; ++i) {
+            mbar_wait(bar0 + 8 * s, phase, nullptr, 100000000ull);
+            if (++s == r.stages) s = 0, phase ^= 1u;
+        }
+}
+
+// Rows of one warp: up to 256 columns, 8 per thread, which leaves registers for three CTAs an SM
+// in 16 bits (65536 x 256 24.0 us; 16 columns per thread and two CTAs 45.4, the ring kernel
+// 33.6).  Up to 512 columns the ring kernel, with CTAs of one warp, is ahead of 16 columns per
+// thread here (65536 x 512 41.3 and 53.6 us).
+constexpr int64_t kRmsNarrow = 256;
+constexpr int kNarrowMost = 3;
+template <typename T, int VEC>
+constexpr int kNarrowCtas = sizeof(T) == 2 && VEC != 0 ? kNarrowMost : 2;   // more would spill
+
 // Narrow rows (WARP) and wide ones.  Rows in turn; a thread keeps its columns and their sums
 // over the CTA's rows.  WIDE: blockIdx.y, and blockIdx.z where there are more than 65535, is a
 // slab of 8 VPT blockDim.x columns, and the rows' sums are already there.
 template <typename T, bool SAVED, int VPT, bool WARP, int VEC>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_bwd_kernel(const RmsBwdArgs a) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512, WARP ? kNarrowCtas<T, VEC> : 1)
+    rms_bwd_kernel(const RmsBwdArgs a) {
     using L = Lay<T, VEC>;
     constexpr int E = L::E, P = L::P;
     constexpr bool WIDE = !WARP;
@@ -914,20 +1057,26 @@ cudaError_t rms_fwd_typed(const RmsFwdArgs &a, bool vec, int sms, cudaStream_t s
     return launch_pdl(rms_fwd_wide_kernel<T, RES>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
 }
 
+constexpr int64_t kRingBytes = 200 << 10;   // of an SM's shared memory
+template <typename T, bool SAVED>
+RmsRingArgs ring_args(const RmsBwdArgs &a) {
+    RmsRingArgs r{a, 0, 0, 0, 0, 0};
+    r.dy_span = static_cast<uint32_t>((a.cols * sizeof(T) + 15 + 127) / 128 * 128 + 128);
+    r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
+    r.ds_span = a.dsum != nullptr ? r.dy_span : 0;
+    return r;
+}
+
 // As many rows in flight as the CTAs of an SM have shared memory for.
 template <typename T, bool SAVED, int THREADS, int CTAS, bool ALIGNED>
 cudaError_t rms_bwd_ring_sized(const RmsBwdArgs &a, int grid, unsigned threads, cudaStream_t st) {
-    constexpr int64_t kSize = sizeof(T), kBytes = 200 << 10;
-    RmsRingArgs r{a, 0, 0, 0, 0, 0};
-    r.dy_span = static_cast<uint32_t>((a.cols * kSize + 15 + 127) / 128 * 128 + 128);
-    r.x_span = SAVED ? static_cast<uint32_t>((a.cols + 127) / 128 * 128) : r.dy_span;
-    r.ds_span = a.dsum != nullptr ? r.dy_span : 0;
+    RmsRingArgs r = ring_args<T, SAVED>(a);
     const int64_t place = r.dy_span + r.x_span + r.ds_span;
     if (kGammaShared<THREADS, ALIGNED>) r.gamma_span = static_cast<uint32_t>((a.cols * 4 + 127) / 128 * 128);
-    const int64_t fit = (kBytes / ring_ctas_per_sm(threads) - r.gamma_span) / place;
+    const int64_t fit = (kRingBytes / ring_ctas_per_sm(threads) - r.gamma_span) / place;
     r.stages = static_cast<int>(fit < kRmsRing ? fit : kRmsRing);
     static SmemLimit limit;
-    const cudaError_t err = limit.allow(rms_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, kBytes);
+    const cudaError_t err = limit.allow(rms_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, kRingBytes);
     if (err != cudaSuccess) return err;
     return launch_pdl(rms_bwd_ring_kernel<T, SAVED, THREADS, CTAS, ALIGNED>, dim3(grid), dim3(threads),
                       static_cast<size_t>(r.gamma_span + r.stages * place), st, r);
@@ -941,23 +1090,38 @@ cudaError_t rms_bwd_ring(const RmsBwdArgs &a, int grid, cudaStream_t st) {
     return rms_bwd_ring_sized<T, SAVED, 256, 2, ALIGNED>(a, grid, threads, st);
 }
 
+constexpr int64_t kRmsLong = 16384;   // columns of 512 threads, 32 each
+static_assert(3 * (kRmsLong * 4 + 15 + 127 + 128) <= kRingBytes, "a place for a row of any type");
+template <typename T, bool SAVED>
+cudaError_t rms_bwd_long(const RmsBwdArgs &a, int grid, cudaStream_t st) {
+    RmsRingArgs r = ring_args<T, SAVED>(a);
+    const int64_t fit = kRingBytes / (r.dy_span + r.x_span + r.ds_span);
+    r.stages = static_cast<int>(fit < kRmsRing ? fit : kRmsRing);
+    static SmemLimit limit;
+    const cudaError_t err = limit.allow(rms_bwd_long_kernel<T, SAVED>, kRingBytes);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(rms_bwd_long_kernel<T, SAVED>, dim3(grid), dim3(row_threads(a.cols, 32)),
+                      static_cast<size_t>(r.stages * (r.dy_span + r.x_span + r.ds_span)), st, r);
+}
+
 template <typename T, bool SAVED, int VEC>
 cudaError_t rms_bwd_typed(RmsBwdArgs a, float *dgamma, void *ws, int sms, cudaStream_t st) {
-    constexpr int VPT = 2;   // 16 columns per thread
-    const int g = static_cast<int>(bwd_ctas(a.rows, a.cols, sms));
+    const int g = static_cast<int>(bwd_ctas(a.rows, a.cols, sms, kRmsNarrow, kNarrowCtas<T, VEC>));
     a.part = static_cast<float *>(ws);
     cudaError_t e;
-    if (a.cols <= kBwdNarrow) {
-        e = launch_pdl(rms_bwd_kernel<T, SAVED, VPT, true, VEC>, dim3(g), dim3(32 * kWarps), 0, st, a);
+    if (a.cols <= kRmsNarrow) {
+        e = launch_pdl(rms_bwd_kernel<T, SAVED, 1, true, VEC>, dim3(g), dim3(32 * kWarps), 0, st, a);
     } else if (a.cols <= kBwdWide) {
         e = rms_bwd_ring<T, SAVED, VEC != 0>(a, g, st);
+    } else if (VEC != 0 && a.cols <= kRmsLong) {
+        e = rms_bwd_long<T, SAVED>(a, g, st);
     } else {
         a.row_sums = a.part + static_cast<int64_t>(g) * up8(a.cols);
         e = launch_pdl(rms_bwd_sums_kernel<T, SAVED>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
         if (e != cudaSuccess) return e;
         const unsigned slabs = static_cast<unsigned>((a.cols + kBwdSlab - 1) / kBwdSlab);
         const unsigned z = (slabs + 65534) / 65535;
-        e = launch_pdl(rms_bwd_kernel<T, SAVED, VPT, false, VEC>, dim3(g, (slabs + z - 1) / z, z), dim3(256),
+        e = launch_pdl(rms_bwd_kernel<T, SAVED, 2, false, VEC>, dim3(g, (slabs + z - 1) / z, z), dim3(256),
                        0, st, a);
     }
     if (e != cudaSuccess) return e;
@@ -986,7 +1150,7 @@ cudaError_t launch_rms_fwd(const MatView &x, const MatView &residual, const void
 }
 
 int64_t rms_bwd_workspace(int64_t rows, int64_t cols) {
-    return bwd_ctas_most(rows, cols) * up8(cols) * 4 + (cols > kBwdWide ? rows * 4 : 0);
+    return bwd_ctas(rows, cols, kBwdSms, kRmsNarrow, kNarrowMost) * up8(cols) * 4 + (cols > kBwdWide ? rows * 4 : 0);
 }
 
 cudaError_t launch_rms_bwd(const MatView &dy, const MatView &x, const BlockView &x8, const void *gamma,

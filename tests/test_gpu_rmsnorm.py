@@ -186,6 +186,17 @@ def test_backward(rows, cols, dtype, wtype, saved):
         near(dgamma, dg, tol_dg, "dgamma")
 
 
+@pytest.mark.parametrize("rows,cols", [(5000, 256), (5000, 251), (9000, 384), (6001, 511), (20000, 264),
+                                       (1000, 8200), (700, 12288), (500, 16384), (160, 16392)])
+@pytest.mark.parametrize("dtype,wtype,saved", [(torch.float32, torch.bfloat16, False),
+                                               (torch.bfloat16, torch.float32, False),
+                                               (torch.bfloat16, torch.bfloat16, True),
+                                               (torch.float32, torch.float32, True)])
+def test_backward_of_several_rows_each(rows, cols, dtype, wtype, saved):
+    """More rows than a CTA or a warp has places for, at the widths where the kernels change."""
+    test_backward(rows, cols, dtype, wtype, saved)
+
+
 @pytest.mark.parametrize("rows,cols", [(50, 77), (300, 1024), (170, 4103), (40, 12288)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_backward_in_place_and_repeated(rows, cols, dtype):
