@@ -137,7 +137,7 @@ struct RecomputeSmem {
 // The forward's formula on the codes, so the same roundings.  8192 x 4096: 21.5 us, bound
 // by instructions; reading and writing alone is 10.  (With scalar arithmetic, a bound on
 // every element and the rows' statistics fetched when needed: 32.)
-// RMS: the RMS norm's output, without mean and beta.
+// RMS: the RMS norm's output, without mean and beta (21.1 us).
 template <int FMT, bool RMS>
 __global__ void __launch_bounds__(kTileThreads, 2)
     norm_recompute_kernel(const BlockView x8, const void *__restrict__ gamma,

@@ -4,8 +4,9 @@
 //   out  = round(g * c),  c = max_norm / norm where max_norm < norm < inf, else 1
 //
 // Both are bound by HBM: 1.08 G BF16 values take 323 us (6.69 TB/s, 0.99 of a copy's rate) and,
-// to BF16, 680 us (6.37 TB/s, 0.94): the second reading cannot come from L2.  A launch takes up to kManyVectors tensors, described in its
-// arguments, and cuts them into chunks of kChunk elements that its CTAs take in turn.
+// to BF16, 680 us (6.37 TB/s, 0.94); the second reading comes from L2 only as far as that
+// reaches.  A launch takes up to kManyVectors tensors, described in its arguments, and cuts
+// them into chunks of kChunk elements that its CTAs take in turn.
 //
 // Squares are summed in 32 bits over a thread's 32 elements of a chunk, and those sums
 // with the rounding error of each addition beside them (Knuth's two-sum), so that a sum
