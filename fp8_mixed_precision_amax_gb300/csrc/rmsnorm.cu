@@ -29,6 +29,11 @@ __device__ unsigned g_rms_error_flags = 0;
 // warp instruction along 32 of them, instead of 16-byte blocks shifted into place.  A thread
 // has kSpread columns 32 apart, a warp 512 in a row, four whole blocks of 128.
 constexpr int kSpread = 16;
+// Forward, CTAs of up to 320 threads (5120 columns) have 96 registers, so that two of them fit an
+// SM, and larger ones 128: 8000 x 4099 bf16 with the sum 62.1 us, and 91.4 with 128 throughout; in
+// 8 bits with the sum kept 89.1 and 134.3.  (Aligned rows, which take 118 registers: from 4097
+// columns on, 8192 x 4608 in 8 bits 57.9 us, and 71.9.)
+constexpr int kFwdHalf = 320;
 
 template <typename T>
 __device__ __forceinline__ uint32_t raw_of(const T *p) {
@@ -166,11 +171,11 @@ __device__ __forceinline__ void rms_finish(const RmsFwdArgs &a, T *yr, const Row
 
 // A team works on R rows side by side, one step apart: their sums share the exchanges and
 // the barrier.  The rows after those in work are already being loaded, into registers.
-// 8192 x 4096 bf16 with the sum and both in 8 bits 45.2 us = 5.95 TB/s, 0.88 of a copy's rate;
+// 8192 x 4096 bf16 with the sum and both in 8 bits 44.8 us = 6.0 TB/s, 0.89 of a copy's rate;
 // half of the issue slots are busy, and 16 warps an SM (118 registers) do not hide the way from a
 // row's sum to its codes any better.  One row of 4096 2.3 us.
-template <typename T, int VPT, bool WARP, int VEC, bool RES>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_kernel(const RmsFwdArgs a) {
+template <typename T, int VPT, int THREADS, bool WARP, int VEC, bool RES>
+__global__ void __launch_bounds__(THREADS, WARP || THREADS > kFwdHalf ? 1 : 2) rms_fwd_kernel(const RmsFwdArgs a) {
     using L = Lay<T, VEC>;
     constexpr int E = L::E, P = L::P, R = VEC && VPT * P <= 8 ? 2 : 1;
     __shared__ __align__(16) uint64_t buf[2][16];
@@ -270,10 +275,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_kernel(const
     }
 }
 
-// Rows that start anywhere, up to 8192 columns: 3001 x 2731 fp32 with the sum 23.0 us = 5.7 TB/s
+// Rows that start anywhere, up to 8192 columns: 3001 x 2731 fp32 with the sum 22.5 us = 5.8 TB/s
 // (in 16-byte blocks shifted into place 39.2).
-template <typename T, bool WARP, bool RES>
-__global__ void __launch_bounds__(WARP ? 32 * kWarps : 512) rms_fwd_spread_kernel(const RmsFwdArgs a) {
+template <typename T, int THREADS, bool WARP, bool RES>
+__global__ void __launch_bounds__(THREADS, THREADS == kFwdHalf ? 2 : 1) rms_fwd_spread_kernel(const RmsFwdArgs a) {
     __shared__ __align__(16) uint64_t buf[2][16];
     const Team<WARP> team;
     clear_sums(buf);
@@ -1025,34 +1030,42 @@ __global__ void __launch_bounds__(1024) rms_bwd_reduce_kernel(const float *__res
 
 // --------------------------------------------------------------------- host --
 
-template <typename T, int VPT, bool WARP, int VEC, bool RES>
-cudaError_t rms_fwd_rows(const RmsFwdArgs &a, int sms, cudaStream_t st) {
-    const unsigned threads = WARP ? 32 * kWarps : row_threads(a.cols, VPT * Lay<T, VEC>::E);
-    // CTAs that the registers allow at once
-    const int64_t resident = static_cast<int64_t>(sms) * (threads < 640 ? 640 / threads : 1);
-    const unsigned grid = capped(WARP ? (a.rows + kWarps - 1) / kWarps : a.rows, resident);
-    return launch_pdl(rms_fwd_kernel<T, VPT, WARP, VEC, RES>, dim3(grid), dim3(threads), 0, st, a);
+// CTAs that the registers allow at once: 96 of them per thread, or 128
+template <int THREADS>
+int64_t fwd_ctas_per_sm(unsigned threads) {
+    return (THREADS == kFwdHalf ? 2 * kFwdHalf : 512) / threads;
 }
 
-template <typename T, bool WARP, bool RES>
+template <typename T, int VPT, int THREADS, bool WARP, int VEC, bool RES>
+cudaError_t rms_fwd_rows(const RmsFwdArgs &a, int sms, cudaStream_t st) {
+    const unsigned threads = WARP ? 32 * kWarps : row_threads(a.cols, VPT * Lay<T, VEC>::E);
+    const int64_t resident = static_cast<int64_t>(sms) * fwd_ctas_per_sm<THREADS>(threads);
+    const unsigned grid = capped(WARP ? (a.rows + kWarps - 1) / kWarps : a.rows, resident);
+    return launch_pdl(rms_fwd_kernel<T, VPT, THREADS, WARP, VEC, RES>, dim3(grid), dim3(threads), 0, st, a);
+}
+
+template <typename T, int THREADS, bool WARP, bool RES>
 cudaError_t rms_fwd_spread(const RmsFwdArgs &a, int sms, cudaStream_t st) {
     const unsigned threads = WARP ? 32 * kWarps : row_threads(a.cols, kSpread);
-    // CTAs that the registers allow at once
-    const int64_t resident = static_cast<int64_t>(sms) * (threads < 640 ? 640 / threads : 1);
+    const int64_t resident = static_cast<int64_t>(sms) * fwd_ctas_per_sm<THREADS>(threads);
     const unsigned grid = capped(WARP ? (a.rows + kWarps - 1) / kWarps : a.rows, resident);
-    return launch_pdl(rms_fwd_spread_kernel<T, WARP, RES>, dim3(grid), dim3(threads), 0, st, a);
+    return launch_pdl(rms_fwd_spread_kernel<T, THREADS, WARP, RES>, dim3(grid), dim3(threads), 0, st, a);
 }
 
 template <typename T, bool RES>
 cudaError_t rms_fwd_typed(const RmsFwdArgs &a, bool vec, int sms, cudaStream_t st) {
     if (vec) {
-        if (a.cols <= 512) return rms_fwd_rows<T, 1, true, 16, RES>(a, sms, st);
-        if (a.cols <= 8192) return rms_fwd_rows<T, 1, false, 16, RES>(a, sms, st);
-        if (a.cols <= 16384) return rms_fwd_rows<T, 2, false, 16, RES>(a, sms, st);
+        if (a.cols <= 512) return rms_fwd_rows<T, 1, 32 * kWarps, true, 16, RES>(a, sms, st);
+        if (a.cols <= 4096) return rms_fwd_rows<T, 1, 256, false, 16, RES>(a, sms, st);
+        if constexpr (sizeof(T) == 2)   // fp32 spills: 8192 x 4608 124.9 us, and 109.9 in one CTA
+            if (a.cols <= 16 * kFwdHalf) return rms_fwd_rows<T, 1, kFwdHalf, false, 16, RES>(a, sms, st);
+        if (a.cols <= 8192) return rms_fwd_rows<T, 1, 512, false, 16, RES>(a, sms, st);
+        if (a.cols <= 16384) return rms_fwd_rows<T, 2, 512, false, 16, RES>(a, sms, st);
     } else {
-        if (a.cols <= 512) return rms_fwd_spread<T, true, RES>(a, sms, st);
-        if (a.cols <= 8192) return rms_fwd_spread<T, false, RES>(a, sms, st);
-        if (a.cols <= 16384) return rms_fwd_rows<T, 4, false, 0, RES>(a, sms, st);
+        if (a.cols <= 512) return rms_fwd_spread<T, 32 * kWarps, true, RES>(a, sms, st);
+        if (a.cols <= kSpread * kFwdHalf) return rms_fwd_spread<T, kFwdHalf, false, RES>(a, sms, st);
+        if (a.cols <= 8192) return rms_fwd_spread<T, 512, false, RES>(a, sms, st);
+        if (a.cols <= 16384) return rms_fwd_rows<T, 4, 512, false, 0, RES>(a, sms, st);
     }
     return launch_pdl(rms_fwd_wide_kernel<T, RES>, dim3(capped(a.rows, 4 * sms)), dim3(512), 0, st, a);
 }
