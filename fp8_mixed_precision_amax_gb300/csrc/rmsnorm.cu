@@ -174,8 +174,11 @@ __device__ __forceinline__ void rms_finish(const RmsFwdArgs &a, T *yr, const Row
 // 8192 x 4096 bf16 with the sum and both in 8 bits 44.8 us = 6.0 TB/s, 0.89 of a copy's rate;
 // half of the issue slots are busy, and 16 warps an SM (118 registers) do not hide the way from a
 // row's sum to its codes any better.  One row of 4096 2.3 us.
+// (A warp's rows in fp32 have more registers and one CTA an SM: with two they spill, 16384 x 512
+// 28.3 us and 24.6; in 16 bits 12.7 with two and 15.6.)
 template <typename T, int VPT, int THREADS, bool WARP, int VEC, bool RES>
-__global__ void __launch_bounds__(THREADS, WARP || THREADS > kFwdHalf ? 1 : 2) rms_fwd_kernel(const RmsFwdArgs a) {
+__global__ void __launch_bounds__(THREADS, (WARP && sizeof(T) == 4) || THREADS > kFwdHalf ? 1 : 2)
+    rms_fwd_kernel(const RmsFwdArgs a) {
     using L = Lay<T, VEC>;
     constexpr int E = L::E, P = L::P, R = VEC && VPT * P <= 8 ? 2 : 1;
     __shared__ __align__(16) uint64_t buf[2][16];
