@@ -38,6 +38,7 @@
 #include <cstdint>
 
 #include "block_mma.cuh"
+#include "error_flag.h"
 #include "raster.cuh"
 
 namespace fp8k {
@@ -1306,10 +1307,7 @@ cudaError_t launch_gated_bwd(const BlockView &A, const BlockView &B, const Block
 }
 
 cudaError_t read_and_clear_gated_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_gated_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_gated_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_gated_error_flags, flags);
 }
 
 }  // namespace fp8k

@@ -17,6 +17,7 @@
 #include <cstdint>
 
 #include "block_mma.cuh"
+#include "error_flag.h"
 #include "raster.cuh"
 
 namespace fp8k {
@@ -1259,10 +1260,7 @@ cudaError_t launch_block_gemm(const BlockView &A, const BlockView &B, const MatV
 }
 
 cudaError_t read_and_clear_block_gemm_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_block_gemm_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_block_gemm_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_block_gemm_error_flags, flags);
 }
 
 }  // namespace fp8k

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "error_flag.h"
 #include "kernels.h"
 #include "once_per_device.h"
 
@@ -1287,10 +1288,7 @@ cudaError_t launch_selftest_wait(uint64_t limit_ns, cudaStream_t st) {
 }
 
 cudaError_t read_and_clear_cast_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_cast_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_cast_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_cast_error_flags, flags);
 }
 
 }  // namespace fp8k

@@ -39,6 +39,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "error_flag.h"
 #include "kernels.h"
 #include "once_per_device.h"
 #include "raster.cuh"
@@ -556,10 +557,7 @@ cudaError_t launch_gemm_tn(const uint8_t *A, int fa, const uint8_t *B, int fb, i
 cudaError_t read_and_clear_error_flag(unsigned *flags, cudaStream_t st) {
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return e;
-    e = cudaMemcpyFromSymbol(flags, g_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    e = cudaMemcpyToSymbol(g_error_flags, &zero, sizeof(unsigned));
+    e = take_error_flags(&g_error_flags, flags);
     if (e != cudaSuccess) return e;
     unsigned cast_flags = 0, sum_flags = 0;
     e = read_and_clear_cast_error_flag(&cast_flags);

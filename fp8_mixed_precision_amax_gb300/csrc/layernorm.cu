@@ -11,6 +11,7 @@
 // in its CTA's registers between the sums and the use of the sums.
 #include <cstdint>
 
+#include "error_flag.h"
 #include "norm_rows.cuh"
 #include "once_per_device.h"
 
@@ -735,10 +736,7 @@ cudaError_t launch_ln_bwd(const MatView &dy, const MatView &x, const BlockView &
 }
 
 cudaError_t read_and_clear_ln_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_ln_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_ln_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_ln_error_flags, flags);
 }
 
 }  // namespace fp8k

@@ -24,6 +24,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "error_flag.h"
 #include "kernels.h"
 #include "once_per_device.h"
 
@@ -1015,10 +1016,7 @@ cudaError_t launch_dequant_sum(const uint8_t *parts, int nranks, int64_t n, int 
 }
 
 cudaError_t read_and_clear_sum_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_sum_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_sum_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_sum_error_flags, flags);
 }
 
 cudaError_t launch_adam_init(const AdamInitSpec &s, int sm_count, cudaStream_t st) {

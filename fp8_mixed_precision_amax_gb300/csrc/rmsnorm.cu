@@ -16,6 +16,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "error_flag.h"
 #include "norm_rows.cuh"
 #include "once_per_device.h"
 
@@ -1191,10 +1192,7 @@ cudaError_t launch_rms_bwd(const MatView &dy, const MatView &x, const BlockView 
 }
 
 cudaError_t read_and_clear_rms_error_flag(unsigned *flags) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_rms_error_flags, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    const unsigned zero = 0;
-    return cudaMemcpyToSymbol(g_rms_error_flags, &zero, sizeof(unsigned));
+    return take_error_flags(&g_rms_error_flags, flags);
 }
 
 }  // namespace fp8k
