@@ -995,8 +995,8 @@ def fp8_rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float, rstd: torc
                     y: torch.Tensor | None = None, y8: BlockFp8 | None = None,
                     x8: BlockFp8 | None = None, stream=None) -> None:
     """Root-mean-square norm of s = x + residual (x alone without one): rstd (float32), and any
-    of sum (s itself, rounded to x's type, which the norm is taken of; may be x or residual),
-    y (of x's type), y8 (y block quantized) and x8 (s kept in 8 bits for the backward pass)."""
+    of sum (s itself, rounded to x's type, which the norm is taken of), y (of x's type; both may
+    be x or residual), y8 (y block quantized) and x8 (s kept in 8 bits for the backward pass)."""
     xm = _matrix(x, "x")
     rows, cols = x.shape
     _here(x, gamma, rstd, residual, sum, y, y8, x8)
@@ -1011,7 +1011,7 @@ def fp8_rmsnorm_bwd(dy: torch.Tensor, x: "torch.Tensor | BlockFp8", gamma: torch
                     dsum: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                     stream=None) -> None:
     """Backward of the RMS norm from s, the forward's ``sum`` (``x`` without a residual), or its
-    8-bit copy (the forward's ``x8``): dx (of dy's type; may be dy or dsum), the gradient of x
+    8-bit copy (the forward's ``x8``): dx (of dy's type; may be dy, dsum or x), the gradient of x
     and of the residual alike, and dgamma (float32).  ``dsum``: the gradient that reaches s by
     the residual's way.  ``workspace``: at least ``fp8_rmsnorm_bwd_workspace(rows, cols)``
     bytes of CUDA memory; taken from torch's allocator when None."""

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libfp8amax.so")
 SOURCES = ["abi.cu", "block_abi.cu", "block_gated.cu", "block_gemm.cu", "block_quant.cu", "cast.cu", "clip.cu",
            "gemm.cu", "layernorm.cu", "noalloc.cu", "optim.cu", "rmsnorm.cu", "tmap.cu"]
 HEADERS = ["abi_checks.h", "block.cuh", "block_mma.cuh", "common.cuh", "error_flag.h", "kernels.h", "ln_plan.h",
-           "norm_rows.cuh", "once_per_device.h", "raster.cuh"]
+           "norm_rows.cuh", "once_per_device.h", "overlap.h", "raster.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",

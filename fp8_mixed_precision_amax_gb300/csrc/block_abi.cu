@@ -4,6 +4,7 @@
 // 8,388,480 columns, a list of gradients one for every 1000).  No device memory is allocated and
 // the stream is never synchronized.
 #include "abi_checks.h"
+#include "overlap.h"
 
 #include <algorithm>
 #include <memory>
@@ -12,6 +13,8 @@
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;   // as the TMA coordinates allow
+
+int64_t size_of(int32_t type) { return type == FP8_DTYPE_F32 ? 4 : 2; }
 
 fp8_status check_type(const char *fn, int32_t type, const char *name) {
     if (type != FP8_DTYPE_F32 && type != FP8_DTYPE_BF16 && type != FP8_DTYPE_F16)
@@ -106,6 +109,35 @@ fp8_status check_like(const char *fn, const fp8_matrix *m, const fp8k::MatView &
     return FP8_OK;
 }
 
+using fp8k::Area;
+using fp8k::area;
+Area area(const char *name, const fp8k::MatView &m) {
+    const int64_t each = size_of(m.type);
+    return area(name, m.data, m.rows, m.cols * each, m.ld * each, true);
+}
+Area codes_area(const char *name, const fp8k::BlockView &q, bool replace = false) {
+    return area(name, q.codes, q.rows, q.cols, q.ld, replace);
+}
+Area scales_area(const char *name, const fp8k::BlockView &q, bool replace = false) {
+    const int64_t each = q.scale_f32 ? 4 : 1;
+    return area(name, q.scales, q.block_rows > 0 ? (q.rows + q.block_rows - 1) / q.block_rows : 0,
+                (q.cols + 127) / 128 * each, q.ld_s * each, replace);
+}
+
+// What a call writes overlaps neither what else it writes nor what it reads.
+template <int OUTS, int INS>
+fp8_status check_outputs(const char *fn, const Area (&outs)[OUTS], const Area (&ins)[INS]) {
+    for (int i = 0; i < OUTS; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[j], outs[i]))
+                return fail(FP8_ERR_ARG, "%s: %s and %s overlap", fn, outs[j].name, outs[i].name);
+        for (const Area &in : ins)
+            if (meet(outs[i], in) && !same_place(outs[i], in))
+                return fail(FP8_ERR_ARG, "%s: %s and %s overlap", fn, outs[i].name, in.name);
+    }
+    return FP8_OK;
+}
+
 fp8_status check_tiles(const char *fn, int64_t rows, int64_t cols) {
     if (((rows + 127) / 128) * ((cols + 127) / 128) >= kMaxDim)
         return fail(FP8_ERR_ARG, "%s: more than 2^31 tiles", fn);
@@ -148,7 +180,7 @@ struct Span {
 };
 Span span_of(const fp8_vector &v, int32_t i) {
     const uintptr_t from = reinterpret_cast<uintptr_t>(v.data);
-    return {from, from + static_cast<uintptr_t>(v.n) * (v.dtype == FP8_DTYPE_F32 ? 4 : 2), i};
+    return {from, from + static_cast<uintptr_t>(v.n) * size_of(v.dtype), i};
 }
 
 // Each of outs apart from the others, and from all grads but its own, whose place it may take.
@@ -374,6 +406,11 @@ fp8_status fp8_rmsnorm_fwd(const fp8_matrix *x, const fp8_matrix *residual, cons
     FP8_TRY(check_rows_out(fn, y8, vy8, "y8", vx.rows, vx.cols));
     FP8_TRY(check_rows_out(fn, x8, vx8, "x8", vx.rows, vx.cols));
     FP8_TRY(check_scalar(fn, rstd, "rstd", vx.rows == 0));
+    FP8_TRY(check_outputs(fn,
+                          {area("sum", vs), area("y", vy), codes_area("y8's codes", vy8),
+                           scales_area("y8's scales", vy8), codes_area("x8's codes", vx8),
+                           scales_area("x8's scales", vx8), area("rstd", rstd, vx.rows * 4)},
+                          {area("x", vx), area("residual", vr), area("gamma", gamma, vx.cols * size_of(wtype))}));
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_rms_fwd(vx, vr, gamma, wtype, eps, vs, vy, vy8, vx8, rstd, sms,
@@ -416,6 +453,11 @@ fp8_status fp8_rmsnorm_bwd(const fp8_matrix *dy, const fp8_matrix *x, const fp8_
     if (workspace_bytes < need)
         return fail(FP8_ERR_ARG, "%s: workspace of %lld bytes, %lld are needed", fn,
                     static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    FP8_TRY(check_outputs(fn,
+                          {area("dx", vdx), area("dgamma", dgamma, vdy.cols * 4), area("workspace", workspace, need)},
+                          {area("dy", vdy), area("x", vx), codes_area("x8's codes", vx8), scales_area("x8's scales", vx8),
+                           area("dsum", vds), area("rstd", rstd, vdy.rows * 4),
+                           area("gamma", gamma, vdy.cols * size_of(wtype))}));
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_rms_bwd(vdy, vx, vx8, gamma, wtype, rstd, vds, vdx, dgamma, workspace, sms,
@@ -437,6 +479,9 @@ fp8_status fp8_rmsnorm_recompute(const fp8_block_tensor *x8, const void *gamma, 
     FP8_TRY(check_param(fn, gamma, wtype, "gamma"));
     FP8_TRY(check_scalar(fn, rstd, "rstd", vx8.rows == 0 || vx8.cols == 0));
     FP8_TRY(check_tiles(fn, vx8.rows, vx8.cols));
+    FP8_TRY(check_outputs(fn, {codes_area("yt's codes", vyt), scales_area("yt's scales", vyt)},
+                          {codes_area("x8's codes", vx8), scales_area("x8's scales", vx8),
+                           area("rstd", rstd, vx8.rows * 4), area("gamma", gamma, vx8.cols * size_of(wtype))}));
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_rms_recompute(vx8, gamma, wtype, rstd, vyt, sms,

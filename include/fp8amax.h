@@ -569,9 +569,11 @@ fp8_status fp8_layernorm_recompute(const fp8_block_tensor *x8, const void *gamma
  * sum, s itself (with a residual only); y (both of x's type); y8, y block
  * quantized straight from fp32 (block_rows 1), the operand of a following product;
  * x8, s in 8 bits (block_rows 1), which fp8_rmsnorm_bwd and
- * fp8_rmsnorm_recompute take in s's place.  residual is of x's type; sum may be
- * x's or the residual's own memory (same address and stride), the other outputs
- * overlap nothing.  gamma [cols] is of type wtype (fp8_dtype).  cols >= 1. */
+ * fp8_rmsnorm_recompute take in s's place.  residual is of x's type; sum and y may
+ * each be x's or the residual's own memory (same address and stride).  Outputs that
+ * overlap each other, or an input in any other way, are refused (FP8_ERR_ARG), as in
+ * the two calls below; rows may lie between another matrix's.  gamma [cols] is of
+ * type wtype (fp8_dtype).  cols >= 1. */
 fp8_status fp8_rmsnorm_fwd(const fp8_matrix *x, const fp8_matrix *residual, const void *gamma,
                            int32_t wtype, float eps, const fp8_matrix *sum, const fp8_matrix *y,
                            const fp8_block_tensor *y8, const fp8_block_tensor *x8, float *rstd,
@@ -584,7 +586,7 @@ fp8_status fp8_rmsnorm_fwd(const fp8_matrix *x, const fp8_matrix *residual, cons
  *   dgamma = sum over rows of dy * xhat.
  * dsum: the gradient that reaches s by the residual's way (NULL: none).  dx is the
  * gradient of x and of the residual alike.  dy, x, dsum and dx are of one type;
- * dgamma is fp32 [cols], overwritten; dx may be dy or dsum (same address and
+ * dgamma is fp32 [cols], overwritten; dx may be dy, dsum or x (same address and
  * stride).  workspace: DEVICE, 16-byte aligned, of at least
  * fp8_rmsnorm_bwd_workspace(rows, cols) bytes, in use until the call's kernels
  * are done.  The sums' order is fixed: equal calls give equal bits. */

@@ -1,0 +1,99 @@
+"""GPU tests of calls whose arguments lie between each other's rows in one buffer, or take an
+input's very place: they share nothing, or what they may, and give the same bits as in
+buffers of their own."""
+import pytest
+import torch
+
+from test_gpu_rmsnorm import EPS, _lib, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def interleaved(rows, *cols, dtype=torch.bfloat16, gap=0):
+    """Matrices side by side in the rows of one buffer."""
+    wide = torch.full((rows, sum(cols) + gap * len(cols)), 9, dtype=dtype, device="cuda")
+    out, at = [], 0
+    for c in cols:
+        out.append(wide[:, at:at + c])
+        at += c + gap
+    return out
+
+
+def held(rows, cols):
+    """An 8-bit matrix whose codes and scales share the rows of one buffer."""
+    pitch, words = -(-cols // 16) * 16, -(-cols // 512) * 4
+    wide = torch.zeros(rows, -(-(pitch + words) // 16) * 16, dtype=torch.uint8, device="cuda")
+    return _lib().BlockFp8(wide[:, :pitch], wide[:, pitch:pitch + words], cols)
+
+
+def same(p, q):
+    nb = -(-p.cols // 128)
+    assert torch.equal(p.codes[:, :p.cols], q.codes[:, :q.cols]) and torch.equal(p.scales[:, :nb], q.scales[:, :nb])
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 64), (37, 301), (300, 4096), (200, 8200), (50, 16400)])
+@pytest.mark.parametrize("gap", [0, 3])
+def test_rmsnorm_between_each_others_rows(rows, cols, gap):
+    f = _lib()
+    x0, r0, gamma = inputs(rows, cols, torch.bfloat16, torch.float32, cols)
+    x, r, total, y, dsum, dx = interleaved(rows, *[cols] * 6, gap=gap)
+    x.copy_(x0), r.copy_(r0), dsum.copy_(r0)
+    small = torch.empty(rows + cols + 8, device="cuda")
+    rstd, dgamma = small[:rows], small[rows:rows + cols]
+    y8, x8 = held(rows, cols), held(rows, cols)
+    f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, residual=r, sum=total, y=y, y8=y8, x8=x8)
+    f.fp8_rmsnorm_bwd(y, total, gamma, rstd, dx, dgamma, dsum=dsum)
+    yt = f.BlockFp8.empty(cols, rows)
+    f.fp8_rmsnorm_recompute(x8, gamma, rstd, yt)
+    # each in a buffer of its own, in the same place within it, so that sums have the same order
+    places = [interleaved(rows, *[cols] * 6, gap=gap)[k] for k in range(6)]
+    x2, r2, total2, y2, dsum2, dx2 = places
+    x2.copy_(x0), r2.copy_(r0), dsum2.copy_(r0)
+    rstd2, dgamma2 = torch.empty(rows, device="cuda"), torch.empty(cols, device="cuda")
+    y82, x82, yt2 = f.BlockFp8.empty(rows, cols), f.BlockFp8.empty(rows, cols), f.BlockFp8.empty(cols, rows)
+    f.fp8_rmsnorm_fwd(x2, gamma, EPS, rstd2, residual=r2, sum=total2, y=y2, y8=y82, x8=x82)
+    f.fp8_rmsnorm_bwd(y2, total2, gamma, rstd2, dx2, dgamma2, dsum=dsum2)
+    f.fp8_rmsnorm_recompute(x82, gamma, rstd2, yt2)
+    f.fp8_sync_status()
+    for p, q in ((x, x2), (r, r2), (total, total2), (y, y2), (dsum, dsum2), (dx, dx2), (rstd, rstd2), (dgamma, dgamma2)):
+        assert torch.equal(p, q)
+    same(y8, y82), same(x8, x82), same(yt, yt2)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 8), (1300, 512), (700, 301), (900, 4096), (300, 8200), (300, 12288), (200, 16400)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rmsnorm_in_an_inputs_very_place(rows, cols, dtype):
+    """sum and y in x's and in the residual's place, dx in x's and in dy's."""
+    f = _lib()
+    x, r, gamma = inputs(rows, cols, dtype, torch.float32, cols)
+    e = torch.empty_like
+    rstd, total, y, dx, dg = torch.empty(rows, device="cuda"), e(x), e(x), e(x), torch.empty(cols, device="cuda")
+    f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, residual=r, sum=total, y=y)
+    f.fp8_rmsnorm_bwd(y, total, gamma, rstd, dx, dg, dsum=r)
+    for k in range(2):
+        a, b = x.clone(), r.clone()
+        f.fp8_rmsnorm_fwd(a, gamma, EPS, rstd, residual=b, sum=(a, b)[k], y=(b, a)[k])
+        c, d, s = y.clone(), r.clone(), total.clone()
+        out, dg2 = (s, c)[k], torch.empty_like(dg)
+        f.fp8_rmsnorm_bwd(c, s, gamma, rstd, out, dg2, dsum=d)
+        f.fp8_sync_status()
+        assert torch.equal((a, b)[k], total) and torch.equal((b, a)[k], y)
+        assert torch.equal(out, dx) and torch.equal(dg2, dg)
+
+
+def test_calls_that_overlap_are_refused():
+    f = _lib()
+    rows, cols = 6, 64
+    wide = torch.ones(rows, 200, dtype=torch.bfloat16, device="cuda")
+    gamma, rstd = torch.ones(cols, device="cuda"), torch.empty(rows, device="cuda")
+    x, dg = wide[:, :cols], torch.empty(cols, device="cuda")
+    for kw in (dict(residual=wide[:, 100:164], sum=wide[:, 8:72]), dict(y=wide[:, 63:127]), dict(y=wide[:, :cols], residual=x, sum=x)):
+        with pytest.raises(f.Fp8Error, match="overlap"):
+            f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, **kw)
+    q = f.BlockFp8.empty(rows, cols)
+    with pytest.raises(f.Fp8Error, match="overlap"):
+        f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, y8=q, x8=q)
+    with pytest.raises(f.Fp8Error, match="overlap"):
+        f.fp8_rmsnorm_bwd(x, x, gamma, rstd, wide[:, 1:65], dg)
+    f.fp8_sync_status()
+    assert (wide == 1).all()

@@ -1,0 +1,90 @@
+"""Refusals of calls whose outputs share memory with each other, or with an input in any other
+way than in its very place: found on the host, before any CUDA call (CPU only).  Calls that
+share nothing are tested where a GPU runs them."""
+import pytest
+
+import fp8_mixed_precision_amax_gb300 as f
+from test_block_abi import ERR_ARG, refused
+from test_host_setup import run_check
+from fp8_mixed_precision_amax_gb300 import api
+
+BASE = 1 << 32
+
+
+def test_areas_against_a_table_of_bytes(tmp_path):
+    run_check("overlap_check", tmp_path)
+
+
+class Memory:
+    """Places far apart from each other, for arguments that share nothing."""
+
+    def __init__(self):
+        self.next = BASE
+
+    def place(self):
+        self.next += 1 << 24
+        return self.next
+
+    def mat(self, rows, cols, ld=None, at=None, dtype=1):
+        return api.fp8_matrix(self.place() if at is None else at, rows, cols, ld or cols, dtype)
+
+    def blk(self, rows, cols, codes=None, scales=None, br=1):
+        return api.fp8_block_tensor(codes or self.place(), rows, cols, -(-cols // 16) * 16,
+                                    scales or self.place(), -(-cols // 512) * 4, 0, br, 0)
+
+
+def rms_fwd(m, rows=50, cols=100, **k):
+    a = dict(x=m.mat(rows, cols), residual=m.mat(rows, cols), gamma=m.place(), wtype=0, eps=1e-5, sum=m.mat(rows, cols),
+             y=m.mat(rows, cols), y8=m.blk(rows, cols), x8=m.blk(rows, cols), rstd=m.place())
+    a.update(k)
+    return list(a.values())
+
+
+def rms_bwd(m, rows=50, cols=100, **k):
+    a = dict(dy=m.mat(rows, cols), x=m.mat(rows, cols), x8=None, gamma=m.place(), wtype=0, rstd=m.place(),
+             dsum=m.mat(rows, cols), dx=m.mat(rows, cols), dgamma=m.place(), workspace=m.place(),
+             room=f.fp8_rmsnorm_bwd_workspace(rows, cols))
+    a.update(k)
+    return list(a.values())
+
+
+def test_rmsnorm_forward():
+    m = Memory()
+    at, other = m.place(), m.place()
+    for words, k in [
+            ("sum and x overlap", dict(x=m.mat(50, 100, at=at), sum=m.mat(50, 100, at=at + 2))),
+            ("sum and x overlap", dict(x=m.mat(50, 100, at=at), sum=m.mat(50, 100, ld=104, at=at))),
+            ("sum and residual overlap", dict(residual=m.mat(50, 100, 120, at=at), sum=m.mat(50, 100, 120, at=at - 198))),
+            ("sum and residual overlap", dict(residual=m.mat(50, 100, 120, at=at), sum=m.mat(50, 100, 120, at=at + 42))),
+            ("y and x overlap", dict(x=m.mat(50, 100, at=at), y=m.mat(50, 100, at=at + 9998))),
+            ("sum and y overlap", dict(sum=m.mat(50, 100, at=at), y=m.mat(50, 100, at=at))),
+            ("y8's codes and x8's codes overlap", dict(y8=m.blk(50, 100, codes=at), x8=m.blk(50, 100, codes=at))),
+            ("y8's scales and x8's scales overlap", dict(y8=m.blk(50, 100, scales=at), x8=m.blk(50, 100, scales=at))),
+            ("y8's codes and y8's scales overlap", dict(y8=m.blk(50, 100, codes=at, scales=at + 16))),
+            ("x8's codes and x overlap", dict(x=m.mat(50, 100, at=at), x8=m.blk(50, 100, codes=at))),
+            ("rstd and gamma overlap", dict(gamma=at, rstd=at + 4 * 99)),
+            ("x8's scales and rstd overlap", dict(x8=m.blk(50, 100, scales=at), rstd=at + 4 * 49))]:
+        refused(ERR_ARG, words, "fp8_rmsnorm_fwd", *rms_fwd(m, **k))
+    # one row's stride says nothing, and a shifted row is no place of its own
+    refused(ERR_ARG, "sum and x overlap", "fp8_rmsnorm_fwd",
+            *rms_fwd(m, 1, 8, x=m.mat(1, 8, 50, at=other), sum=m.mat(1, 8, 8, at=other + 4)))
+
+
+def test_rmsnorm_backward_and_recompute():
+    m = Memory()
+    at = m.place()
+    need = f.fp8_rmsnorm_bwd_workspace(50, 100)
+    for words, k in [
+            ("dx and dy overlap", dict(dy=m.mat(50, 100, at=at), dx=m.mat(50, 100, at=at + 200))),
+            ("dx and dsum overlap", dict(dsum=m.mat(50, 100, 128, at=at), dx=m.mat(50, 100, 136, at=at))),
+            ("dx and x overlap", dict(x=m.mat(50, 100, at=at), dx=m.mat(50, 100, at=at + 2))),
+            ("dx and x8's codes overlap", dict(x=None, x8=m.blk(50, 100, codes=at), dx=m.mat(50, 100, at=at))),
+            ("dgamma and gamma overlap", dict(gamma=at, dgamma=at)),
+            ("dgamma and workspace overlap", dict(dgamma=at + need - 4, workspace=at)),
+            ("dx and workspace overlap", dict(dx=m.mat(50, 100, at=at), workspace=at + 9984)),
+            ("workspace and rstd overlap", dict(rstd=at + 16, workspace=at))]:
+        refused(ERR_ARG, words, "fp8_rmsnorm_bwd", *rms_bwd(m, **k))
+    for words, x8, yt in [("yt's codes and x8's codes", m.blk(64, 64, codes=at), m.blk(64, 64, codes=at)),
+                          ("yt's scales and x8's scales", m.blk(64, 64, scales=at), m.blk(64, 64, scales=at)),
+                          ("yt's codes and yt's scales", m.blk(64, 64), m.blk(64, 64, codes=at, scales=at + 4092))]:
+        refused(ERR_ARG, words, "fp8_rmsnorm_recompute", x8, m.place(), 0, m.place(), yt)
