@@ -570,6 +570,11 @@ fp8_status fp8_block_gemm_swiglu_fwd(const fp8_block_tensor *A, const fp8_block_
     FP8_TRY(check_rows_out(fn, a8, va8, "a8", a.rows, b.rows / 2));
     FP8_TRY(check_rows_out(fn, h8, vh8, "h8", a.rows, b.rows));
     FP8_TRY(check_tiles(fn, a.rows, b.rows));
+    FP8_TRY(check_outputs(fn,
+                          {codes_area("a8's codes", va8), scales_area("a8's scales", va8),
+                           codes_area("h8's codes", vh8), scales_area("h8's scales", vh8)},
+                          {codes_area("A's codes", a), scales_area("A's scales", a), codes_area("B's codes", b),
+                           scales_area("B's scales", b)}));
     int sms;
     FP8_TRY(current_device(&sms));
     const char *what = nullptr;
@@ -607,6 +612,13 @@ fp8_status fp8_block_gemm_swiglu_bwd(const fp8_block_tensor *A, const fp8_block_
     if (dh8 != nullptr && dh8t != nullptr && vdh8.fmt != vdh8t.fmt)
         return fail(FP8_ERR_ARG, "%s: dh8 and dh8t differ in format", fn);
     FP8_TRY(check_tiles(fn, M, F));
+    FP8_TRY(check_outputs(fn,
+                          {codes_area("dh8's codes", vdh8, true), scales_area("dh8's scales", vdh8, true),
+                           codes_area("dh8t's codes", vdh8t), scales_area("dh8t's scales", vdh8t),
+                           codes_area("a8t's codes", va8t), scales_area("a8t's scales", va8t)},
+                          {codes_area("A's codes", a), scales_area("A's scales", a), codes_area("B's codes", b),
+                           scales_area("B's scales", b), codes_area("h8's codes", vh8, true),
+                           scales_area("h8's scales", vh8, true)}));
     int sms;
     FP8_TRY(current_device(&sms));
     const char *what = nullptr;

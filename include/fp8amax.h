@@ -628,7 +628,8 @@ fp8_status fp8_swiglu_bwd(const fp8_matrix *da, const fp8_block_tensor *h8,
  *   a = g / (1 + exp(-g)) * u,
  * a block quantized into a8 [M][F], and [g | u] into h8 [M][2F] (or NULL) for
  * fp8_block_gemm_swiglu_bwd, both straight from fp32 (block_rows 1).  F a multiple
- * of 128, K >= 1, M >= 0.  fp8_block_gemm_tn and fp8_swiglu_fwd do the same in two steps
+ * of 128, K >= 1, M >= 0.  What is written overlaps nothing else (FP8_ERR_ARG where
+ * it does; rows may lie between another tensor's).  fp8_block_gemm_tn and fp8_swiglu_fwd do the same in two steps
  * with h in between, which serves float scales and one wanting h. */
 fp8_status fp8_block_gemm_swiglu_fwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
                                      const fp8_block_tensor *a8, const fp8_block_tensor *h8,
@@ -640,8 +641,9 @@ fp8_status fp8_block_gemm_swiglu_fwd(const fp8_block_tensor *A, const fp8_block_
  *   d g = da * u * s * (1 + g * (1 - s)),  d u = da * (g * s)
  * block quantized into dh8 [M][2F] and dh8t [2F][M], and a again, g * s * u, into
  * a8t [F][M]: what fp8_swiglu_bwd writes, from the product itself, in one kernel.
- * All block_rows 1; any of the three may be NULL, not all; dh8 and dh8t have the
- * same format. */
+ * The outputs' block_rows and h8's are 1; any of the three may be NULL, not all; dh8
+ * and dh8t have the same format.  dh8 may be h8's own memory (same addresses and
+ * strides); otherwise what is written overlaps nothing else, as above. */
 fp8_status fp8_block_gemm_swiglu_bwd(const fp8_block_tensor *A, const fp8_block_tensor *B,
                                      const fp8_block_tensor *h8, const fp8_block_tensor *dh8,
                                      const fp8_block_tensor *dh8t, const fp8_block_tensor *a8t,

@@ -4,6 +4,7 @@ buffers of their own."""
 import pytest
 import torch
 
+from test_gpu_gated import held as filled
 from test_gpu_rmsnorm import EPS, _lib, inputs
 
 pytestmark = pytest.mark.gpu
@@ -97,3 +98,27 @@ def test_calls_that_overlap_are_refused():
         f.fp8_rmsnorm_bwd(x, x, gamma, rstd, wide[:, 1:65], dg)
     f.fp8_sync_status()
     assert (wide == 1).all()
+
+
+@pytest.mark.parametrize("M,F,K", [(5, 256, 200), (300, 640, 512), (1100, 1408, 256), (2100, 2688, 300)])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_gated_product_between_rows_and_in_place(M, F, K, fmt):
+    """Outputs whose codes and scales share a buffer's rows; dh8 in h8's place; an infinite value
+    among them, which takes a second pass over its rows."""
+    f = _lib()
+    A, B, W = filled(M, K, 1.0, 0, 1, 1), filled(2 * F, K, 1.5 * K ** -0.5, 0, 128, 2), filled(F, K, K ** -0.5, 0, 128, 4)
+    a8, h8, e = held(M, F), held(M, 2 * F), f.BlockFp8.empty
+    f.fp8_block_gemm_swiglu_fwd(A, B, a8, h8)
+    a82, h82 = e(M, F), e(M, 2 * F)
+    f.fp8_block_gemm_swiglu_fwd(A, B, a82, h82)
+    same(a8, a82), same(h8, h82)
+    h8.fmt = h82.fmt = fmt   # as E5M2 the same bytes are other values, infinities among them
+    if fmt:
+        h8.codes[0, 3] = h82.codes[0, 3] = 0x7C
+    dh8, dh8t, a8t = e(M, 2 * F, fmt), e(2 * F, M, fmt), e(F, M)
+    f.fp8_block_gemm_swiglu_bwd(A, W, h82, dh8, dh8t, a8t)
+    dh8t2, a8t2 = held(2 * F, M), held(F, M)
+    dh8t2.fmt = fmt
+    f.fp8_block_gemm_swiglu_bwd(A, W, h8, f.BlockFp8(h8.codes, h8.scales, 2 * F, fmt), dh8t2, a8t2)
+    f.fp8_sync_status()
+    same(h8, dh8), same(dh8t2, dh8t), same(a8t2, a8t)

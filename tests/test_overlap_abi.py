@@ -88,3 +88,33 @@ def test_rmsnorm_backward_and_recompute():
                           ("yt's scales and x8's scales", m.blk(64, 64, scales=at), m.blk(64, 64, scales=at)),
                           ("yt's codes and yt's scales", m.blk(64, 64), m.blk(64, 64, codes=at, scales=at + 4092))]:
         refused(ERR_ARG, words, "fp8_rmsnorm_recompute", x8, m.place(), 0, m.place(), yt)
+
+
+def gated(m, backward, **k):
+    a = dict(A=m.blk(60, 200), B=m.blk(128 if backward else 256, 200, br=128))
+    a |= dict(h8=m.blk(60, 256), dh8=m.blk(60, 256), dh8t=m.blk(256, 60), a8t=m.blk(128, 60)) if backward else \
+        dict(a8=m.blk(60, 128), h8=m.blk(60, 256))
+    a.update(k)
+    return list(a.values())
+
+
+def test_gated_product():
+    m = Memory()
+    at = m.place()
+    for words, k in [
+            ("a8's codes and h8's codes overlap", dict(a8=m.blk(60, 128, at), h8=m.blk(60, 256, at + 128))),
+            ("a8's codes and a8's scales overlap", dict(a8=m.blk(60, 128, at, at + 16))),
+            ("a8's scales and h8's scales overlap", dict(a8=m.blk(60, 128, scales=at), h8=m.blk(60, 256, scales=at))),
+            ("a8's codes and A's codes overlap", dict(A=m.blk(60, 128, at), B=m.blk(256, 128), a8=m.blk(60, 128, at))),
+            ("h8's codes and A's scales overlap", dict(A=m.blk(60, 200, scales=at + 64), h8=m.blk(60, 256, at))),
+            ("h8's codes and B's codes overlap", dict(B=m.blk(256, 200, at, br=128), h8=m.blk(60, 256, at + 256 * 208 - 16)))]:
+        refused(ERR_ARG, words, "fp8_block_gemm_swiglu_fwd", *gated(m, False, **k))
+    for words, k in [
+            ("dh8's codes and dh8t's codes overlap", dict(dh8=m.blk(60, 256, at), dh8t=m.blk(256, 60, at))),
+            ("dh8t's scales and a8t's scales overlap", dict(dh8t=m.blk(256, 60, scales=at), a8t=m.blk(128, 60, scales=at))),
+            ("dh8's codes and h8's codes overlap", dict(h8=m.blk(60, 256, at), dh8=m.blk(60, 256, at + 256))),
+            ("dh8's scales and h8's scales overlap", dict(h8=m.blk(60, 256, scales=at), dh8=m.blk(60, 256, scales=at + 4))),
+            ("a8t's codes and A's codes overlap", dict(A=m.blk(60, 200, at), a8t=m.blk(128, 60, at))),
+            ("dh8t's codes and B's codes overlap", dict(B=m.blk(128, 200, at, br=128), dh8t=m.blk(256, 60, at))),
+            ("a8t's codes and h8's codes overlap", dict(h8=m.blk(60, 256, at), a8t=m.blk(128, 60, at)))]:
+        refused(ERR_ARG, words, "fp8_block_gemm_swiglu_bwd", *gated(m, True, **k))
