@@ -183,8 +183,10 @@ Span span_of(const fp8_vector &v, int32_t i) {
     return {from, from + static_cast<uintptr_t>(v.n) * size_of(v.dtype), i};
 }
 
-// Each of outs apart from the others, and from all grads but its own, whose place it may take.
-fp8_status check_apart(const char *fn, const fp8_vector *grads, const fp8_vector *outs, int32_t count) {
+// Each of outs apart from the others, from the norm, and from all grads but its own, whose place
+// it may take.
+fp8_status check_apart(const char *fn, const fp8_vector *grads, const fp8_vector *outs, int32_t count,
+                       const float *norm) {
     Span few[64];
     std::unique_ptr<Span[]> many(count > 64 ? new (std::nothrow) Span[count] : nullptr);
     Span *s = count > 64 ? many.get() : few;
@@ -196,15 +198,21 @@ fp8_status check_apart(const char *fn, const fp8_vector *grads, const fp8_vector
     for (int32_t k = 1; k < n; ++k)
         if (s[k].from < s[k - 1].to)
             return fail(FP8_ERR_ARG, "%s: outs[%d] and outs[%d] overlap", fn, s[k - 1].i, s[k].i);
-    if (outs == grads) return FP8_OK;
-    for (int32_t j = 0; j < count; ++j) {
+    const auto first_past = [&](uintptr_t place) {   // the first of them that ends behind it
+        return std::upper_bound(s, s + n, place, [](uintptr_t v, const Span &x) { return v < x.to; });
+    };
+    for (int32_t j = 0; j < count && outs != grads; ++j) {
         if (grads[j].n == 0) continue;
         const Span g = span_of(grads[j], j);
-        const Span *at = std::upper_bound(s, s + n, g.from, [](uintptr_t v, const Span &x) { return v < x.to; });
+        const Span *at = first_past(g.from);
         for (; at < s + n && at->from < g.to; ++at)
             if (at->i != j || at->from != g.from || outs[j].dtype != grads[j].dtype)
                 return fail(FP8_ERR_ARG, "%s: outs[%d] and grads[%d] overlap", fn, at->i, j);
     }
+    const uintptr_t at_norm = reinterpret_cast<uintptr_t>(norm);
+    const Span *over = first_past(at_norm);
+    if (over < s + n && over->from < at_norm + sizeof *norm)
+        return fail(FP8_ERR_ARG, "%s: outs[%d] and norm overlap", fn, over->i);
     return FP8_OK;
 }
 
@@ -643,6 +651,11 @@ fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, vo
     if (workspace_bytes < need)
         return fail(FP8_ERR_ARG, "%s: workspace of %lld bytes, %lld are needed", fn,
                     static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    const Area ws = area("workspace", workspace, need);
+    if (meet(ws, area("norm", norm, sizeof *norm))) return fail(FP8_ERR_ARG, "%s: norm and workspace overlap", fn);
+    for (int32_t i = 0; i < count; ++i)
+        if (meet(ws, area("grads", grads[i].data, grads[i].n * size_of(grads[i].dtype))))
+            return fail(FP8_ERR_ARG, "%s: grads[%d] and workspace overlap", fn, i);
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_grad_norm(reinterpret_cast<const fp8k::VectorView *>(grads), count, norm,
@@ -664,7 +677,7 @@ fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_
                         static_cast<long long>(outs[i].n), i, static_cast<long long>(grads[i].n));
     FP8_TRY(check_scalar(fn, norm, "norm", false));
     if (!(max_norm >= 0.0f)) return fail(FP8_ERR_ARG, "%s: max_norm must be >= 0", fn);
-    FP8_TRY(check_apart(fn, grads, outs, count));
+    FP8_TRY(check_apart(fn, grads, outs, count, norm));
     int sms;
     FP8_TRY(current_device(&sms));
     FP8_CUDA(fp8k::launch_grad_clip(reinterpret_cast<const fp8k::VectorView *>(grads),

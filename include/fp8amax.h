@@ -666,7 +666,8 @@ typedef struct {
  * in 64 bits.  A NaN or an infinity among the elements gives NaN or infinity, no
  * elements 0.  grads: HOST array of count vectors (count >= 0), read before the call
  * returns.  workspace: DEVICE, 8-byte aligned, of at least
- * fp8_grad_norm_workspace(count) bytes, in use until the call's kernels are done.
+ * fp8_grad_norm_workspace(count) bytes, in use until the call's kernels are done;
+ * it overlaps neither norm nor a vector (FP8_ERR_ARG).
  * The sums' order is fixed: equal calls give equal bits.  One kernel for each 1000
  * vectors, and one that joins their sums; for few elements one alone. */
 fp8_status fp8_grad_norm(const fp8_vector *grads, int32_t count, float *norm, void *workspace,
@@ -679,8 +680,8 @@ int64_t fp8_grad_norm_workspace(int32_t count);
  * so that gradients whose norm is not finite pass through as they are (the caller
  * sees it by the norm, and skips the step).  outs (NULL: grads, in place): HOST
  * array of count vectors of the grads' lengths; outs[i] may be grads[i] (same
- * address and type), and overlaps no other vector (FP8_ERR_ARG where it does: a
- * gradient is twice in the list).  max_norm >= 0.  One kernel for each 1000
+ * address and type), and overlaps no other vector and not norm (FP8_ERR_ARG where
+ * it does: a gradient is twice in the list).  max_norm >= 0.  One kernel for each 1000
  * vectors. */
 fp8_status fp8_grad_clip(const fp8_vector *grads, const fp8_vector *outs, int32_t count,
                          const float *norm, float max_norm, void *stream);

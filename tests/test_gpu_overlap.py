@@ -122,3 +122,27 @@ def test_gated_product_between_rows_and_in_place(M, F, K, fmt):
     f.fp8_block_gemm_swiglu_bwd(A, W, h8, f.BlockFp8(h8.codes, h8.scales, 2 * F, fmt), dh8t2, a8t2)
     f.fp8_sync_status()
     same(h8, dh8), same(dh8t2, dh8t), same(a8t2, a8t)
+
+
+def test_norm_beside_the_gradients_it_is_of():
+    """The norm, the gradients and the clipped ones one behind the other in one buffer."""
+    f = _lib()
+    flat = torch.randn(5000, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    grads, norm, outs = [flat[:1000], flat[1000:2000]], flat[2000:2001], [flat[2001:3001], flat[3001:4001]]
+    want = flat[:2000].double().norm()
+    kept = flat.clone()
+    f.fp8_grad_norm(grads, norm)
+    f.fp8_grad_clip(grads, norm, 1.0, outs)
+    f.fp8_sync_status()
+    assert abs(norm.item() - want) <= 2.0 ** -20 * want
+    c = torch.ones(1, device="cuda") / norm
+    assert torch.equal(flat[2001:4001], kept[:2000] * c)
+    assert torch.equal(flat[:2000], kept[:2000]) and torch.equal(flat[4001:], kept[4001:])
+    f.fp8_grad_clip(outs, norm, 2.0)
+    for bad in ([flat[1990:2010]], [flat[2000:2001]]):
+        with pytest.raises(f.Fp8Error, match="norm overlap"):
+            f.fp8_grad_clip(bad, norm, 1.0)
+    ws = flat.view(torch.uint8)[4096:]
+    with pytest.raises(f.Fp8Error, match="workspace overlap"):
+        f.fp8_grad_norm(grads, norm, ws)
+    f.fp8_sync_status()

@@ -118,3 +118,16 @@ def test_gated_product():
             ("dh8t's codes and B's codes overlap", dict(B=m.blk(128, 200, at, br=128), dh8t=m.blk(256, 60, at))),
             ("a8t's codes and h8's codes overlap", dict(h8=m.blk(60, 256, at), a8t=m.blk(128, 60, at)))]:
         refused(ERR_ARG, words, "fp8_block_gemm_swiglu_bwd", *gated(m, True, **k))
+
+
+def test_norm_and_clipping():
+    m = Memory()
+    at, elsewhere = m.place(), m.place()
+    v = lambda *places: (api.fp8_vector * len(places))(*[api.fp8_vector(p, 8, 0) for p in places])
+    for norm in (elsewhere, elsewhere + 28):   # its first and its last element
+        refused(ERR_ARG, "outs[1] and norm overlap", "fp8_grad_clip", v(at, elsewhere), None, 2, norm, 1.0)
+        refused(ERR_ARG, "outs[1] and norm overlap", "fp8_grad_clip", v(at, at + 32), v(at, elsewhere), 2, norm, 1.0)
+    room = f.fp8_grad_norm_workspace(2)
+    for ws in (elsewhere - room + 8, elsewhere + 24):
+        refused(ERR_ARG, "grads[1] and workspace overlap", "fp8_grad_norm", v(at, elsewhere), 2, m.place(), ws, room)
+    refused(ERR_ARG, "norm and workspace overlap", "fp8_grad_norm", v(at), 1, elsewhere + 8, elsewhere, room)
