@@ -1241,7 +1241,10 @@ cudaError_t launch_gated_few(const GatedArgs &g, int sm_count, cudaStream_t st, 
     const cudaError_t err = limit.allow(gated_few_kernel<NT, AFMT, HFMT>, C::SMEM);
     if (err != cudaSuccess) return err;
     const int64_t tf = g.F / kTile, tx = (g.M + NT - 1) / NT;
-    // as many CTAs as run at once, with at least two k-blocks each
+    // as many CTAs as the SMs have places for, with at least two k-blocks each.  A cluster stays
+    // within a GPC, so that not all places can be used: with one CTA an SM 152 SMs run 36 clusters
+    // of 4 at once, 28 of 5, 23 of 6, and 15 of 7 or 8.  Those beyond are a second wave (256 x 4096 ->
+    // 1024, 16 clusters of 8: 19.3 us; 512 tokens, 32 of 4: 11.8).
     int64_t splits = static_cast<int64_t>(C::CTAS) * sm_count / (tf * tx);
     if (splits > a.num_kb / 2) splits = a.num_kb / 2;
     if (splits > C::MOST_SPLITS) splits = C::MOST_SPLITS;
@@ -1256,9 +1259,11 @@ cudaError_t launch_gated_few(const GatedArgs &g, int sm_count, cudaStream_t st, 
 // The few kernel takes up to 128 tokens, and more as long as they are so few pair tiles that
 // most SMs would idle, an eighth of the SMs' number.  M x K -> F with h kept, few and pair kernel in us:
 // 128 x 4096 -> 11008 27.8 and 34.2, 128 x 1000 -> 2688 9.2 and 9.4; 512 x 4096 -> 1024 (16
-// pair tiles) 11.7 and 15.6, 129 x 4096 -> 1024 (8) 11.7 and 15.5, 200 x 4096 -> 1024 (8) 16.7 and
-// 15.5; 256 x 1000 -> 2688 (21) 10.1 and 9.4, 600 x 1024 -> 1024 (24) 9.4 and 9.2, 777 x 1000 -> 2688
-// (84) 15.9 and 13.1.
+// pair tiles) 11.8 and 15.7, 129 x 4096 -> 1024 (8) 11.8 and 15.4, 256 x 4096 -> 2048 (16) 12.2 and 17.5;
+// 256 x 1000 -> 2688 (21) 10.1 and 9.4, 600 x 1024 -> 1024 (24) 9.4 and 9.2, 777 x 1000 -> 2688
+// (84) 15.9 and 13.1.  The rule does not see the second wave of clusters, and takes the slower
+// kernel where there is one with work: 200 x 4096 -> 1024 16.8 and 15.4, 256 x 4096 -> 1024 19.3
+// and 15.5, 256 x 1000 -> 2432 (19; 38 clusters of 4) 17.2 and 9.4.
 constexpr int64_t kFewTokens = 128;
 
 template <int AFMT, int HFMT>

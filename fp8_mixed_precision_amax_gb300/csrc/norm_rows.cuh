@@ -11,8 +11,9 @@ namespace fp8k {
 // whole CTA.  Thread i of the team holds columns E (i + k team) .. + E - 1 for k < VPT,
 // as packed pairs.  VEC is E where rows are 16-byte aligned and a multiple of E columns
 // long, and 0 where anything goes (then E = 8).  The forward takes 16: fewer lanes
-// share a block's maximum.  The backward takes 8 like the general case, so that its
-// sums are the same bits at any alignment.
+// share a block's maximum.  LayerNorm's backward takes 8 like the general case, so that its
+// sums are the same bits at any alignment.  (RMS norm's rows of up to 8192 columns that start
+// anywhere have another order, 32 columns apart: other bits than the same values aligned.)
 
 template <typename T, int VEC>
 struct Lay {

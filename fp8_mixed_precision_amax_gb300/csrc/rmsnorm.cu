@@ -11,8 +11,14 @@
 // dsum is the gradient that reaches s on the residual's way (0 where it is not given);
 // x and the residual have the same gradient, dx.
 //
-// Both are bound by HBM: each value is read and written once, and a row stays in its
-// CTA's registers between the sum and the use of the sum.
+// Both are bound by HBM.  Forward, up to 16384 columns, and backward, up to 8192, a row stays
+// in its CTA's registers between the sum and the use of the sum, and each value is read and
+// written once; backward, aligned rows of up to 16384 columns wait in shared memory and are
+// read from there twice.  Longer rows, and unaligned ones past 8192 columns backward, are read
+// from memory twice.
+// dgamma: a thread adds its CTA's rows one after the other in fp32 (54 of them at 8192 x 8192),
+// and CTAs' sums are joined by a tree: known to that many and some 2^-24 of the sum of the terms'
+// magnitudes.
 #include <cstdint>
 #include <type_traits>
 
@@ -176,7 +182,10 @@ __device__ __forceinline__ void rms_finish(const RmsFwdArgs &a, T *yr, const Row
 // half of the issue slots are busy, and 16 warps an SM (118 registers) do not hide the way from a
 // row's sum to its codes any better.  One row of 4096 2.3 us.
 // (A warp's rows in fp32 have more registers and one CTA an SM: with two they spill, 16384 x 512
-// 28.3 us and 24.6; in 16 bits 12.7 with two and 15.6.)
+// 28.3 us and 24.6; in 16 bits 12.7 with two and 15.6.  A CTA's rows spill and have two all the
+// same.  fp32 with a residual, 256 threads, 336 bytes: 16384 x 2048 with sum and y 91.7 us, with
+// one CTA 119.3; 8192 x 4096 91.6 and 87.6.  16 bits, 320 threads, 152 bytes and with a residual 392:
+// see kFwdHalf.  Unaligned rows past 8192 columns with a residual spill 156 bytes, in fp32 384.)
 template <typename T, int VPT, int THREADS, bool WARP, int VEC, bool RES>
 __global__ void __launch_bounds__(THREADS, (WARP && sizeof(T) == 4) || THREADS > kFwdHalf ? 1 : 2)
     rms_fwd_kernel(const RmsFwdArgs a) {
@@ -912,7 +921,10 @@ template <typename T, int VEC>
 constexpr int kNarrowCtas = sizeof(T) == 2 && VEC != 0 ? kNarrowMost : 2;   // more would spill
 
 // Narrow rows (WARP) and wide ones.  Rows in turn; a thread keeps its columns and their sums
-// over the CTA's rows.  WIDE: blockIdx.y, and blockIdx.z where there are more than 65535, is a
+// over the CTA's rows.  Wide: bounded as for 512 threads, of which 256 start, so that two CTAs
+// fit an SM; all but aligned 16-bit rows spill 208 to 596 bytes then (with dsum, as it is and
+// bounded by 256: bf16 4000 x 20000 186.5 and 211 us, 4000 x 12001 239 and 190; fp32 4000 x 20000
+// 340 and 309, 2000 x 20001 278 and 198).  WIDE: blockIdx.y, and blockIdx.z where there are more than 65535, is a
 // slab of 8 VPT blockDim.x columns, and the rows' sums are already there.
 template <typename T, bool SAVED, int VPT, bool WARP, int VEC>
 __global__ void __launch_bounds__(WARP ? 32 * kWarps : 512, WARP ? kNarrowCtas<T, VEC> : 1)
@@ -1034,7 +1046,8 @@ __global__ void __launch_bounds__(1024) rms_bwd_reduce_kernel(const float *__res
 
 // --------------------------------------------------------------------- host --
 
-// CTAs that the registers allow at once: 96 of them per thread, or 128
+// CTAs that the registers allow at once: 96 of them per thread, or 128.  (A warp's fp32 rows
+// take up to 180, and their grid is two waves: 16384 x 512 24.8 us, in one 23.7.)
 template <int THREADS>
 int64_t fwd_ctas_per_sm(unsigned threads) {
     return (THREADS == kFwdHalf ? 2 * kFwdHalf : 512) / threads;
