@@ -1,10 +1,9 @@
 """The pre-norm gated MLP layer step by step: each tensor of a pass, kept, shared or returned,
 against 64 bits from the operands that the step before it left.
 
-Tolerances are the operators' own (test_gpu_rmsnorm, test_gpu_rmsnorm_rows,
-test_gpu_gated): a product known to
-(128 + K / 128) 2^-23 of the sum of its terms' magnitudes and half a step of BF16, 2^-8; quantized
-inputs bit for bit."""
+Tolerances are the operators' own (test_gpu_rmsnorm, test_gpu_rmsnorm_rows, test_gpu_gated):
+a product is known to (128 + K / 128) 2^-23 of the sum of its terms' magnitudes and half a step of
+BF16, 2^-8; quantized inputs bit for bit."""
 import pytest
 import torch
 

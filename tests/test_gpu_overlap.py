@@ -80,6 +80,14 @@ def test_rmsnorm_in_an_inputs_very_place(rows, cols, dtype):
         f.fp8_sync_status()
         assert torch.equal((a, b)[k], total) and torch.equal((b, a)[k], y)
         assert torch.equal(out, dx) and torch.equal(dg2, dg)
+    # without a residual, and without the sum being kept
+    f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, y=y)
+    f.fp8_rmsnorm_fwd(x, gamma, EPS, rstd, residual=r, y=total)
+    for res, want in ((None, y), (r, total)):
+        a = x.clone()
+        f.fp8_rmsnorm_fwd(a, gamma, EPS, rstd, residual=res, y=a)
+        f.fp8_sync_status()
+        assert torch.equal(a, want)
 
 
 def test_calls_that_overlap_are_refused():
